@@ -271,9 +271,6 @@ def prepare(case, seed):
         if op == "tree":
             need = qb.tree_workspace_size(st["shape"], st["params"])
             st["ws"] = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
-        if op == "evict":
-            need = qb.kv_evict_workspace_size(B, Hkv, st["Lmax"], d, case["budget"])
-            st["ws"] = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
     return st
 
 
@@ -429,7 +426,7 @@ def run(state):
     if op == "evict":
         c = s["case"]
         qb.kv_evict(s["kc"], s["vc"], s["w"], c["budget"], s["ko"], s["vo"], s["wo"], s["kept"], s["lo"],
-                    s["am"], s["ws"], lengths=s["lengths"], n_sink=c["sink"], n_recent=c["recent"])
+                    s["am"], lengths=s["lengths"], n_sink=c["sink"], n_recent=c["recent"])
         return {k: s[k] for k in ("ko", "vo", "wo", "kept", "lo", "am")}
     qb.tree_commit(s["K"], s["V"], s["path"], s["n"], s["ks"], s["vs"], s["lengths"], s["mean"],
                    s["amax"], s["kc"], s["vc"], lengths_out=s["lengths_out"], k_mean_out=s["mean_out"],
