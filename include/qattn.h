@@ -429,6 +429,150 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
                                   int64_t d, int64_t capacity, float* v_code_amax,
                                   qattn_stream_t stream);
 
+/* Attention of a tree of drafted tokens over an int8 KV cache (speculative
+ * decoding's verification step; the pages have no counterpart).  T = shape->Nq
+ * <= 128 query tokens per sequence attend to the rows in use of the cache and to
+ * the drafted tokens' own K and V, which are not in the cache: K_new and V_new
+ * are encoded on the fly exactly as qattn_kv_append would encode them with the
+ * header as it stands,
+ *   kc = clamp(rint((K - k_mean) / k_chan_scale), -127, 127)
+ *   vc = clamp(rint(V / v_chan_scale), -127, 127)
+ * and cache and header stay as they are until qattn_tree_commit appends the
+ * accepted path.  Per query row, over its visible keys:
+ *   t = S * c,  S the exact int32 score of the codes,
+ *       c = fp32(fp32(sq * sm_scale) * log2 e)
+ *   O = v_chan_scale * sum 2^(t - m) vc / sum 2^(t - m),  m the running max;
+ *       lse = natural log of sum e^(t ln 2)
+ * The PV product takes P = 2^(t - m) <= 1 rounded to fp16 and the V codes as
+ * they are (qattn_decode follows the e4m3 recipe instead); sums and statistics
+ * are fp32.  A row that sees nothing gives O = 0 and lse = -inf.
+ *   q_codes/q_scales  as written by qattn_quantize_qk with k_dtype QATTN_I8
+ *                     (the cache's K channel scales folded in)
+ *   k_codes, v_codes  int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)
+ *   k_chan_scale, v_chan_scale, k_mean  fp32 [B][Hkv][d], the cache's (k_mean
+ *                     and k_chan_scale are read for drafts only)
+ *   lengths           NULL (Nk rows in use everywhere), or int32 [B], device:
+ *                     rows in use per sequence, 0 <= lengths[b] <= Nk
+ *   K_new, V_new      bf16 [B][Hkv][T][d], strides as in the conventions; both
+ *                     or neither.  NULL: the T tokens' rows are in the cache
+ *                     already, and the queries see the cache alone
+ *   tree_mask         NULL, or uint32 [B][T][ceil(T / 32)]: draft j is visible
+ *                     to token i iff bit j % 32 of word j / 32 of row (b, i) is
+ *                     set (j = i itself included).  With drafts and NULL: j <= i
+ *                     if params->causal, else every draft.  Every cached row is
+ *                     visible to every token
+ *   params            causal without drafts: cached row k is visible to token i
+ *                     iff k <= lengths[b] - T + i; q_pos0 must be
+ *                     QATTN_POS0_BOTTOM_RIGHT; q_gran, out_dtype, sm_scale,
+ *                     kv_capacity as for qattn_decode; pv_mode 0
+ *   workspace         at least qattn_tree_workspace_size() bytes; calls that may
+ *                     overlap need one each
+ * Limits: d in {64, 128}, Nq <= 128.  A length outside 0 .. Nk is clamped and
+ * reported: qattn_get_error() returns QATTN_ERR_INVALID_ARG.
+ */
+qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales,
+                               const int8_t* k_codes, const int8_t* v_codes,
+                               const float* k_chan_scale, const float* v_chan_scale,
+                               const float* k_mean, const int32_t* lengths,
+                               const uint16_t* K_new, const int64_t* k_strides,
+                               const uint16_t* V_new, const int64_t* v_strides,
+                               const uint32_t* tree_mask, const qattn_shape* shape,
+                               const qattn_params* params, void* O, float* lse,
+                               void* workspace, size_t workspace_bytes, qattn_stream_t stream);
+
+/* Bytes of workspace qattn_tree_decode accepts for this shape and parameters,
+ * with or without drafts (0 for an empty or unsupported problem).  Host only. */
+size_t qattn_tree_workspace_size(const qattn_shape* shape, const qattn_params* params);
+
+/* Append the accepted path of a drafted tree to an int8 KV cache: token
+ * path[b][t], t < n_accept[b], of K_new and V_new becomes row lengths[b] + t of
+ * sequence b, encoded and entered in the header as qattn_kv_append does, one
+ * after the other, with n = seen[b] + t earlier tokens behind the running mean:
+ *   kc = clamp(rint((K - mu) / s_k), -127, 127);  mu = mu + (K - mu) / (n + 1)
+ *   vc = clamp(rint(V / s_v), -127, 127);  amax = max(amax, |vc|)
+ *   K_new, V_new   bf16 [B][Hkv][T][d], strides as in the conventions (NULL =
+ *                  dense); 2-byte aligned
+ *   path           int32 [B][T], device (entries past n_accept[b] are not read)
+ *   n_accept       int32 [B], device, 0 .. T
+ *   lengths        int32 [B], device: rows in use;  lengths_out = + n_accept
+ *   seen           NULL (the rows in use), or int32 [B]: tokens behind the mean
+ *                  (more than the rows in use once rows have been evicted);
+ *                  seen_out = + n_accept; both or neither
+ *   k_mean, v_code_amax  fp32 [B][Hkv][d], the header; *_out the updated one.
+ *                  Each *_out may be the array it is computed from
+ *   weights        NULL, or fp32 [B][Hkv][capacity]: the new rows' entries are
+ *                  set to 0 (see qattn_kv_weights)
+ *   k_codes, v_codes  int8 [B][Hkv][capacity][d], device: the new rows are written
+ * A sequence whose n_accept, path, length or seen is out of range, or whose
+ * path does not fit the capacity, is left as it is (its header and length are
+ * copied) and reported: qattn_get_error() returns QATTN_ERR_INVALID_ARG.
+ * Limits: B <= 65535, capacity <= 2^24, 1 <= d <= 1024, B * Hkv * d < 2^31.
+ */
+qattn_status qattn_tree_commit(const uint16_t* K_new, const int64_t* k_strides,
+                               const uint16_t* V_new, const int64_t* v_strides,
+                               const int32_t* path, const int32_t* n_accept, int64_t B,
+                               int64_t Hkv, int64_t T, int64_t d, int64_t capacity,
+                               const float* k_chan_scale, const float* v_chan_scale,
+                               const int32_t* lengths, const int32_t* seen,
+                               const float* k_mean, const float* v_code_amax,
+                               int32_t* lengths_out, int32_t* seen_out, float* k_mean_out,
+                               float* v_code_amax_out, float* weights, int8_t* k_codes,
+                               int8_t* v_codes, qattn_stream_t stream);
+
+/* The attention weight each cached row received from a call's queries:
+ *   weights[b][hk][k] = base[b][hk][k] + sum over the query heads h of KV head hk
+ *       and the tokens i that see row k of exp(s_hik - lse[b][h][i])
+ * with s the scaled score of the codes (sm_scale * sq * sk * S) and lse as
+ * qattn_fwd, qattn_decode or qattn_tree_decode wrote it: each query hands out a
+ * total of 1 per head, less what its drafts took.  Accumulated over decode steps,
+ * or taken over a prompt's last tokens, it says which rows qattn_kv_evict keeps.
+ * A query with lse = -inf gives nothing.
+ *   q_codes/q_scales, k_codes/k_scales  as for qattn_fwd (k_scales NULL: all 1);
+ *       k_codes int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)
+ *   lse       fp32 [B][Hq][Nq]
+ *   lengths   NULL, or int32 [B]: rows in use, 0 <= lengths[b] <= Nk
+ *   base      NULL (0), or fp32 [B][Hkv][cap]; may be `weights` itself
+ *   weights   (out) fp32 [B][Hkv][cap], rows 0 .. lengths[b]-1; the rows behind
+ *             stay as they are
+ *   params    causal: row k is visible to token i iff k <= p + i, p = q_pos0, or
+ *             lengths[b] - Nq for QATTN_POS0_BOTTOM_RIGHT; q_gran, k_gran,
+ *             sm_scale, kv_capacity
+ * The additions' order is fixed (no atomics): equal calls give equal bits.
+ * Limits: d in {64, 128}.  No workspace.  A length outside 0 .. Nk is clamped
+ * and reported as by qattn_tree_decode.
+ */
+qattn_status qattn_kv_weights(const int8_t* q_codes, const float* q_scales,
+                              const int8_t* k_codes, const float* k_scales, const float* lse,
+                              const int32_t* lengths, const qattn_shape* shape,
+                              const qattn_params* params, const float* base, float* weights,
+                              qattn_stream_t stream);
+
+/* Keep the `budget` rows of most weight of an int8 KV cache, per (sequence, KV
+ * head): the first n_sink rows and the last n_recent ones always, then the rows
+ * of the largest weights (ties: the lowest row; NaN counts as -inf).  The kept
+ * rows go to a second cache in their order: min(lengths[b], budget) of them.
+ *   k_codes, v_codes, weights  the cache, rows 0 .. lengths[b]-1 in use of
+ *                 `capacity`; weights fp32 [B][Hkv][capacity]
+ *   lengths       NULL (Nk rows everywhere), or int32 [B], 0 <= lengths[b] <= Nk
+ *   k_out, v_out  (out) int8 [B][Hkv][out_capacity][d];  weights_out fp32
+ *                 [B][Hkv][out_capacity];  kept int32 [B][Hkv][budget]: the rows
+ *                 the kept ones came from, ascending.  Entries past the rows kept
+ *                 stay as they are
+ *   lengths_out   (out) int32 [B], not `lengths` itself
+ *   v_code_amax   (out) fp32 [B][Hkv][d]: max |V code| over the kept rows, the
+ *                 header's V part as qattn_kv_header_init gives it.  K's mean and
+ *                 the channel scales stay what they were
+ * The outputs may not overlap the cache.  Limits: d in {32, 64, 128}, B * Hkv <=
+ * 65535, capacities <= 2^24, budget >= 1, n_sink + n_recent <= budget.  No
+ * workspace.  A length outside 0 .. Nk is clamped and reported as above.
+ */
+qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const float* weights,
+                            const int32_t* lengths, int64_t B, int64_t Hkv, int64_t Nk, int64_t d,
+                            int64_t capacity, int64_t budget, int64_t n_sink, int64_t n_recent,
+                            int8_t* k_out, int8_t* v_out, int64_t out_capacity,
+                            float* weights_out, int32_t* kept, int32_t* lengths_out,
+                            float* v_code_amax, qattn_stream_t stream);
+
 /* a4 alone (debug) -- the int32 score tiles S = q_codes . k_codes^T
  * ("QFlash", eq. (3)), through the same tensor-core path as qattn_fwd.
  *   S (out) int32 [B][Hq][Nq][Nk]
@@ -463,8 +607,8 @@ qattn_status qattn_debug_bounds_probe(qattn_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the device error word of
  * the current device (QATTN_ERR_TIMEOUT if a kernel gave up on a wait,
- * QATTN_ERR_INVALID_ARG if a kernel found device-held scales outside its
- * domain). */
+ * QATTN_ERR_INVALID_ARG if a kernel found device-held scales, lengths or paths
+ * outside its domain). */
 qattn_status qattn_get_error(qattn_stream_t stream);
 
 /* Failure-path check (debug; no counterpart on the pages): one thread runs

@@ -33,6 +33,8 @@ EXPORTED = (
     "qattn_kv_append", "qattn_fwd_exact24", "qattn_fwd_intsoftmax", "qattn_prepare",
     "qattn_fwd_kernel_choice", "qattn_prepare_launches", "qattn_debug_wait_timeout",
     "qattn_peak_loop", "qattn_kv_header_init", "qattn_checked", "qattn_debug_bounds_probe",
+    "qattn_tree_decode", "qattn_tree_workspace_size", "qattn_tree_commit", "qattn_kv_weights",
+    "qattn_kv_evict",
 )
 
 
@@ -90,6 +92,12 @@ def lib() -> ctypes.CDLL:
     L.qattn_kv_header_init.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp]
     L.qattn_fwd_exact24.argtypes = [vp, vp, vp, vp, vp, PS, PP, vp, vp, vp, sz, vp]
     L.qattn_fwd_intsoftmax.argtypes = [vp, vp, vp, vp, vp, PS, PP, vp, vp]
+    L.qattn_tree_decode.argtypes = [vp] * 13 + [PS, PP, vp, vp, vp, sz, vp]
+    L.qattn_tree_workspace_size.argtypes = [PS, PP]
+    L.qattn_tree_workspace_size.restype = sz
+    L.qattn_tree_commit.argtypes = [vp] * 6 + [i64] * 5 + [vp] * 14
+    L.qattn_kv_weights.argtypes = [vp] * 6 + [PS, PP, vp, vp, vp]
+    L.qattn_kv_evict.argtypes = [vp] * 4 + [i64] * 8 + [vp, vp, i64, vp, vp, vp, vp, vp]
     L.qattn_get_error.argtypes = [vp]
     L.qattn_debug_wait_timeout.argtypes = [vp, vp]
     L.qattn_fwd_kernel_choice.argtypes = [PS, PP]
@@ -106,7 +114,8 @@ def lib() -> ctypes.CDLL:
                  "qattn_decode", "qattn_kv_append", "qattn_fwd_exact24", "qattn_fwd_intsoftmax",
                  "qattn_debug_qk_scores", "qattn_get_error", "qattn_quantize_v_noalloc",
                  "qattn_prepare", "qattn_debug_wait_timeout", "qattn_kv_header_init",
-                 "qattn_debug_bounds_probe"):
+                 "qattn_debug_bounds_probe", "qattn_tree_decode", "qattn_tree_commit",
+                 "qattn_kv_weights", "qattn_kv_evict"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -334,6 +343,158 @@ def kv_header_init(v_codes, Nk, v_code_amax, stream=None):
     _check(lib().qattn_kv_header_init(_p(v_codes), B, H, int(Nk), d, cap, _p(v_code_amax),
                                       _stream(stream)),
            "qattn_kv_header_init")
+
+
+def _want(name: str, t: Optional[torch.Tensor], dtype, shape, optional=False):
+    """A dense tensor of this type and shape (None in a dimension: any size) on the
+    current CUDA device, whose kernels and stream the call uses."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is missing")
+    _dense(t, dtype, name)
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _want_input(name: str, t: Optional[torch.Tensor], shape):
+    """A bf16 input at any strides (see _input), its shape and device checked."""
+    st = _input(t, torch.bfloat16, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return st
+
+
+def tree_workspace_size(shape: Shape, params: Params) -> int:
+    return lib().qattn_tree_workspace_size(ctypes.byref(shape), ctypes.byref(params))
+
+
+def tree_decode(q_codes, q_scales, k_codes, v_codes, k_chan_scale, v_chan_scale, shape, params, O,
+                lse, workspace, *, lengths=None, K_new=None, V_new=None, k_mean=None,
+                tree_mask=None, stream=None):
+    """Attention of T drafted tokens over an int8 KV cache and over the drafts
+    themselves (see qattn_tree_decode in include/qattn.h).  lengths: int32 [B];
+    K_new, V_new: bf16 [B, Hkv, T, d] (None: the tokens' rows are in the cache);
+    tree_mask: int32 [B, T, ceil(T / 32)] ancestor words (None: a chain if
+    params.causal, else every draft sees every draft)."""
+    B, Hq, Hkv, T, d = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d
+    cap = params.kv_capacity or shape.Nk
+    f32 = torch.float32
+    _want("q_codes", q_codes, torch.int8, (B, Hq, T, d))
+    if q_scales.numel() < n_scales(params.q_gran, B, Hq, T):
+        raise ValueError("q_scales: too few for the granularity")
+    _dense(q_scales, f32, "q_scales")
+    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d), optional=shape.Nk == 0)
+    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d), optional=shape.Nk == 0)
+    head = (B, Hkv, d)
+    _want("v_chan_scale", v_chan_scale, f32, head)
+    _want("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, (B, Hq, T, d))
+    _want("lse", lse, f32, (B, Hq, T), optional=True)
+    _want("lengths", lengths, torch.int32, (B,), optional=True)
+    _want("tree_mask", tree_mask, torch.int32, (B, T, (T + 31) // 32), optional=True)
+    ks = vs = None
+    if K_new is not None or V_new is not None:
+        if K_new is None or V_new is None:
+            raise ValueError("K_new and V_new go together")
+        ks = _want_input("K_new", K_new, (B, Hkv, T, d))
+        vs = _want_input("V_new", V_new, (B, Hkv, T, d))
+        _want("k_chan_scale", k_chan_scale, f32, head)
+        _want("k_mean", k_mean, f32, head)
+    _check(lib().qattn_tree_decode(_p(q_codes), _p(q_scales), _p(k_codes), _p(v_codes),
+                                   _p(k_chan_scale), _p(v_chan_scale), _p(k_mean), _p(lengths),
+                                   _p(K_new), ks, _p(V_new), vs, _p(tree_mask),
+                                   ctypes.byref(shape), ctypes.byref(params), _p(O), _p(lse),
+                                   _p(workspace), _nbytes(workspace), _stream(stream)),
+           "qattn_tree_decode")
+
+
+def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, lengths, k_mean,
+                v_code_amax, k_codes, v_codes, *, lengths_out=None, k_mean_out=None,
+                v_code_amax_out=None, seen=None, seen_out=None, weights=None, stream=None):
+    """Append each sequence's accepted path of the drafts K_new, V_new (bf16 [B, Hkv,
+    T, d]) to the cache (see qattn_tree_commit in include/qattn.h).  path: int32
+    [B, T] draft indices, n_accept: int32 [B].  An output not given is written
+    over the array it is computed from."""
+    B, Hkv, T, d = K_new.shape
+    cap, f32, i32 = k_codes.shape[2], torch.float32, torch.int32
+    lengths_out = lengths if lengths_out is None else lengths_out
+    k_mean_out = k_mean if k_mean_out is None else k_mean_out
+    v_code_amax_out = v_code_amax if v_code_amax_out is None else v_code_amax_out
+    seen_out = seen if seen_out is None else seen_out
+    ks = _want_input("K_new", K_new, (B, Hkv, T, d))
+    vs = _want_input("V_new", V_new, (B, Hkv, T, d))
+    _want("path", path, i32, (B, T))
+    for name, t in (("n_accept", n_accept), ("lengths", lengths), ("lengths_out", lengths_out)):
+        _want(name, t, i32, (B,))
+    _want("seen", seen, i32, (B,), optional=True)
+    _want("seen_out", seen_out, i32, (B,), optional=True)
+    for name, t in (("k_chan_scale", k_chan_scale), ("v_chan_scale", v_chan_scale), ("k_mean", k_mean),
+                    ("v_code_amax", v_code_amax), ("k_mean_out", k_mean_out),
+                    ("v_code_amax_out", v_code_amax_out)):
+        _want(name, t, f32, (B, Hkv, d))
+    _want("weights", weights, f32, (B, Hkv, cap), optional=True)
+    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
+    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d))
+    _check(lib().qattn_tree_commit(_p(K_new), ks, _p(V_new), vs, _p(path), _p(n_accept), B, Hkv, T, d,
+                                   cap, _p(k_chan_scale), _p(v_chan_scale), _p(lengths), _p(seen),
+                                   _p(k_mean), _p(v_code_amax), _p(lengths_out), _p(seen_out),
+                                   _p(k_mean_out), _p(v_code_amax_out), _p(weights), _p(k_codes),
+                                   _p(v_codes), _stream(stream)),
+           "qattn_tree_commit")
+
+
+def kv_weights(q_codes, q_scales, k_codes, k_scales, lse, shape, params, weights, *, base=None,
+               lengths=None, stream=None):
+    """Attention weight that each cached row received from these queries, added to
+    base (see qattn_kv_weights in include/qattn.h).  weights, base: fp32 [B, Hkv,
+    capacity]; lse: fp32 [B, Hq, Nq]."""
+    B, Hq, Hkv, T, d = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d
+    cap, f32 = params.kv_capacity or shape.Nk, torch.float32
+    _want("q_codes", q_codes, torch.int8, (B, Hq, T, d))
+    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
+    _want("lse", lse, f32, (B, Hq, T))
+    _want("weights", weights, f32, (B, Hkv, cap))
+    _want("base", base, f32, (B, Hkv, cap), optional=True)
+    _want("lengths", lengths, torch.int32, (B,), optional=True)
+    _dense(q_scales, f32, "q_scales")
+    if q_scales.numel() < n_scales(params.q_gran, B, Hq, T):
+        raise ValueError("q_scales: too few for the granularity")
+    if k_scales is not None:
+        _dense(k_scales, f32, "k_scales")
+        if k_scales.numel() < n_scales(params.k_gran, B, Hkv, shape.Nk):
+            raise ValueError("k_scales: too few for the granularity")
+    _check(lib().qattn_kv_weights(_p(q_codes), _p(q_scales), _p(k_codes), _p(k_scales), _p(lse),
+                                  _p(lengths), ctypes.byref(shape), ctypes.byref(params), _p(base),
+                                  _p(weights), _stream(stream)),
+           "qattn_kv_weights")
+
+
+def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept, lengths_out,
+             v_code_amax, *, lengths=None, Nk=None, n_sink=0, n_recent=0, stream=None):
+    """Keep the budget rows of most weight per KV head (see qattn_kv_evict in
+    include/qattn.h).  Nk: most rows in use (default: the capacity)."""
+    B, Hkv, cap, d = k_codes.shape
+    Nk = cap if Nk is None else int(Nk)
+    ocap = k_out.shape[2]
+    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
+    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d))
+    _want("weights", weights, torch.float32, (B, Hkv, cap))
+    _want("k_out", k_out, torch.int8, (B, Hkv, ocap, d))
+    _want("v_out", v_out, torch.int8, (B, Hkv, ocap, d))
+    _want("weights_out", weights_out, torch.float32, (B, Hkv, ocap))
+    _want("kept", kept, torch.int32, (B, Hkv, int(budget)))
+    _want("lengths_out", lengths_out, torch.int32, (B,))
+    _want("lengths", lengths, torch.int32, (B,), optional=True)
+    _want("v_code_amax", v_code_amax, torch.float32, (B, Hkv, d))
+    _check(lib().qattn_kv_evict(_p(k_codes), _p(v_codes), _p(weights), _p(lengths), B, Hkv, Nk, d, cap,
+                                int(budget), int(n_sink), int(n_recent), _p(k_out), _p(v_out), ocap,
+                                _p(weights_out), _p(kept), _p(lengths_out), _p(v_code_amax),
+                                _stream(stream)),
+           "qattn_kv_evict")
 
 
 def debug_qk_scores(q_codes, k_codes, shape, S, workspace, stream=None):

@@ -1,6 +1,7 @@
 // The C ABI of libqattn.so (declared in include/qattn.h): host-side argument
 // validation, workspace carving, TMA descriptor encoding and kernel launches.
 // No entry point allocates device memory; every failure becomes a status.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -285,6 +286,52 @@ bool encode_carrier(CUtensorMap* map, const void* ptr, int64_t planes, int64_t r
 bool decode_shape_ok(const qattn_shape* s) {
   return s->Hkv > 0 && s->Nq >= 1 && (s->Hq / s->Hkv) * s->Nq <= qattn::kMaxDecodeRows &&
          (s->d == 64 || s->d == 128);
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+float sm_scale_of(const qattn_shape* s, const qattn_params* p) {
+  return p->sm_scale > 0.f ? p->sm_scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(s->d)));
+}
+
+// qattn_tree_decode's split: CTAs over the flattened list of steps (an upper
+// bound from Nk; the kernel divides the steps that the lengths give), and the
+// workspace of their shares.  The layout depends on the shape alone.
+struct TreeSplit {
+  int blocks, rows, drafts, ctas;
+  size_t slots, off_m, off_l, bytes;
+};
+TreeSplit tree_split(const qattn_shape* s, bool drafts) {
+  TreeSplit t{};
+  const int64_t R = s->Hq / s->Hkv * s->Nq;
+  const int step = qattn::tree_warp_step_keys();
+  t.rows = qattn::kTreeRows;
+  t.blocks = static_cast<int>((R + t.rows - 1) / t.rows);
+  t.drafts = drafts ? static_cast<int>((s->Nq + step - 1) / step) : 0;
+  const int64_t steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + step - 1) / step);
+  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(qattn::kTreeWarpCtas, (steps + 3) / 4)));
+  t.slots = 2 * static_cast<size_t>(t.ctas);
+  t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
+  t.off_l = t.off_m + align256(t.slots * t.rows * 4);
+  t.bytes = t.off_l + align256(t.slots * t.rows * 4);
+  return t;
+}
+
+qattn_status tree_shape_ok(const qattn_shape* shape) {
+  const qattn_status st = check_shape(shape);
+  if (st != QATTN_OK) return st;
+  if (shape->d != 64 && shape->d != 128) return QATTN_ERR_UNSUPPORTED;
+  if (shape->Nq > qattn::kTreeMaxTokens) return QATTN_ERR_UNSUPPORTED;
+  return QATTN_OK;
+}
+
+// Map over int8 cache codes [planes][cap][d], rows 0 .. rows-1 in use, boxes of
+// box_rows rows; 128-byte swizzle for d = 128, 64-byte for d = 64.
+bool encode_cache(CUtensorMap* map, const void* ptr, int64_t planes, int64_t rows, int64_t cap,
+                  int64_t d, uint32_t box_rows) {
+  return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, d, rows, planes, d,
+                   static_cast<uint32_t>(d), box_rows,
+                   d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, cap);
 }
 
 // The pipeline kernels' bounded mbarrier wait, run on a barrier that nothing
@@ -878,6 +925,269 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
                                              v_code_amax, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t qattn_tree_workspace_size(const qattn_shape* shape, const qattn_params* params) {
+  if (tree_shape_ok(shape) != QATTN_OK || check_params(params) != QATTN_OK || empty_problem(shape)) return 0;
+  return std::max(tree_split(shape, true).bytes, tree_split(shape, false).bytes);
+}
+
+qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, const int8_t* k_codes,
+                               const int8_t* v_codes, const float* k_chan_scale,
+                               const float* v_chan_scale, const float* k_mean,
+                               const int32_t* lengths, const uint16_t* K_new,
+                               const int64_t* k_strides, const uint16_t* V_new,
+                               const int64_t* v_strides, const uint32_t* tree_mask,
+                               const qattn_shape* shape, const qattn_params* params, void* O,
+                               float* lse, void* workspace, size_t workspace_bytes,
+                               qattn_stream_t stream) {
+  qattn_status st = tree_shape_ok(shape);
+  if (st != QATTN_OK) return st;
+  if ((st = check_params(params)) != QATTN_OK) return st;
+  if (empty_problem(shape)) return QATTN_OK;
+  if (params->pv_mode != QATTN_PV_E4M3 || params->q_pos0 != QATTN_POS0_BOTTOM_RIGHT)
+    return QATTN_ERR_UNSUPPORTED;
+  if (params->kv_capacity != 0 &&
+      (params->kv_capacity < shape->Nk || params->kv_capacity > (int64_t{1} << 31)))
+    return QATTN_ERR_INVALID_ARG;
+  const bool drafts = K_new != nullptr || V_new != nullptr;
+  if (!q_codes || !aligned16(q_codes) || !q_scales || !aligned_to(q_scales, 4) || !v_chan_scale ||
+      !aligned16(v_chan_scale) || !O || !aligned16(O) || !aligned_to(lse, 4) ||
+      !aligned_to(lengths, 4) || !aligned_to(tree_mask, 4))
+    return QATTN_ERR_INVALID_ARG;
+  if (shape->Nk > 0 && (!k_codes || !aligned16(k_codes) || !v_codes || !aligned16(v_codes)))
+    return QATTN_ERR_INVALID_ARG;
+  if (drafts && (!K_new || !aligned16(K_new) || !V_new || !aligned16(V_new) || !k_chan_scale ||
+                 !aligned16(k_chan_scale) || !k_mean || !aligned16(k_mean)))
+    return QATTN_ERR_INVALID_ARG;
+  if (!drafts && tree_mask) return QATTN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (shape->Nk == 0 && !drafts) return no_key_rows(shape, params, O, lse, s);
+  const TreeSplit sp = tree_split(shape, drafts);
+  if (!workspace || workspace_bytes < sp.bytes || !aligned16(workspace)) return QATTN_ERR_WORKSPACE;
+  qattn::TreeArgs a{};
+  if (drafts) {
+    qattn::Src ks, vs;
+    if (!make_src(K_new, k_strides, shape->Hkv, shape->Nq, shape->d, 2, &ks) ||
+        !make_src(V_new, v_strides, shape->Hkv, shape->Nq, shape->d, 2, &vs))
+      return QATTN_ERR_INVALID_ARG;
+    a.ksB = ks.sB;
+    a.ksH = ks.sH;
+    a.ksN = ks.sN;
+    a.vsB = vs.sB;
+    a.vsH = vs.sH;
+    a.vsN = vs.sN;
+  }
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(shape->B);
+  a.Hq = static_cast<int>(shape->Hq);
+  a.Hkv = static_cast<int>(shape->Hkv);
+  a.G = a.Hq / a.Hkv;
+  a.T = static_cast<int>(shape->Nq);
+  a.Nk = static_cast<int>(shape->Nk);
+  a.d = static_cast<int>(shape->d);
+  a.blocks = sp.blocks;
+  a.drafts = sp.drafts;
+  a.draft_causal = drafts && params->causal;
+  a.cached_causal = !drafts && params->causal;
+  a.q_gran = params->q_gran;
+  a.sm_scale = sm_scale_of(shape, params);
+  a.q_codes = q_codes;
+  a.q_scales = q_scales;
+  a.k_chan_scale = k_chan_scale;
+  a.v_chan_scale = v_chan_scale;
+  a.k_mean = k_mean;
+  a.lengths = lengths;
+  a.k_new = K_new;
+  a.v_new = V_new;
+  a.tree_mask = tree_mask;
+  a.out = O;
+  a.out_bf16 = params->out_dtype == QATTN_BF16;
+  a.lse = lse;
+  a.ctas = sp.ctas;
+  a.slots = sp.slots;
+  a.rows_total = static_cast<size_t>(shape->B * shape->Hq * shape->Nq);
+  char* w = static_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_m = reinterpret_cast<float*>(w + sp.off_m);
+  a.part_l = reinterpret_cast<float*>(w + sp.off_l);
+  CUtensorMap tk{}, tv{};
+  if (shape->Nk > 0) {
+    const int64_t cap = params->kv_capacity ? params->kv_capacity : shape->Nk;
+    const uint32_t box = static_cast<uint32_t>(qattn::tree_warp_step_keys());
+    if (!encode_cache(&tk, k_codes, shape->B * shape->Hkv, shape->Nk, cap, shape->d, box) ||
+        !encode_cache(&tv, v_codes, shape->B * shape->Hkv, shape->Nk, cap, shape->d, box))
+      return QATTN_ERR_CUDA;
+  }
+  char sb[128];
+  QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: tree_warp_kernel + tree_join_kernel, %d CTAs",
+                 shape_str(shape, sb, sizeof sb), drafts ? a.T : 0, sp.ctas);
+  return from_cuda(qattn::launch_tree_warp(tk, tv, a, s));
+}
+
+qattn_status qattn_tree_commit(const uint16_t* K_new, const int64_t* k_strides,
+                               const uint16_t* V_new, const int64_t* v_strides,
+                               const int32_t* path, const int32_t* n_accept, int64_t B,
+                               int64_t Hkv, int64_t T, int64_t d, int64_t capacity,
+                               const float* k_chan_scale, const float* v_chan_scale,
+                               const int32_t* lengths, const int32_t* seen, const float* k_mean,
+                               const float* v_code_amax, int32_t* lengths_out, int32_t* seen_out,
+                               float* k_mean_out, float* v_code_amax_out, float* weights,
+                               int8_t* k_codes, int8_t* v_codes, qattn_stream_t stream) {
+  if (B < 0 || B > 65535 || Hkv <= 0 || T < 0 || d < 1 || d > 1024 || capacity < 0 ||
+      capacity > (int64_t{1} << 24) || T > (int64_t{1} << 24) || B * Hkv * d >= (int64_t{1} << 31))
+    return QATTN_ERR_INVALID_ARG;
+  if (B == 0) return QATTN_OK;
+  if ((T > 0 && (!K_new || !V_new || !path)) || !n_accept || !k_chan_scale || !v_chan_scale ||
+      !lengths || !k_mean || !v_code_amax || !lengths_out || !k_mean_out || !v_code_amax_out ||
+      !k_codes || !v_codes || (seen == nullptr) != (seen_out == nullptr))
+    return QATTN_ERR_INVALID_ARG;
+  if (!aligned_to(K_new, 2) || !aligned_to(V_new, 2)) return QATTN_ERR_INVALID_ARG;
+  for (const void* f : {static_cast<const void*>(path), static_cast<const void*>(n_accept),
+                        static_cast<const void*>(k_chan_scale), static_cast<const void*>(v_chan_scale),
+                        static_cast<const void*>(lengths), static_cast<const void*>(seen),
+                        static_cast<const void*>(k_mean), static_cast<const void*>(v_code_amax),
+                        static_cast<const void*>(lengths_out), static_cast<const void*>(seen_out),
+                        static_cast<const void*>(k_mean_out), static_cast<const void*>(v_code_amax_out),
+                        static_cast<const void*>(weights)})
+    if (!aligned_to(f, 4)) return QATTN_ERR_INVALID_ARG;
+  qattn::Src ks, vs;
+  if (!make_src(K_new, k_strides, Hkv, T, d, 2, &ks) || !make_src(V_new, v_strides, Hkv, T, d, 2, &vs))
+    return QATTN_ERR_INVALID_ARG;
+  qattn::CommitArgs a{};
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(B);
+  a.Hkv = static_cast<int>(Hkv);
+  a.T = static_cast<int>(T);
+  a.d = static_cast<int>(d);
+  a.cap = capacity;
+  a.k_new = K_new;
+  a.v_new = V_new;
+  a.ksB = ks.sB;
+  a.ksH = ks.sH;
+  a.ksN = ks.sN;
+  a.vsB = vs.sB;
+  a.vsH = vs.sH;
+  a.vsN = vs.sN;
+  a.path = path;
+  a.n_accept = n_accept;
+  a.k_chan_scale = k_chan_scale;
+  a.v_chan_scale = v_chan_scale;
+  a.lengths = lengths;
+  a.seen = seen;
+  a.k_mean = k_mean;
+  a.v_code_amax = v_code_amax;
+  a.lengths_out = lengths_out;
+  a.seen_out = seen_out;
+  a.k_mean_out = k_mean_out;
+  a.v_code_amax_out = v_code_amax_out;
+  a.weights = weights;
+  a.k_codes = k_codes;
+  a.v_codes = v_codes;
+  QATTN_LOG_LINE("qattn_tree_commit B=%d Hkv=%d T=%d d=%d capacity=%lld: tree_commit_kernel", a.B, a.Hkv,
+                 a.T, a.d, static_cast<long long>(a.cap));
+  return from_cuda(qattn::launch_tree_commit(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_kv_weights(const int8_t* q_codes, const float* q_scales, const int8_t* k_codes,
+                              const float* k_scales, const float* lse, const int32_t* lengths,
+                              const qattn_shape* shape, const qattn_params* params,
+                              const float* base, float* weights, qattn_stream_t stream) {
+  qattn_status st = check_shape(shape);
+  if (st != QATTN_OK) return st;
+  if ((st = check_params(params)) != QATTN_OK) return st;
+  if (shape->d != 64 && shape->d != 128) return QATTN_ERR_UNSUPPORTED;
+  if (shape->B == 0 || shape->Nk == 0) return QATTN_OK;
+  if (params->kv_capacity != 0 &&
+      (params->kv_capacity < shape->Nk || params->kv_capacity > (int64_t{1} << 31)))
+    return QATTN_ERR_INVALID_ARG;
+  if (!weights || !aligned_to(weights, 4) || !aligned_to(base, 4) || !aligned_to(lengths, 4) ||
+      !k_codes || !aligned16(k_codes) || !aligned_to(k_scales, 4))
+    return QATTN_ERR_INVALID_ARG;
+  if (shape->Hq * shape->Nq > 0 && (!q_codes || !aligned16(q_codes) || !q_scales || !aligned_to(q_scales, 4) ||
+                                    !lse || !aligned_to(lse, 4)))
+    return QATTN_ERR_INVALID_ARG;
+  const bool from_len = params->q_pos0 == QATTN_POS0_BOTTOM_RIGHT;
+  const int64_t pos0 = from_len ? 0 : params->q_pos0;
+  if (params->causal && (pos0 <= -(int64_t{1} << 30) || pos0 >= (int64_t{1} << 30))) return QATTN_ERR_UNSUPPORTED;
+  qattn::WeightArgs a{};
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(shape->B);
+  a.Hq = static_cast<int>(shape->Hq);
+  a.Hkv = static_cast<int>(shape->Hkv);
+  a.G = a.Hq / a.Hkv;
+  a.Nq = static_cast<int>(shape->Nq);
+  a.Nk = static_cast<int>(shape->Nk);
+  a.d = static_cast<int>(shape->d);
+  a.cap = params->kv_capacity ? params->kv_capacity : shape->Nk;
+  a.causal = params->causal;
+  a.pos0_len = from_len;
+  a.pos0 = params->causal ? static_cast<int>(pos0) : 0;
+  a.sm_scale = sm_scale_of(shape, params);
+  a.q_gran = params->q_gran;
+  a.k_gran = params->k_gran;
+  a.q_codes = q_codes;
+  a.q_scales = q_scales;
+  a.k_codes = k_codes;
+  a.k_scales = k_scales;
+  a.lse = lse;
+  a.lengths = lengths;
+  a.base = base;
+  a.weights = weights;
+  char sb[128];
+  QATTN_LOG_LINE("qattn_kv_weights %s causal=%d: kv_weights_warp_kernel", shape_str(shape, sb, sizeof sb),
+                 a.causal);
+  return from_cuda(qattn::launch_kv_weights(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const float* weights,
+                            const int32_t* lengths, int64_t B, int64_t Hkv, int64_t Nk, int64_t d,
+                            int64_t capacity, int64_t budget, int64_t n_sink, int64_t n_recent,
+                            int8_t* k_out, int8_t* v_out, int64_t out_capacity, float* weights_out,
+                            int32_t* kept, int32_t* lengths_out, float* v_code_amax,
+                            qattn_stream_t stream) {
+  if (B < 0 || Hkv <= 0 || Nk < 0 || capacity < Nk || capacity > (int64_t{1} << 24) || budget < 1 ||
+      out_capacity < budget || out_capacity > (int64_t{1} << 24) || n_sink < 0 || n_recent < 0 ||
+      n_sink > budget || n_recent > budget - n_sink)
+    return QATTN_ERR_INVALID_ARG;
+  if (!valid_d(d) || B * Hkv > 65535) return QATTN_ERR_UNSUPPORTED;
+  if (B == 0) return QATTN_OK;
+  if (!lengths_out || !kept || !weights_out || !v_code_amax || !k_out || !v_out || !aligned16(k_out) ||
+      !aligned16(v_out) || lengths_out == lengths || !aligned_to(lengths, 4) ||
+      !aligned_to(lengths_out, 4) || !aligned_to(kept, 4) || !aligned_to(weights_out, 4) ||
+      !aligned_to(v_code_amax, 4))
+    return QATTN_ERR_INVALID_ARG;
+  if (Nk > 0 && (!k_codes || !aligned16(k_codes) || !v_codes || !aligned16(v_codes) || !weights ||
+                 !aligned_to(weights, 4) || k_codes == k_out || v_codes == v_out || weights == weights_out))
+    return QATTN_ERR_INVALID_ARG;
+  qattn::EvictArgs a{};
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(B);
+  a.Hkv = static_cast<int>(Hkv);
+  a.Nk = static_cast<int>(Nk);
+  a.d = static_cast<int>(d);
+  a.cap = capacity;
+  a.out_cap = out_capacity;
+  a.budget = static_cast<int>(budget);
+  a.n_sink = static_cast<int>(n_sink);
+  a.n_recent = static_cast<int>(n_recent);
+  a.k_codes = k_codes;
+  a.v_codes = v_codes;
+  a.weights = weights;
+  a.lengths = lengths;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.weights_out = weights_out;
+  a.kept = kept;
+  a.lengths_out = lengths_out;
+  a.v_code_amax = v_code_amax;
+  QATTN_LOG_LINE("qattn_kv_evict B=%d Hkv=%d Nk=%d d=%d budget=%d: evict_select_kernel + evict_gather_kernel",
+                 a.B, a.Hkv, a.Nk, a.d, a.budget);
+  return from_cuda(qattn::launch_kv_evict(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int qattn_fwd_kernel_choice(const qattn_shape* shape, const qattn_params* params) {
   if (check_shape(shape) != QATTN_OK || check_params(params) != QATTN_OK) return -1;
   const int c = fwd_choice(shape, params);
@@ -925,7 +1235,9 @@ qattn_status qattn_get_error(qattn_stream_t stream) {
   }
   const unsigned int checks = qattn::check_take_attn_fwd() | qattn::check_take_quant() |
                               qattn::check_take_decode() | qattn::check_take_short() |
-                              qattn::check_take_exact24() | qattn::check_take_intsm();
+                              qattn::check_take_exact24() | qattn::check_take_intsm() |
+                              qattn::check_take_tree_warp() | qattn::check_take_kv_weights() |
+                              qattn::check_take_kv_cache();
   if (v & qattn::kErrTimeout) return QATTN_ERR_TIMEOUT;
   if (checks != 0) return QATTN_ERR_BOUNDS;
   return (v & qattn::kErrDomain) ? QATTN_ERR_INVALID_ARG : QATTN_OK;

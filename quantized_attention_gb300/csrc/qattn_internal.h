@@ -55,6 +55,9 @@ unsigned int check_take_decode();
 unsigned int check_take_short();
 unsigned int check_take_exact24();
 unsigned int check_take_intsm();
+unsigned int check_take_tree_warp();
+unsigned int check_take_kv_weights();
+unsigned int check_take_kv_cache();
 // One guard that fails for 16 of 32 threads, touching no memory (quant_kernels.cu).
 cudaError_t launch_bounds_probe(cudaStream_t s);
 
@@ -194,6 +197,100 @@ cudaError_t launch_kv_append(const uint16_t* K_new, const uint16_t* V_new, int B
                              int pos, long long cap, const float* k_chan_scale,
                              const float* v_chan_scale, float* k_mean, float* v_code_amax,
                              int8_t* k_codes, int8_t* v_codes, cudaStream_t s);
+
+// ---- tree_warp.cu, tree_tc.cu (tree_common.cuh): qattn_tree_decode
+constexpr int kTreeMaxTokens = 128;  // drafted tokens of a sequence
+constexpr int kTreeRows = 16;        // query rows of the warp-level kernel's block
+constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
+struct TreeArgs {
+  int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
+  int blocks;                    // row blocks of a head
+  int drafts;                    // drafted steps of a head (0: no drafts)
+  int draft_causal;              // no mask given: draft j visible to token i iff j <= i (else all)
+  int cached_causal;             // no drafts: cached row k visible to token i iff k <= len - T + i
+  int q_gran;                    // GRAN_TENSOR, else one scale per (sequence, query head)
+  float sm_scale;
+  const int8_t* q_codes;         // [B][Hq][T][d]
+  const float* q_scales;
+  const float* k_chan_scale;     // [B][Hkv][d]
+  const float* v_chan_scale;     // [B][Hkv][d]
+  const float* k_mean;           // [B][Hkv][d]
+  const int32_t* lengths;        // [B] or null (all Nk)
+  const uint16_t* k_new;         // bf16 drafts, element strides
+  const uint16_t* v_new;
+  long long ksB, ksH, ksN, vsB, vsH, vsN;
+  const uint32_t* tree_mask;     // [B][T][ceil(T/32)] or null
+  void* out;                     // [B][Hq][T][d]
+  int out_bf16;
+  float* lse;                    // [B][Hq][T] or null
+  unsigned int* err;
+  // the split and its workspace
+  int ctas;
+  size_t slots, rows_total;      // 2 ctas; B Hq T
+  float* part_o;                 // [slots][block rows][d]
+  float* part_m;                 // [slots][block rows]
+  float* part_l;
+};
+int tree_warp_step_keys();
+// tk, tv: maps over the int8 K and V codes, box d x 32 x 1 (128-byte swizzle
+// for d = 128, 64-byte for d = 64).
+cudaError_t launch_tree_warp(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
+                             cudaStream_t s);
+
+// ---- kv_weights.cu
+struct WeightArgs {
+  int B, Hq, Hkv, G, Nq, Nk, d;
+  long long cap;             // cache rows per (sequence, KV head)
+  int causal;
+  int pos0_len;              // 1: query row 0 sits on row length - Nq; 0: on pos0
+  int pos0;
+  float sm_scale;
+  int q_gran, k_gran;
+  const int8_t* q_codes;     // [B][Hq][Nq][d]
+  const float* q_scales;
+  const int8_t* k_codes;     // [B][Hkv][cap][d]
+  const float* k_scales;     // null: 1
+  const float* lse;          // [B][Hq][Nq]
+  const int32_t* lengths;    // [B] or null
+  const float* base;         // [B][Hkv][cap] or null
+  float* weights;            // [B][Hkv][cap]
+  unsigned int* err;
+};
+cudaError_t launch_kv_weights(const WeightArgs& a, cudaStream_t s);
+
+// ---- kv_cache.cu
+struct CommitArgs {
+  int B, Hkv, T, d;
+  long long cap;
+  const uint16_t *k_new, *v_new;
+  long long ksB, ksH, ksN, vsB, vsH, vsN;
+  const int32_t *path, *n_accept;      // [B][T], [B]
+  const float *k_chan_scale, *v_chan_scale;
+  const int32_t *lengths, *seen;       // seen null: lengths
+  const float *k_mean, *v_code_amax;
+  int32_t *lengths_out, *seen_out;
+  float *k_mean_out, *v_code_amax_out;
+  float* weights;                      // null, or [B][Hkv][cap]: new rows zeroed
+  int8_t *k_codes, *v_codes;
+  unsigned int* err;
+};
+cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s);
+
+struct EvictArgs {
+  int B, Hkv, Nk, d;
+  long long cap, out_cap;
+  int budget, n_sink, n_recent;
+  const int8_t *k_codes, *v_codes;
+  const float* weights;
+  const int32_t* lengths;
+  int8_t *k_out, *v_out;
+  float* weights_out;
+  int32_t* kept;        // [B][Hkv][budget]
+  int32_t* lengths_out;
+  float* v_code_amax;
+  unsigned int* err;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 
 // ---- exact24.cu
 struct Exact24Args {

@@ -267,6 +267,110 @@ class QFlashProblem:
         return 2 + 2 + 1
 
 
+def tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """qattn_tree_decode's ancestor words, int32 [B, T, ceil(T / 32)], of drafted
+    trees given by their parents: parents[b, j] is the draft that j continues
+    (any i < j), -1 if j continues the last cached token, -2 for a padding entry,
+    which sees nothing and is seen by no other draft.  Set-up in plain tensor
+    operations, on the parents' device."""
+    B, T = parents.shape
+    j = torch.arange(T, device=parents.device)
+    if bool(((parents < -2) | (parents >= j)).any()):
+        raise ValueError("parents[b, j] must be -2, -1 or a draft before j")
+    live = parents > -2
+    if bool((torch.gather(parents, 1, parents.clamp_min(0).long()) == -2)[parents >= 0].any()):
+        raise ValueError("a draft continues a padding entry")
+    see = torch.zeros(B, T, T, dtype=torch.float32, device=parents.device)
+    see[:, j, j] = live.float()
+    up = torch.zeros_like(see)
+    up.scatter_(2, parents.clamp_min(0).long()[:, :, None], (parents >= 0).float()[:, :, None])
+    see, span = ((see + up) > 0).float(), 1
+    while span < T:  # paths of up to 2 span edges
+        see, span = (see @ see > 0).float(), 2 * span
+    words = (T + 31) // 32
+    bits = torch.zeros(B, T, words * 32, dtype=torch.int64, device=parents.device)
+    bits[:, :, :T] = see.long()
+    w = (bits.view(B, T, words, 32) << torch.arange(32, device=parents.device)).sum(-1)
+    return torch.where(w >= 2 ** 31, w - 2 ** 32, w).to(torch.int32)
+
+
+class TreeCache:
+    """An int8 KV cache served by speculative decoding: each step verifies a tree
+    of drafted tokens (``verify``), appends the accepted path (``commit``) and may
+    keep account of the attention each row receives (``weigh``), by which
+    ``evict`` cuts the cache to a budget of rows.
+
+    k_codes, v_codes: int8 [B, Hkv, capacity, d], the cache; k_scale, v_scale: its
+    channel scales and k_mean, v_code_amax: its header, fp32 [B, Hkv, d]; lengths:
+    int32 [B], rows in use.  The arrays are used and updated in place; ``evict``
+    moves to a second set of the same capacity and back.  All calls go to the
+    current stream (or ``stream``) and none waits for the GPU."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, k_mean, v_code_amax, lengths, Hq, T, *,
+                 out_dtype=qb.DT_BF16, sm_scale=0.0, max_rows=None):
+        B, Hkv, cap, d = k_codes.shape
+        dev = k_codes.device
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.k_mean, self.v_code_amax, self.lengths = k_mean, v_code_amax, lengths
+        self.seen = lengths.clone()
+        f32 = torch.float32
+        self.weights = torch.zeros((B, Hkv, cap), dtype=f32, device=dev)
+        self.shape = qb.make_shape(B, Hq, Hkv, T, cap if max_rows is None else max_rows, d)
+        self.params = qb.make_params(causal=True, out_dtype=out_dtype, sm_scale=sm_scale,
+                                     kv_capacity=cap)
+        self._all = qb.make_params(out_dtype=out_dtype, sm_scale=sm_scale, kv_capacity=cap)
+        self._q = (qb.make_shape(B, Hq, Hkv, T, 0, d), qb.make_params())
+        self.q_codes = torch.empty((B, Hq, T, d), dtype=torch.int8, device=dev)
+        self.q_scales = torch.empty(qb.n_scales(qb.GRAN_BLOCK, B, Hq, T), dtype=f32, device=dev)
+        self.O = torch.empty((B, Hq, T, d), device=dev,
+                             dtype=torch.bfloat16 if out_dtype == qb.DT_BF16 else f32)
+        self.lse = torch.empty((B, Hq, T), dtype=f32, device=dev)
+        ws = max(qb.tree_workspace_size(self.shape, self.params), qb.workspace_size(*self._q), 256)
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self._spare = None
+
+    def verify(self, Q, K_new=None, V_new=None, tree_mask=None, stream=None):
+        """Attention of the T drafted tokens (Q bf16 [B, Hq, T, d]) over the cache and
+        the drafts' own K_new, V_new (bf16 [B, Hkv, T, d]); tree_mask None: a chain.
+        K_new None: the T last rows in use are the tokens' own."""
+        qb.quantize_qk(Q, None, qb.DT_I8, None, self.k_scale, *self._q, self.q_codes, self.q_scales,
+                       None, None, self.workspace, stream)
+        qb.tree_decode(self.q_codes, self.q_scales, self.k_codes, self.v_codes, self.k_scale,
+                       self.v_scale, self.shape, self.params, self.O, self.lse, self.workspace,
+                       lengths=self.lengths, K_new=K_new, V_new=V_new, k_mean=self.k_mean,
+                       tree_mask=tree_mask, stream=stream)
+        return self.O
+
+    def weigh(self, lse=None, stream=None):
+        """Add the weight the last ``verify``'s drafts gave each cached row.  lse: its
+        ``lse`` with -inf for the drafts that do not count (the rejected ones).
+        Call it before ``commit``: it reads the rows in use then."""
+        qb.kv_weights(self.q_codes, self.q_scales, self.k_codes, None, self.lse if lse is None else lse,
+                      self.shape, self._all, self.weights, base=self.weights, lengths=self.lengths,
+                      stream=stream)
+
+    def commit(self, K_new, V_new, path, n_accept, stream=None):
+        """Append drafts path[b, :n_accept[b]] (int32, device) to each sequence."""
+        qb.tree_commit(K_new, V_new, path, n_accept, self.k_scale, self.v_scale, self.lengths,
+                       self.k_mean, self.v_code_amax, self.k_codes, self.v_codes, seen=self.seen,
+                       weights=self.weights, stream=stream)
+
+    def evict(self, budget, n_sink=0, n_recent=0, stream=None):
+        """Keep the budget rows of most weight per KV head; returns the kept rows'
+        former indices, int32 [B, Hkv, budget]."""
+        if self._spare is None:
+            self._spare = [torch.zeros_like(t) for t in (self.k_codes, self.v_codes, self.weights,
+                                                         self.lengths)]
+        k, v, w, n = self._spare
+        kept = torch.empty((*self.weights.shape[:2], budget), dtype=torch.int32, device=w.device)
+        qb.kv_evict(self.k_codes, self.v_codes, self.weights, budget, k, v, w, kept, n,
+                    self.v_code_amax, lengths=self.lengths, Nk=self.shape.Nk, n_sink=n_sink,
+                    n_recent=n_recent, stream=stream)
+        self._spare = [self.k_codes, self.v_codes, self.weights, self.lengths]
+        self.k_codes, self.v_codes, self.weights, self.lengths = k, v, w, n
+        return kept
+
+
 def problem_for(wl, **kw) -> Problem:
     """A Problem sized for a workload from quantized_attention_gb300.inputs."""
     return Problem(wl.B, wl.Hq, wl.Hkv, wl.Nq, wl.Nk, wl.d, causal=wl.causal, q_gran=wl.q_gran,
