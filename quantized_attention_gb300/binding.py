@@ -345,28 +345,51 @@ def kv_header_init(v_codes, Nk, v_code_amax, stream=None):
            "qattn_kv_header_init")
 
 
-def _want(name: str, t: Optional[torch.Tensor], dtype, shape, optional=False):
-    """A dense tensor of this type and shape (None in a dimension: any size) on the
-    current CUDA device, whose kernels and stream the call uses."""
+def _reject(name: str, t, dtype, shape, dev: int):
+    """Says what is wrong with an argument that failed _expect's test."""
     if t is None:
-        if optional:
-            return
         raise ValueError(f"{name} is missing")
-    _dense(t, dtype, name)
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-
-
-def _want_input(name: str, t: Optional[torch.Tensor], shape):
-    """A bf16 input at any strides (see _input), its shape and device checked."""
-    st = _input(t, torch.bfloat16, name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return st
+    _dense(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _expect(*args) -> int:
+    """Dense tensors of these types and shapes on the current CUDA device, whose
+    kernels and stream the call uses: (name, tensor, dtype, shape) each.  A
+    serving step makes these calls between short kernels, so a good argument costs
+    one line of tests.  Returns the device."""
+    dev = torch.cuda.current_device()
+    for name, t, dtype, shape in args:
+        if (t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                or not t.is_contiguous()):
+            _reject(name, t, dtype, shape, dev)
+    return dev
+
+
+def _expect_input(name: str, t, shape, dev: int):
+    """A bf16 input at any strides (see _input), its shape and device checked."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+        _reject(name, t, torch.bfloat16, shape, dev)
+    return None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
+
+
+def _expect_scales(name: str, t, count: int, dev: int):
+    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
+        _reject(name, t, torch.float32, t.shape, dev)
+    if t.numel() < count:
+        raise ValueError(f"{name}: too few for the granularity")
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
 def tree_workspace_size(shape: Shape, params: Params) -> int:
@@ -381,35 +404,35 @@ def tree_decode(q_codes, q_scales, k_codes, v_codes, k_chan_scale, v_chan_scale,
     K_new, V_new: bf16 [B, Hkv, T, d] (None: the tokens' rows are in the cache);
     tree_mask: int32 [B, T, ceil(T / 32)] ancestor words (None: a chain if
     params.causal, else every draft sees every draft)."""
-    B, Hq, Hkv, T, d = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d
-    cap = params.kv_capacity or shape.Nk
-    f32 = torch.float32
-    _want("q_codes", q_codes, torch.int8, (B, Hq, T, d))
-    if q_scales.numel() < n_scales(params.q_gran, B, Hq, T):
-        raise ValueError("q_scales: too few for the granularity")
-    _dense(q_scales, f32, "q_scales")
-    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d), optional=shape.Nk == 0)
-    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d), optional=shape.Nk == 0)
-    head = (B, Hkv, d)
-    _want("v_chan_scale", v_chan_scale, f32, head)
-    _want("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, (B, Hq, T, d))
-    _want("lse", lse, f32, (B, Hq, T), optional=True)
-    _want("lengths", lengths, torch.int32, (B,), optional=True)
-    _want("tree_mask", tree_mask, torch.int32, (B, T, (T + 31) // 32), optional=True)
-    ks = vs = None
-    if K_new is not None or V_new is not None:
+    B, Hq, Hkv, T, d, Nk = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d, shape.Nk
+    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    head, cache = (B, Hkv, d), (B, Hkv, params.kv_capacity or Nk, d)
+    args = [("q_codes", q_codes, i8, (B, Hq, T, d)), ("v_chan_scale", v_chan_scale, f32, head),
+            ("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, (B, Hq, T, d))]
+    if Nk > 0 or k_codes is not None:
+        args += [("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache)]
+    if lse is not None:
+        args.append(("lse", lse, f32, (B, Hq, T)))
+    if lengths is not None:
+        args.append(("lengths", lengths, i32, (B,)))
+    if tree_mask is not None:
+        args.append(("tree_mask", tree_mask, i32, (B, T, (T + 31) // 32)))
+    drafts = K_new is not None or V_new is not None
+    if drafts:
         if K_new is None or V_new is None:
             raise ValueError("K_new and V_new go together")
-        ks = _want_input("K_new", K_new, (B, Hkv, T, d))
-        vs = _want_input("V_new", V_new, (B, Hkv, T, d))
-        _want("k_chan_scale", k_chan_scale, f32, head)
-        _want("k_mean", k_mean, f32, head)
-    _check(lib().qattn_tree_decode(_p(q_codes), _p(q_scales), _p(k_codes), _p(v_codes),
-                                   _p(k_chan_scale), _p(v_chan_scale), _p(k_mean), _p(lengths),
-                                   _p(K_new), ks, _p(V_new), vs, _p(tree_mask),
-                                   ctypes.byref(shape), ctypes.byref(params), _p(O), _p(lse),
-                                   _p(workspace), _nbytes(workspace), _stream(stream)),
-           "qattn_tree_decode")
+        args += [("k_chan_scale", k_chan_scale, f32, head), ("k_mean", k_mean, f32, head)]
+    dev = _expect(*args)
+    _expect_scales("q_scales", q_scales, n_scales(params.q_gran, B, Hq, T), dev)
+    ks = _expect_input("K_new", K_new, (B, Hkv, T, d), dev) if drafts else None
+    vs = _expect_input("V_new", V_new, (B, Hkv, T, d), dev) if drafts else None
+    st = lib().qattn_tree_decode(_ptr(q_codes), _ptr(q_scales), _ptr(k_codes), _ptr(v_codes),
+                                 _ptr(k_chan_scale), _ptr(v_chan_scale), _ptr(k_mean), _ptr(lengths),
+                                 _ptr(K_new), ks, _ptr(V_new), vs, _ptr(tree_mask),
+                                 shape, params, _ptr(O), _ptr(lse), _ptr(workspace), _nbytes(workspace),
+                                 _raw_stream(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_tree_decode")
 
 
 def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, lengths, k_mean,
@@ -420,31 +443,32 @@ def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, length
     [B, T] draft indices, n_accept: int32 [B].  An output not given is written
     over the array it is computed from."""
     B, Hkv, T, d = K_new.shape
-    cap, f32, i32 = k_codes.shape[2], torch.float32, torch.int32
+    cap, i8, f32, i32 = k_codes.shape[2], torch.int8, torch.float32, torch.int32
     lengths_out = lengths if lengths_out is None else lengths_out
     k_mean_out = k_mean if k_mean_out is None else k_mean_out
     v_code_amax_out = v_code_amax if v_code_amax_out is None else v_code_amax_out
     seen_out = seen if seen_out is None else seen_out
-    ks = _want_input("K_new", K_new, (B, Hkv, T, d))
-    vs = _want_input("V_new", V_new, (B, Hkv, T, d))
-    _want("path", path, i32, (B, T))
-    for name, t in (("n_accept", n_accept), ("lengths", lengths), ("lengths_out", lengths_out)):
-        _want(name, t, i32, (B,))
-    _want("seen", seen, i32, (B,), optional=True)
-    _want("seen_out", seen_out, i32, (B,), optional=True)
-    for name, t in (("k_chan_scale", k_chan_scale), ("v_chan_scale", v_chan_scale), ("k_mean", k_mean),
-                    ("v_code_amax", v_code_amax), ("k_mean_out", k_mean_out),
-                    ("v_code_amax_out", v_code_amax_out)):
-        _want(name, t, f32, (B, Hkv, d))
-    _want("weights", weights, f32, (B, Hkv, cap), optional=True)
-    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
-    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d))
-    _check(lib().qattn_tree_commit(_p(K_new), ks, _p(V_new), vs, _p(path), _p(n_accept), B, Hkv, T, d,
-                                   cap, _p(k_chan_scale), _p(v_chan_scale), _p(lengths), _p(seen),
-                                   _p(k_mean), _p(v_code_amax), _p(lengths_out), _p(seen_out),
-                                   _p(k_mean_out), _p(v_code_amax_out), _p(weights), _p(k_codes),
-                                   _p(v_codes), _stream(stream)),
-           "qattn_tree_commit")
+    head, cache, seqs = (B, Hkv, d), (B, Hkv, cap, d), (B,)
+    args = [("path", path, i32, (B, T)), ("n_accept", n_accept, i32, seqs), ("lengths", lengths, i32, seqs),
+            ("lengths_out", lengths_out, i32, seqs), ("k_chan_scale", k_chan_scale, f32, head),
+            ("v_chan_scale", v_chan_scale, f32, head), ("k_mean", k_mean, f32, head),
+            ("v_code_amax", v_code_amax, f32, head), ("k_mean_out", k_mean_out, f32, head),
+            ("v_code_amax_out", v_code_amax_out, f32, head), ("k_codes", k_codes, i8, cache),
+            ("v_codes", v_codes, i8, cache)]
+    if seen is not None or seen_out is not None:
+        args += [("seen", seen, i32, seqs), ("seen_out", seen_out, i32, seqs)]
+    if weights is not None:
+        args.append(("weights", weights, f32, (B, Hkv, cap)))
+    dev = _expect(*args)
+    ks = _expect_input("K_new", K_new, (B, Hkv, T, d), dev)
+    vs = _expect_input("V_new", V_new, (B, Hkv, T, d), dev)
+    st = lib().qattn_tree_commit(_ptr(K_new), ks, _ptr(V_new), vs, _ptr(path), _ptr(n_accept), B, Hkv, T, d,
+                                 cap, _ptr(k_chan_scale), _ptr(v_chan_scale), _ptr(lengths), _ptr(seen),
+                                 _ptr(k_mean), _ptr(v_code_amax), _ptr(lengths_out), _ptr(seen_out),
+                                 _ptr(k_mean_out), _ptr(v_code_amax_out), _ptr(weights), _ptr(k_codes),
+                                 _ptr(v_codes), _raw_stream(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_tree_commit")
 
 
 def kv_weights(q_codes, q_scales, k_codes, k_scales, lse, shape, params, weights, *, base=None,
@@ -452,25 +476,23 @@ def kv_weights(q_codes, q_scales, k_codes, k_scales, lse, shape, params, weights
     """Attention weight that each cached row received from these queries, added to
     base (see qattn_kv_weights in include/qattn.h).  weights, base: fp32 [B, Hkv,
     capacity]; lse: fp32 [B, Hq, Nq]."""
-    B, Hq, Hkv, T, d = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d
-    cap, f32 = params.kv_capacity or shape.Nk, torch.float32
-    _want("q_codes", q_codes, torch.int8, (B, Hq, T, d))
-    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
-    _want("lse", lse, f32, (B, Hq, T))
-    _want("weights", weights, f32, (B, Hkv, cap))
-    _want("base", base, f32, (B, Hkv, cap), optional=True)
-    _want("lengths", lengths, torch.int32, (B,), optional=True)
-    _dense(q_scales, f32, "q_scales")
-    if q_scales.numel() < n_scales(params.q_gran, B, Hq, T):
-        raise ValueError("q_scales: too few for the granularity")
+    B, Hq, Hkv, T, d, Nk = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d, shape.Nk
+    cap, i8, f32 = params.kv_capacity or Nk, torch.int8, torch.float32
+    args = [("q_codes", q_codes, i8, (B, Hq, T, d)), ("k_codes", k_codes, i8, (B, Hkv, cap, d)),
+            ("lse", lse, f32, (B, Hq, T)), ("weights", weights, f32, (B, Hkv, cap))]
+    if base is not None:
+        args.append(("base", base, f32, (B, Hkv, cap)))
+    if lengths is not None:
+        args.append(("lengths", lengths, torch.int32, (B,)))
+    dev = _expect(*args)
+    _expect_scales("q_scales", q_scales, n_scales(params.q_gran, B, Hq, T), dev)
     if k_scales is not None:
-        _dense(k_scales, f32, "k_scales")
-        if k_scales.numel() < n_scales(params.k_gran, B, Hkv, shape.Nk):
-            raise ValueError("k_scales: too few for the granularity")
-    _check(lib().qattn_kv_weights(_p(q_codes), _p(q_scales), _p(k_codes), _p(k_scales), _p(lse),
-                                  _p(lengths), ctypes.byref(shape), ctypes.byref(params), _p(base),
-                                  _p(weights), _stream(stream)),
-           "qattn_kv_weights")
+        _expect_scales("k_scales", k_scales, n_scales(params.k_gran, B, Hkv, Nk), dev)
+    st = lib().qattn_kv_weights(_ptr(q_codes), _ptr(q_scales), _ptr(k_codes), _ptr(k_scales), _ptr(lse),
+                                _ptr(lengths), shape, params, _ptr(base), _ptr(weights),
+                                _raw_stream(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_kv_weights")
 
 
 def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept, lengths_out,
@@ -478,23 +500,22 @@ def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept,
     """Keep the budget rows of most weight per KV head (see qattn_kv_evict in
     include/qattn.h).  Nk: most rows in use (default: the capacity)."""
     B, Hkv, cap, d = k_codes.shape
-    Nk = cap if Nk is None else int(Nk)
-    ocap = k_out.shape[2]
-    _want("k_codes", k_codes, torch.int8, (B, Hkv, cap, d))
-    _want("v_codes", v_codes, torch.int8, (B, Hkv, cap, d))
-    _want("weights", weights, torch.float32, (B, Hkv, cap))
-    _want("k_out", k_out, torch.int8, (B, Hkv, ocap, d))
-    _want("v_out", v_out, torch.int8, (B, Hkv, ocap, d))
-    _want("weights_out", weights_out, torch.float32, (B, Hkv, ocap))
-    _want("kept", kept, torch.int32, (B, Hkv, int(budget)))
-    _want("lengths_out", lengths_out, torch.int32, (B,))
-    _want("lengths", lengths, torch.int32, (B,), optional=True)
-    _want("v_code_amax", v_code_amax, torch.float32, (B, Hkv, d))
-    _check(lib().qattn_kv_evict(_p(k_codes), _p(v_codes), _p(weights), _p(lengths), B, Hkv, Nk, d, cap,
-                                int(budget), int(n_sink), int(n_recent), _p(k_out), _p(v_out), ocap,
-                                _p(weights_out), _p(kept), _p(lengths_out), _p(v_code_amax),
-                                _stream(stream)),
-           "qattn_kv_evict")
+    Nk, budget, ocap = cap if Nk is None else int(Nk), int(budget), k_out.shape[2]
+    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    cache, out = (B, Hkv, cap, d), (B, Hkv, ocap, d)
+    args = [("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache),
+            ("weights", weights, f32, (B, Hkv, cap)), ("k_out", k_out, i8, out), ("v_out", v_out, i8, out),
+            ("weights_out", weights_out, f32, (B, Hkv, ocap)), ("kept", kept, i32, (B, Hkv, budget)),
+            ("lengths_out", lengths_out, i32, (B,)), ("v_code_amax", v_code_amax, f32, (B, Hkv, d))]
+    if lengths is not None:
+        args.append(("lengths", lengths, i32, (B,)))
+    dev = _expect(*args)
+    st = lib().qattn_kv_evict(_ptr(k_codes), _ptr(v_codes), _ptr(weights), _ptr(lengths), B, Hkv, Nk, d, cap,
+                              budget, int(n_sink), int(n_recent), _ptr(k_out), _ptr(v_out), ocap,
+                              _ptr(weights_out), _ptr(kept), _ptr(lengths_out), _ptr(v_code_amax),
+                              _raw_stream(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_kv_evict")
 
 
 def debug_qk_scores(q_codes, k_codes, shape, S, workspace, stream=None):

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
 
 unsigned int check_take_kv_weights() { return check_take_local(); }
 
-cudaError_t launch_kv_weights(const WeightArgs& a, cudaStream_t s) {
+cudaError_t launch_kv_weights_warp(const WeightArgs& a, cudaStream_t s) {
   const dim3 grid((a.Nk + kKeys - 1) / kKeys, a.B * a.Hkv);
   return a.d == 64 ? launch_pdl(kv_weights_warp_kernel<64>, grid, dim3(kThreads), 0, s, a)
                    : launch_pdl(kv_weights_warp_kernel<128>, grid, dim3(kThreads), 0, s, a);

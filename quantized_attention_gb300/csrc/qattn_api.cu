@@ -1135,10 +1135,15 @@ qattn_status qattn_kv_weights(const int8_t* q_codes, const float* q_scales, cons
   a.lengths = lengths;
   a.base = base;
   a.weights = weights;
+  const bool warp = static_cast<int64_t>(a.G) * a.Nq <= qattn::kWeightWarpRows;
   char sb[128];
-  QATTN_LOG_LINE("qattn_kv_weights %s causal=%d: kv_weights_warp_kernel", shape_str(shape, sb, sizeof sb),
-                 a.causal);
-  return from_cuda(qattn::launch_kv_weights(a, reinterpret_cast<cudaStream_t>(stream)));
+  QATTN_LOG_LINE("qattn_kv_weights %s causal=%d: %s", shape_str(shape, sb, sizeof sb), a.causal,
+                 warp ? "kv_weights_warp_kernel" : "kv_weights_tc_kernel");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (warp) return from_cuda(qattn::launch_kv_weights_warp(a, s));
+  CUtensorMap tk;
+  if (!encode_cache(&tk, k_codes, shape->B * shape->Hkv, shape->Nk, a.cap, shape->d, 128)) return QATTN_ERR_CUDA;
+  return from_cuda(qattn::launch_kv_weights_tc(tk, a, s));
 }
 
 qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const float* weights,
@@ -1237,6 +1242,7 @@ qattn_status qattn_get_error(qattn_stream_t stream) {
                               qattn::check_take_decode() | qattn::check_take_short() |
                               qattn::check_take_exact24() | qattn::check_take_intsm() |
                               qattn::check_take_tree_warp() | qattn::check_take_kv_weights() |
+                              qattn::check_take_kv_weights_tc() |
                               qattn::check_take_kv_cache();
   if (v & qattn::kErrTimeout) return QATTN_ERR_TIMEOUT;
   if (checks != 0) return QATTN_ERR_BOUNDS;

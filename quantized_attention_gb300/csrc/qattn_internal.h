@@ -57,6 +57,7 @@ unsigned int check_take_exact24();
 unsigned int check_take_intsm();
 unsigned int check_take_tree_warp();
 unsigned int check_take_kv_weights();
+unsigned int check_take_kv_weights_tc();
 unsigned int check_take_kv_cache();
 // One guard that fails for 16 of 32 threads, touching no memory (quant_kernels.cu).
 cudaError_t launch_bounds_probe(cudaStream_t s);
@@ -256,7 +257,15 @@ struct WeightArgs {
   float* weights;            // [B][Hkv][cap]
   unsigned int* err;
 };
-cudaError_t launch_kv_weights(const WeightArgs& a, cudaStream_t s);
+// Query rows (query heads of the group x tokens) up to which the warp-level
+// kernel runs; above, the tensor-core one.
+#ifndef QATTN_WEIGHT_ROWS
+#define QATTN_WEIGHT_ROWS 24
+#endif
+constexpr int kWeightWarpRows = QATTN_WEIGHT_ROWS;
+cudaError_t launch_kv_weights_warp(const WeightArgs& a, cudaStream_t s);
+// ---- kv_weights_tc.cu.  tk: map over the K codes, box d x 128 x 1.
+cudaError_t launch_kv_weights_tc(const CUtensorMap& tk, const WeightArgs& a, cudaStream_t s);
 
 // ---- kv_cache.cu
 struct CommitArgs {
