@@ -19,7 +19,7 @@ LIB = os.path.join(OUT_DIR, "libqattn.so")
 CHECK_DIR = os.path.join(OUT_DIR, "check")
 CHECK_LIB = os.path.join(CHECK_DIR, "libqattn.so")
 SOURCES = ["qattn_api.cu", "quant_kernels.cu", "attn_fwd.cu", "qattn_noalloc.cu", "decode.cu", "exact24.cu",
-           "intsm.cu", "attn_short.cu", "peaks.cu", "tree_warp.cu", "kv_weights.cu", "kv_weights_tc.cu",
+           "intsm.cu", "attn_short.cu", "peaks.cu", "tree_warp.cu", "tree_tc.cu", "kv_weights.cu", "kv_weights_tc.cu",
            "kv_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

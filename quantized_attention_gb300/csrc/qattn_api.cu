@@ -298,18 +298,22 @@ float sm_scale_of(const qattn_shape* s, const qattn_params* p) {
 // bound from Nk; the kernel divides the steps that the lengths give), and the
 // workspace of their shares.  The layout depends on the shape alone.
 struct TreeSplit {
-  int blocks, rows, drafts, ctas;
+  bool tc;  // the tensor-core kernel
+  int step, blocks, rows, drafts, ctas;
   size_t slots, off_m, off_l, bytes;
 };
 TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   TreeSplit t{};
   const int64_t R = s->Hq / s->Hkv * s->Nq;
-  const int step = qattn::tree_warp_step_keys();
-  t.rows = qattn::kTreeRows;
+  t.tc = R > qattn::kTreeRows;
+  t.step = t.tc ? qattn::kTreeTcStep : qattn::kTreeWarpStep;
+  t.rows = t.tc ? qattn::kTreeTcRows : qattn::kTreeRows;
   t.blocks = static_cast<int>((R + t.rows - 1) / t.rows);
-  t.drafts = drafts ? static_cast<int>((s->Nq + step - 1) / step) : 0;
-  const int64_t steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + step - 1) / step);
-  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(qattn::kTreeWarpCtas, (steps + 3) / 4)));
+  t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
+  const int64_t steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
+  const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
+  // a step per warp of a CTA of four, or per CTA
+  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? steps : (steps + 3) / 4)));
   t.slots = 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);
@@ -1013,15 +1017,15 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   CUtensorMap tk{}, tv{};
   if (shape->Nk > 0) {
     const int64_t cap = params->kv_capacity ? params->kv_capacity : shape->Nk;
-    const uint32_t box = static_cast<uint32_t>(qattn::tree_warp_step_keys());
+    const uint32_t box = static_cast<uint32_t>(sp.step);
     if (!encode_cache(&tk, k_codes, shape->B * shape->Hkv, shape->Nk, cap, shape->d, box) ||
         !encode_cache(&tv, v_codes, shape->B * shape->Hkv, shape->Nk, cap, shape->d, box))
       return QATTN_ERR_CUDA;
   }
   char sb[128];
-  QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: tree_warp_kernel + tree_join_kernel, %d CTAs",
-                 shape_str(shape, sb, sizeof sb), drafts ? a.T : 0, sp.ctas);
-  return from_cuda(qattn::launch_tree_warp(tk, tv, a, s));
+  QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s + tree_join_kernel, %d CTAs", shape_str(shape, sb, sizeof sb),
+                 drafts ? a.T : 0, sp.tc ? "tree_tc_kernel" : "tree_warp_kernel", sp.ctas);
+  return from_cuda(sp.tc ? qattn::launch_tree_tc(tk, tv, a, s) : qattn::launch_tree_warp(tk, tv, a, s));
 }
 
 qattn_status qattn_tree_commit(const uint16_t* K_new, const int64_t* k_strides,
@@ -1241,7 +1245,8 @@ qattn_status qattn_get_error(qattn_stream_t stream) {
   const unsigned int checks = qattn::check_take_attn_fwd() | qattn::check_take_quant() |
                               qattn::check_take_decode() | qattn::check_take_short() |
                               qattn::check_take_exact24() | qattn::check_take_intsm() |
-                              qattn::check_take_tree_warp() | qattn::check_take_kv_weights() |
+                              qattn::check_take_tree_warp() | qattn::check_take_tree_tc() |
+                              qattn::check_take_kv_weights() |
                               qattn::check_take_kv_weights_tc() |
                               qattn::check_take_kv_cache();
   if (v & qattn::kErrTimeout) return QATTN_ERR_TIMEOUT;

@@ -56,6 +56,7 @@ unsigned int check_take_short();
 unsigned int check_take_exact24();
 unsigned int check_take_intsm();
 unsigned int check_take_tree_warp();
+unsigned int check_take_tree_tc();
 unsigned int check_take_kv_weights();
 unsigned int check_take_kv_weights_tc();
 unsigned int check_take_kv_cache();
@@ -203,6 +204,9 @@ cudaError_t launch_kv_append(const uint16_t* K_new, const uint16_t* V_new, int B
 constexpr int kTreeMaxTokens = 128;  // drafted tokens of a sequence
 constexpr int kTreeRows = 16;        // query rows of the warp-level kernel's block
 constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
+constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
+constexpr int kTreeTcCtas = 152;     // its CTAs, at most
+constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
   int blocks;                    // row blocks of a head
@@ -232,11 +236,12 @@ struct TreeArgs {
   float* part_m;                 // [slots][block rows]
   float* part_l;
 };
-int tree_warp_step_keys();
-// tk, tv: maps over the int8 K and V codes, box d x 32 x 1 (128-byte swizzle
-// for d = 128, 64-byte for d = 64).
+// tk, tv: maps over the int8 K and V codes, box d x (keys of a step) x 1
+// (128-byte swizzle for d = 128, 64-byte for d = 64).
 cudaError_t launch_tree_warp(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
                              cudaStream_t s);
+cudaError_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
+                           cudaStream_t s);
 
 // ---- kv_weights.cu
 struct WeightArgs {

@@ -186,6 +186,19 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t sbo_bytes,
   return d;
 }
 
+// The same for an operand whose M or N index runs fastest in memory ("MN-major"),
+// 128-byte swizzle: rows of one k, 64 16-bit elements each; 8-row groups
+// sbo_bytes apart, the next 64 elements of M or N lbo_bytes away.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(kSwizzle128B) << 61;
+  return d;
+}
+
 // Instruction descriptor (kind::f16 / kind::f8f6f4): D format F32 (bits 4-5 =
 // 1), A/B formats in bits 7-9 / 10-12 (F16 = 0 for kind::f16, E4M3 = 0 for
 // kind::f8f6f4), both operands K-major (bits 15, 16 = 0), N >> 3 in bits
@@ -194,6 +207,8 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t M, uint32_t N, uint32
                                                   uint32_t b_fmt) {
   return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B is MN-major
 
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {

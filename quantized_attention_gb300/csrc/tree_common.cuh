@@ -138,10 +138,12 @@ __device__ __forceinline__ TreeSeg tree_segment(const TreeArgs& a, TreePlan& pla
 }
 
 // c = fp32(fp32(sq * sm_scale) * log2 e) of a query head's tokens (T <= 128: one
-// scale block).
+// scale block).  A factor of 0 (all the head's codes 0) becomes 1e-30: 2^(S c) is
+// 1 all the same for every |S| < 2^21, and a hidden key's -inf stays -inf.
 __device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq) {
   const float sq = a.q_gran == 0 ? a.q_scales[0] : a.q_scales[b * a.Hq + hq];
-  return __fmul_rn(__fmul_rn(sq, a.sm_scale), kLog2e);
+  const float c = __fmul_rn(__fmul_rn(sq, a.sm_scale), kLog2e);
+  return c > 0.f ? c : 1e-30f;
 }
 
 // Cached rows visible to token i: all of them, or (tokens already appended,
@@ -153,6 +155,7 @@ __device__ __forceinline__ int tree_limit(const TreeArgs& a, int len, int i) {
 // Drafts 32 s .. 32 s + 31 visible to token i of sequence b, one bit each.
 __device__ __forceinline__ uint32_t tree_draft_word(const TreeArgs& a, int b, int i, int s) {
   const uint32_t real = first_bits(a.T - 32 * s);
+  if (real == 0u) return 0u;  // past the mask's words
   if (!a.tree_mask) return a.draft_causal ? first_bits(i + 1 - 32 * s) & real : real;
   const int words = (a.T + 31) / 32;
   return a.tree_mask[(static_cast<size_t>(b) * a.T + i) * words + s] & real;

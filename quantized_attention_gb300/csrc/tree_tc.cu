@@ -1,0 +1,479 @@
+// Attention of drafted tokens over an int8 KV cache (qattn_tree_decode), for
+// more than 16 query rows of a KV head: 128 rows at a time on the
+// 5th-generation tensor cores.  Mathematics, work division and joining as in
+// tree_warp.cu, with steps of 128 keys.
+//
+//   warp 0       TMA: the steps' K and V codes into a ring of raw stages
+//   warp 1       TMEM and the MMAs
+//   warps 4-11   softmax: two threads a row (keys 0-63 and 64-127 of a step)
+//   warps 12-15  codes -> fp16 tiles K16, V16 [key][channel] in shared memory;
+//                a drafted step's codes are made by them first
+//
+// Per step: S = Q K16^T (Q as the A operand in TMEM), P = 2^(S c - m) rounded to
+// fp16 into TMEM, O += P V16 (V16 as it lies: the B operand with its N index
+// fastest).  Q and P in TMEM leave shared memory to the codes: 32 KB in, 32 KB
+// read, 64 KB of fp16 written and 64 KB read by the MMAs a step, ~1540 cycles
+// against ~1460 of the step's share of HBM and ~1030 of tensor work.  The
+// reference m moves only when a row's maximum has grown by more than 2^8 (P stays
+// below 2^8, far inside fp16), so O is rarely rescaled.
+#include <cuda_fp16.h>
+
+#include "qattn_check.cuh"
+#include "qattn_internal.h"
+#include "sm103_ptx.cuh"
+#include "tree_common.cuh"
+
+namespace qattn {
+namespace {
+
+constexpr int kStep = kTreeTcStep;
+constexpr int kRows = kTreeTcRows;
+static_assert(kStep == 128 && kRows == 128, "one TMEM lane per row, one block of keys per step");
+constexpr int kThreads = 512;
+constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
+constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;  // TMEM columns
+
+template <int D>
+struct Cfg {
+  static constexpr int kRawTile = kStep * D;          // K (or V) codes of a step
+  static constexpr int kHalf = kStep * D * 2;         // K16 (or V16): D / 64 blocks of [128][128 B]
+  static constexpr int kOff16 = 2 * 2 * kRawTile;     // after two raw stages
+  static constexpr int kOffX = kOff16 + 2 * 2 * kHalf;
+  static constexpr int kOffBar = kOffX + 2 * 2 * kRows * 4;  // row maxima: [buffer][half][row]
+  static constexpr int kBytes = kOffBar + 512 + 1024;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+enum {
+  kRawFull = 0,    // [2] TMA bytes (a drafted step: the loader's arrival)
+  kRawEmpty = 2,   // [2] 128 converting threads
+  kKFull = 4,      // [2] 128
+  kKEmpty = 6,     // [2] the step's QK MMAs
+  kVFull = 8,      // [2] 128
+  kVEmpty = 10,    // [2] the step's PV MMAs
+  kQReady = 12,    // 128 threads wrote Q
+  kSFull = 13,     // [2] QK MMAs
+  kPReady = 15,    // 256
+  kPvDone = 16,    // PV MMAs
+  kXFull = 17,     // [2 buffers][4 quadrants] 64
+  kDrafts = 25,    // 128 converting threads wrote a drafted step's codes
+  kDrain = 26,
+  kNumBars = 27
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const TreeArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ TreePlan plan;
+  pdl_trigger();
+  const uint32_t raw0 = smem_u32(raw_smem);
+  const uint32_t base = (raw0 + 1023u) & ~1023u;
+  uint8_t* smem = raw_smem + (base - raw0);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
+    return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
+  };
+  auto raw_k = [&](int st) { return base + st * 2 * C::kRawTile; };
+  auto raw_v = [&](int st) { return base + st * 2 * C::kRawTile + C::kRawTile; };
+  auto k16 = [&](int st) { return base + C::kOff16 + st * 2 * C::kHalf; };
+  auto v16 = [&](int st) { return base + C::kOff16 + st * 2 * C::kHalf + C::kHalf; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t n = 1;
+      if ((i >= kRawEmpty && i < kRawEmpty + 2) || (i >= kKFull && i < kKFull + 2) ||
+          (i >= kVFull && i < kVFull + 2) || i == kQReady || i == kDrafts)
+        n = 128;
+      if (i == kPReady) n = 256;
+      if (i >= kXFull && i < kXFull + 8) n = 64;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  tree_plan(a, kStep, &plan);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA
+      if (a.Nk > 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      bool ok = true;
+      uint32_t it = 0;
+      for (long long p = plan.begin; ok && p < plan.end;) {
+        const TreeSeg sg = tree_segment(a, plan, p, kStep);
+        p += sg.s1 - sg.s0;
+        const int bkv = sg.b * a.Hkv + sg.hkv;
+        for (int s = sg.s0; s < sg.s1; ++s, ++it) {
+          const int st = it & 1;
+          if (it >= 2 && !(ok = wait(kRawEmpty + st, (it >> 1) - 1))) break;
+          if (s < a.drafts) {
+            mbar_arrive(bar(kRawFull + st));
+          } else {
+            const int key = (s - a.drafts) * kStep;
+            mbar_arrive_expect_tx(bar(kRawFull + st), 2 * C::kRawTile);
+            tma_load_3d(raw_k(st), &tmK, bar(kRawFull + st), 0, key, bkv);
+            tma_load_3d(raw_v(st), &tmV, bar(kRawFull + st), 0, key, bkv);
+          }
+        }
+      }
+      // every load this thread issued lands before the CTA may exit
+      volatile int never = 0;
+      for (uint32_t back = 1; back <= 2; ++back)
+        if (it >= back)
+          mbar_wait(bar(kRawFull + ((it - back) & 1)), ((it - back) >> 1) & 1, &never, a.err, kErrTimeout);
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA
+      constexpr uint32_t idesc_qk = make_idesc(kRows, kStep, 0, 0);
+      constexpr uint32_t idesc_pv = make_idesc(kRows, D, 0, 0) | kIdescBMnMajor;
+      const uint64_t kd0 = smem_desc(k16(0), 1024, kSwizzle128B);
+      const uint64_t vd0 = smem_desc_mn(v16(0), kStep * 128, 1024);
+      bool ok = true;
+      uint32_t it = 0, seg = 0;  // steps and segments done
+      auto qk = [&](uint32_t t) -> bool {
+        const uint32_t st = t & 1;
+        if (!wait(kKFull + st, t >> 1)) return false;
+        tc_fence_after();
+        const uint64_t kd = kd0 + st * (2 * C::kHalf >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_f16_ts(tmem + kTmS + 128 * st, tmem + kTmQ + 8 * k, kd + ((k / 4) * (kStep * 128) + 32 * (k % 4)) / 16,
+                     idesc_qk, k > 0 ? 1u : 0u);
+        mma_commit(bar(kSFull + st));
+        mma_commit(bar(kKEmpty + st));
+        return true;
+      };
+      for (long long p = plan.begin; ok && p < plan.end; ++seg) {
+        const TreeSeg sg = tree_segment(a, plan, p, kStep);
+        const int n = sg.s1 - sg.s0;
+        p += n;
+        if (!(ok = wait(kQReady, seg))) break;
+        if (!(ok = qk(it))) break;
+        for (int j = 0; j < n; ++j, ++it) {
+          if (j + 1 < n && !(ok = qk(it + 1))) break;
+          const uint32_t st = it & 1;
+          if (!(ok = wait(kVFull + st, it >> 1) && wait(kPReady, it))) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + st * (2 * C::kHalf >> 4);
+#pragma unroll
+          for (int k = 0; k < kStep / 16; ++k)
+            mma_f16_ts(tmem + kTmO, tmem + kTmP + 8 * k, vd + (k * 2048) / 16, idesc_pv,
+                       (j > 0 || k > 0) ? 1u : 0u);
+          mma_commit(bar(kPvDone));
+          mma_commit(bar(kVEmpty + st));
+        }
+      }
+      mma_commit(bar(kDrain));
+      volatile int never = 0;
+      mbar_wait(bar(kDrain), 0, &never, a.err, kErrTimeout);
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
+    // -------------------------------------------------------------- softmax
+    const int quad = warp & 3, hf = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;  // TMEM lane, row of the block
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const int R = a.G * a.T;
+    float* xch = reinterpret_cast<float*>(smem + C::kOffX);
+    uint32_t it = 0, nx = 0;
+    bool ok = true;
+    // this half's value to the other half's thread of the row, and back
+    auto exchange = [&](float v, float& other) -> bool {
+      const int b2 = nx & 1;
+      xch[(b2 * 2 + hf) * kRows + r] = v;
+      mbar_arrive(bar(kXFull + 4 * b2 + quad));
+      const bool o = wait(kXFull + 4 * b2 + quad, nx >> 1);
+      ++nx;
+      if (!__all_sync(0xffffffffu, o)) return false;
+      other = xch[(b2 * 2 + 1 - hf) * kRows + r];
+      return true;
+    };
+    for (long long p = plan.begin; ok && p < plan.end;) {
+      const TreeSeg sg = tree_segment(a, plan, p, kStep);
+      p += sg.s1 - sg.s0;
+      const int rr = sg.rb * kRows + r;
+      const bool in = rr < R;
+      const int hq = in ? rr / a.T : 0, tok = in ? rr % a.T : 0;
+      const size_t row = (static_cast<size_t>(sg.b) * a.Hq + sg.hkv * a.G + hq) * a.T + tok;
+      if (hf == 0) {  // Q's row -> A in TMEM
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+          uint32_t x[32];
+          const uint4* src = reinterpret_cast<const uint4*>(a.q_codes + row * D) + 4 * e;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (in && QATTN_IN_BOUNDS(row < a.rows_total)) v = src[c];
+            codes4_to_f16x2(v.x, x[8 * c + 0], x[8 * c + 1]);
+            codes4_to_f16x2(v.y, x[8 * c + 2], x[8 * c + 3]);
+            codes4_to_f16x2(v.z, x[8 * c + 4], x[8 * c + 5]);
+            codes4_to_f16x2(v.w, x[8 * c + 6], x[8 * c + 7]);
+          }
+          tmem_st32(tmem + lane_base + kTmQ + 32 * e, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kQReady));
+      }
+      const float cf = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq) : 1.f;
+      const int lim = tree_limit(a, sg.len, tok);
+      float m = kNegInf, l = 0.f;  // the row's reference; this half's share of the sum
+      for (int s = sg.s0; s < sg.s1; ++s, ++it) {
+        const uint32_t st = it & 1;
+        ok = wait(kSFull + st, it >> 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v0[32], v1[32];
+        float mx0, mx1;
+        const uint32_t src = tmem + lane_base + kTmS + 128 * st + 64 * hf;
+        tmem_ld32_max(src, v0, mx0);
+        tmem_ld32_max(src + 32, v1, mx1);
+        tmem_wait_ld();
+        // ---- visibility
+        uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
+        if (s < a.drafts) {
+          w0 = tree_draft_word(a, sg.b, tok, 4 * s + 2 * hf);
+          w1 = tree_draft_word(a, sg.b, tok, 4 * s + 2 * hf + 1);
+        } else {
+          const int room = lim - (s - a.drafts) * kStep - 64 * hf;
+          w0 = first_bits(room);
+          w1 = first_bits(room - 32);
+        }
+        if (!__all_sync(0xffffffffu, (w0 & w1) == 0xffffffffu)) {
+          mx0 = mx1 = kNegInf;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!((w0 >> k) & 1u)) v0[k] = __float_as_uint(kNegInf);
+            if (!((w1 >> k) & 1u)) v1[k] = __float_as_uint(kNegInf);
+            mx0 = fmaxf(mx0, __uint_as_float(v0[k]));
+            mx1 = fmaxf(mx1, __uint_as_float(v1[k]));
+          }
+        }
+        float mx = fmaxf(mx0, mx1), other;
+        if (!(ok = exchange(mx, other))) break;
+        mx = fmaxf(mx, other);
+        // max S c = c max S (c > 0); a row that sees nothing stays at -inf
+        const float top = mx * cf;
+        const float mn = top > m + kLazy || m == kNegInf ? top : m;
+        const float ref = mn == kNegInf ? 0.f : mn;
+        const float2 c2 = make_float2(cf, cf), n2 = make_float2(-ref, -ref);
+        float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+        uint32_t pk[32];
+        auto half = [&](const uint32_t (&v)[32], uint32_t* out) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float2 t0 = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, n2);
+            float2 t1 = ffma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), c2, n2);
+            t0 = make_float2(ex2_approx(t0.x), ex2_approx(t0.y));
+            t1 = make_float2(ex2_approx(t1.x), ex2_approx(t1.y));
+            s0 = fadd2(s0, t0);
+            s1 = fadd2(s1, t1);
+            const __half2 h0 = __floats2half2_rn(t0.x, t0.y), h1 = __floats2half2_rn(t1.x, t1.y);
+            out[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+            out[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          }
+        };
+        half(v0, pk);
+        half(v1, pk + 16);
+        const float al = m == kNegInf ? 0.f : ex2_approx(m - ref);
+        l = l * (mn == m ? 1.f : al) + ((s0.x + s0.y) + (s1.x + s1.y));
+        // ---- O and P belong to the previous step's PV until it is done
+        if (it > 0) {
+          ok = wait(kPvDone, it - 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        if (s > sg.s0 && __any_sync(0xffffffffu, mn != m)) {
+          const float f = mn == m ? 1.f : al;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t x[32];
+            const uint32_t oc = tmem + lane_base + kTmO + (D / 2) * hf + 32 * c;
+            tmem_ld32(oc, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+            tmem_st32(oc, x);
+          }
+        }
+        tmem_st32(tmem + lane_base + kTmP + 32 * hf, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPReady));
+        m = mn;
+      }
+      if (!ok) break;
+      // ---- the segment's share: O from TMEM, l of both halves
+      float l_other;
+      if (!(ok = exchange(l, l_other))) break;
+      l += l_other;
+      ok = wait(kPvDone, it - 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t x[32];
+        const int ch = (D / 2) * hf + 32 * c;
+        tmem_ld32(tmem + lane_base + kTmO + ch, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
+                                       __uint_as_float(x[k + 3]));
+          if (whole) {
+            tree_write_out<D>(a, sg.b, sg.hkv, rr, ch + k, y, m, l);
+          } else if (in && QATTN_IN_BOUNDS(slot < a.slots)) {
+            *reinterpret_cast<float4*>(a.part_o + (slot * kRows + r) * D + ch + k) = y;
+          }
+        }
+      }
+      if (!whole && in && hf == 0 && QATTN_IN_BOUNDS(slot < a.slots)) {
+        a.part_m[slot * kRows + r] = m;
+        a.part_l[slot * kRows + r] = l;
+      }
+      tc_fence_before();  // the next segment's MMAs overwrite O
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp >= 12) {
+    // -------------------------------------------------------------- codes -> fp16
+    // Thread: 16-byte chunk 4 cb + cc of rows rw, rw + RS, ...  The eight lanes of an
+    // access take four chunks of rows r and r ^ 5, which differ in the swizzle's
+    // low and high bit: eight bank groups for the loads and for the stores.
+    constexpr int NB = D / 64, RS = 32 / NB, CH = kStep / RS;
+    const int tid = threadIdx.x - 384;
+    const int cc = tid & 3, cb = NB == 2 ? (tid >> 3) & 1 : 0;
+    const int u = tid >> (3 + NB - 1);  // row pair: 4 of an 8-row group
+    const int rw = 8 * (u >> 2) + ((u & 3) ^ (((tid >> 2) & 1) * 5));
+    const int chunk = 4 * cb + cc;
+    const uint32_t src0 = rw * D + 16 * (chunk ^ ((D == 128) ? (rw & 7) : ((rw >> 1) & 3)));
+    const uint32_t dst0 = cb * (kStep * 128) + rw * 128;
+    const uint32_t c0 = ((2 * cc) ^ (rw & 7)) << 4, c1 = ((2 * cc + 1) ^ (rw & 7)) << 4;
+    auto convert = [&](uint32_t src, uint32_t dst) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const uint4 v = lds128(src + src0 + RS * D * i);
+        uint32_t h[8];
+        codes4_to_f16x2(v.x, h[0], h[1]);
+        codes4_to_f16x2(v.y, h[2], h[3]);
+        codes4_to_f16x2(v.z, h[4], h[5]);
+        codes4_to_f16x2(v.w, h[6], h[7]);
+        sts128(dst + dst0 + RS * 128 * i + c0, h[0], h[1], h[2], h[3]);
+        sts128(dst + dst0 + RS * 128 * i + c1, h[4], h[5], h[6], h[7]);
+      }
+    };
+    bool ok = true;
+    uint32_t it = 0, nd = 0;
+    for (long long p = plan.begin; ok && p < plan.end;) {
+      const TreeSeg sg = tree_segment(a, plan, p, kStep);
+      p += sg.s1 - sg.s0;
+      for (int s = sg.s0; s < sg.s1; ++s, ++it) {
+        const int st = it & 1;
+        ok = wait(kRawFull + st, it >> 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (s < a.drafts) {
+          uint8_t* kr = smem + (raw_k(st) - base);
+          uint8_t* vr = smem + (raw_v(st) - base);
+          auto at = [](uint8_t* t, int rr, int c) {
+            return t + rr * D + 16 * (c ^ ((D == 128) ? (rr & 7) : ((rr >> 1) & 3)));
+          };
+          tree_encode_drafts<D>(a, sg.b, sg.hkv, s * kStep, kStep, tid, 128,
+                                [&](int rr, int c) { return at(kr, rr, c); },
+                                [&](int rr, int c) { return at(vr, rr, c); });
+          mbar_arrive(bar(kDrafts));
+          ok = wait(kDrafts, nd);
+          ++nd;
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+        if (it >= 2) {
+          ok = wait(kKEmpty + st, (it >> 1) - 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+        convert(raw_k(st), k16(st));
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kKFull + st));
+        if (it >= 2) {
+          ok = wait(kVEmpty + st, (it >> 1) - 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+        convert(raw_v(st), v16(st));
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kVFull + st));
+        mbar_arrive(bar(kRawEmpty + st));
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
+  constexpr int smem = Cfg<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(tree_tc_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
+  if (e != cudaSuccess || (a.ctas == 1 && a.drafts > 0)) return e;
+  return launch_pdl(tree_join_kernel<D, kRows, kStep>, dim3(a.B * a.Hkv * a.blocks, kRows),
+                    dim3(kTreeJoinThreads), 0, s, a);
+}
+
+}  // namespace
+
+unsigned int check_take_tree_tc() { return check_take_local(); }
+
+cudaError_t launch_tree_tc(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
+  return a.d == 64 ? launch_d<64>(tk, tv, a, s) : launch_d<128>(tk, tv, a, s);
+}
+
+}  // namespace qattn

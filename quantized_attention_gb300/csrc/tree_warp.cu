@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;  // keys per warp step
+constexpr int kStep = kTreeWarpStep;  // keys per warp step
 constexpr int kRing = 3;   // stages of a warp's ring (K and V of one step each)
 
 template <int D>
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         codes4_to_f16x2(x.z, qa[4 * w4 + 2][h], qa[4 * w4 + 2][2 + h]);
         codes4_to_f16x2(x.w, qa[4 * w4 + 3][h], qa[4 * w4 + 3][2 + h]);
       }
-      cf[h] = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq) : 0.f;
+      cf[h] = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq) : 1.f;
       lim[h] = tree_limit(a, sg.len, i);
       tok[h] = i;
     }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 4; ++e)
             if (!((vis[e >> 1] >> (8 * j + 2 * t4 + (e & 1))) & 1u)) s[j][e] = kNegInf;
       }
-      // running maxima: max S c = c max S (c >= 0); -inf stays -inf
+      // running maxima: max S c = c max S (c > 0); -inf stays -inf
       float al[2], ref[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; j < 4; ++j) x = fmax3(x, s[j][2 * h], s[j][2 * h + 1]);
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = (x == kNegInf) ? m[h] : fmaxf(m[h], x * cf[h]);
+        const float mn = fmaxf(m[h], x * cf[h]);
         ref[h] = (mn == kNegInf) ? 0.f : mn;
         al[h] = (m[h] == kNegInf) ? 0.f : ex2_approx(m[h] - ref[h]);
         m[h] = mn;
@@ -221,9 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float pr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // a masked S of -inf times a factor of 0 would be NaN: select first
-          const float x = masked && s[j][e] == kNegInf ? kNegInf : fmaf(s[j][e], cf[e >> 1], -ref[e >> 1]);
-          pr[e] = ex2_approx(x);
+          pr[e] = ex2_approx(fmaf(s[j][e], cf[e >> 1], -ref[e >> 1]));
         }
         l[0] += pr[0] + pr[1];
         l[1] += pr[2] + pr[3];
@@ -369,8 +367,6 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
 }  // namespace
 
 unsigned int check_take_tree_warp() { return check_take_local(); }
-
-int tree_warp_step_keys() { return kStep; }
 
 cudaError_t launch_tree_warp(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a,
                              cudaStream_t s) {
