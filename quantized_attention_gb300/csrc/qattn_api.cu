@@ -300,6 +300,7 @@ float sm_scale_of(const qattn_shape* s, const qattn_params* p) {
 struct TreeSplit {
   bool tc;  // the tensor-core kernel
   int step, blocks, rows, drafts, ctas;
+  int64_t steps;  // of all heads, at most
   size_t slots, off_m, off_l, bytes;
 };
 TreeSplit tree_split(const qattn_shape* s, bool drafts) {
@@ -310,10 +311,10 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.rows = t.tc ? qattn::kTreeTcRows : qattn::kTreeRows;
   t.blocks = static_cast<int>((R + t.rows - 1) / t.rows);
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
-  const int64_t steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
+  t.steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
   // a step per warp of a CTA of four, or per CTA
-  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? steps : (steps + 3) / 4)));
+  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
   t.slots = 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);
@@ -966,6 +967,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (shape->Nk == 0 && !drafts) return no_key_rows(shape, params, O, lse, s);
   const TreeSplit sp = tree_split(shape, drafts);
+  if (sp.steps >= (int64_t{1} << 31)) return QATTN_ERR_UNSUPPORTED;  // counted in 32 bits
   if (!workspace || workspace_bytes < sp.bytes || !aligned16(workspace)) return QATTN_ERR_WORKSPACE;
   qattn::TreeArgs a{};
   if (drafts) {

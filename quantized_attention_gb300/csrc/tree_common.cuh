@@ -33,16 +33,17 @@ __device__ __forceinline__ int tree_length(const TreeArgs& a, int b) {
 }
 
 // Steps of one head of a sequence: its drafted steps, then its cached ones.
-__device__ __forceinline__ long long tree_steps(const TreeArgs& a, int len, int step) {
+__device__ __forceinline__ int tree_steps(const TreeArgs& a, int len, int step) {
   return a.drafts + (len + step - 1) / step;
 }
 
-struct TreePlan {
-  long long begin, end;  // this CTA's steps in the flattened list
-  long long total;       // all steps
-  long long seq0;        // first step of sequence seq
-  int seq;               // the sequence that holds `begin`
-  long long warp_sum[32];
+// A CTA's share of the flattened list of W steps (ordered by sequence, KV head,
+// row block, step; W < 2^31): CTA c of G takes W / G of them, the first W % G
+// CTAs one more.  A segment is a run of the share inside one head.
+struct TreeWalk {
+  int p, end;         // the next step of the share in the list, its end
+  int b, head, s0;    // where p lies: sequence, (KV head, row block), step of the head
+  int len, steps;     // the sequence's rows in use, steps of each of its heads
 };
 
 struct TreeSeg {
@@ -52,91 +53,101 @@ struct TreeSeg {
   int steps;       // all steps of the head
 };
 
-// Fills the plan (all threads of the CTA; one barrier or more, the last one
-// after the plan is complete).  The flattened list is ordered by sequence, KV
-// head, row block, step; CTA c of G takes [c W / G, (c + 1) W / G).
-__device__ __forceinline__ void tree_plan(const TreeArgs& a, int step, TreePlan* plan) {
-  const int per = a.Hkv * a.blocks, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nw = blockDim.x >> 5;
-  if (!a.lengths) {
-    if (threadIdx.x == 0) {
-      const long long seq = per * tree_steps(a, a.Nk, step);
-      plan->total = seq * a.B;
-      plan->begin = blockIdx.x * plan->total / gridDim.x;
-      plan->end = (blockIdx.x + 1) * plan->total / gridDim.x;
-      plan->seq = seq > 0 ? static_cast<int>(plan->begin / seq) : 0;
-      plan->seq0 = plan->seq * seq;
-    }
-    __syncthreads();
-    return;
+// Steps of all sequences, and of those before sequence b0 (a whole warp).
+__device__ __forceinline__ void tree_totals(const TreeArgs& a, int step, int b0, int& total, int& before) {
+  const int per = a.Hkv * a.blocks, lane = threadIdx.x & 31;
+  total = before = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const int n = per * tree_steps(a, tree_length(a, b), step);
+    total += n;
+    if (b < b0) before += n;
   }
-  long long sum = 0;
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) sum += per * tree_steps(a, tree_length(a, b), step);
 #pragma unroll
-  for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
-  if (lane == 0) plan->warp_sum[warp] = sum;
-  __syncthreads();
-  if (warp == 0) {
-    long long total = lane < nw ? plan->warp_sum[lane] : 0;
-#pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) total += __shfl_xor_sync(0xffffffffu, total, sh);
-    const long long begin = blockIdx.x * total / gridDim.x;
-    // the sequence that holds `begin`: 32 sequences at a time
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const long long n = b0 + lane < a.B ? per * tree_steps(a, tree_length(a, b0 + lane), step) : 0;
-      long long inc = n;
-#pragma unroll
-      for (int sh = 1; sh < 32; sh <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, inc, sh);
-        if (lane >= sh) inc += o;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, base + inc > begin);
-      if (past) {
-        const int w = __ffs(past) - 1;
-        const long long before = __shfl_sync(0xffffffffu, inc - n, w);
-        if (lane == 0) {
-          plan->seq = b0 + w;
-          plan->seq0 = base + before;
-        }
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) {
-      plan->total = total;
-      plan->begin = begin;
-      plan->end = (blockIdx.x + 1) * total / gridDim.x;
-    }
+  for (int sh = 16; sh > 0; sh >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, sh);
+    before += __shfl_xor_sync(0xffffffffu, before, sh);
   }
-  __syncthreads();
 }
 
-// The segment that starts at step p (plan.begin <= p < plan.end) of the
-// flattened list, cut at the plan's end.  Segments are taken in order.
-__device__ __forceinline__ TreeSeg tree_segment(const TreeArgs& a, TreePlan& plan, long long p, int step) {
-  TreeSeg s;
-  int b = plan.seq;
-  long long seq0 = plan.seq0;
-  const long long per = static_cast<long long>(a.Hkv) * a.blocks;
-  s.len = tree_length(a, b);
-  long long n = tree_steps(a, s.len, step);
-  while (p >= seq0 + per * n && b + 1 < a.B) {  // sequences of no steps are passed over
-    seq0 += per * n;
-    s.len = tree_length(a, ++b);
-    n = tree_steps(a, s.len, step);
+// Where this CTA's share begins.  Called by whole warps, each for itself: no CTA
+// barrier, one round of loads up to 32 sequences.
+__device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& a, int step) {
+  const int per = a.Hkv * a.blocks, lane = threadIdx.x & 31;
+  TreeWalk w;
+  int my_len = 0, my_n = 0, total = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const int len = tree_length(a, b), n = tree_steps(a, len, step);
+    if (b < 32) {
+      my_len = len;
+      my_n = n;
+    }
+    total += per * n;
   }
-  const long long off = p - seq0, head = off / n;
-  s.b = b;
-  s.hkv = static_cast<int>(head / a.blocks);
-  s.rb = static_cast<int>(head % a.blocks);
-  s.steps = static_cast<int>(n);
-  s.s0 = static_cast<int>(off - head * n);
-  const long long left = plan.end - p;
-  s.s1 = static_cast<int>(min(static_cast<long long>(s.s0) + left, n));
-  return s;
+#pragma unroll
+  for (int sh = 16; sh > 0; sh >>= 1) total += __shfl_xor_sync(0xffffffffu, total, sh);
+  const int G = gridDim.x, c = blockIdx.x, q = total / G, r = total - q * G;
+  w.p = c * q + min(c, r);
+  w.end = w.p + q + (c < r ? 1 : 0);
+  w.b = w.head = w.s0 = w.len = w.steps = 0;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B && w.p < w.end; b0 += 32) {
+    if (b0 > 0) {
+      my_len = b0 + lane < a.B ? tree_length(a, b0 + lane) : 0;
+      my_n = b0 + lane < a.B ? tree_steps(a, my_len, step) : 0;
+    }
+    const int n = b0 + lane < a.B ? per * my_n : 0;
+    int inc = n;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, sh);
+      if (lane >= sh) inc += o;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.p);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int off = w.p - before - __shfl_sync(0xffffffffu, inc - n, l);
+      w.b = b0 + l;
+      w.len = __shfl_sync(0xffffffffu, my_len, l);
+      w.steps = __shfl_sync(0xffffffffu, my_n, l);
+      w.head = off / w.steps;
+      w.s0 = off - w.head * w.steps;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return w;
 }
 
+// The next segment of the share; false when it is done.
+__device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk& w, TreeSeg& s) {
+  if (w.p >= w.end) return false;
+  if (w.s0 == w.steps) {  // the next head; the next sequence that has steps
+    w.s0 = 0;
+    if (++w.head == a.Hkv * a.blocks) {
+      w.head = 0;
+      do {
+        w.len = tree_length(a, ++w.b);
+        w.steps = tree_steps(a, w.len, step);
+      } while (w.steps == 0);
+    }
+  }
+  s.b = w.b;
+  s.hkv = a.blocks == 1 ? w.head : w.head / a.blocks;
+  s.rb = a.blocks == 1 ? 0 : w.head - s.hkv * a.blocks;
+  s.len = w.len;
+  s.steps = w.steps;
+  s.s0 = w.s0;
+  s.s1 = min(w.s0 + (w.end - w.p), w.steps);
+  w.p += s.s1 - s.s0;
+  w.s0 = s.s1;
+  return true;
+}
+
+// The CTA whose share holds step x of a list of `total`.
+__device__ __forceinline__ int tree_owner(int x, int total, int G) {
+  const int q = total / G, r = total - q * G, big = r * (q + 1);
+  return x < big ? x / (q + 1) : r + (x - big) / q;
+}
 // c = fp32(fp32(sq * sm_scale) * log2 e) of a query head's tokens (T <= 128: one
 // scale block).  A factor of 0 (all the head's codes 0) becomes 1e-30: 2^(S c) is
 // 1 all the same for every |S| < 2^21, and a hidden key's -inf stays -inf.
@@ -161,19 +172,27 @@ __device__ __forceinline__ uint32_t tree_draft_word(const TreeArgs& a, int b, in
   return a.tree_mask[(static_cast<size_t>(b) * a.T + i) * words + s] & real;
 }
 
-__device__ __forceinline__ uint32_t code_byte(float x) {
-  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu;
+// rint(x / s) clamped to +-127, as a byte.  The quotient by the reciprocal is off
+// by at most 2 ulp (3e-5 below 128), so it rounds as the IEEE quotient does unless
+// it lies next to a half: those few, and anything not finite, are divided.
+__device__ __forceinline__ uint32_t code_byte(float x, float s, float inv) {
+  const float q = x * inv;
+  float r = rintf(q);
+  if (!(fabsf(q - r) <= 0.4999f)) r = rintf(__fdiv_rn(x, s));
+  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -127.f), 127.f))) & 0xffu;
 }
 
-// The codes of drafts j0 .. j0 + n - 1 (zero past T) of (b, hkv), as
-// qattn_kv_append would store them with the header as it stands: kc =
-// clamp(rint((K - mu) / s_k)), vc = clamp(rint(V / s_v)).  `nthr` threads (a
-// multiple of 32), this one `tid`; k_at(r, c) and v_at(r, c) give the address of
-// 16-byte chunk c of row r.
+// The codes of drafts j0 .. min(j0 + n, T) - 1 of (b, hkv), as qattn_kv_append
+// would store them with the header as it stands: kc = clamp(rint((K - mu) / s_k)),
+// vc = clamp(rint(V / s_v)).  The step's other rows keep what they held: any byte
+// is a finite code, and no query sees them.  `nthr` threads (a multiple of 32),
+// this one `tid`; k_at(r, c) and v_at(r, c) give the address of 16-byte chunk c of
+// row r.
 template <int D, typename FK, typename FV>
 __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int hkv, int j0, int n,
                                                    int tid, int nthr, FK k_at, FV v_at) {
   constexpr int W = D / 4;  // words of a row
+  constexpr int U = 4;      // rows in flight
   const int w = tid % W;    // W <= 32 divides nthr
   const size_t ch = (static_cast<size_t>(b) * a.Hkv + hkv) * D + 4 * w;
   const float4 ks = *reinterpret_cast<const float4*>(a.k_chan_scale + ch);
@@ -181,22 +200,35 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
   const float4 vs = *reinterpret_cast<const float4*>(a.v_chan_scale + ch);
   const uint16_t* K = a.k_new + b * a.ksB + hkv * a.ksH + 4 * w;
   const uint16_t* V = a.v_new + b * a.vsB + hkv * a.vsH + 4 * w;
-  for (int r = tid / W; r < n; r += nthr / W) {
-    uint32_t kc = 0u, vc = 0u;
-    if (j0 + r < a.T) {
-      const uint2 k = *reinterpret_cast<const uint2*>(K + (j0 + r) * a.ksN);
-      const uint2 v = *reinterpret_cast<const uint2*>(V + (j0 + r) * a.vsN);
-      kc = code_byte(__fdiv_rn(__fsub_rn(bf16_bits_to_f32(k.x & 0xffffu), mu.x), ks.x)) |
-           code_byte(__fdiv_rn(__fsub_rn(bf16_bits_to_f32(k.x >> 16), mu.y), ks.y)) << 8 |
-           code_byte(__fdiv_rn(__fsub_rn(bf16_bits_to_f32(k.y & 0xffffu), mu.z), ks.z)) << 16 |
-           code_byte(__fdiv_rn(__fsub_rn(bf16_bits_to_f32(k.y >> 16), mu.w), ks.w)) << 24;
-      vc = code_byte(__fdiv_rn(bf16_bits_to_f32(v.x & 0xffffu), vs.x)) |
-           code_byte(__fdiv_rn(bf16_bits_to_f32(v.x >> 16), vs.y)) << 8 |
-           code_byte(__fdiv_rn(bf16_bits_to_f32(v.y & 0xffffu), vs.z)) << 16 |
-           code_byte(__fdiv_rn(bf16_bits_to_f32(v.y >> 16), vs.w)) << 24;
+  const int rows = min(n, a.T - j0), dr = nthr / W;
+  const float4 ki = make_float4(__frcp_rn(ks.x), __frcp_rn(ks.y), __frcp_rn(ks.z), __frcp_rn(ks.w));
+  const float4 vi = make_float4(__frcp_rn(vs.x), __frcp_rn(vs.y), __frcp_rn(vs.z), __frcp_rn(vs.w));
+  for (int r0 = tid / W; r0 < rows; r0 += U * dr) {
+    uint2 k[U], v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int r = r0 + i * dr;
+      k[i] = v[i] = make_uint2(0u, 0u);
+      if (r < rows) {
+        k[i] = *reinterpret_cast<const uint2*>(K + (j0 + r) * a.ksN);
+        v[i] = *reinterpret_cast<const uint2*>(V + (j0 + r) * a.vsN);
+      }
     }
-    *reinterpret_cast<uint32_t*>(k_at(r, w >> 2) + 4 * (w & 3)) = kc;
-    *reinterpret_cast<uint32_t*>(v_at(r, w >> 2) + 4 * (w & 3)) = vc;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int r = r0 + i * dr;
+      if (r >= rows) break;
+      const uint32_t kc = code_byte(__fsub_rn(bf16_bits_to_f32(k[i].x & 0xffffu), mu.x), ks.x, ki.x) |
+                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].x >> 16), mu.y), ks.y, ki.y) << 8 |
+                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].y & 0xffffu), mu.z), ks.z, ki.z) << 16 |
+                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].y >> 16), mu.w), ks.w, ki.w) << 24;
+      const uint32_t vc = code_byte(bf16_bits_to_f32(v[i].x & 0xffffu), vs.x, vi.x) |
+                          code_byte(bf16_bits_to_f32(v[i].x >> 16), vs.y, vi.y) << 8 |
+                          code_byte(bf16_bits_to_f32(v[i].y & 0xffffu), vs.z, vi.z) << 16 |
+                          code_byte(bf16_bits_to_f32(v[i].y >> 16), vs.w, vi.w) << 24;
+      *reinterpret_cast<uint32_t*>(k_at(r, w >> 2) + 4 * (w & 3)) = kc;
+      *reinterpret_cast<uint32_t*>(v_at(r, w >> 2) + 4 * (w & 3)) = vc;
+    }
   }
 }
 
@@ -228,77 +260,83 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
 
 // Joins the shares of the heads that more than one CTA worked on: one CTA per
 // (row of the block, head and row block).  A head's steps are [x0, x1) of the
-// flattened list, so its CTAs are those whose shares meet that range; CTA c left
-// its share in slot 2 c when the head began before it, else in 2 c + 1.
+// flattened list, so its CTAs are the owners of those steps; CTA c left its share
+// in slot 2 c when the head began before it, else in 2 c + 1.  The attention
+// kernel releases this grid after its own dependency wait, so the lengths are
+// final and the division is known before the shares arrive.  A warp takes every
+// fourth share: the weights 2^(m_c - m) of 32 shares come first, one a lane, then
+// the shares' rows in independent loads.
 template <int D, int ROWS, int STEP>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
   constexpr int NW = kTreeJoinThreads / 32;
   constexpr int CPL = D / 32;  // channels per lane
-  __shared__ TreePlan plan;
   __shared__ float sm[NW], sl[NW];
   __shared__ __align__(16) float so[NW][D];
   const int r = blockIdx.y;
   const int rb = blockIdx.x % a.blocks, bkv = blockIdx.x / a.blocks;
   const int b = bkv / a.Hkv, hkv = bkv % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
-  if (rb * ROWS + r >= a.G * a.T) return;
+  if (rb * ROWS + r >= a.G * a.T) {
+    pdl_trigger();
+    return;
+  }
+  int tot, x0;
+  tree_totals(a, STEP, b, tot, x0);
+  const int n = tree_steps(a, tree_length(a, b), STEP);
+  x0 += (hkv * a.blocks + rb) * n;
+  const int c0 = n > 0 ? tree_owner(x0, tot, a.ctas) : 0;
+  const int c1 = n > 0 ? tree_owner(x0 + n - 1, tot, a.ctas) : 0;
+  const int first = c0 + warp;  // this warp's shares: first, first + NW, ...
   pdl_wait();
-  // total steps, and the steps of the sequences before b
-  const int per = a.Hkv * a.blocks;
-  long long tot = 0, before = 0;
-  for (int x = threadIdx.x; x < a.B; x += kTreeJoinThreads) {
-    const long long n = per * tree_steps(a, tree_length(a, x), STEP);
-    tot += n;
-    if (x < b) before += n;
-  }
-#pragma unroll
-  for (int sh = 16; sh > 0; sh >>= 1) {
-    tot += __shfl_xor_sync(0xffffffffu, tot, sh);
-    before += __shfl_xor_sync(0xffffffffu, before, sh);
-  }
-  if (lane == 0) {
-    plan.warp_sum[warp] = tot;
-    plan.warp_sum[NW + warp] = before;
-  }
-  __syncthreads();
-  tot = before = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    tot += plan.warp_sum[w];
-    before += plan.warp_sum[NW + w];
-  }
-  const long long n = tree_steps(a, tree_length(a, b), STEP);
+  pdl_trigger();
   if (n == 0) {  // no cached row and no draft: nothing is visible
     if (warp == 0 && lane < D / 4)
       tree_write_out<D>(a, b, hkv, rb * ROWS + r, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f);
     return;
   }
-  const long long x0 = before + (static_cast<long long>(hkv) * a.blocks + rb) * n, x1 = x0 + n;
-  const long long G = a.ctas;
-  // the CTA that holds step x: the largest c with floor(c W / G) <= x
-  const int c0 = static_cast<int>(((x0 + 1) * G - 1) / tot);
-  const int c1 = static_cast<int>((x1 * G - 1) / tot);
   if (c0 == c1) return;  // written whole
   float m = kNegInf, l = 0.f, o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += NW) {
-    const long long start = c * tot / G;
-    const size_t slot = 2 * static_cast<size_t>(c) + (x0 < start ? 0 : 1);
-    if (!QATTN_IN_BOUNDS(slot < a.slots)) break;
-    const float mc = a.part_m[slot * ROWS + r], lc = a.part_l[slot * ROWS + r];
-    const float* po = a.part_o + (slot * ROWS + r) * D + CPL * lane;
-    float oc[CPL];
+  for (int cb = first; cb <= c1; cb += 32 * NW) {
+    const int c = cb + lane * NW;
+    // only the head's first CTA began before the head
+    const size_t slot = 2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0);
+    const bool in = c <= c1 && QATTN_IN_BOUNDS(slot < a.slots);
+    const float mc = in ? a.part_m[slot * ROWS + r] : kNegInf, lc = in ? a.part_l[slot * ROWS + r] : 0.f;
+    float mx = mc;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) oc[k] = po[k];
-    if (mc == kNegInf) continue;
-    const float mn = fmaxf(m, mc);
-    const float f = (m == kNegInf) ? 0.f : ex2_approx(m - mn), w = ex2_approx(mc - mn);
-    l = fmaf(w, lc, l * f);
+    for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+    const float mn = fmaxf(m, mx);
+    if (mn == kNegInf) continue;  // (the whole warp)
+    const float f = m == kNegInf ? 0.f : ex2_approx(m - mn);
+    const float w = mc == kNegInf ? 0.f : ex2_approx(mc - mn);
+    float ls = w * lc;
 #pragma unroll
-    for (int k = 0; k < CPL; ++k) o[k] = fmaf(w, oc[k], o[k] * f);
+    for (int sh = 16; sh > 0; sh >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
+    l = l * f + ls;
     m = mn;
+#pragma unroll
+    for (int k = 0; k < CPL; ++k) o[k] *= f;
+    const int cnt = min(32, (c1 - cb) / NW + 1);
+#pragma unroll 8
+    for (int i = 0; i < cnt; ++i) {
+      const int ci = cb + i * NW;
+      const size_t si = 2 * static_cast<size_t>(ci) + (ci == c0 ? 1 : 0);
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* po = a.part_o + (si * ROWS + r) * D + CPL * lane;
+      if constexpr (CPL == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(po);
+        o[0] = fmaf(wi, y.x, o[0]);
+        o[1] = fmaf(wi, y.y, o[1]);
+        o[2] = fmaf(wi, y.z, o[2]);
+        o[3] = fmaf(wi, y.w, o[3]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(po);
+        o[0] = fmaf(wi, y.x, o[0]);
+        o[1] = fmaf(wi, y.y, o[1]);
+      }
+    }
   }
   if (lane == 0) {
     sm[warp] = m;

@@ -67,8 +67,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const TreeArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ TreePlan plan;
-  pdl_trigger();
   const uint32_t raw0 = smem_u32(raw_smem);
   const uint32_t base = (raw0 + 1023u) & ~1023u;
   uint8_t* smem = raw_smem + (base - raw0);
@@ -107,7 +105,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  tree_plan(a, kStep, &plan);
+  pdl_trigger();  // after the wait: the join reads the lengths before its own
+  TreeWalk walk = tree_walk(a, kStep);
+  TreeSeg sg;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -118,9 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool ok = true;
       uint32_t it = 0;
-      for (long long p = plan.begin; ok && p < plan.end;) {
-        const TreeSeg sg = tree_segment(a, plan, p, kStep);
-        p += sg.s1 - sg.s0;
+      while (ok && tree_next(a, kStep, walk, sg)) {
         const int bkv = sg.b * a.Hkv + sg.hkv;
         for (int s = sg.s0; s < sg.s1; ++s, ++it) {
           const int st = it & 1;
@@ -165,10 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(bar(kKEmpty + st));
         return true;
       };
-      for (long long p = plan.begin; ok && p < plan.end; ++seg) {
-        const TreeSeg sg = tree_segment(a, plan, p, kStep);
+      for (; ok && tree_next(a, kStep, walk, sg); ++seg) {
         const int n = sg.s1 - sg.s0;
-        p += n;
         if (!(ok = wait(kQReady, seg))) break;
         if (!(ok = qk(it))) break;
         for (int j = 0; j < n; ++j, ++it) {
@@ -211,9 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       other = xch[(b2 * 2 + 1 - hf) * kRows + r];
       return true;
     };
-    for (long long p = plan.begin; ok && p < plan.end;) {
-      const TreeSeg sg = tree_segment(a, plan, p, kStep);
-      p += sg.s1 - sg.s0;
+    while (ok && tree_next(a, kStep, walk, sg)) {
       const int rr = sg.rb * kRows + r;
       const bool in = rr < R;
       const int hq = in ? rr / a.T : 0, tok = in ? rr % a.T : 0;
@@ -397,9 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     uint32_t it = 0, nd = 0;
-    for (long long p = plan.begin; ok && p < plan.end;) {
-      const TreeSeg sg = tree_segment(a, plan, p, kStep);
-      p += sg.s1 - sg.s0;
+    while (ok && tree_next(a, kStep, walk, sg)) {
       for (int s = sg.s0; s < sg.s1; ++s, ++it) {
         const int st = it & 1;
         ok = wait(kRawFull + st, it >> 1);

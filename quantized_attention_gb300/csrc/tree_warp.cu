@@ -72,9 +72,15 @@ __device__ __forceinline__ void pair_f16x2(uint32_t x, uint32_t y, uint32_t (&o)
   for (int e = 0; e < 4; ++e) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(o[e]) : "r"(0x64806480u));
 }
 
+// Place of 16-byte chunk c of row r of a warp's O in shared memory.
+template <int D>
+__device__ __forceinline__ int join_chunk(int r, int c) {
+  return c ^ (((c >> ((D == 128) ? 3 : 2)) & 3) + 4 * (r & 1));
+}
+
 // ------------------------------------------------------------------ attention
-// CTA c takes steps [c W / G, (c + 1) W / G) of the flattened list of W steps
-// (sequence, KV head, 16-row block, step): exact balance whatever the lengths.
+// Each CTA takes an equal share of the flattened list of steps (sequence, KV head,
+// 16-row block, step): balance to one step whatever the lengths.
 // Each run of steps inside one head is a segment; its steps go round the four
 // warps, each with its own ring of TMA tiles and its own (m, l, O), so the main
 // loop has no CTA barrier.  A head's drafted steps come first and are encoded
@@ -90,13 +96,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[kWarps][kRing];
-  __shared__ TreePlan plan;
   __shared__ float red_m[kWarps][kTreeRows], red_l[kWarps][kTreeRows];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   uint8_t* ring = smem + warp * SM::kWarp;
-  pdl_trigger();
   if (lane == 0) {
     for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&full[warp][s]), 1);
     fence_mbar_init();
@@ -109,13 +113,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   pdl_wait();
-  tree_plan(a, kStep, &plan);  // ends with a CTA barrier
+  pdl_trigger();  // after the wait: the join reads the lengths before its own
+  TreeWalk walk = tree_walk(a, kStep);
+  __syncthreads();  // the abort flag is set
   const int R = a.G * a.T;
   uint32_t used = 0;  // tiles this warp has taken through its ring
 
-  for (long long p = plan.begin; p < plan.end;) {
-    const TreeSeg sg = tree_segment(a, plan, p, kStep);
-    p += sg.s1 - sg.s0;
+  for (TreeSeg sg; tree_next(a, kStep, walk, sg);) {
     const int bkv = sg.b * a.Hkv + sg.hkv;
     const int nd = a.drafts;  // drafted steps of a head
     // this warp's steps: sg.s0 + warp, + kWarps, ...; the first cached one
@@ -310,11 +314,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w][g + 8 * h]);
       const float f = (m[h] == kNegInf) ? 0.f : ex2_approx(m[h] - mx);
+      // n-tile n, column 2 t4 (+ 1) is channel NT * column + n; 16-byte chunks XORed
+      // so that the eight lanes of a store hit eight bank groups
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // n-tile n, column 2 t4 (+ 1) is channel NT * column + n
-        mine[(g + 8 * h) * D + NT * (2 * t4) + n] = o[n][2 * h] * f;
-        mine[(g + 8 * h) * D + NT * (2 * t4 + 1) + n] = o[n][2 * h + 1] * f;
+      for (int cl = 0; cl < 2; ++cl) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+          const int ch = (NT * (2 * t4 + cl) + n) / 4;
+          *reinterpret_cast<float4*>(mine + (g + 8 * h) * D + 4 * join_chunk<D>(g, ch)) =
+              make_float4(o[n][2 * h + cl] * f, o[n + 1][2 * h + cl] * f, o[n + 2][2 * h + cl] * f,
+                          o[n + 3][2 * h + cl] * f);
+        }
       }
     }
     __syncthreads();
@@ -330,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int w = 0; w < kWarps; ++w) {
         const float mw = red_m[w][r];
         lt += (mw == kNegInf) ? 0.f : red_l[w][r] * ex2_approx(mw - mx);
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * SM::kWarp + 4 * (r * D + c));
+        const float4 y =
+            *reinterpret_cast<const float4*>(smem + w * SM::kWarp + 4 * (r * D + 4 * join_chunk<D>(r, c / 4)));
         x.x += y.x;
         x.y += y.y;
         x.z += y.z;
