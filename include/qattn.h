@@ -482,7 +482,8 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales,
                                void* workspace, size_t workspace_bytes, qattn_stream_t stream);
 
 /* Bytes of workspace qattn_tree_decode accepts for this shape and parameters,
- * with or without drafts (0 for an empty or unsupported problem).  Host only. */
+ * with or without drafts (0: none is needed, or the problem is empty or
+ * unsupported).  Host only. */
 size_t qattn_tree_workspace_size(const qattn_shape* shape, const qattn_params* params);
 
 /* Append the accepted path of a drafted tree to an int8 KV cache: token

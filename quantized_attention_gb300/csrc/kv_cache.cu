@@ -8,20 +8,9 @@
 namespace qattn {
 namespace {
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // A 32-bit word of another CTA's shared memory (the same offset as `p` here).
 __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
-  uint32_t addr, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+  return ld_cluster_u32(cluster_addr(smem_u32(p), rank));
 }
 
 // ------------------------------------------------------------------ commit
@@ -85,16 +74,20 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
 }
 
 // ------------------------------------------------------------------ eviction
-// Selection: one cluster of 8 CTAs per (sequence, KV head); each holds the
-// ordered keys of a contiguous slice of rows in shared memory (re-read from
-// global memory where a slice does not fit).  Three histogram rounds (11, 11
-// and 10 bits, the cluster's counts summed through distributed shared memory)
-// give the budget-th largest key exactly; the rows above it and the first of
-// its ties are kept, in row order, at positions from a prefix sum over the
-// slices.  One read of the weights; bound by the rounds' barriers.
-constexpr int kSelThreads = 512;
-constexpr int kSelCluster = 8;
-constexpr int kBins = 2048;
+// One cluster per (sequence, KV head), of a size that fills the GPU.  Selection:
+// each CTA holds the ordered keys of a contiguous slice of rows in shared memory
+// (re-read from global memory where a slice does not fit); four rounds of 8-bit
+// histograms, summed over the cluster through distributed shared memory, give the
+// budget-th largest key exactly; the rows above it and the first of its ties are
+// kept, in row order, at positions from a prefix sum over the slices.  Then the
+// cluster copies the kept rows, each CTA an equal share of the output, 16 bytes a
+// thread, the V codes' channel maxima on the way.  The weights are read once, the
+// kept rows read and written once; a short cache is bound by the rounds' barriers
+// (~1 us each), a long one by the copy.
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 256;
 constexpr int kSelRows = 40960;  // rows of a slice kept in shared memory (160 KB)
 
 // Order-preserving key of a weight: larger weight, larger key; NaN counts as
@@ -115,24 +108,33 @@ __device__ __forceinline__ int rows_in_use(const EvictArgs& a, int b) {
   return n;
 }
 
-__global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThreads)
-    evict_select_kernel(const EvictArgs a) {
+__device__ __forceinline__ uint32_t abs4_max(uint32_t m, uint32_t x) { return __vmaxu4(m, __vabs4(x)); }
+
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a) {
+  constexpr int LPR = D / 16;                  // threads per row of the copy
+  constexpr int RPI = kEvictThreads / LPR;     // rows the CTA copies at once
+  constexpr int U = 4;                         // of them in flight
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[kBins];      // this CTA's counts of a round
-  __shared__ uint32_t total[kBins];     // the cluster's
-  __shared__ uint32_t wsum[2][kSelThreads / 32];
-  __shared__ uint32_t pick[2];          // the round's bin, rows still wanted in it
-  __shared__ uint32_t mine[2];          // this slice's rows above / at the threshold
-  const int bkv = blockIdx.y, b = bkv / a.Hkv;
-  const uint32_t rank = cluster_rank();
+  __shared__ uint32_t hist[2][kBins];          // this CTA's counts of a round, alternating
+  __shared__ uint32_t wsum[2][kEvictWarps];
+  __shared__ uint32_t pick[2][2];              // a round's bin, rows still wanted in it
+  __shared__ uint32_t mine[2];                 // this slice's rows above / at the threshold
+  __shared__ uint4 red[kEvictWarps][LPR];
+  const int NC = a.cluster;
+  const uint32_t rank = NC > 1 ? cluster_rank() : 0u;
+  const int bkv = blockIdx.x / NC, b = bkv / a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto sync = [&] {
+    if (NC > 1) cluster_sync();
+    else __syncthreads();
+  };
   pdl_trigger();
   pdl_wait();
   const int len = rows_in_use(a, b);
   const int want = min(len, a.budget);
-  const int slice = (len + kSelCluster - 1) / kSelCluster;
-  const int r0 = min(len, static_cast<int>(rank) * slice), r1 = min(len, r0 + slice);
-  const int nr = r1 - r0;
+  const int slice = (len + NC - 1) / NC;
+  const int r0 = min(len, static_cast<int>(rank) * slice), nr = min(len, r0 + slice) - r0;
   const float* w = a.weights + static_cast<size_t>(bkv) * a.cap;
   const bool fits = slice <= kSelRows;
   auto fresh = [&](int r) {
@@ -140,51 +142,48 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
   };
   auto key = [&](int i) { return fits ? keys[i] : fresh(r0 + i); };
   if (fits)
-    for (int i = threadIdx.x; i < nr; i += kSelThreads) keys[i] = fresh(r0 + i);
-  if (rank == 0) {  // the header's maxima start from 0; the gather raises them
-    for (int c = threadIdx.x; c < a.d; c += kSelThreads)
-      a.v_code_amax[static_cast<size_t>(bkv) * a.d + c] = 0.f;
+    for (int i = threadIdx.x; i < nr; i += kEvictThreads) keys[i] = fresh(r0 + i);
+  if (rank == 0) {  // the header's maxima start from 0; the copies raise them
+    if (threadIdx.x < D) a.v_code_amax[static_cast<size_t>(bkv) * D + threadIdx.x] = 0.f;
     if (threadIdx.x == 0 && bkv % a.Hkv == 0) a.lengths_out[b] = want;
   }
   if (want == 0) return;  // the whole cluster: no row in use
+  if (threadIdx.x < kBins) hist[0][threadIdx.x] = 0u;
+  __syncthreads();
 
   uint32_t prefix = 0, left = want;  // the threshold's leading bits; rows wanted among its ties
-  int shift = 32;
+  const bool all = want == len;      // nothing to choose: every row is above the threshold
 #pragma unroll 1
-  for (int round = 0; round < 3; ++round) {
-    const int bits = round == 2 ? 10 : 11;
-    const uint32_t high = shift == 32 ? 0u : (0xffffffffu << shift);
-    shift -= bits;
-    for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < nr; i += kSelThreads) {
-      const uint32_t k = key(i);
-      if ((k & high) == prefix) {
-        const uint32_t bin = (k >> shift) & ((1u << bits) - 1u);
-        // one addition for the lanes that agree with the first one (runs of
-        // equal weights would otherwise queue up on one bin)
-        const uint32_t act = __activemask();
-        const uint32_t same = __ballot_sync(act, bin == __shfl_sync(act, bin, __ffs(act) - 1));
-        if ((same >> lane) & 1u) {
-          if (lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
-        } else {
-          atomicAdd(&hist[bin], 1u);
-        }
+  for (int round = 0; round < 4 && !all; ++round) {
+    const int shift = 24 - 8 * round;
+    const uint32_t high = round == 0 ? 0u : (0xffffffffu << (shift + 8));
+    uint32_t* h = hist[round & 1];
+    for (int i0 = 0; i0 < nr; i0 += kEvictThreads) {
+      const int i = i0 + threadIdx.x;
+      const uint32_t k = i < nr ? key(i) : 0u;
+      const bool live = i < nr && (k & high) == prefix;
+      const uint32_t act = __ballot_sync(0xffffffffu, live);
+      if (live) {  // one addition per distinct bin of the warp
+        const uint32_t bin = (k >> shift) & 255u;
+        const uint32_t same = __match_any_sync(act, bin);
+        if (lane == __ffs(same) - 1) atomicAdd(&h[bin], __popc(same));
+      }
+      __syncwarp();
+    }
+    sync();  // the cluster's counts are in
+    // thread i < 256: bin 255 - i, counted from the top
+    uint32_t c = 0;
+    if (threadIdx.x < kBins) {
+      hist[(round + 1) & 1][threadIdx.x] = 0u;  // last read a round ago, behind a barrier
+      const uint32_t addr = smem_u32(&h[kBins - 1 - threadIdx.x]);
+      if (NC == 1) {
+        c = h[kBins - 1 - threadIdx.x];
+      } else {
+#pragma unroll 8
+        for (int q = 0; q < NC; ++q) c += ld_cluster_u32(cluster_addr(addr, q));
       }
     }
-    cluster_sync();
-    for (int i = threadIdx.x; i < (1 << bits); i += kSelThreads) {
-      uint32_t c = 0;
-#pragma unroll
-      for (int q = 0; q < kSelCluster; ++q) c += ld_cluster(&hist[i], q);
-      total[i] = c;
-    }
-    __syncthreads();
-    // the bin that holds the left-th largest: thread i owns bins from the top
-    const int per = (1 << bits) / kSelThreads;
-    uint32_t sum = 0;
-    for (int e = 0; e < per; ++e) sum += total[(1 << bits) - 1 - (threadIdx.x * per + e)];
-    uint32_t inc = sum;
+    uint32_t inc = c;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
       const uint32_t o = __shfl_up_sync(0xffffffffu, inc, sh);
@@ -192,28 +191,24 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     }
     if (lane == 31) wsum[0][warp] = inc;
     __syncthreads();
-    uint32_t before = inc - sum;
-    for (int q = 0; q < warp; ++q) before += wsum[0][q];
-    if (before < left && before + sum >= left) {
-      for (int e = 0; e < per; ++e) {
-        const int bin = (1 << bits) - 1 - (threadIdx.x * per + e);
-        if (before + total[bin] >= left) {
-          pick[0] = bin;
-          pick[1] = left - before;
-          break;
-        }
-        before += total[bin];
+    if (threadIdx.x < kBins) {
+      uint32_t before = inc - c;
+      for (int q = 0; q < warp; ++q) before += wsum[0][q];
+      if (before < left && before + c >= left) {
+        pick[round & 1][0] = kBins - 1 - threadIdx.x;
+        pick[round & 1][1] = left - before;
       }
     }
     __syncthreads();
-    prefix |= pick[0] << shift;
-    left = pick[1];
-    cluster_sync();  // every CTA has read this round's counts
+    prefix |= pick[round & 1][0] << shift;
+    left = pick[round & 1][1];
   }
-  const uint32_t thr = prefix;  // keep keys above it, and the first `left` ties
+  // keep keys above the threshold, and the first `left` of its ties
+  const uint32_t thr = all ? 0u : prefix;  // (no key is 0: the lowest is that of -inf)
+  if (all) left = 0;
 
   // each thread owns a run of consecutive rows (an odd length: no bank conflicts)
-  const int run = ((nr + kSelThreads - 1) / kSelThreads) | 1;
+  const int run = ((nr + kEvictThreads - 1) / kEvictThreads) | 1;
   const int i0 = min(nr, static_cast<int>(threadIdx.x) * run), i1 = min(nr, i0 + run);
   uint32_t gt = 0, eq = 0;
   for (int i = i0; i < i1; ++i) {
@@ -230,28 +225,34 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
       ie += oe;
     }
   }
+  __syncthreads();  // wsum's last readers are done
   if (lane == 31) {
     wsum[0][warp] = ig;
     wsum[1][warp] = ie;
   }
   __syncthreads();
-  uint32_t pg = ig - gt, pe = ie - eq, tg = 0, te = 0;
-  for (int q = 0; q < kSelThreads / 32; ++q) {
-    if (q < warp) {
-      pg += wsum[0][q];
-      pe += wsum[1][q];
+  // the warps' sums: one a lane, exclusive prefixes by shuffles
+  uint32_t vg = wsum[0][lane], ve = wsum[1][lane], sg = vg, se = ve;
+#pragma unroll
+  for (int sh = 1; sh < 32; sh <<= 1) {
+    const uint32_t og = __shfl_up_sync(0xffffffffu, sg, sh), oe = __shfl_up_sync(0xffffffffu, se, sh);
+    if (lane >= sh) {
+      sg += og;
+      se += oe;
     }
-    tg += wsum[0][q];
-    te += wsum[1][q];
   }
-  if (threadIdx.x == 0) {
-    mine[0] = tg;
-    mine[1] = te;
+  uint32_t pg = __shfl_sync(0xffffffffu, sg - vg, warp) + ig - gt;
+  uint32_t pe = __shfl_sync(0xffffffffu, se - ve, warp) + ie - eq;
+  if (threadIdx.x == kEvictThreads - 1) {
+    mine[0] = sg;
+    mine[1] = se;
   }
-  cluster_sync();
-  for (uint32_t q = 0; q < rank; ++q) {
-    pg += ld_cluster(&mine[0], q);
-    pe += ld_cluster(&mine[1], q);
+  if (NC > 1) {
+    cluster_sync();
+    for (uint32_t q = 0; q < rank; ++q) {
+      pg += ld_cluster(&mine[0], q);
+      pe += ld_cluster(&mine[1], q);
+    }
   }
   int32_t* kept = a.kept + static_cast<size_t>(bkv) * a.budget;
   float* wo = a.weights_out + static_cast<size_t>(bkv) * a.out_cap;
@@ -267,78 +268,58 @@ __global__ void __cluster_dims__(kSelCluster, 1, 1) __launch_bounds__(kSelThread
     pg += k > thr;
     pe += k == thr;
   }
-  cluster_sync();  // no CTA leaves while another reads its counts
-}
+  sync();  // the list is complete, and no CTA reads another's counts any more
 
-// Gather: a warp takes kRowsPerWarp kept rows, 16 bytes a lane, all loads of a
-// batch before its stores; the V codes' channel maxima stay in registers and
-// meet in one integer maximum per channel and CTA.
-constexpr int kGatherWarps = 8;
-constexpr int kRowsPerWarp = 16;
-
-__device__ __forceinline__ uint32_t abs4_max(uint32_t m, uint32_t x) { return __vmaxu4(m, __vabs4(x)); }
-
-template <int D>
-__global__ void __launch_bounds__(32 * kGatherWarps) evict_gather_kernel(const EvictArgs a) {
-  constexpr int LPR = D / 16;        // lanes per row
-  constexpr int RPI = 32 / LPR;      // rows per warp load
-  constexpr int NI = kRowsPerWarp / RPI;
-  __shared__ uint4 red[kGatherWarps][32];
-  const int bkv = blockIdx.y, b = bkv / a.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane / LPR, c = lane % LPR;
-  pdl_trigger();
-  pdl_wait();
-  const int n = a.lengths_out[b];
-  const int p0 = (blockIdx.x * kGatherWarps + warp) * kRowsPerWarp;
-  if (blockIdx.x * kGatherWarps * kRowsPerWarp >= n) return;
-  const int32_t* kept = a.kept + static_cast<size_t>(bkv) * a.budget;
-  const uint4* ks = reinterpret_cast<const uint4*>(a.k_codes + static_cast<size_t>(bkv) * a.cap * D);
-  const uint4* vs = reinterpret_cast<const uint4*>(a.v_codes + static_cast<size_t>(bkv) * a.cap * D);
-  uint4* ko = reinterpret_cast<uint4*>(a.k_out + static_cast<size_t>(bkv) * a.out_cap * D);
-  uint4* vo = reinterpret_cast<uint4*>(a.v_out + static_cast<size_t>(bkv) * a.out_cap * D);
-  uint4 kx[NI], vx[NI];
-  int row[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int p = p0 + RPI * i + sub;
-    row[i] = p < n ? kept[p] : -1;
-  }
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (row[i] >= 0 && QATTN_IN_BOUNDS(row[i] < a.cap)) {
-      kx[i] = ks[static_cast<size_t>(row[i]) * LPR + c];
-      vx[i] = vs[static_cast<size_t>(row[i]) * LPR + c];
-    }
-  }
+  // ---- copy this CTA's share of the kept rows
+  const int p0 = static_cast<int>(static_cast<long long>(want) * rank / NC);
+  const int p1 = static_cast<int>(static_cast<long long>(want) * (rank + 1) / NC);
+  const int c = threadIdx.x % LPR;
+  const uint4* ks = reinterpret_cast<const uint4*>(a.k_codes + static_cast<size_t>(bkv) * a.cap * D) + c;
+  const uint4* vs = reinterpret_cast<const uint4*>(a.v_codes + static_cast<size_t>(bkv) * a.cap * D) + c;
+  uint4* ko = reinterpret_cast<uint4*>(a.k_out + static_cast<size_t>(bkv) * a.out_cap * D) + c;
+  uint4* vo = reinterpret_cast<uint4*>(a.v_out + static_cast<size_t>(bkv) * a.out_cap * D) + c;
   uint4 m = make_uint4(0u, 0u, 0u, 0u);
+  for (int p = p0 + threadIdx.x / LPR; p < p1; p += U * RPI) {
+    int row[U];
+    uint4 kx[U], vx[U];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int p = p0 + RPI * i + sub;
-    if (p < n && QATTN_IN_BOUNDS(p < a.out_cap)) {
-      ko[static_cast<size_t>(p) * LPR + c] = kx[i];
-      vo[static_cast<size_t>(p) * LPR + c] = vx[i];
-    }
-    m.x = abs4_max(m.x, vx[i].x);
-    m.y = abs4_max(m.y, vx[i].y);
-    m.z = abs4_max(m.z, vx[i].z);
-    m.w = abs4_max(m.w, vx[i].w);
-  }
-  red[warp][lane] = m;
-  __syncthreads();
-  // thread c < D: channel c's byte over the warps and row lanes
-  if (threadIdx.x < D) {
-    const int l0 = threadIdx.x / 16, word = (threadIdx.x / 4) % 4, byte = threadIdx.x % 4;
-    uint32_t x = 0;
+    for (int i = 0; i < U; ++i) row[i] = p + i * RPI < p1 ? kept[p + i * RPI] : -1;
 #pragma unroll
-    for (int w = 0; w < kGatherWarps; ++w) {
-#pragma unroll
-      for (int q = 0; q < RPI; ++q) {
-        const uint32_t v = reinterpret_cast<const uint32_t*>(&red[w][q * LPR + l0])[word];
-        x = max(x, (v >> (8 * byte)) & 0xffu);
+    for (int i = 0; i < U; ++i) {
+      kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row[i] >= 0 && QATTN_IN_BOUNDS(row[i] < a.cap)) {
+        kx[i] = ks[static_cast<size_t>(row[i]) * LPR];
+        vx[i] = vs[static_cast<size_t>(row[i]) * LPR];
       }
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (row[i] >= 0 && QATTN_IN_BOUNDS(p + i * RPI < a.out_cap)) {
+        ko[static_cast<size_t>(p + i * RPI) * LPR] = kx[i];
+        vo[static_cast<size_t>(p + i * RPI) * LPR] = vx[i];
+      }
+      m.x = abs4_max(m.x, vx[i].x);
+      m.y = abs4_max(m.y, vx[i].y);
+      m.z = abs4_max(m.z, vx[i].z);
+      m.w = abs4_max(m.w, vx[i].w);
+    }
+  }
+  // ---- the channel maxima: lanes of a column, warps, then the cluster's CTAs
+#pragma unroll
+  for (int sh = LPR; sh < 32; sh <<= 1) {
+    m.x = __vmaxu4(m.x, __shfl_xor_sync(0xffffffffu, m.x, sh));
+    m.y = __vmaxu4(m.y, __shfl_xor_sync(0xffffffffu, m.y, sh));
+    m.z = __vmaxu4(m.z, __shfl_xor_sync(0xffffffffu, m.z, sh));
+    m.w = __vmaxu4(m.w, __shfl_xor_sync(0xffffffffu, m.w, sh));
+  }
+  if (lane < LPR) red[warp][lane] = m;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    const int col = threadIdx.x / 16, word = (threadIdx.x / 4) % 4, byte = threadIdx.x % 4;
+    uint32_t x = 0;
+#pragma unroll
+    for (int q = 0; q < kEvictWarps; ++q)
+      x = max(x, (reinterpret_cast<const uint32_t*>(&red[q][col])[word] >> (8 * byte)) & 0xffu);
     // non-negative floats order like their bits
     atomicMax(reinterpret_cast<int*>(a.v_code_amax + static_cast<size_t>(bkv) * D + threadIdx.x),
               __float_as_int(static_cast<float>(x)));
@@ -346,12 +327,22 @@ __global__ void __launch_bounds__(32 * kGatherWarps) evict_gather_kernel(const E
 }
 
 template <int D>
-cudaError_t launch_gather(const EvictArgs& a, cudaStream_t s) {
-  const int per = kGatherWarps * kRowsPerWarp;
-  const int most = min(a.budget, a.Nk);
-  if (most == 0) return cudaSuccess;
-  return launch_pdl(evict_gather_kernel<D>, dim3((most + per - 1) / per, a.B * a.Hkv),
-                    dim3(32 * kGatherWarps), 0, s, a);
+cudaError_t launch_evict_d(EvictArgs a, cudaStream_t s) {
+  // CTAs per head: as many as fill the SMs, and enough that a slice fits.  (Clusters
+  // of 16 took 36.6 us where 8 take 18.4, 8 heads of 32K rows: the chip places fewer
+  // than eight of them at once.)
+  const long long heads = static_cast<long long>(a.B) * a.Hkv;
+  const int sms = num_sms();
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && (2 * a.cluster * heads <= sms || a.Nk > static_cast<long long>(a.cluster) * kSelRows))
+    a.cluster *= 2;
+  const int slice = (a.Nk + a.cluster - 1) / a.cluster;
+  const int smem = 4 * min(slice, kSelRows);
+  cudaError_t e = cudaFuncSetAttribute(evict_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelRows);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned int>(heads * a.cluster));
+  if (a.cluster == 1) return launch_pdl(evict_kernel<D>, grid, dim3(kEvictThreads), smem, s, a);
+  return launch_pdl_cluster(evict_kernel<D>, grid, dim3(kEvictThreads), a.cluster, smem, s, a);
 }
 
 }  // namespace
@@ -361,31 +352,11 @@ unsigned int check_take_kv_cache() { return check_take_local(); }
 cudaError_t launch_tree_commit(const CommitArgs& a, cudaStream_t s) {
   const int nch = a.Hkv * a.d;
   const int ctas = min(kCommitCluster, (nch + kCommitThreads - 1) / kCommitThreads);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, a.B);
-  cfg.blockDim = dim3(kCommitThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, tree_commit_kernel, a);
+  return launch_pdl_cluster(tree_commit_kernel, dim3(ctas, a.B), dim3(kCommitThreads), ctas, 0, s, a);
 }
 
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s) {
-  const int slice = (a.Nk + kSelCluster - 1) / kSelCluster;
-  const int smem = 4 * min(slice, kSelRows);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       4 * kSelRows);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(evict_select_kernel, dim3(kSelCluster, a.B * a.Hkv), dim3(kSelThreads), smem, s, a);
-  if (e != cudaSuccess) return e;
-  return a.d == 32 ? launch_gather<32>(a, s) : a.d == 64 ? launch_gather<64>(a, s) : launch_gather<128>(a, s);
+  return a.d == 32 ? launch_evict_d<32>(a, s) : a.d == 64 ? launch_evict_d<64>(a, s) : launch_evict_d<128>(a, s);
 }
 
 }  // namespace qattn

@@ -298,7 +298,8 @@ float sm_scale_of(const qattn_shape* s, const qattn_params* p) {
 // bound from Nk; the kernel divides the steps that the lengths give), and the
 // workspace of their shares.  The layout depends on the shape alone.
 struct TreeSplit {
-  bool tc;  // the tensor-core kernel
+  bool tc;         // the tensor-core kernel
+  bool clustered;  // a cluster per head and row block
   int step, blocks, rows, drafts, ctas;
   int64_t steps;  // of all heads, at most
   size_t slots, off_m, off_l, bytes;
@@ -313,9 +314,11 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
   t.steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
+  t.clustered = !t.tc && qattn::tree_clustered(s->B * s->Hkv * t.blocks, t.drafts + (s->Nk + t.step - 1) / t.step);
   // a step per warp of a CTA of four, or per CTA
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
-  t.slots = 2 * static_cast<size_t>(t.ctas);
+  if (t.clustered) t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * qattn::kTreeCluster);
+  t.slots = t.clustered ? 0 : 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);
   t.bytes = t.off_l + align256(t.slots * t.rows * 4);
@@ -968,7 +971,8 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   if (shape->Nk == 0 && !drafts) return no_key_rows(shape, params, O, lse, s);
   const TreeSplit sp = tree_split(shape, drafts);
   if (sp.steps >= (int64_t{1} << 31)) return QATTN_ERR_UNSUPPORTED;  // counted in 32 bits
-  if (!workspace || workspace_bytes < sp.bytes || !aligned16(workspace)) return QATTN_ERR_WORKSPACE;
+  if (sp.bytes > 0 && (!workspace || workspace_bytes < sp.bytes || !aligned16(workspace)))
+    return QATTN_ERR_WORKSPACE;
   qattn::TreeArgs a{};
   if (drafts) {
     qattn::Src ks, vs;
@@ -1009,6 +1013,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   a.out = O;
   a.out_bf16 = params->out_dtype == QATTN_BF16;
   a.lse = lse;
+  a.clustered = sp.clustered;
   a.ctas = sp.ctas;
   a.slots = sp.slots;
   a.rows_total = static_cast<size_t>(shape->B * shape->Hq * shape->Nq);
@@ -1025,8 +1030,11 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
       return QATTN_ERR_CUDA;
   }
   char sb[128];
-  QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s + tree_join_kernel, %d CTAs", shape_str(shape, sb, sizeof sb),
-                 drafts ? a.T : 0, sp.tc ? "tree_tc_kernel" : "tree_warp_kernel", sp.ctas);
+  QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb),
+                 drafts ? a.T : 0,
+                 sp.tc ? "tree_tc_kernel + tree_join_kernel"
+                       : sp.clustered ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel",
+                 sp.ctas);
   return from_cuda(sp.tc ? qattn::launch_tree_tc(tk, tv, a, s) : qattn::launch_tree_warp(tk, tv, a, s));
 }
 
@@ -1194,7 +1202,7 @@ qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const 
   a.kept = kept;
   a.lengths_out = lengths_out;
   a.v_code_amax = v_code_amax;
-  QATTN_LOG_LINE("qattn_kv_evict B=%d Hkv=%d Nk=%d d=%d budget=%d: evict_select_kernel + evict_gather_kernel",
+  QATTN_LOG_LINE("qattn_kv_evict B=%d Hkv=%d Nk=%d d=%d budget=%d: evict_kernel",
                  a.B, a.Hkv, a.Nk, a.d, a.budget);
   return from_cuda(qattn::launch_kv_evict(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -27,6 +27,27 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The same with clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster,
+                                      size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned int>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // Streaming multiprocessors of the current device (1 if the query fails).
 inline int num_sms() {
   int dev = 0, n = 0;
@@ -207,6 +228,17 @@ constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
 constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
 constexpr int kTreeTcCtas = 152;     // its CTAs, at most
 constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
+constexpr int kTreeCluster = 8;      // CTAs of a head in the warp-level kernel's clustered form
+// The clustered form is taken for few heads with short caches: one wave of
+// clusters (two CTAs an SM) and at most 264 steps a head, or two and 72.
+// Measured, clustered against shares + join, us: 8 heads of 2K / 8K / 16K rows
+// 8.1 / 13.5 / 20.8 against 12.5 / 15.5 / 20.1; 32 heads of 8K 19.6 against 25.6;
+// 16 heads of 16K 27.7 against 22.4; 48 heads of 2K (d = 64) 9.0 against 13.0, of
+// 4K 25.8 against 22.1; 80 heads of 1K 22.6 against 15.4.
+inline bool tree_clustered(long long heads, long long steps) {
+  const long long ctas = heads * kTreeCluster;
+  return ctas <= kTreeWarpCtas ? steps <= 264 : ctas <= 2 * kTreeWarpCtas && steps <= 72;
+}
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
   int blocks;                    // row blocks of a head
@@ -230,6 +262,7 @@ struct TreeArgs {
   float* lse;                    // [B][Hq][T] or null
   unsigned int* err;
   // the split and its workspace
+  int clustered;                 // one cluster per (head, row block): no join, no workspace
   int ctas;
   size_t slots, rows_total;      // 2 ctas; B Hq T
   float* part_o;                 // [slots][block rows][d]
@@ -303,6 +336,7 @@ struct EvictArgs {
   int32_t* lengths_out;
   float* v_code_amax;
   unsigned int* err;
+  int cluster;          // CTAs per (sequence, KV head); set by launch_kv_evict
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
 

@@ -6,8 +6,8 @@
 //   warp 0       TMA: the steps' K and V codes into a ring of raw stages
 //   warp 1       TMEM and the MMAs
 //   warps 4-11   softmax: two threads a row (keys 0-63 and 64-127 of a step)
-//   warps 12-15  codes -> fp16 tiles K16, V16 [key][channel] in shared memory;
-//                a drafted step's codes are made by them first
+//   warps 12-15  codes -> fp16 tiles K16, V16 [key][channel] in shared memory; a
+//                drafted step's codes are made by these and the softmax warps first
 //
 // Per step: S = Q K16^T (Q as the A operand in TMEM), P = 2^(S c - m) rounded to
 // fp16 into TMEM, O += P V16 (V16 as it lies: the B operand with its N index
@@ -30,6 +30,8 @@ constexpr int kStep = kTreeTcStep;
 constexpr int kRows = kTreeTcRows;
 static_assert(kStep == 128 && kRows == 128, "one TMEM lane per row, one block of keys per step");
 constexpr int kThreads = 512;
+constexpr int kRaw = 6;      // raw ring: K and V tiles of codes, one after the other
+constexpr int kEncode = 384; // threads that encode a drafted step: softmax and converting warps
 constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;  // TMEM columns
 
@@ -37,28 +39,28 @@ template <int D>
 struct Cfg {
   static constexpr int kRawTile = kStep * D;          // K (or V) codes of a step
   static constexpr int kHalf = kStep * D * 2;         // K16 (or V16): D / 64 blocks of [128][128 B]
-  static constexpr int kOff16 = 2 * 2 * kRawTile;     // after two raw stages
+  static constexpr int kOff16 = kRaw * kRawTile;      // after the raw ring
   static constexpr int kOffX = kOff16 + 2 * 2 * kHalf;
   static constexpr int kOffBar = kOffX + 2 * 2 * kRows * 4;  // row maxima: [buffer][half][row]
-  static constexpr int kBytes = kOffBar + 512 + 1024;
+  static constexpr int kBytes = kOffBar + 512;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
 enum {
-  kRawFull = 0,    // [2] TMA bytes (a drafted step: the loader's arrival)
-  kRawEmpty = 2,   // [2] 128 converting threads
-  kKFull = 4,      // [2] 128
-  kKEmpty = 6,     // [2] the step's QK MMAs
-  kVFull = 8,      // [2] 128
-  kVEmpty = 10,    // [2] the step's PV MMAs
-  kQReady = 12,    // 128 threads wrote Q
-  kSFull = 13,     // [2] QK MMAs
-  kPReady = 15,    // 256
-  kPvDone = 16,    // PV MMAs
-  kXFull = 17,     // [2 buffers][4 quadrants] 64
-  kDrafts = 25,    // 128 converting threads wrote a drafted step's codes
-  kDrain = 26,
-  kNumBars = 27
+  kRawFull = 0,    // [kRaw] TMA bytes (a drafted step: the loader's arrival)
+  kRawEmpty = 6,   // [kRaw] 128 converting threads
+  kKFull = 12,     // [2] 128
+  kKEmpty = 14,    // [2] the step's QK MMAs
+  kVFull = 16,     // [2] 128
+  kVEmpty = 18,    // [2] the step's PV MMAs
+  kQReady = 20,    // 128 threads wrote Q
+  kSFull = 21,     // [2] QK MMAs
+  kPReady = 23,    // 256
+  kPvDone = 24,    // PV MMAs
+  kXFull = 25,     // [2 buffers][4 quadrants] 64
+  kDrafts = 33,    // kEncode threads wrote a drafted step's codes
+  kDrain = 34,
+  kNumBars = 35
 };
 
 template <int D>
@@ -66,10 +68,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const TreeArgs a) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t raw_smem[];
-  const uint32_t raw0 = smem_u32(raw_smem);
-  const uint32_t base = (raw0 + 1023u) & ~1023u;
-  uint8_t* smem = raw_smem + (base - raw0);
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  uint8_t* smem = dyn_smem;
+  const uint32_t base = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
@@ -77,8 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
     return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
   };
-  auto raw_k = [&](int st) { return base + st * 2 * C::kRawTile; };
-  auto raw_v = [&](int st) { return base + st * 2 * C::kRawTile + C::kRawTile; };
+  auto raw = [&](uint32_t slot) { return base + slot * C::kRawTile; };
   auto k16 = [&](int st) { return base + C::kOff16 + st * 2 * C::kHalf; };
   auto v16 = [&](int st) { return base + C::kOff16 + st * 2 * C::kHalf + C::kHalf; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -86,9 +86,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= kRawEmpty && i < kRawEmpty + 2) || (i >= kKFull && i < kKFull + 2) ||
-          (i >= kVFull && i < kVFull + 2) || i == kQReady || i == kDrafts)
+      if ((i >= kRawEmpty && i < kRawEmpty + kRaw) || (i >= kKFull && i < kKFull + 2) ||
+          (i >= kVFull && i < kVFull + 2) || i == kQReady)
         n = 128;
+      if (i == kDrafts) n = kEncode;
       if (i == kPReady) n = 256;
       if (i >= kXFull && i < kXFull + 8) n = 64;
       mbar_init(bar(i), n);
@@ -107,7 +108,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();  // after the wait: the join reads the lengths before its own
   TreeWalk walk = tree_walk(a, kStep);
-  TreeSeg sg;
+  TreeSeg sg{};
+
+  // A drafted step's codes, into its raw tiles n and n + 1: the softmax warps (idle
+  // until the segment's first scores) and the converting ones together, thread e of
+  // kEncode.  Returns when every one has written.
+  auto encode = [&](uint32_t n, int s, int e, uint32_t nd) -> bool {
+    bool ok = wait(kRawFull + n % kRaw, n / kRaw) && wait(kRawFull + (n + 1) % kRaw, (n + 1) / kRaw);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    uint8_t* kr = smem + (n % kRaw) * C::kRawTile;
+    uint8_t* vr = smem + ((n + 1) % kRaw) * C::kRawTile;
+    auto at = [](uint8_t* t, int r, int c) {
+      return t + r * D + 16 * (c ^ ((D == 128) ? (r & 7) : ((r >> 1) & 3)));
+    };
+    tree_encode_drafts<D>(a, sg.b, sg.hkv, s * kStep, kStep, e, kEncode,
+                          [&](int r, int c) { return at(kr, r, c); }, [&](int r, int c) { return at(vr, r, c); });
+    fence_proxy_async_smem();  // the tiles go back to the TMA engine
+    mbar_arrive(bar(kDrafts));
+    ok = wait(kDrafts, nd);
+    return __all_sync(0xffffffffu, ok);
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -117,27 +137,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
       }
       bool ok = true;
-      uint32_t it = 0;
+      uint32_t n = 0;  // tiles: K and V of each step
       while (ok && tree_next(a, kStep, walk, sg)) {
         const int bkv = sg.b * a.Hkv + sg.hkv;
-        for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-          const int st = it & 1;
-          if (it >= 2 && !(ok = wait(kRawEmpty + st, (it >> 1) - 1))) break;
-          if (s < a.drafts) {
-            mbar_arrive(bar(kRawFull + st));
-          } else {
-            const int key = (s - a.drafts) * kStep;
-            mbar_arrive_expect_tx(bar(kRawFull + st), 2 * C::kRawTile);
-            tma_load_3d(raw_k(st), &tmK, bar(kRawFull + st), 0, key, bkv);
-            tma_load_3d(raw_v(st), &tmV, bar(kRawFull + st), 0, key, bkv);
+        for (int s = sg.s0; ok && s < sg.s1; ++s) {
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t slot = n % kRaw;
+            if (n >= kRaw && !(ok = wait(kRawEmpty + slot, n / kRaw - 1))) break;
+            if (s < a.drafts) {
+              mbar_arrive(bar(kRawFull + slot));
+            } else {
+              mbar_arrive_expect_tx(bar(kRawFull + slot), C::kRawTile);
+              tma_load_3d(raw(slot), kv ? &tmV : &tmK, bar(kRawFull + slot), 0, (s - a.drafts) * kStep, bkv);
+            }
           }
         }
       }
       // every load this thread issued lands before the CTA may exit
       volatile int never = 0;
-      for (uint32_t back = 1; back <= 2; ++back)
-        if (it >= back)
-          mbar_wait(bar(kRawFull + ((it - back) & 1)), ((it - back) >> 1) & 1, &never, a.err, kErrTimeout);
+      for (uint32_t back = 1; back <= kRaw; ++back)
+        if (n >= back)
+          mbar_wait(bar(kRawFull + (n - back) % kRaw), ((n - back) / kRaw) & 1, &never, a.err, kErrTimeout);
       if (!ok) *abort_flag = 1;
     }
     __syncwarp();
@@ -194,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const int R = a.G * a.T;
     float* xch = reinterpret_cast<float*>(smem + C::kOffX);
-    uint32_t it = 0, nx = 0;
+    uint32_t it = 0, nx = 0, nd = 0;
     bool ok = true;
     // this half's value to the other half's thread of the row, and back
     auto exchange = [&](float v, float& other) -> bool {
@@ -208,6 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     while (ok && tree_next(a, kStep, walk, sg)) {
+      for (int s = sg.s0; ok && s < min(sg.s1, a.drafts); ++s) {
+        ok = encode(2 * (it + s - sg.s0), s, threadIdx.x - 128, nd);
+        ++nd;
+      }
+      if (!ok) break;
       const int rr = sg.rb * kRows + r;
       const bool in = rr < R;
       const int hq = in ? rr / a.T : 0, tok = in ? rr % a.T : 0;
@@ -368,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // access take four chunks of rows r and r ^ 5, which differ in the swizzle's
     // low and high bit: eight bank groups for the loads and for the stores.
     constexpr int NB = D / 64, RS = 32 / NB, CH = kStep / RS;
-    const int tid = threadIdx.x - 384;
+    const int tid = threadIdx.x & 127;
     const int cc = tid & 3, cb = NB == 2 ? (tid >> 3) & 1 : 0;
     const int u = tid >> (3 + NB - 1);  // row pair: 4 of an 8-row group
     const int rw = 8 * (u >> 2) + ((u & 3) ^ (((tid >> 2) & 1) * 5));
@@ -377,14 +402,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t dst0 = cb * (kStep * 128) + rw * 128;
     const uint32_t c0 = ((2 * cc) ^ (rw & 7)) << 4, c1 = ((2 * cc + 1) ^ (rw & 7)) << 4;
     auto convert = [&](uint32_t src, uint32_t dst) {
+      uint4 v[CH];  // every load before the first store: one latency, not CH
+#pragma unroll
+      for (int i = 0; i < CH; ++i) v[i] = lds128(src + src0 + RS * D * i);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const uint4 v = lds128(src + src0 + RS * D * i);
         uint32_t h[8];
-        codes4_to_f16x2(v.x, h[0], h[1]);
-        codes4_to_f16x2(v.y, h[2], h[3]);
-        codes4_to_f16x2(v.z, h[4], h[5]);
-        codes4_to_f16x2(v.w, h[6], h[7]);
+        codes4_to_f16x2(v[i].x, h[0], h[1]);
+        codes4_to_f16x2(v[i].y, h[2], h[3]);
+        codes4_to_f16x2(v[i].z, h[4], h[5]);
+        codes4_to_f16x2(v[i].w, h[6], h[7]);
         sts128(dst + dst0 + RS * 128 * i + c0, h[0], h[1], h[2], h[3]);
         sts128(dst + dst0 + RS * 128 * i + c1, h[4], h[5], h[6], h[7]);
       }
@@ -393,50 +420,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, nd = 0;
     while (ok && tree_next(a, kStep, walk, sg)) {
       for (int s = sg.s0; s < sg.s1; ++s, ++it) {
-        const int st = it & 1;
-        ok = wait(kRawFull + st, it >> 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        const uint32_t st = it & 1;
         if (s < a.drafts) {
-          uint8_t* kr = smem + (raw_k(st) - base);
-          uint8_t* vr = smem + (raw_v(st) - base);
-          auto at = [](uint8_t* t, int rr, int c) {
-            return t + rr * D + 16 * (c ^ ((D == 128) ? (rr & 7) : ((rr >> 1) & 3)));
-          };
-          tree_encode_drafts<D>(a, sg.b, sg.hkv, s * kStep, kStep, tid, 128,
-                                [&](int rr, int c) { return at(kr, rr, c); },
-                                [&](int rr, int c) { return at(vr, rr, c); });
-          mbar_arrive(bar(kDrafts));
-          ok = wait(kDrafts, nd);
+          ok = encode(2 * it, s, threadIdx.x - 128, nd);
           ++nd;
+          if (!ok) break;
+        }
+#pragma unroll 1
+        for (uint32_t kv = 0; kv < 2; ++kv) {
+          const uint32_t n = 2 * it + kv, slot = n % kRaw;
+          ok = wait(kRawFull + slot, n / kRaw) && (it < 2 || wait((kv ? kVEmpty : kKEmpty) + st, (it >> 1) - 1));
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
+          convert(raw(slot), kv ? v16(st) : k16(st));
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kRawEmpty + slot));
+          mbar_arrive(bar((kv ? kVFull : kKFull) + st));
         }
-        if (it >= 2) {
-          ok = wait(kKEmpty + st, (it >> 1) - 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-        }
-        convert(raw_k(st), k16(st));
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kKFull + st));
-        if (it >= 2) {
-          ok = wait(kVEmpty + st, (it >> 1) - 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-        }
-        convert(raw_v(st), v16(st));
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kVFull + st));
-        mbar_arrive(bar(kRawEmpty + st));
+        if (!ok) break;
       }
     }
     if (!ok) *abort_flag = 1;

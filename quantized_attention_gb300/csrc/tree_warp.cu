@@ -36,7 +36,9 @@ struct WarpSmem {
   static constexpr int kTile = kStep * D;       // bytes of a step's K (or V) codes
   static constexpr int kStage = 2 * kTile;
   static constexpr int kWarp = kRing * kStage;  // one warp's ring
-  static constexpr int kBytes = kWarps * kWarp + 1024;
+  static constexpr int kDraft = kWarps * kWarp;  // the drafted step's codes
+  static constexpr int kBytes = kDraft + kStage + 1024;
+  static_assert(kTreeRows * D * 4 <= kStage, "a CTA's O does not fit the drafted step's room");
   static_assert(kTreeRows * D * 4 <= kWarp, "a warp's O does not fit its ring");
 };
 
@@ -85,7 +87,7 @@ __device__ __forceinline__ int join_chunk(int r, int c) {
 // warps, each with its own ring of TMA tiles and its own (m, l, O), so the main
 // loop has no CTA barrier.  A head's drafted steps come first and are encoded
 // by the warp that takes them while its first tiles are in flight.
-template <int D>
+template <int D, bool CL>
 __global__ void __launch_bounds__(kThreads, 2)
     tree_warp_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const TreeArgs a) {
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full[kWarps][kRing];
   __shared__ float red_m[kWarps][kTreeRows], red_l[kWarps][kTreeRows];
+  __shared__ float cl_m[kTreeRows], cl_l[kTreeRows];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -114,12 +117,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   pdl_wait();
   pdl_trigger();  // after the wait: the join reads the lengths before its own
-  TreeWalk walk = tree_walk(a, kStep);
+  TreeWalk walk;
+  if constexpr (!CL) walk = tree_walk(a, kStep);
   __syncthreads();  // the abort flag is set
   const int R = a.G * a.T;
   uint32_t used = 0;  // tiles this warp has taken through its ring
 
-  for (TreeSeg sg; tree_next(a, kStep, walk, sg);) {
+  TreeSeg sg;
+  if constexpr (CL) {  // this CTA's eighth of its head
+    const int rank = static_cast<int>(cluster_rank());
+    int head = blockIdx.x / kTreeCluster;
+    sg.rb = head % a.blocks;
+    head /= a.blocks;
+    sg.hkv = head % a.Hkv;
+    sg.b = head / a.Hkv;
+    sg.len = tree_length(a, sg.b);
+    sg.steps = tree_steps(a, sg.len, kStep);
+    const int q = sg.steps / kTreeCluster, r = sg.steps - q * kTreeCluster;
+    sg.s0 = rank * q + min(rank, r);
+    sg.s1 = sg.s0 + q + (rank < r ? 1 : 0);
+  }
+  while (CL || tree_next(a, kStep, walk, sg)) {
     const int bkv = sg.b * a.Hkv + sg.hkv;
     const int nd = a.drafts;  // drafted steps of a head
     // this warp's steps: sg.s0 + warp, + kWarps, ...; the first cached one
@@ -136,6 +154,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     if (lane == 0)
       for (int i = 0; i < min(kRing - 1, ntile); ++i) issue(i);
+    // at most 16 drafts, one step: the CTA encodes its codes while the first tiles
+    // are in flight
+    const bool draft = sg.s0 < nd && sg.s0 < sg.s1;
+    if (draft) {
+      uint8_t* st = smem + SM::kDraft;
+      tree_encode_drafts<D>(a, sg.b, sg.hkv, 0, kStep, threadIdx.x, kThreads,
+                            [&](int r, int c) { return st + swz<D>(r, c); },
+                            [&](int r, int c) { return st + SM::kTile + swz<D>(r, c); });
+    }
 
     // ---- this lane's rows g and g + 8 of the block: codes, factor, key limit
     uint32_t qa[KS][4];
@@ -265,32 +292,29 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
 
-    // ---- drafted steps of this warp, encoded in the stage not yet filled
-    for (int s = sg.s0 + warp; s < min(sg.s1, nd); s += kWarps) {
-      uint8_t* st = ring + ((used + kRing - 1) % kRing) * SM::kStage;
-      const int j0 = s * kStep;
-      tree_encode_drafts<D>(a, sg.b, sg.hkv, j0, kStep, lane, 32,
-                            [&](int r, int c) { return st + swz<D>(r, c); },
-                            [&](int r, int c) { return st + SM::kTile + swz<D>(r, c); });
-      __syncwarp();
-      const uint32_t vis[2] = {tree_draft_word(a, sg.b, tok[0], s), tree_draft_word(a, sg.b, tok[1], s)};
-      step(st, true, vis);
-      __syncwarp();
-    }
-    if (sg.s0 < nd) fence_proxy_async_smem();  // the stage goes back to the TMA engine
-    __syncwarp();
-
-    // ---- cached steps
-    for (int i = 0; i < ntile; ++i) {
-      if (lane == 0 && i + kRing - 1 < ntile) issue(i + kRing - 1);
-      const uint32_t q = used + i, slot = q % kRing;
-      const bool ok = mbar_wait(smem_u32(&full[warp][slot]), (q / kRing) & 1, &abort_flag, a.err, kErrTimeout);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int key = (first + i * kWarps - nd) * kStep;
-      const int room0 = lim[0] - key, room1 = lim[1] - key;  // visible keys of the step
-      const bool masked = __any_sync(0xffffffffu, room0 < kStep || room1 < kStep);
-      const uint32_t vis[2] = {first_bits(room0), first_bits(room1)};
-      step(ring + slot * SM::kStage, masked, vis);
+    // ---- this warp's steps, the drafted one (warp 0's first) among them
+    if (draft) __syncthreads();
+    const bool mine_draft = draft && warp == 0;
+    for (int i = mine_draft ? -1 : 0; i < ntile; ++i) {
+      const uint8_t* st = smem + SM::kDraft;
+      uint32_t vis[2];
+      bool masked = true;
+      if (i < 0) {
+        vis[0] = tree_draft_word(a, sg.b, tok[0], 0);
+        vis[1] = tree_draft_word(a, sg.b, tok[1], 0);
+      } else {
+        if (lane == 0 && i + kRing - 1 < ntile) issue(i + kRing - 1);
+        const uint32_t q = used + i, slot = q % kRing;
+        const bool ok = mbar_wait(smem_u32(&full[warp][slot]), (q / kRing) & 1, &abort_flag, a.err, kErrTimeout);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        st = ring + slot * SM::kStage;
+        const int key = (first + i * kWarps - nd) * kStep;
+        const int room0 = lim[0] - key, room1 = lim[1] - key;  // visible keys of the step
+        masked = __any_sync(0xffffffffu, room0 < kStep || room1 < kStep);
+        vis[0] = first_bits(room0);
+        vis[1] = first_bits(room1);
+      }
+      step(st, masked, vis);
       __syncwarp();  // the stage is read
     }
     used += ntile;
@@ -330,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
     const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
+    float* share = reinterpret_cast<float*>(smem + SM::kDraft);  // CL: this CTA's O, for the cluster
     for (int idx = threadIdx.x; idx < kTreeRows * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), c = 4 * (idx % (D / 4));
       float mx = kNegInf, lt = 0.f;
@@ -347,7 +372,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         x.z += y.z;
         x.w += y.w;
       }
-      if (whole) {
+      if constexpr (CL) {
+        *reinterpret_cast<float4*>(share + r * D + c) = x;
+        if (c == 0) {
+          cl_m[r] = mx;
+          cl_l[r] = lt;
+        }
+      } else if (whole) {
         tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
       } else if (QATTN_IN_BOUNDS(slot < a.slots)) {
         *reinterpret_cast<float4*>(a.part_o + (slot * kTreeRows + r) * D + c) = x;
@@ -357,20 +388,57 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
+    if constexpr (CL) break;
     fence_proxy_async_smem();  // the rings go back to the TMA engine
     __syncthreads();
+  }
+  if constexpr (CL) {
+    // ---- join the cluster: CTA `rank` writes rows rank and rank + 8.  Every CTA
+    // reaches both barriers, one that gave up on a wait too
+    cluster_sync();
+    const uint32_t rank = cluster_rank();
+    for (int idx = threadIdx.x; idx < 2 * (D / 4); idx += kThreads) {
+      const int r = static_cast<int>(rank) + kTreeCluster * (idx / (D / 4)), c = 4 * (idx % (D / 4));
+      if (sg.rb * kTreeRows + r >= R) continue;
+      float mc[kTreeCluster], lc[kTreeCluster], mx = kNegInf, lt = 0.f;
+      float4 y[kTreeCluster], x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (uint32_t q = 0; q < kTreeCluster; ++q) {
+        mc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_m[r]), q)));
+        lc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_l[r]), q)));
+        y[q] = ld_cluster_f4(cluster_addr(smem_u32(smem + SM::kDraft) + 4 * (r * D + c), q));
+      }
+#pragma unroll
+      for (int q = 0; q < kTreeCluster; ++q) mx = fmaxf(mx, mc[q]);
+#pragma unroll
+      for (int q = 0; q < kTreeCluster; ++q) {
+        const float f = mc[q] == kNegInf ? 0.f : ex2_approx(mc[q] - mx);
+        lt = fmaf(f, lc[q], lt);
+        x.x = fmaf(f, y[q].x, x.x);
+        x.y = fmaf(f, y[q].y, x.y);
+        x.z = fmaf(f, y[q].z, x.z);
+        x.w = fmaf(f, y[q].w, x.w);
+      }
+      tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
+    }
+    cluster_sync();  // no CTA leaves while another reads its share
   }
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = WarpSmem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(tree_warp_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e;
+  if (a.clustered) {
+    e = cudaFuncSetAttribute(tree_warp_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(tree_warp_kernel<D, true>, dim3(a.ctas), dim3(kThreads), kTreeCluster, smem, s, tk, tv,
+                              a);
+  }
+  e = cudaFuncSetAttribute(tree_warp_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_warp_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
-  // one CTA holds every head whole; without drafts a head may have no step at
-  // all, and the join writes its rows
-  if (e != cudaSuccess || (a.ctas == 1 && a.drafts > 0)) return e;
+  e = launch_pdl(tree_warp_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
+  if (e != cudaSuccess) return e;
   return launch_pdl(tree_join_kernel<D, kTreeRows, kStep>, dim3(a.B * a.Hkv * a.blocks, kTreeRows),
                     dim3(kTreeJoinThreads), 0, s, a);
 }
