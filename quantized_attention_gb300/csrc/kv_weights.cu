@@ -21,7 +21,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeysPerWarp = 32;
 constexpr int kKeys = kWarps * kKeysPerWarp;  // keys of a CTA
-constexpr int kRowsChunk = 64;                // query rows in shared memory at a time
+constexpr int kRows = kWeightWarpRows;        // query rows, at most (a multiple of 8)
+static_assert(kRows % 8 == 0, "rows come in fragments of 8");
 
 __device__ __forceinline__ int row_count(const WeightArgs& a, int b) {
   if (!a.lengths) return a.Nk;
@@ -47,40 +48,94 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // ------------------------------------------------------------------ few queries
-// One CTA per 256 keys of a (sequence, KV head); a warp holds 32 keys as fp16 A
-// fragments in registers (their codes are read once, straight from global
-// memory: 4 lanes cover a key's row) and every query row of the group passes by
-// in chunks of 64 rows of codes in shared memory.  Lane (g, t) takes channels
-// D/4 t .. of its keys and rows, so a k-step's fragment is one word of each.
+// One CTA per 256 keys of a (sequence, KV head) and at most kWeightWarpRows query
+// rows (query head of the group, token): a decode step.  A warp holds 32 keys as
+// fp16 A fragments in registers (their codes are read once, straight from global
+// memory); the rows wait in shared memory as fp16 B fragments with their
+// constants.  Lane (g, t) takes 16-byte chunks t and t + 4 of its keys and rows
+// (four lanes read 64 consecutive bytes), so a k-step's fragment is one word of
+// each.  Bound by the latency of a warp's chain (load, widen, eight dependent MMAs,
+// exponentials) at 16 warps an SM.  A CTA walking over several key blocks with the
+// next block's loads in flight measured no faster (17.8 against 16.1 us for a step
+// over 32K rows of 8 heads): fewer warps fit.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightArgs a) {
   constexpr int KS = D / 16;
-  __shared__ __align__(16) uint8_t sq[kRowsChunk * D];
-  __shared__ float2 rowc[kRowsChunk];  // {factor sq sm log2 e, lse log2 e}
-  __shared__ int rowi[kRowsChunk];     // token of the row
+  constexpr int NC = D / 16;  // 16-byte chunks of a row's codes, 32 bytes as fp16
+  __shared__ __align__(16) uint8_t sq[kRows * NC * 32];
+  __shared__ float2 rowc[kRows];  // {factor sq sm log2 e, lse log2 e}
+  __shared__ int rowi[kRows];     // token of the row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   pdl_trigger();
   pdl_wait();
   const int bkv = blockIdx.y, b = bkv / a.Hkv, hkv = bkv % a.Hkv;
-  const int len = row_count(a, b);
   const int k0 = blockIdx.x * kKeys;
-  if (k0 >= len) return;
   const int kw = k0 + warp * kKeysPerWarp;
-  const int pos0 = a.pos0_len ? len - a.Nq : a.pos0;
+  const int R = a.G * a.Nq;
+  const int len = row_count(a, b);
+  if (k0 >= len) return;
 
-  // the warp's 32 keys: key 16 mt + g + 8 h, words of this lane's channels
-  uint32_t ka[2][KS][4];
+  // the warp's 32 keys: key 16 mt + g + 8 h, this lane's chunks
+  uint4 kx[2][2][KS / 4];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int key = kw + 16 * mt + 8 * h + g;
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.k_codes) +
-                           (static_cast<size_t>(bkv) * a.cap + key) * D + (D / 4) * t4;
+                           (static_cast<size_t>(bkv) * a.cap + key) * D + 16 * t4;
 #pragma unroll
       for (int w4 = 0; w4 < KS / 4; ++w4) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (key < len && QATTN_IN_BOUNDS(key < a.cap)) x = *reinterpret_cast<const uint4*>(src + 16 * w4);
+        kx[mt][h][w4] = make_uint4(0u, 0u, 0u, 0u);
+        if (key < len && QATTN_IN_BOUNDS(key < a.cap))
+          kx[mt][h][w4] = *reinterpret_cast<const uint4*>(src + 64 * w4);
+      }
+    }
+  }
+  const int nkb = (a.Nk + 127) / 128, nqb = (a.Nq + 127) / 128;
+  const float sk = a.k_scales ? scale_of(a.k_scales, a.k_gran, bkv, nkb, min(kw, a.Nk - 1) / 128) : 1.f;
+  const int pos0 = a.pos0_len ? len - a.Nq : a.pos0;
+  const size_t row0 = (static_cast<size_t>(b) * a.Hq + hkv * a.G) * a.Nq;
+  // rows, widened once: chunk c of row r at 32 (r NC + c), its two 16-byte halves
+  // exchanged in odd rows (eight lanes of a read, four chunks of two rows, hit
+  // eight bank groups)
+  const int rows8 = (R + 7) & ~7;
+  for (int x = threadIdx.x; x < rows8 * NC; x += kThreads) {
+    const int r = x / NC, c = x % NC;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < R) v = *reinterpret_cast<const uint4*>(a.q_codes + (row0 + r) * D + 16 * c);
+    uint32_t h[8];
+    codes4_to_f16x2(v.x, h[0], h[1]);
+    codes4_to_f16x2(v.y, h[2], h[3]);
+    codes4_to_f16x2(v.z, h[4], h[5]);
+    codes4_to_f16x2(v.w, h[6], h[7]);
+    uint8_t* dst = sq + 32 * (r * NC + c);
+    *reinterpret_cast<uint4*>(dst + 16 * (r & 1)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(dst + 16 * (1 - (r & 1))) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+  if (threadIdx.x < rows8) {
+    const int r = threadIdx.x;
+    float2 f = make_float2(0.f, -kNegInf);  // a row past the end: 2^(0 - inf) = 0
+    int i = 0;
+    if (r < R) {
+      const int hq = r / a.Nq;
+      i = r - hq * a.Nq;
+      const float s = scale_of(a.q_scales, a.q_gran, b * a.Hq + hkv * a.G + hq, nqb, i / 128);
+      const float e = a.lse[row0 + r];
+      // a query that saw nothing (lse = -inf) gives nothing
+      f = make_float2(__fmul_rn(__fmul_rn(s, a.sm_scale), kLog2e), e == kNegInf ? -kNegInf : e * kLog2e);
+    }
+    rowc[r] = f;
+    rowi[r] = i;
+  }
+  uint32_t ka[2][KS][4];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int w4 = 0; w4 < KS / 4; ++w4) {
+        const uint4 x = kx[mt][h][w4];
         codes4_to_f16x2(x.x, ka[mt][4 * w4 + 0][h], ka[mt][4 * w4 + 0][2 + h]);
         codes4_to_f16x2(x.y, ka[mt][4 * w4 + 1][h], ka[mt][4 * w4 + 1][2 + h]);
         codes4_to_f16x2(x.z, ka[mt][4 * w4 + 2][h], ka[mt][4 * w4 + 2][2 + h]);
@@ -88,65 +143,55 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
       }
     }
   }
-  const int nkb = (a.Nk + 127) / 128, nqb = (a.Nq + 127) / 128;
-  const float sk = a.k_scales ? scale_of(a.k_scales, a.k_gran, bkv, nkb, min(kw, a.Nk - 1) / 128) : 1.f;
+  float old[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // the keys' base, in flight meanwhile
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = kw + 16 * mt + 8 * h + g;
+      if (a.base && t4 == 0 && key < len && QATTN_IN_BOUNDS(key < a.cap))
+        old[mt][h] = a.base[static_cast<size_t>(bkv) * a.cap + key];
+    }
+  }
+  __syncthreads();
   float acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-
-  // queries that can see any of this CTA's keys: causal, tokens >= k0 - pos0
-  const int i_first = a.causal ? max(0, k0 - pos0) : 0;
-  for (int hq = 0; hq < a.G; ++hq) {
-    const int bh = b * a.Hq + hkv * a.G + hq;
-    for (int i0 = i_first; i0 < a.Nq; i0 += kRowsChunk) {
-      const int n = min(kRowsChunk, a.Nq - i0);
-      __syncthreads();
-      const size_t row0 = static_cast<size_t>(bh) * a.Nq + i0;
-      for (int x = threadIdx.x; x < kRowsChunk * (D / 16); x += kThreads) {
-        const int r = x / (D / 16), c = x % (D / 16);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n) v = *reinterpret_cast<const uint4*>(a.q_codes + (row0 + r) * D + 16 * c);
-        *reinterpret_cast<uint4*>(sq + r * D + 16 * (c ^ (r & (D / 16 - 1)))) = v;
-      }
-      for (int r = threadIdx.x; r < kRowsChunk; r += kThreads) {
-        float2 f = make_float2(0.f, -kNegInf);  // a row past the end: 2^(0 - inf) = 0
-        if (r < n) {
-          const float s = scale_of(a.q_scales, a.q_gran, bh, nqb, (i0 + r) / 128);
-          const float e = a.lse[row0 + r];
-          // a query that saw nothing (lse = -inf) gives nothing
-          f = make_float2(__fmul_rn(__fmul_rn(s, a.sm_scale), kLog2e), e == kNegInf ? -kNegInf : e * kLog2e);
-        }
-        rowc[r] = f;
-        rowi[r] = i0 + r;
-      }
-      __syncthreads();
-      for (int r0 = 0; r0 < n; r0 += 8) {
-        // B fragments: row r0 + g, this lane's channels
-        uint32_t qb[KS][2];
+#pragma unroll 1
+  for (int r0 = 0; r0 < R; r0 += 8) {
+    uint32_t qb[KS][2];  // B fragments: row r0 + g, this lane's chunks
 #pragma unroll
-        for (int w4 = 0; w4 < KS / 4; ++w4) {
-          const int r = r0 + g, c = (KS / 4) * t4 + w4;
-          const uint4 x = *reinterpret_cast<const uint4*>(sq + r * D + 16 * (c ^ (r & (D / 16 - 1))));
-          codes4_to_f16x2(x.x, qb[4 * w4 + 0][0], qb[4 * w4 + 0][1]);
-          codes4_to_f16x2(x.y, qb[4 * w4 + 1][0], qb[4 * w4 + 1][1]);
-          codes4_to_f16x2(x.z, qb[4 * w4 + 2][0], qb[4 * w4 + 2][1]);
-          codes4_to_f16x2(x.w, qb[4 * w4 + 3][0], qb[4 * w4 + 3][1]);
-        }
-        const float2 f0 = rowc[r0 + 2 * t4], f1 = rowc[r0 + 2 * t4 + 1];
-        const float c0 = f0.x * sk, c1 = f1.x * sk;
-        const int lim0 = a.causal ? pos0 + rowi[r0 + 2 * t4] : 0x7fffffff;
-        const int lim1 = a.causal ? pos0 + rowi[r0 + 2 * t4 + 1] : 0x7fffffff;
+    for (int w4 = 0; w4 < KS / 4; ++w4) {
+      const uint8_t* src = sq + 32 * ((r0 + g) * NC + t4 + 4 * w4);
+      const uint4 lo = *reinterpret_cast<const uint4*>(src + 16 * (g & 1));
+      const uint4 hi = *reinterpret_cast<const uint4*>(src + 16 * (1 - (g & 1)));
+      qb[4 * w4 + 0][0] = lo.x;
+      qb[4 * w4 + 0][1] = lo.y;
+      qb[4 * w4 + 1][0] = lo.z;
+      qb[4 * w4 + 1][1] = lo.w;
+      qb[4 * w4 + 2][0] = hi.x;
+      qb[4 * w4 + 2][1] = hi.y;
+      qb[4 * w4 + 3][0] = hi.z;
+      qb[4 * w4 + 3][1] = hi.w;
+    }
+    const float2 f0 = rowc[r0 + 2 * t4], f1 = rowc[r0 + 2 * t4 + 1];
+    const float c0 = f0.x * sk, c1 = f1.x * sk;
+    const int lim0 = a.causal ? pos0 + rowi[r0 + 2 * t4] : 0x7fffffff;
+    const int lim1 = a.causal ? pos0 + rowi[r0 + 2 * t4 + 1] : 0x7fffffff;
+    float s[2][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int mt = 0; mt < 2; ++mt) s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) mma16816(s, ka[mt][ks], qb[ks][0], qb[ks][1]);
+    for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = kw + 16 * mt + 8 * h + g;
-            const float p0 = ex2_approx(fmaf(s[2 * h], c0, -f0.y));
-            const float p1 = ex2_approx(fmaf(s[2 * h + 1], c1, -f1.y));
-            acc[mt][h] += (key <= lim0 ? p0 : 0.f) + (key <= lim1 ? p1 : 0.f);
-          }
-        }
+      for (int mt = 0; mt < 2; ++mt) mma16816(s[mt], ka[mt][ks], qb[ks][0], qb[ks][1]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = kw + 16 * mt + 8 * h + g;
+        const float p0 = ex2_approx(fmaf(s[mt][2 * h], c0, -f0.y));
+        const float p1 = ex2_approx(fmaf(s[mt][2 * h + 1], c1, -f1.y));
+        acc[mt][h] += (key <= lim0 ? p0 : 0.f) + (key <= lim1 ? p1 : 0.f);
       }
     }
   }
@@ -158,10 +203,8 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
       const int key = kw + 16 * mt + 8 * h + g;
-      if (t4 == 0 && key < len && QATTN_IN_BOUNDS(key < a.cap)) {
-        const size_t o = static_cast<size_t>(bkv) * a.cap + key;
-        a.weights[o] = (a.base ? a.base[o] : 0.f) + x;
-      }
+      if (t4 == 0 && key < len && QATTN_IN_BOUNDS(key < a.cap))
+        a.weights[static_cast<size_t>(bkv) * a.cap + key] = old[mt][h] + x;
     }
   }
 }
