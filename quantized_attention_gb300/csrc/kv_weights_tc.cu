@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
-    return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
+    return mbar_wait_fast(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
   };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = a.G * a.Nq;

@@ -81,6 +81,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same for a thread whose next instructions a pipeline waits for: a completed
+// phase costs the one try_wait, the polling loop is a call out of line.  (Inlined,
+// the loop made a completed wait ~190 cycles of the MMA thread; so it is ~90.)
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                   unsigned int* err, unsigned int code) {
+  return mbar_wait(bar, parity, abort_flag, err, code);
+}
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               unsigned int* err, unsigned int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_slow(bar, parity, abort_flag, err, code);
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

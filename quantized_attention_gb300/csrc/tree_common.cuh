@@ -258,39 +258,36 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
   if (a.lse && c == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
 }
 
-// Joins the shares of the heads that more than one CTA worked on: one CTA per
-// (row of the block, head and row block).  A head's steps are [x0, x1) of the
-// flattened list, so its CTAs are the owners of those steps; CTA c left its share
-// in slot 2 c when the head began before it, else in 2 c + 1.  The attention
-// kernel releases this grid after its own dependency wait, so the lengths are
-// final and the division is known before the shares arrive.  A warp takes every
-// fourth share: the weights 2^(m_c - m) of 32 shares come first, one a lane, then
-// the shares' rows in independent loads.
-template <int D, int ROWS, int STEP>
+// Joins the shares of the heads that more than one CTA worked on.  A head's steps
+// are [x0, x0 + n) of the flattened list, so its CTAs are the owners of those
+// steps; CTA c left its share in slot 2 c when the head began before it, else in
+// 2 c + 1.  The attention kernel releases this grid after its own dependency wait,
+// so the lengths are final and the division is known before the shares arrive.
+// NW warps work on a row (one CTA, blockIdx.y the row), or one on each of four rows
+// (NW = 1: few shares a head, many rows); a warp takes every NW-th share: the
+// weights 2^(m_c - m) of 32 shares come first, one a lane, then the shares' rows in
+// independent loads.
+template <int D, int ROWS, int STEP, int NW>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
-  constexpr int NW = kTreeJoinThreads / 32;
   constexpr int CPL = D / 32;  // channels per lane
-  __shared__ float sm[NW], sl[NW];
-  __shared__ __align__(16) float so[NW][D];
-  const int r = blockIdx.y;
+  constexpr int RPC = kTreeJoinThreads / 32 / NW;  // rows of a CTA
+  __shared__ float sm[RPC][NW], sl[RPC][NW];
+  __shared__ __align__(16) float so[RPC][NW][D];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW, rw = (threadIdx.x >> 5) / NW;
+  const int r = blockIdx.y * RPC + rw;
   const int rb = blockIdx.x % a.blocks, bkv = blockIdx.x / a.blocks;
   const int b = bkv / a.Hkv, hkv = bkv % a.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (rb * ROWS + r >= a.G * a.T) {
-    pdl_trigger();
-    return;
-  }
+  const bool in = rb * ROWS + r < a.G * a.T;
   int tot, x0;
   tree_totals(a, STEP, b, tot, x0);
   const int n = tree_steps(a, tree_length(a, b), STEP);
   x0 += (hkv * a.blocks + rb) * n;
   const int c0 = n > 0 ? tree_owner(x0, tot, a.ctas) : 0;
   const int c1 = n > 0 ? tree_owner(x0 + n - 1, tot, a.ctas) : 0;
-  const int first = c0 + warp;  // this warp's shares: first, first + NW, ...
   pdl_wait();
   pdl_trigger();
   if (n == 0) {  // no cached row and no draft: nothing is visible
-    if (warp == 0 && lane < D / 4)
+    if (in && warp == 0 && lane < D / 4)
       tree_write_out<D>(a, b, hkv, rb * ROWS + r, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f);
     return;
   }
@@ -298,12 +295,12 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
   float m = kNegInf, l = 0.f, o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-  for (int cb = first; cb <= c1; cb += 32 * NW) {
+  for (int cb = c0 + warp; in && cb <= c1; cb += 32 * NW) {
     const int c = cb + lane * NW;
     // only the head's first CTA began before the head
     const size_t slot = 2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0);
-    const bool in = c <= c1 && QATTN_IN_BOUNDS(slot < a.slots);
-    const float mc = in ? a.part_m[slot * ROWS + r] : kNegInf, lc = in ? a.part_l[slot * ROWS + r] : 0.f;
+    const bool mine = c <= c1 && QATTN_IN_BOUNDS(slot < a.slots);
+    const float mc = mine ? a.part_m[slot * ROWS + r] : kNegInf, lc = mine ? a.part_l[slot * ROWS + r] : 0.f;
     float mx = mc;
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
@@ -339,24 +336,25 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
     }
   }
   if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    sm[rw][warp] = m;
+    sl[rw][warp] = l;
   }
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) so[warp][CPL * lane + k] = o[k];
-  __syncthreads();
-  if (threadIdx.x < D / 4) {
-    const int c = 4 * threadIdx.x;
+  for (int k = 0; k < CPL; ++k) so[rw][warp][CPL * lane + k] = o[k];
+  if constexpr (NW > 1) __syncthreads();
+  else __syncwarp();
+  const int c = 4 * (NW > 1 ? static_cast<int>(threadIdx.x) : lane);
+  if (in && c < D) {
     float mx = kNegInf, lt = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w]);
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[rw][w]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (sm[w] == kNegInf) continue;
-      const float f = ex2_approx(sm[w] - mx);
-      lt = fmaf(f, sl[w], lt);
-      const float4 y = *reinterpret_cast<const float4*>(&so[w][c]);
+      if (sm[rw][w] == kNegInf) continue;
+      const float f = ex2_approx(sm[rw][w] - mx);
+      lt = fmaf(f, sl[rw][w], lt);
+      const float4 y = *reinterpret_cast<const float4*>(&so[rw][w][c]);
       x.x = fmaf(f, y.x, x.x);
       x.y = fmaf(f, y.y, x.y);
       x.z = fmaf(f, y.z, x.z);

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
-    return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
+    return mbar_wait_fast(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
   };
   auto raw = [&](uint32_t slot) { return base + slot * C::kRawTile; };
   auto k16 = [&](int st) { return base + C::kOff16 + st * 2 * C::kHalf; };
@@ -401,10 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t src0 = rw * D + 16 * (chunk ^ ((D == 128) ? (rw & 7) : ((rw >> 1) & 3)));
     const uint32_t dst0 = cb * (kStep * 128) + rw * 128;
     const uint32_t c0 = ((2 * cc) ^ (rw & 7)) << 4, c1 = ((2 * cc + 1) ^ (rw & 7)) << 4;
-    auto convert = [&](uint32_t src, uint32_t dst) {
-      uint4 v[CH];  // every load before the first store: one latency, not CH
+    uint4 v[CH];  // a tile's codes: all loads before the first store
+    auto load = [&](uint32_t slot) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) v[i] = lds128(src + src0 + RS * D * i);
+      for (int i = 0; i < CH; ++i) v[i] = lds128(raw(slot) + src0 + RS * D * i);
+    };
+    auto convert = [&](uint32_t dst) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         uint32_t h[8];
@@ -418,28 +420,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     uint32_t it = 0, nd = 0;
+    uint32_t slot = 0, lap = 0;  // the raw tile to convert next: counted, not divided
     while (ok && tree_next(a, kStep, walk, sg)) {
-      for (int s = sg.s0; s < sg.s1; ++s, ++it) {
+      bool loaded = false;  // v holds the next tile already
+      for (int s = sg.s0; ok && s < sg.s1; ++s, ++it) {
         const uint32_t st = it & 1;
         if (s < a.drafts) {
           ok = encode(2 * it, s, threadIdx.x - 128, nd);
           ++nd;
           if (!ok) break;
         }
-#pragma unroll 1
+#pragma unroll
         for (uint32_t kv = 0; kv < 2; ++kv) {
-          const uint32_t n = 2 * it + kv, slot = n % kRaw;
-          ok = wait(kRawFull + slot, n / kRaw) && (it < 2 || wait((kv ? kVEmpty : kKEmpty) + st, (it >> 1) - 1));
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
+          if (!loaded) {
+            if (!(ok = wait(kRawFull + slot, lap))) break;
+            load(slot);
           }
-          convert(raw(slot), kv ? v16(st) : k16(st));
-          fence_proxy_async_smem();
+          if (it >= 2 && !(ok = wait((kv ? kVEmpty : kKEmpty) + st, (it >> 1) - 1))) break;
+          convert(kv ? v16(st) : k16(st));
           mbar_arrive(bar(kRawEmpty + slot));
+          if (++slot == kRaw) {
+            slot = 0;
+            ++lap;
+          }
+          // the next tile's loads go out ahead of the fence, if it is there
+          loaded = (kv == 0 || s + 1 < sg.s1) && mbar_test(bar(kRawFull + slot), lap & 1);
+          if (loaded) load(slot);
+          fence_proxy_async_smem();
           mbar_arrive(bar((kv ? kVFull : kKFull) + st));
         }
-        if (!ok) break;
       }
     }
     if (!ok) *abort_flag = 1;
@@ -459,7 +468,7 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_tc_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess || (a.ctas == 1 && a.drafts > 0)) return e;
-  return launch_pdl(tree_join_kernel<D, kRows, kStep>, dim3(a.B * a.Hkv * a.blocks, kRows),
+  return launch_pdl(tree_join_kernel<D, kRows, kStep, 1>, dim3(a.B * a.Hkv * a.blocks, kRows / 4),
                     dim3(kTreeJoinThreads), 0, s, a);
 }
 
