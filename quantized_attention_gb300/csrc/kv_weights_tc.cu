@@ -8,7 +8,8 @@
 // converted once per unit (K) or tile (Q) to exact fp16; S is an exact integer.
 //
 //   warp 0       TMA: the units' K codes into a ring of two raw stages
-//   warp 1       TMEM and the MMAs
+//   warps 1-2    the MMAs of the two M tiles, a thread each (one thread's waits and
+//                commits left the tensor pipe idle); warp 1 owns TMEM
 //   warps 4-7    K codes -> fp16 A operand in TMEM (lane = key)
 //   warps 8-11   Q codes -> fp16 B tiles in shared memory, their rows' factors
 //   warps 12-19  p = 2^(S c - lse2) summed along the columns; one thread a key
@@ -55,11 +56,11 @@ enum {
   kAFull = 4,     // [2 M tiles] 128 producer threads
   kAEmpty = 6,    // [2 M tiles] the unit's MMAs on it are done
   kQFull = 8,     // [kQS] 128 producer threads
-  kQEmpty = 12,   // [kQS] the tile's MMAs, and the 256 threads that read its constants
+  kQEmpty = 12,   // [kQS] the MMAs of both M tiles, and the 256 threads that read its constants
   kSFull = 16,    // [kNS] an MMA's commit
   kSEmpty = 19,   // [kNS] 128 threads
-  kDrain = 22,
-  kNumBars = 23
+  kDrain = 22,    // [2] an issuing thread's MMAs are done
+  kNumBars = 24
 };
 
 // What every role walks through in the same order: this CTA's units, and the
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((i >= kRawEmpty && i < kRawEmpty + 2) || (i >= kAFull && i < kAFull + 2) || (i >= kQFull && i < kQFull + kQS) ||
           (i >= kSEmpty && i < kSEmpty + kNS))
         n = 128;
-      if (i >= kQEmpty && i < kQEmpty + kQS) n = 257;
+      if (i >= kQEmpty && i < kQEmpty + kQS) n = 258;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -288,59 +289,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(bar(kRawFull + ((cnt - back) & 1)), ((cnt - back) >> 1) & 1, &never, a.err, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     if (lane == 0) {
+      const int m = warp - 1;
       constexpr uint32_t idesc = make_idesc(128, kTileQ, 0, 0);  // F16 x F16 -> F32
       const uint64_t desc0 = smem_desc(base + C::kOffQ, 1024, kSwizzle128B);
+      const uint32_t acol = tmem + m * (D / 2);
       bool ok = true, kept = false;
       uint32_t cnt = 0, qn = 0;  // units, Q tiles released
-      // the S ring: slot, and the completion of its kSEmpty to wait for.  Counted, not
-      // divided: this one thread's instructions are what an item waits for
-      int slot = 0, lap = -1;
+      // this tile's items are every other one of the S ring: slot, and the completion
+      // of its kSEmpty to wait for.  Counted, not divided
+      int slot = m, lap = -1;
       for (; ok && take(); ++cnt) {
         const bool stay = w.stay;
         uint32_t q = qn;
-        bool fresh = true;
-        if (!more(til, w, Tile{0, w.first})) {  // no query sees the unit: take A as it comes
-          if (!(ok = wait(kAFull, cnt) && wait(kAFull + 1, cnt))) break;
-          mma_commit(bar(kAEmpty));
-          mma_commit(bar(kAEmpty + 1));
-        }
-        for (Tile t{0, w.first}; ok && more(til, w, t);) {
+        if (!(ok = wait(kAFull + m, cnt))) break;
+        for (Tile t{0, w.first}; more(til, w, t); ++q) {
           const int st = q % kQS;
           if (!kept && !(ok = wait(kQFull + st, q / kQS))) break;
+          if (lap >= 0 && !(ok = wait(kSEmpty + slot, lap))) break;
           next(til, w, t);
-          const bool last = !more(til, w, t);
+          tc_fence_after();
+          // descriptors step by constants from the stage's first one
+          const uint64_t bd = desc0 + static_cast<uint32_t>(st * (C::kQTile >> 4));
+          const uint32_t dcol = tmem + kTmemS + 128 * slot;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (fresh && !(ok = wait(kAFull + m, cnt))) break;
-            if (lap >= 0 && !(ok = wait(kSEmpty + slot, lap))) break;
-            tc_fence_after();
-            // descriptors step by constants from the stage's first one
-            const uint64_t bd = desc0 + static_cast<uint32_t>(st * (C::kQTile >> 4));
-            const uint32_t dcol = tmem + kTmemS + 128 * slot, acol = tmem + m * (D / 2);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_f16_ts(dcol, acol + 8 * k, bd + ((k / 4) * (kTileQ * 128) + 32 * (k % 4)) / 16, idesc,
-                         k > 0 ? 1u : 0u);
-            mma_commit(bar(kSFull + slot));
-            if (last) mma_commit(bar(kAEmpty + m));
-            if (++slot == kNS) {
-              slot = 0;
-              ++lap;
-            }
+          for (int k = 0; k < D / 16; ++k)
+            mma_f16_ts(dcol, acol + 8 * k, bd + ((k / 4) * (kTileQ * 128) + 32 * (k % 4)) / 16, idesc,
+                       k > 0 ? 1u : 0u);
+          mma_commit(bar(kSFull + slot));
+          if (!stay) mma_commit(bar(kQEmpty + st));
+          slot += 2;
+          if (slot >= kNS) {
+            slot -= kNS;
+            ++lap;
           }
-          fresh = false;
-          if (ok && !stay) mma_commit(bar(kQEmpty + st));
-          ++q;
         }
         if (!ok) break;
+        mma_commit(bar(kAEmpty + m));
         if (!stay) qn = q;
         kept = stay;
       }
-      mma_commit(bar(kDrain));
+      mma_commit(bar(kDrain + m));
       volatile int never = 0;
-      mbar_wait(bar(kDrain), 0, &never, a.err, kErrTimeout);
+      mbar_wait(bar(kDrain + m), 0, &never, a.err, kErrTimeout);
       if (!ok) *abort_flag = 1;
     }
     __syncwarp();
