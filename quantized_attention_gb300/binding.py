@@ -346,7 +346,7 @@ def kv_header_init(v_codes, Nk, v_code_amax, stream=None):
 
 
 def _reject(name: str, t, dtype, shape, dev: int):
-    """Says what is wrong with an argument that failed _expect's test."""
+    """Says what is wrong with an argument that failed the tests of _ptrs."""
     if t is None:
         raise ValueError(f"{name} is missing")
     if tuple(t.shape) != tuple(shape):
@@ -355,41 +355,46 @@ def _reject(name: str, t, dtype, shape, dev: int):
     raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _expect(*args) -> int:
-    """Dense tensors of these types and shapes on the current CUDA device, whose
-    kernels and stream the call uses: (name, tensor, dtype, shape) each.  A
-    serving step makes these calls between short kernels, so a good argument costs
-    one line of tests.  Returns the device."""
-    dev = torch.cuda.current_device()
+def _ptrs(dev: int, *args) -> list:
+    """The addresses of dense tensors of these types and shapes on the current CUDA
+    device `dev`, whose kernels and stream the call uses: (name, tensor, dtype,
+    shape) each.  A serving step makes these calls between kernels of a few
+    microseconds, so a good argument costs one line of tests."""
+    out = []
     for name, t, dtype, shape in args:
         if (t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
                 or not t.is_contiguous()):
             _reject(name, t, dtype, shape, dev)
-    return dev
+        out.append(t.data_ptr())
+    return out
 
 
-def _expect_input(name: str, t, shape, dev: int):
-    """A bf16 input at any strides (see _input), its shape and device checked."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+def _opt_ptr(dev: int, name: str, t, dtype, shape):
+    return None if t is None else _ptrs(dev, (name, t, dtype, shape))[0]
+
+
+def _input_ptr(dev: int, name: str, t, shape):
+    """A bf16 input at any strides (see _input): its address and strides."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.shape != shape or t.get_device() != dev:
         _reject(name, t, torch.bfloat16, shape, dev)
-    return None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
+    return t.data_ptr(), None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
 
 
-def _expect_scales(name: str, t, count: int, dev: int):
+def _scales_ptr(dev: int, name: str, t, gran: int, B: int, H: int, N: int) -> int:
     if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
         _reject(name, t, torch.float32, t.shape, dev)
-    if t.numel() < count:
+    if t.numel() < (1 if gran == GRAN_TENSOR else B * H * (1 if gran == GRAN_HEAD else (N + 127) // 128)):
         raise ValueError(f"{name}: too few for the granularity")
+    return t.data_ptr()
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+_current_raw_stream = torch._C._cuda_getCurrentRawStream  # no Stream object on the way
 
 
-def _raw_stream(stream, dev: int) -> int:
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+def _stream_handle(stream, dev: int) -> int:
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def tree_workspace_size(shape: Shape, params: Params) -> int:
@@ -406,31 +411,26 @@ def tree_decode(q_codes, q_scales, k_codes, v_codes, k_chan_scale, v_chan_scale,
     params.causal, else every draft sees every draft)."""
     B, Hq, Hkv, T, d, Nk = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d, shape.Nk
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
-    head, cache = (B, Hkv, d), (B, Hkv, params.kv_capacity or Nk, d)
-    args = [("q_codes", q_codes, i8, (B, Hq, T, d)), ("v_chan_scale", v_chan_scale, f32, head),
-            ("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, (B, Hq, T, d))]
+    dev = torch.cuda.current_device()
+    head, cache, rows = (B, Hkv, d), (B, Hkv, params.kv_capacity or Nk, d), (B, Hq, T, d)
+    q, vs, o = _ptrs(dev, ("q_codes", q_codes, i8, rows), ("v_chan_scale", v_chan_scale, f32, head),
+                     ("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, rows))
+    kc = vc = ks = mu = None
     if Nk > 0 or k_codes is not None:
-        args += [("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache)]
-    if lse is not None:
-        args.append(("lse", lse, f32, (B, Hq, T)))
-    if lengths is not None:
-        args.append(("lengths", lengths, i32, (B,)))
-    if tree_mask is not None:
-        args.append(("tree_mask", tree_mask, i32, (B, T, (T + 31) // 32)))
-    drafts = K_new is not None or V_new is not None
-    if drafts:
+        kc, vc = _ptrs(dev, ("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache))
+    kn = kst = vn = vst = None
+    if K_new is not None or V_new is not None:
         if K_new is None or V_new is None:
             raise ValueError("K_new and V_new go together")
-        args += [("k_chan_scale", k_chan_scale, f32, head), ("k_mean", k_mean, f32, head)]
-    dev = _expect(*args)
-    _expect_scales("q_scales", q_scales, n_scales(params.q_gran, B, Hq, T), dev)
-    ks = _expect_input("K_new", K_new, (B, Hkv, T, d), dev) if drafts else None
-    vs = _expect_input("V_new", V_new, (B, Hkv, T, d), dev) if drafts else None
-    st = lib().qattn_tree_decode(_ptr(q_codes), _ptr(q_scales), _ptr(k_codes), _ptr(v_codes),
-                                 _ptr(k_chan_scale), _ptr(v_chan_scale), _ptr(k_mean), _ptr(lengths),
-                                 _ptr(K_new), ks, _ptr(V_new), vs, _ptr(tree_mask),
-                                 shape, params, _ptr(O), _ptr(lse), _ptr(workspace), _nbytes(workspace),
-                                 _raw_stream(stream, dev))
+        kn, kst = _input_ptr(dev, "K_new", K_new, (B, Hkv, T, d))
+        vn, vst = _input_ptr(dev, "V_new", V_new, (B, Hkv, T, d))
+        ks, mu = _ptrs(dev, ("k_chan_scale", k_chan_scale, f32, head), ("k_mean", k_mean, f32, head))
+    st = lib().qattn_tree_decode(
+        q, _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc, vc, ks, vs, mu,
+        _opt_ptr(dev, "lengths", lengths, i32, (B,)), kn, kst, vn, vst,
+        _opt_ptr(dev, "tree_mask", tree_mask, i32, (B, T, (T + 31) // 32)), shape, params, o,
+        _opt_ptr(dev, "lse", lse, f32, (B, Hq, T)), None if workspace is None else workspace.data_ptr(),
+        _nbytes(workspace), _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_tree_decode")
 
@@ -442,31 +442,25 @@ def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, length
     T, d]) to the cache (see qattn_tree_commit in include/qattn.h).  path: int32
     [B, T] draft indices, n_accept: int32 [B].  An output not given is written
     over the array it is computed from."""
-    B, Hkv, T, d = K_new.shape
+    shape = B, Hkv, T, d = K_new.shape
     cap, i8, f32, i32 = k_codes.shape[2], torch.int8, torch.float32, torch.int32
-    lengths_out = lengths if lengths_out is None else lengths_out
-    k_mean_out = k_mean if k_mean_out is None else k_mean_out
-    v_code_amax_out = v_code_amax if v_code_amax_out is None else v_code_amax_out
-    seen_out = seen if seen_out is None else seen_out
+    dev = torch.cuda.current_device()
     head, cache, seqs = (B, Hkv, d), (B, Hkv, cap, d), (B,)
-    args = [("path", path, i32, (B, T)), ("n_accept", n_accept, i32, seqs), ("lengths", lengths, i32, seqs),
-            ("lengths_out", lengths_out, i32, seqs), ("k_chan_scale", k_chan_scale, f32, head),
-            ("v_chan_scale", v_chan_scale, f32, head), ("k_mean", k_mean, f32, head),
-            ("v_code_amax", v_code_amax, f32, head), ("k_mean_out", k_mean_out, f32, head),
-            ("v_code_amax_out", v_code_amax_out, f32, head), ("k_codes", k_codes, i8, cache),
-            ("v_codes", v_codes, i8, cache)]
-    if seen is not None or seen_out is not None:
-        args += [("seen", seen, i32, seqs), ("seen_out", seen_out, i32, seqs)]
-    if weights is not None:
-        args.append(("weights", weights, f32, (B, Hkv, cap)))
-    dev = _expect(*args)
-    ks = _expect_input("K_new", K_new, (B, Hkv, T, d), dev)
-    vs = _expect_input("V_new", V_new, (B, Hkv, T, d), dev)
-    st = lib().qattn_tree_commit(_ptr(K_new), ks, _ptr(V_new), vs, _ptr(path), _ptr(n_accept), B, Hkv, T, d,
-                                 cap, _ptr(k_chan_scale), _ptr(v_chan_scale), _ptr(lengths), _ptr(seen),
-                                 _ptr(k_mean), _ptr(v_code_amax), _ptr(lengths_out), _ptr(seen_out),
-                                 _ptr(k_mean_out), _ptr(v_code_amax_out), _ptr(weights), _ptr(k_codes),
-                                 _ptr(v_codes), _raw_stream(stream, dev))
+    pp, pn, pl, pks, pvs, pm, pa, pkc, pvc = _ptrs(
+        dev, ("path", path, i32, (B, T)), ("n_accept", n_accept, i32, seqs), ("lengths", lengths, i32, seqs),
+        ("k_chan_scale", k_chan_scale, f32, head), ("v_chan_scale", v_chan_scale, f32, head),
+        ("k_mean", k_mean, f32, head), ("v_code_amax", v_code_amax, f32, head),
+        ("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache))
+    plo = pl if lengths_out is None else _opt_ptr(dev, "lengths_out", lengths_out, i32, seqs)
+    pmo = pm if k_mean_out is None else _opt_ptr(dev, "k_mean_out", k_mean_out, f32, head)
+    pao = pa if v_code_amax_out is None else _opt_ptr(dev, "v_code_amax_out", v_code_amax_out, f32, head)
+    ps = _opt_ptr(dev, "seen", seen, i32, seqs)
+    pso = ps if seen_out is None else _opt_ptr(dev, "seen_out", seen_out, i32, seqs)
+    kn, kst = _input_ptr(dev, "K_new", K_new, shape)
+    vn, vst = _input_ptr(dev, "V_new", V_new, shape)
+    st = lib().qattn_tree_commit(kn, kst, vn, vst, pp, pn, B, Hkv, T, d, cap, pks, pvs, pl, ps, pm, pa, plo,
+                                 pso, pmo, pao, _opt_ptr(dev, "weights", weights, f32, (B, Hkv, cap)), pkc,
+                                 pvc, _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_tree_commit")
 
@@ -478,19 +472,15 @@ def kv_weights(q_codes, q_scales, k_codes, k_scales, lse, shape, params, weights
     capacity]; lse: fp32 [B, Hq, Nq]."""
     B, Hq, Hkv, T, d, Nk = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d, shape.Nk
     cap, i8, f32 = params.kv_capacity or Nk, torch.int8, torch.float32
-    args = [("q_codes", q_codes, i8, (B, Hq, T, d)), ("k_codes", k_codes, i8, (B, Hkv, cap, d)),
-            ("lse", lse, f32, (B, Hq, T)), ("weights", weights, f32, (B, Hkv, cap))]
-    if base is not None:
-        args.append(("base", base, f32, (B, Hkv, cap)))
-    if lengths is not None:
-        args.append(("lengths", lengths, torch.int32, (B,)))
-    dev = _expect(*args)
-    _expect_scales("q_scales", q_scales, n_scales(params.q_gran, B, Hq, T), dev)
-    if k_scales is not None:
-        _expect_scales("k_scales", k_scales, n_scales(params.k_gran, B, Hkv, Nk), dev)
-    st = lib().qattn_kv_weights(_ptr(q_codes), _ptr(q_scales), _ptr(k_codes), _ptr(k_scales), _ptr(lse),
-                                _ptr(lengths), shape, params, _ptr(base), _ptr(weights),
-                                _raw_stream(stream, dev))
+    dev = torch.cuda.current_device()
+    q, kc, pl, w = _ptrs(dev, ("q_codes", q_codes, i8, (B, Hq, T, d)), ("k_codes", k_codes, i8, (B, Hkv, cap, d)),
+                         ("lse", lse, f32, (B, Hq, T)), ("weights", weights, f32, (B, Hkv, cap)))
+    st = lib().qattn_kv_weights(
+        q, _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc,
+        None if k_scales is None else _scales_ptr(dev, "k_scales", k_scales, params.k_gran, B, Hkv, Nk), pl,
+        _opt_ptr(dev, "lengths", lengths, torch.int32, (B,)), shape, params,
+        w if base is weights else _opt_ptr(dev, "base", base, f32, (B, Hkv, cap)), w,
+        _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_kv_weights")
 
@@ -499,21 +489,19 @@ def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept,
              v_code_amax, *, lengths=None, Nk=None, n_sink=0, n_recent=0, stream=None):
     """Keep the budget rows of most weight per KV head (see qattn_kv_evict in
     include/qattn.h).  Nk: most rows in use (default: the capacity)."""
-    B, Hkv, cap, d = k_codes.shape
+    cache = B, Hkv, cap, d = k_codes.shape
     Nk, budget, ocap = cap if Nk is None else int(Nk), int(budget), k_out.shape[2]
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
-    cache, out = (B, Hkv, cap, d), (B, Hkv, ocap, d)
-    args = [("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache),
-            ("weights", weights, f32, (B, Hkv, cap)), ("k_out", k_out, i8, out), ("v_out", v_out, i8, out),
-            ("weights_out", weights_out, f32, (B, Hkv, ocap)), ("kept", kept, i32, (B, Hkv, budget)),
-            ("lengths_out", lengths_out, i32, (B,)), ("v_code_amax", v_code_amax, f32, (B, Hkv, d))]
-    if lengths is not None:
-        args.append(("lengths", lengths, i32, (B,)))
-    dev = _expect(*args)
-    st = lib().qattn_kv_evict(_ptr(k_codes), _ptr(v_codes), _ptr(weights), _ptr(lengths), B, Hkv, Nk, d, cap,
-                              budget, int(n_sink), int(n_recent), _ptr(k_out), _ptr(v_out), ocap,
-                              _ptr(weights_out), _ptr(kept), _ptr(lengths_out), _ptr(v_code_amax),
-                              _raw_stream(stream, dev))
+    dev = torch.cuda.current_device()
+    out = (B, Hkv, ocap, d)
+    kc, vc, w, ko, vo, wo, kp, lo, am = _ptrs(
+        dev, ("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache),
+        ("weights", weights, f32, (B, Hkv, cap)), ("k_out", k_out, i8, out), ("v_out", v_out, i8, out),
+        ("weights_out", weights_out, f32, (B, Hkv, ocap)), ("kept", kept, i32, (B, Hkv, budget)),
+        ("lengths_out", lengths_out, i32, (B,)), ("v_code_amax", v_code_amax, f32, (B, Hkv, d)))
+    st = lib().qattn_kv_evict(kc, vc, w, _opt_ptr(dev, "lengths", lengths, i32, (B,)), B, Hkv, Nk, d, cap,
+                              budget, int(n_sink), int(n_recent), ko, vo, ocap, wo, kp, lo, am,
+                              _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_kv_evict")
 
