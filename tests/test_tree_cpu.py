@@ -42,7 +42,8 @@ def test_tree_decode_refusals(L):
     for n in ("q_codes", "k_codes", "v_codes", "O", "K_new", "V_new", "k_mean", "v_chan_scale", "lengths", "tree_mask",
               "lse", "q_scales"):
         assert tree(L, **{n: ODD}) == INVALID, n
-    assert tree(L, workspace=None) == WORKSPACE and tree(L, ws=16) == WORKSPACE
+    long = (2, 8, 2, 5, 100, 128)  # 20 rows: shares of a head in the workspace
+    assert tree(L, shape=long, workspace=None) == WORKSPACE and tree(L, shape=long, ws=16) == WORKSPACE
     assert tree(L, shape=(2, 8, 2, 129, 100, 128)) == UNSUPPORTED  # more drafts than a mask holds
     assert tree(L, shape=(2, 8, 2, 4, 100, 32)) == UNSUPPORTED
     assert tree(L, shape=(2, 7, 2, 4, 100, 128)) == INVALID
