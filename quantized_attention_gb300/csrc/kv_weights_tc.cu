@@ -35,6 +35,7 @@ constexpr int kUnit = 256;    // keys of a unit
 constexpr int kTileQ = 128;   // query rows of a tile
 constexpr int kQS = 4;        // Q stages
 constexpr int kNS = 3;        // S slots (128 TMEM columns each)
+static_assert(kNS == 3, "the slots' order is written out for three");
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemS = 128;  // first column of the S slots; A sits below
 
@@ -50,6 +51,10 @@ struct Cfg {
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
+// Item n of the S ring (slot n % kNS) is M tile n % 2 of Q tile n / 2.  The slots'
+// barriers are kept per M tile: the two tiles' threads drift apart, and on a shared
+// barrier a thread could look for a completion two phases away, which a parity
+// cannot tell from none.  M tile m uses a slot every third item of its own.
 enum {
   kRawFull = 0,   // [2] TMA bytes
   kRawEmpty = 2,  // [2] 128 producer threads
@@ -57,10 +62,10 @@ enum {
   kAEmpty = 6,    // [2 M tiles] the unit's MMAs on it are done
   kQFull = 8,     // [kQS] 128 producer threads
   kQEmpty = 12,   // [kQS] the MMAs of both M tiles, and the 256 threads that read its constants
-  kSFull = 16,    // [kNS] an MMA's commit
-  kSEmpty = 19,   // [kNS] 128 threads
-  kDrain = 22,    // [2] an issuing thread's MMAs are done
-  kNumBars = 24
+  kSFull = 16,    // [2 M tiles][kNS] an MMA's commit
+  kSEmpty = 22,   // [2 M tiles][kNS] 128 threads
+  kDrain = 28,    // [2] an issuing thread's MMAs are done
+  kNumBars = 30
 };
 
 // What every role walks through in the same order: this CTA's units, and the
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if ((i >= kRawEmpty && i < kRawEmpty + 2) || (i >= kAFull && i < kAFull + 2) || (i >= kQFull && i < kQFull + kQS) ||
-          (i >= kSEmpty && i < kSEmpty + kNS))
+          (i >= kSEmpty && i < kSEmpty + 2 * kNS))
         n = 128;
       if (i >= kQEmpty && i < kQEmpty + kQS) n = 258;
       mbar_init(bar(i), n);
@@ -297,9 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acol = tmem + m * (D / 2);
       bool ok = true, kept = false;
       uint32_t cnt = 0, qn = 0;  // units, Q tiles released
-      // this tile's items are every other one of the S ring: slot, and the completion
-      // of its kSEmpty to wait for.  Counted, not divided
-      int slot = m, lap = -1;
+      // this tile's items are every other one of the S ring: the slot, and which of the
+      // other tile's releases of it to wait for (item n - 3 is the other tile's: none
+      // for the first 2 - m items).  Counted, not divided
+      int slot = m, idle = 2 - m, lap = 0, third = 0;
       for (; ok && take(); ++cnt) {
         const bool stay = w.stay;
         uint32_t q = qn;
@@ -307,7 +313,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (Tile t{0, w.first}; more(til, w, t); ++q) {
           const int st = q % kQS;
           if (!kept && !(ok = wait(kQFull + st, q / kQS))) break;
-          if (lap >= 0 && !(ok = wait(kSEmpty + slot, lap))) break;
+          if (idle > 0) {
+            --idle;
+          } else {
+            if (!(ok = wait(kSEmpty + kNS * (1 - m) + slot, lap))) break;
+            if (++third == 3) {
+              third = 0;
+              ++lap;
+            }
+          }
           next(til, w, t);
           tc_fence_after();
           // descriptors step by constants from the stage's first one
@@ -317,13 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < D / 16; ++k)
             mma_f16_ts(dcol, acol + 8 * k, bd + ((k / 4) * (kTileQ * 128) + 32 * (k % 4)) / 16, idesc,
                        k > 0 ? 1u : 0u);
-          mma_commit(bar(kSFull + slot));
+          mma_commit(bar(kSFull + kNS * m + slot));
           if (!stay) mma_commit(bar(kQEmpty + st));
-          slot += 2;
-          if (slot >= kNS) {
-            slot -= kNS;
-            ++lap;
-          }
+          slot += slot == 0 ? 2 : -1;  // (slot + 2) % 3
         }
         if (!ok) break;
         mma_commit(bar(kAEmpty + m));
@@ -462,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool one = !til.packed || a.q_gran == 0 || a.G == 1;
     bool ok = true;
     uint32_t qn = 0;
-    int slot = m, lap = 0;  // this half's items are every other one of the S ring
+    int slot = m, lap = 0, third = 0;  // this half's items are every other one of the S ring
     while (ok && take()) {
       const bool stay = w.stay;
       const int key = w.k0 + 128 * m + quad * 32 + lane;
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t q = qn;
       for (Tile t{0, w.first}; more(til, w, t); next(til, w, t), ++q) {
         const int st = q % kQS;
-        ok = wait(kQFull + st, q / kQS) && wait(kSFull + slot, lap);
+        ok = wait(kQFull + st, q / kQS) && wait(kSFull + kNS * m + slot, lap);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum32(va, 2);
           tmem_wait_ld();
           tc_fence_before();
-          mbar_arrive(bar(kSEmpty + slot));
+          mbar_arrive(bar(kSEmpty + kNS * m + slot));
           sum32(vb, 3);
         } else {
 #pragma unroll 1
@@ -528,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             if (j == kTileQ / 32 - 1) {
               tc_fence_before();
-              mbar_arrive(bar(kSEmpty + slot));
+              mbar_arrive(bar(kSEmpty + kNS * m + slot));
             }
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -546,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        slot += 2;
-        if (slot >= kNS) {
-          slot -= kNS;
+        slot += slot == 0 ? 2 : -1;  // (slot + 2) % 3
+        if (++third == 3) {
+          third = 0;
           ++lap;
         }
         total += (s0.x + s0.y) + (s1.x + s1.y);

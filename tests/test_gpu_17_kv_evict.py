@@ -60,6 +60,10 @@ CASES = [
     (1, 4, 1, 128, 200, [150], True, None),       # the first queries see nothing
     (1, 2, 1, 64, 20, [100], True, 40),           # tokens in the middle of the cache
     (1, 3, 1, 64, 9, [70], True, -4),
+    (3, 8, 2, 128, 300, [985, 1500, 0], True, None),   # many tiles a unit, ragged
+    (3, 16, 1, 64, 200, [700, 100, 1300], True, None),  # some sequences shorter than their queries
+    (2, 6, 2, 128, 40, [1300, 513], False, None),       # one packed tile that stays for a run of units
+    (4, 4, 4, 64, 400, [300, 900, 1, 650], False, None),  # the most tiles that stay
 ]
 
 
