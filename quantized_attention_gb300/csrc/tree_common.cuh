@@ -154,7 +154,7 @@ __device__ __forceinline__ int tree_owner(int x, int total, int G) {
 __device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq) {
   const float sq = a.q_gran == 0 ? a.q_scales[0] : a.q_scales[b * a.Hq + hq];
   const float c = __fmul_rn(__fmul_rn(sq, a.sm_scale), kLog2e);
-  return c > 0.f ? c : 1e-30f;
+  return c == 0.f ? 1e-30f : c;
 }
 
 // Cached rows visible to token i: all of them, or (tokens already appended,

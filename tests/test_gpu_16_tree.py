@@ -218,6 +218,46 @@ def test_tree_decode_long_split(T):
     assert torch.equal(O, O2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("T", [2, 40])
+def test_offsets_past_32_bits(T):
+    """The last sequence's rows lie 4.9 GB into each cache array."""
+    B, Hq, Hkv, d, cap = 8, 16, 8, 128, 600011
+    x = make(14, B, Hq, Hkv, d, T, [1] * (B - 1) + [333], cap=400)
+    big = []
+    for name in ("kc", "vc"):
+        t = torch.empty(B, Hkv, cap, d, dtype=torch.int8, device="cuda")
+        t[:, :, :400] = dev(x[name])
+        big.append(t)
+    shape = qb.make_shape(B, Hq, Hkv, T, 333, d)
+    params = qb.make_params(causal=True, kv_capacity=cap)
+    O = torch.full((B, Hq, T, d), float("nan"), device="cuda")
+    lse = torch.full((B, Hq, T), float("nan"), device="cuda")
+    ws = torch.empty(max(qb.tree_workspace_size(shape, params), 256), dtype=torch.uint8, device="cuda")
+    K, V = dev(x["K"], torch.bfloat16), dev(x["V"], torch.bfloat16)
+    qb.tree_decode(dev(x["qc"]), dev(x["qs"]), *big, dev(x["ks"]), dev(x["vs"]), shape, params, O, lse, ws,
+                   lengths=dev(x["lens"]), K_new=K, V_new=V, k_mean=dev(x["mean"]))
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0
+    check(x, "chain", O, lse)
+    # the same rows through the other operators, last sequence
+    w, w_small = torch.zeros(B, Hkv, cap, device="cuda"), torch.zeros(B, Hkv, 400, device="cuda")
+    small = qb.make_params(kv_capacity=400)
+    wide = qb.make_params(kv_capacity=cap)
+    kw = dict(lengths=dev(x["lens"]))
+    qb.kv_weights(dev(x["qc"]), dev(x["qs"]), big[0], None, lse, shape, wide, w, **kw)
+    qb.kv_weights(dev(x["qc"]), dev(x["qs"]), dev(x["kc"]), None, lse, shape, small, w_small, **kw)
+    assert torch.equal(w[:, :, :400], w_small)
+    outs = []
+    for kc, vc, ww in ((big[0], big[1], w), (dev(x["kc"]), dev(x["vc"]), w_small)):
+        o = [torch.zeros(B, Hkv, 50, d, dtype=torch.int8, device="cuda") for _ in range(2)]
+        o += [torch.zeros(B, Hkv, 50, device="cuda"), torch.zeros(B, Hkv, 50, dtype=torch.int32, device="cuda"),
+              torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, Hkv, d, device="cuda")]
+        qb.kv_evict(kc, vc, ww, 50, *o, Nk=333, n_sink=2, n_recent=5, **kw)
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0 and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 def test_cache_and_drafts_agree():
     """Drafts committed to the cache and read from it (causal) give what the chain
     of drafts gave, up to the two calls' own errors; the cache was not touched."""
@@ -235,10 +275,12 @@ def test_cache_and_drafts_agree():
     check(x, "chain", O, lse)
 
 
-def test_bad_lengths_are_reported_and_clamped():
-    x = make(10, 2, 4, 2, 64, 2, [40, 30])
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("bad", [41, -1, -2 ** 31, 2 ** 31 - 1])
+def test_bad_lengths_are_reported_and_clamped(T, bad):
+    x = make(10, 2, 4, 2, 64, T, [40, 30])
     want, _ = run(x, "chain")
-    y = dict(x, lens=np.array([41, 30], np.int32))
+    y = dict(x, lens=np.array([bad, 30], np.int32))
     with pytest.raises(AssertionError):
         run(y, "chain", Nk=40)  # run() asserts that the error word is clear
     assert qb.get_error() == 0
@@ -246,12 +288,13 @@ def test_bad_lengths_are_reported_and_clamped():
     assert torch.equal(want, got)
 
 
-def test_two_streams_and_a_captured_graph():
+@pytest.mark.parametrize("T", [4, 40])
+def test_two_streams_and_a_captured_graph(T):
     """Two calls at once, each with its own workspace, and a captured call replayed
     with new lengths."""
-    x = make(12, 2, 8, 2, 128, 4, [600, 450])
+    x = make(12, 2, 8, 2, 128, T, [600, 450])
     want, _ = run(x, "chain")
-    B, Hq, Hkv, d, T = 2, 8, 2, 128, 4
+    B, Hq, Hkv, d = 2, 8, 2, 128
     shape = qb.make_shape(B, Hq, Hkv, T, 600, d)
     params = qb.make_params(causal=True, kv_capacity=x["cap"])
     arrays = [dev(x[k]) for k in ("qc", "qs", "kc", "vc", "ks", "vs")]
@@ -323,6 +366,24 @@ def test_commit_bit_exact(B, Hkv, d, T, n, strided, in_place):
     assert np.array_equal(got["k_mean_out"].cpu().numpy().view(np.uint32),
                           np.stack([r[0] for r in ref]).view(np.uint32))
     assert np.array_equal(got["v_code_amax_out"].cpu().numpy(), np.stack([r[1] for r in ref]))
+
+
+def test_commit_the_same_draft_twice_and_nothing():
+    """A path may name a draft twice; T = 0 appends nothing."""
+    x = make(23, 1, 2, 2, 64, 3, [4], cap=9)
+    kc, vc = x["kc"].copy(), x["vc"].copy()
+    am = np.zeros((1, 2, 64), np.float32)
+    m, a = R.commit(x["K"][0], x["V"][0], [2, 2, 0], 3, 4, 4, x["ks"][0], x["vs"][0], x["mean"][0], am[0], kc[0], vc[0])
+    gk, gv, lens, mean, gam = dev(x["kc"]), dev(x["vc"]), dev(x["lens"]), dev(x["mean"]), dev(am)
+    args = (dev(x["ks"]), dev(x["vs"]), lens, mean, gam, gk, gv)
+    K, V = dev(x["K"], torch.bfloat16), dev(x["V"], torch.bfloat16)
+    qb.tree_commit(K, V, dev(np.array([[2, 2, 0]], np.int32)), dev(np.array([3], np.int32)), *args)
+    none = torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+    qb.tree_commit(K[:, :, :0], V[:, :, :0], none, dev(np.array([0], np.int32)), *args)
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0 and lens.tolist() == [7]
+    assert np.array_equal(gk.cpu().numpy(), kc) and np.array_equal(gv.cpu().numpy(), vc)
+    assert np.array_equal(mean.cpu().numpy()[0], m) and np.array_equal(gam.cpu().numpy()[0], a)
 
 
 @pytest.mark.parametrize("n,p,L", [(5, 0, 0), (-1, 0, 0), (2, 4, 0), (2, -1, 0), (2, 0, 7)])

@@ -136,6 +136,27 @@ def test_weights_in_place_and_repeatable():
     assert torch.equal(b[:, :, :900], 2 * a[:, :, :900]) and qb.get_error() == 0
 
 
+def test_weights_of_no_queries_and_bad_lengths():
+    """No query: the base as it is.  Lengths outside the cache are clamped and
+    reported, for few rows and for many."""
+    base = torch.rand(2, 2, 70, device="cuda")
+    for T in (0, 3, 70):
+        x = make(33, 2, 4, 2, 64, T, [70, 20], 2, 2, cap=70)
+        shape = qb.make_shape(2, 4, 2, T, 70, 64)
+        lse = torch.full((2, 4, T), 5.0, device="cuda")
+        args = (dev(x["qc"]), dev(x["qs"]), dev(x["kc"]), dev(x["ks"]), lse, shape, qb.make_params(kv_capacity=70))
+        w, v = torch.zeros_like(base), torch.zeros_like(base)
+        qb.kv_weights(*args, w, base=base, lengths=dev(x["lens"]))
+        torch.cuda.synchronize()
+        assert qb.get_error() == 0 and torch.all(w[1, :, 20:] == 0)
+        if T == 0:
+            assert torch.equal(w[0], base[0]) and torch.equal(w[1, :, :20], base[1, :, :20])
+        qb.kv_weights(*args, v, base=base, lengths=dev(np.array([71, -5], np.int32)))
+        torch.cuda.synchronize()
+        assert qb.get_error() == qb.ERR_INVALID_ARG
+        assert torch.equal(v[0], w[0]) and torch.all(v[1] == 0)
+
+
 def test_a_prompts_weights_after_prefill():
     """qattn_fwd's own codes and lse: each query hands out 1 per head, up to its
     lse's rounding (|lse| 2^-24 and the kernels' fp32 sums, 2^-17 in all)."""
