@@ -299,7 +299,7 @@ float sm_scale_of(const qattn_shape* s, const qattn_params* p) {
 // workspace of their shares.  The layout depends on the shape alone.
 struct TreeSplit {
   bool tc;         // the tensor-core kernel
-  bool clustered;  // a cluster per head and row block
+  int cluster;     // CTAs of a head's own cluster; 0: shares and the join
   int step, blocks, rows, drafts, ctas;
   int64_t steps;  // of all heads, at most
   size_t slots, off_m, off_l, bytes;
@@ -314,11 +314,11 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
   t.steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
-  t.clustered = !t.tc && qattn::tree_clustered(s->B * s->Hkv * t.blocks, t.drafts + (s->Nk + t.step - 1) / t.step);
+  t.cluster = t.tc ? 0 : qattn::tree_cluster(s->B * s->Hkv * t.blocks, t.drafts + (s->Nk + t.step - 1) / t.step);
   // a step per warp of a CTA of four, or per CTA
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
-  if (t.clustered) t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * qattn::kTreeCluster);
-  t.slots = t.clustered ? 0 : 2 * static_cast<size_t>(t.ctas);
+  if (t.cluster > 0) t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * t.cluster);
+  t.slots = t.cluster > 0 ? 0 : 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);
   t.bytes = t.off_l + align256(t.slots * t.rows * 4);
@@ -1013,7 +1013,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   a.out = O;
   a.out_bf16 = params->out_dtype == QATTN_BF16;
   a.lse = lse;
-  a.clustered = sp.clustered;
+  a.cluster = sp.cluster;
   a.ctas = sp.ctas;
   a.slots = sp.slots;
   a.rows_total = static_cast<size_t>(shape->B * shape->Hq * shape->Nq);
@@ -1033,7 +1033,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb),
                  drafts ? a.T : 0,
                  sp.tc ? "tree_tc_kernel + tree_join_kernel"
-                       : sp.clustered ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel",
+                       : sp.cluster > 0 ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel",
                  sp.ctas);
   return from_cuda(sp.tc ? qattn::launch_tree_tc(tk, tv, a, s) : qattn::launch_tree_warp(tk, tv, a, s));
 }

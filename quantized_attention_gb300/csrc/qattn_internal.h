@@ -228,16 +228,19 @@ constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
 constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
 constexpr int kTreeTcCtas = 152;     // its CTAs, at most
 constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
-constexpr int kTreeCluster = 8;      // CTAs of a head in the warp-level kernel's clustered form
-// The clustered form is taken for few heads with short caches: one wave of
-// clusters (two CTAs an SM) and at most 264 steps a head, or two and 72.
-// Measured, clustered against shares + join, us: 8 heads of 2K / 8K / 16K rows
-// 8.1 / 13.5 / 20.8 against 12.5 / 15.5 / 20.1; 32 heads of 8K 19.6 against 25.6;
-// 16 heads of 16K 27.7 against 22.4; 48 heads of 2K (d = 64) 9.0 against 13.0, of
-// 4K 25.8 against 22.1; 80 heads of 1K 22.6 against 15.4.
-inline bool tree_clustered(long long heads, long long steps) {
-  const long long ctas = heads * kTreeCluster;
-  return ctas <= kTreeWarpCtas ? steps <= 264 : ctas <= 2 * kTreeWarpCtas && steps <= 72;
+constexpr int kTreeCluster = 8;      // most CTAs of a head in the warp-level kernel's clustered form
+// CTAs of the cluster a head gets to itself: as many (a power of two) as fit one
+// wave of two CTAs an SM.  0 -- equal shares of all heads' steps, joined by a second
+// kernel -- where that leaves SMs idle over long caches.  Measured, clusters against
+// shares, us (d = 128): 8 heads of 2K / 8K / 16K / 32K rows 8.5 / 13.9 / 20.8 / 35.6
+// against 12.5 / 15.3 / 20.1 / 25.7; 16 heads of 16K 27.7 / 22.4; 32 of 8K 20.3 / 24.9;
+// 64 of 16K 50.2 / 54.5; 128 of 2K 20.2 / 25.6, of 100 to 8K 47.7 / 56.4; 256 of 300
+// 11.1 / 18.3; 512 of 1K 39.0 / 45.7.  Twice the CTAs (two waves) loses: 64 heads of 1K
+// 16.3 against 10.2.
+inline int tree_cluster(long long heads, long long steps) {
+  int c = kTreeCluster;
+  while (c > 1 && c * heads > kTreeWarpCtas) c /= 2;
+  return c * heads >= 256 || steps <= 384 ? c : 0;
 }
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
@@ -262,7 +265,8 @@ struct TreeArgs {
   float* lse;                    // [B][Hq][T] or null
   unsigned int* err;
   // the split and its workspace
-  int clustered;                 // one cluster per (head, row block): no join, no workspace
+  int cluster;                   // CTAs of the cluster that has a head to itself: no join, no
+                                 // workspace (0: shares of all heads' steps, then the join)
   int ctas;
   size_t slots, rows_total;      // 2 ctas; B Hq T
   float* part_o;                 // [slots][block rows][d]

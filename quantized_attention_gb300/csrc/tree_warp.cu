@@ -124,16 +124,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t used = 0;  // tiles this warp has taken through its ring
 
   TreeSeg sg;
-  if constexpr (CL) {  // this CTA's eighth of its head
+  if constexpr (CL) {  // this CTA's part of its head
     const int rank = static_cast<int>(cluster_rank());
-    int head = blockIdx.x / kTreeCluster;
+    int head = blockIdx.x / a.cluster;
     sg.rb = head % a.blocks;
     head /= a.blocks;
     sg.hkv = head % a.Hkv;
     sg.b = head / a.Hkv;
     sg.len = tree_length(a, sg.b);
     sg.steps = tree_steps(a, sg.len, kStep);
-    const int q = sg.steps / kTreeCluster, r = sg.steps - q * kTreeCluster;
+    const int q = sg.steps / a.cluster, r = sg.steps - q * a.cluster;
     sg.s0 = rank * q + min(rank, r);
     sg.s1 = sg.s0 + q + (rank < r ? 1 : 0);
   }
@@ -393,26 +393,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
   if constexpr (CL) {
-    // ---- join the cluster: CTA `rank` writes rows rank and rank + 8.  Every CTA
-    // reaches both barriers, one that gave up on a wait too
+    // ---- join the cluster: CTA `rank` writes rows rank, rank + cluster, ...  Every
+    // CTA reaches both barriers, one that gave up on a wait too
     cluster_sync();
-    const uint32_t rank = cluster_rank();
-    for (int idx = threadIdx.x; idx < 2 * (D / 4); idx += kThreads) {
-      const int r = static_cast<int>(rank) + kTreeCluster * (idx / (D / 4)), c = 4 * (idx % (D / 4));
+    const int rank = static_cast<int>(cluster_rank());
+    for (int idx = threadIdx.x; idx < (kTreeRows / a.cluster) * (D / 4); idx += kThreads) {
+      const int r = rank + a.cluster * (idx / (D / 4)), c = 4 * (idx % (D / 4));
       if (sg.rb * kTreeRows + r >= R) continue;
       float mc[kTreeCluster], lc[kTreeCluster], mx = kNegInf, lt = 0.f;
       float4 y[kTreeCluster], x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (uint32_t q = 0; q < kTreeCluster; ++q) {
-        mc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_m[r]), q)));
-        lc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_l[r]), q)));
-        y[q] = ld_cluster_f4(cluster_addr(smem_u32(smem + SM::kDraft) + 4 * (r * D + c), q));
+      for (int q = 0; q < kTreeCluster; ++q) {
+        mc[q] = kNegInf;
+        if (q < a.cluster) {
+          mc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_m[r]), q)));
+          lc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_l[r]), q)));
+          y[q] = ld_cluster_f4(cluster_addr(smem_u32(smem + SM::kDraft) + 4 * (r * D + c), q));
+        }
       }
 #pragma unroll
       for (int q = 0; q < kTreeCluster; ++q) mx = fmaxf(mx, mc[q]);
 #pragma unroll
       for (int q = 0; q < kTreeCluster; ++q) {
-        const float f = mc[q] == kNegInf ? 0.f : ex2_approx(mc[q] - mx);
+        if (mc[q] == kNegInf) continue;
+        const float f = ex2_approx(mc[q] - mx);
         lt = fmaf(f, lc[q], lt);
         x.x = fmaf(f, y[q].x, x.x);
         x.y = fmaf(f, y[q].y, x.y);
@@ -429,10 +433,10 @@ template <int D>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = WarpSmem<D>::kBytes;
   cudaError_t e;
-  if (a.clustered) {
+  if (a.cluster > 0) {
     e = cudaFuncSetAttribute(tree_warp_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(tree_warp_kernel<D, true>, dim3(a.ctas), dim3(kThreads), kTreeCluster, smem, s, tk, tv,
+    return launch_pdl_cluster(tree_warp_kernel<D, true>, dim3(a.ctas), dim3(kThreads), a.cluster, smem, s, tk, tv,
                               a);
   }
   e = cudaFuncSetAttribute(tree_warp_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
