@@ -314,7 +314,8 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
   t.steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
-  t.cluster = t.tc ? 0 : qattn::tree_cluster(s->B * s->Hkv * t.blocks, t.drafts + (s->Nk + t.step - 1) / t.step);
+  const int64_t heads = s->B * s->Hkv * t.blocks, head_steps = t.drafts + (s->Nk + t.step - 1) / t.step;
+  t.cluster = t.tc ? qattn::tree_tc_cluster(heads, head_steps) : qattn::tree_cluster(heads, head_steps);
   // a step per warp of a CTA of four, or per CTA
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
   if (t.cluster > 0) t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * t.cluster);
@@ -1032,8 +1033,8 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   char sb[128];
   QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb),
                  drafts ? a.T : 0,
-                 sp.tc ? "tree_tc_kernel + tree_join_kernel"
-                       : sp.cluster > 0 ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel",
+                 sp.tc ? (sp.cluster > 0 ? "tree_tc_kernel (clusters)" : "tree_tc_kernel + tree_join_kernel")
+                       : (sp.cluster > 0 ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel"),
                  sp.ctas);
   return from_cuda(sp.tc ? qattn::launch_tree_tc(tk, tv, a, s) : qattn::launch_tree_warp(tk, tv, a, s));
 }

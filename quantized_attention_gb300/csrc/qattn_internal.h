@@ -242,6 +242,21 @@ inline int tree_cluster(long long heads, long long steps) {
   while (c > 1 && c * heads > kTreeWarpCtas) c /= 2;
   return c * heads >= 256 || steps <= 384 ? c : 0;
 }
+// The same for the tensor-core kernel (heads: KV heads x row blocks; one CTA an SM).
+// Clusters of 8 are taken for 8 heads at most (16 of them are not placed at once: 105
+// us against 89 in fours).  Equal shares cost a plan and a join, ~18 us of a step's
+// 1.4: they pay once the busiest CTA of a cluster would take 13 steps more than its
+// share.  Measured, clusters against shares, us (d = 128): 8 heads of 300 / 8K / 32K
+// rows 13.5 / 24.3 / 51.9 against 16.4 / 37.5 / 50.5; 16 of 8K / 32K 33.5 / 89.4
+// against 40.1 / 67.2; 32 of 8K 36.2 / 45.7; 64 of 5K to 32K 164 / 113; 128 of 2K 35.8 /
+// 51.8, of 100 to 4K 54 / 115; 256 of 2K 65 / 88.
+inline int tree_tc_cluster(long long heads, long long steps) {
+  int c = heads <= 8 ? kTreeCluster : kTreeCluster / 2;
+  while (c > 1 && c * heads > kTreeTcCtas) c /= 2;
+  const long long waves = (heads * c + kTreeTcCtas - 1) / kTreeTcCtas;
+  const long long extra = steps * waves / c - heads * steps / kTreeTcCtas;
+  return extra <= 13 + heads / 26 ? c : 0;
+}
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
   int blocks;                    // row blocks of a head

@@ -143,6 +143,30 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk&
   return true;
 }
 
+// The clustered form: this CTA's part of its cluster's head (the segment; possibly
+// no step), and a walk that yields it once.
+__device__ __forceinline__ TreeWalk tree_cluster_walk(const TreeArgs& a, int step, TreeSeg& s) {
+  const int rank = static_cast<int>(cluster_rank());
+  int head = blockIdx.x / a.cluster;
+  s.rb = head % a.blocks;
+  head /= a.blocks;
+  s.hkv = head % a.Hkv;
+  s.b = head / a.Hkv;
+  s.len = tree_length(a, s.b);
+  s.steps = tree_steps(a, s.len, step);
+  const int q = s.steps / a.cluster, r = s.steps - q * a.cluster;
+  s.s0 = rank * q + min(rank, r);
+  s.s1 = s.s0 + q + (rank < r ? 1 : 0);
+  TreeWalk w{};
+  w.end = s.s1 - s.s0;
+  return w;
+}
+__device__ __forceinline__ bool tree_once(TreeWalk& w, const TreeSeg& s) {
+  if (w.p >= w.end) return false;
+  w.p = w.end;
+  return s.s0 < s.s1;
+}
+
 // The CTA whose share holds step x of a list of `total`.
 __device__ __forceinline__ int tree_owner(int x, int total, int G) {
   const int q = total / G, r = total - q * G, big = r * (q + 1);

@@ -44,6 +44,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffX + 2 * 2 * kRows * 4;  // row maxima: [buffer][half][row]
   static constexpr int kBytes = kOffBar + 512;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
+  static_assert(4 * kRows * D + 8 * kRows <= kOff16, "a CTA's O, m and l for its cluster do not fit the raw ring");
 };
 
 enum {
@@ -63,7 +64,11 @@ enum {
   kNumBars = 35
 };
 
-template <int D>
+// Place of 16-byte chunk c of row r of a CTA's O in shared memory (a thread writes a
+// row: eight rows of a store hit eight bank groups).
+__device__ __forceinline__ int share_chunk(int r, int c) { return c ^ (r & 7); }
+
+template <int D, bool CL>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const TreeArgs a) {
@@ -107,8 +112,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();  // after the wait: the join reads the lengths before its own
-  TreeWalk walk = tree_walk(a, kStep);
+  TreeWalk walk;
   TreeSeg sg{};
+  if constexpr (CL) {
+    walk = tree_cluster_walk(a, kStep, sg);
+  } else {
+    walk = tree_walk(a, kStep);
+  }
+  // the next segment: of this CTA's share, or (once) its part of its own head
+  auto next_segment = [&] { return CL ? tree_once(walk, sg) : tree_next(a, kStep, walk, sg); };
 
   // A drafted step's codes, into its raw tiles n and n + 1: the softmax warps (idle
   // until the segment's first scores) and the converting ones together, thread e of
@@ -138,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool ok = true;
       uint32_t n = 0;  // tiles: K and V of each step
-      while (ok && tree_next(a, kStep, walk, sg)) {
+      while (ok && next_segment()) {
         const int bkv = sg.b * a.Hkv + sg.hkv;
         for (int s = sg.s0; ok && s < sg.s1; ++s) {
           for (int kv = 0; kv < 2; ++kv, ++n) {
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(bar(kKEmpty + st));
         return true;
       };
-      for (; ok && tree_next(a, kStep, walk, sg); ++seg) {
+      for (; ok && next_segment(); ++seg) {
         const int n = sg.s1 - sg.s0;
         if (!(ok = wait(kQReady, seg))) break;
         if (!(ok = qk(it))) break;
@@ -227,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       other = xch[(b2 * 2 + 1 - hf) * kRows + r];
       return true;
     };
-    while (ok && tree_next(a, kStep, walk, sg)) {
+    while (ok && next_segment()) {
       for (int s = sg.s0; ok && s < min(sg.s1, a.drafts); ++s) {
         ok = encode(2 * (it + s - sg.s0), s, threadIdx.x - 128, nd);
         ++nd;
@@ -373,14 +385,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 32; k += 4) {
           const float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
                                        __uint_as_float(x[k + 3]));
-          if (whole) {
+          if constexpr (CL) {  // the raw ring is free: every tile has been converted
+            *reinterpret_cast<float4*>(smem + 4 * (r * D) + 16 * share_chunk(r, (ch + k) / 4)) = y;
+          } else if (whole) {
             tree_write_out<D>(a, sg.b, sg.hkv, rr, ch + k, y, m, l);
           } else if (in && QATTN_IN_BOUNDS(slot < a.slots)) {
             *reinterpret_cast<float4*>(a.part_o + (slot * kRows + r) * D + ch + k) = y;
           }
         }
       }
-      if (!whole && in && hf == 0 && QATTN_IN_BOUNDS(slot < a.slots)) {
+      if constexpr (CL) {
+        if (hf == 0) {
+          float* ml = reinterpret_cast<float*>(smem + 4 * kRows * D);
+          ml[r] = m;
+          ml[kRows + r] = l;
+        }
+      } else if (!whole && in && hf == 0 && QATTN_IN_BOUNDS(slot < a.slots)) {
         a.part_m[slot * kRows + r] = m;
         a.part_l[slot * kRows + r] = l;
       }
@@ -421,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t it = 0, nd = 0;
     uint32_t slot = 0, lap = 0;  // the raw tile to convert next: counted, not divided
-    while (ok && tree_next(a, kStep, walk, sg)) {
+    while (ok && next_segment()) {
       bool loaded = false;  // v holds the next tile already
       for (int s = sg.s0; ok && s < sg.s1; ++s, ++it) {
         const uint32_t st = it & 1;
@@ -459,15 +479,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (CL) {
+    // ---- join the cluster: CTA `rank` writes rows rank, rank + cluster, ...  Every
+    // CTA reaches both barriers, one that gave up on a wait too
+    const int rank = static_cast<int>(cluster_rank());
+    if (threadIdx.x == 0) tmem_slot[2] = sg.s0 < sg.s1 ? 1u : 0u;  // a part of no steps has no share
+    cluster_sync();
+    const uint32_t ml = base + 4 * kRows * D, flags = smem_u32(tmem_slot + 2);
+    for (int idx = threadIdx.x; idx < (kRows / a.cluster) * (D / 4); idx += kThreads) {
+      const int r = rank + a.cluster * (idx / (D / 4)), c = 4 * (idx % (D / 4));
+      if (sg.rb * kRows + r >= a.G * a.T) continue;
+      float mc[kTreeCluster], lc[kTreeCluster], mx = kNegInf, lt = 0.f;
+      float4 y[kTreeCluster], x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kTreeCluster; ++q) {
+        mc[q] = kNegInf;
+        if (q < a.cluster && ld_cluster_u32(cluster_addr(flags, q))) {
+          mc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(ml + 4 * r, q)));
+          lc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(ml + 4 * (kRows + r), q)));
+          y[q] = ld_cluster_f4(cluster_addr(base + 4 * (r * D) + 16 * share_chunk(r, c / 4), q));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kTreeCluster; ++q) mx = fmaxf(mx, mc[q]);
+#pragma unroll
+      for (int q = 0; q < kTreeCluster; ++q) {
+        if (mc[q] == kNegInf) continue;
+        const float f = ex2_approx(mc[q] - mx);
+        lt = fmaf(f, lc[q], lt);
+        x.x = fmaf(f, y[q].x, x.x);
+        x.y = fmaf(f, y[q].y, x.y);
+        x.z = fmaf(f, y[q].z, x.z);
+        x.w = fmaf(f, y[q].w, x.w);
+      }
+      tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kRows + r, c, x, mx, lt);
+    }
+    cluster_sync();  // no CTA leaves while another reads its share
+  }
 }
 
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = Cfg<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e;
+  if (a.cluster > 0) {
+    e = cudaFuncSetAttribute(tree_tc_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(tree_tc_kernel<D, true>, dim3(a.ctas), dim3(kThreads), a.cluster, smem, s, tk, tv, a);
+  }
+  e = cudaFuncSetAttribute(tree_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(tree_tc_kernel<D>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
-  if (e != cudaSuccess || (a.ctas == 1 && a.drafts > 0)) return e;
+  e = launch_pdl(tree_tc_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
+  if (e != cudaSuccess) return e;
   return launch_pdl(tree_join_kernel<D, kRows, kStep, 1>, dim3(a.B * a.Hkv * a.blocks, kRows / 4),
                     dim3(kTreeJoinThreads), 0, s, a);
 }

@@ -124,19 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t used = 0;  // tiles this warp has taken through its ring
 
   TreeSeg sg;
-  if constexpr (CL) {  // this CTA's part of its head
-    const int rank = static_cast<int>(cluster_rank());
-    int head = blockIdx.x / a.cluster;
-    sg.rb = head % a.blocks;
-    head /= a.blocks;
-    sg.hkv = head % a.Hkv;
-    sg.b = head / a.Hkv;
-    sg.len = tree_length(a, sg.b);
-    sg.steps = tree_steps(a, sg.len, kStep);
-    const int q = sg.steps / a.cluster, r = sg.steps - q * a.cluster;
-    sg.s0 = rank * q + min(rank, r);
-    sg.s1 = sg.s0 + q + (rank < r ? 1 : 0);
-  }
+  if constexpr (CL) walk = tree_cluster_walk(a, kStep, sg);
   while (CL || tree_next(a, kStep, walk, sg)) {
     const int bkv = sg.b * a.Hkv + sg.hkv;
     const int nd = a.drafts;  // drafted steps of a head

@@ -206,12 +206,14 @@ def test_granules_and_unused_lengths(T):
     check(x, "chain", O, lse)
 
 
-@pytest.mark.parametrize("T", [1, 48])
-def test_tree_decode_long_split(T):
-    """A long cache over every CTA, and its result bit for bit whatever the
-    workspace held."""
-    x = make(8, 1, 8, 2, 128, T, [20011])
-    see, words = random_mask(x["rng"], 1, T)
+@pytest.mark.parametrize("T,d,lens", [(1, 128, [20011]), (48, 128, [20011]), (3, 64, [700, 16111, 0]),
+                                      (30, 64, [11, 33333, 0, 20000])])
+def test_tree_decode_long_split(T, d, lens):
+    """Long caches in equal shares over every CTA, and their result bit for bit
+    whatever the workspace held."""
+    x = make(8, len(lens), 8, 2, d, T, lens)
+    assert qb.tree_workspace_size(qb.make_shape(len(lens), 8, 2, T, max(lens), d), qb.make_params()) > 0
+    see, words = random_mask(x["rng"], len(lens), T)
     O, lse = run(x, "tree", words)
     check(x, "tree", O, lse, see)
     O2, lse2 = run(x, "tree", words, ws_fill=0)

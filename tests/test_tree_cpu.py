@@ -42,8 +42,10 @@ def test_tree_decode_refusals(L):
     for n in ("q_codes", "k_codes", "v_codes", "O", "K_new", "V_new", "k_mean", "v_chan_scale", "lengths", "tree_mask",
               "lse", "q_scales"):
         assert tree(L, **{n: ODD}) == INVALID, n
-    long = (2, 8, 2, 5, 100, 128)  # 20 rows: shares of a head in the workspace
-    assert tree(L, shape=long, workspace=None) == WORKSPACE and tree(L, shape=long, ws=16) == WORKSPACE
+    long = (2, 8, 2, 5, 128 * 1000, 128)  # long caches, 20 rows: shares in the workspace
+    p = qb.make_params()
+    assert tree(L, shape=long, params=p, workspace=None) == WORKSPACE
+    assert tree(L, shape=long, params=p, ws=16) == WORKSPACE
     assert tree(L, shape=(2, 8, 2, 129, 100, 128)) == UNSUPPORTED  # more drafts than a mask holds
     assert tree(L, shape=(2, 8, 2, 4, 100, 32)) == UNSUPPORTED
     assert tree(L, shape=(2, 7, 2, 4, 100, 128)) == INVALID
@@ -58,12 +60,13 @@ def test_tree_decode_refusals(L):
 
 
 def test_tree_workspace(L):
-    """Bounded: two shares of a row block per CTA, whatever the cache's length."""
+    """None for short caches (a head's cluster joins itself); for long ones two shares
+    of a row block per CTA, whatever the length."""
     p = qb.make_params()
     size = lambda *s: qb.tree_workspace_size(qb.make_shape(*s), p)  # noqa: E731
     assert size(0, 8, 2, 4, 100, 128) == 0 and size(1, 8, 2, 129, 100, 128) == 0
     assert size(1, 8, 2, 1, 100, 128) == 0  # short and few rows: joined inside a cluster
-    assert 0 < size(1, 8, 2, 5, 1, 128) <= size(1, 8, 2, 5, 100000, 128)
+    assert size(1, 8, 2, 5, 100, 128) == 0 < size(1, 8, 2, 5, 100000, 128)
     assert 0 < size(1, 8, 2, 1, 100000, 128)
     assert size(1, 8, 2, 128, 10 ** 6, 128) == size(1, 8, 2, 128, 8 * 10 ** 6, 128) < 64 << 20
 
