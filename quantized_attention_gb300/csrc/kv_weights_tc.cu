@@ -21,6 +21,7 @@
 // queries and consecutive units of one head, the Q tiles stay where they are and
 // the kernel streams K.
 #include <algorithm>
+#include <type_traits>
 
 #include "qattn_check.cuh"
 #include "qattn_internal.h"
@@ -498,39 +499,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool all = !a.causal || w.k0 + 128 * m + 127 <= w.pos0 + (til.packed ? 0 : t.c * kTileQ);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
         const uint32_t src = tmem + lane_base + kTmemS + 128 * slot;
-        if (one && all) {
-          // one factor, nothing hidden
-          const float c0 = fac[0] * sk;
-          const float2 cc = make_float2(c0, c0);
-          auto sum32 = [&](const uint32_t (&v)[32], int j) {
+        const float c0 = fac[0] * sk;
+        // 32 columns; ONE: one factor for the tile, ALL: no key hidden from any row
+        auto sum32 = [&](auto one_c, auto all_c, const uint32_t (&v)[32], int j) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * j + e);
-              const float2 t0 = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc,
-                                      make_float2(l4.x, l4.y));
-              const float2 t1 = ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), cc,
-                                      make_float2(l4.z, l4.w));
-              s0 = fadd2(s0, make_float2(ex2_approx(t0.x), ex2_approx(t0.y)));
-              s1 = fadd2(s1, make_float2(ex2_approx(t1.x), ex2_approx(t1.y)));
+          for (int e = 0; e < 32; e += 4) {
+            float2 c01 = make_float2(c0, c0), c23 = c01;
+            if constexpr (!one_c.value) {
+              const float4 c4 = *reinterpret_cast<const float4*>(fac + 32 * j + e);
+              c01 = fmul2(make_float2(c4.x, c4.y), sk2);
+              c23 = fmul2(make_float2(c4.z, c4.w), sk2);
             }
-          };
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * j + e);
+            float2 t0 = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c01,
+                              make_float2(l4.x, l4.y));
+            float2 t1 = ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), c23,
+                              make_float2(l4.z, l4.w));
+            if constexpr (!all_c.value) {
+              const int4 k4 = *reinterpret_cast<const int4*>(last + 32 * j + e);
+              t0 = make_float2(key <= k4.x ? t0.x : kNegInf, key <= k4.y ? t0.y : kNegInf);
+              t1 = make_float2(key <= k4.z ? t1.x : kNegInf, key <= k4.w ? t1.y : kNegInf);
+            }
+            s0 = fadd2(s0, make_float2(ex2_approx(t0.x), ex2_approx(t0.y)));
+            s1 = fadd2(s1, make_float2(ex2_approx(t1.x), ex2_approx(t1.y)));
+          }
+        };
+        auto tile = [&](auto one_c, auto all_c) {
           // the next 32 columns load while these compute
           uint32_t va[32], vb[32];
           tmem_ld32(src, va);
           tmem_wait_ld();
           tmem_ld32(src + 32, vb);
-          sum32(va, 0);
+          sum32(one_c, all_c, va, 0);
           tmem_wait_ld();
           tmem_ld32(src + 64, va);
-          sum32(vb, 1);
+          sum32(one_c, all_c, vb, 1);
           tmem_wait_ld();
           tmem_ld32(src + 96, vb);
-          sum32(va, 2);
+          sum32(one_c, all_c, va, 2);
           tmem_wait_ld();
           tc_fence_before();
           mbar_arrive(bar(kSEmpty + kNS * m + slot));
-          sum32(vb, 3);
-        } else {
+          sum32(one_c, all_c, vb, 3);
+        };
+        if (all) {
+          if (one) tile(std::true_type{}, std::true_type{});
+          else tile(std::false_type{}, std::true_type{});
+        } else {  // (a tile or two of a unit)
 #pragma unroll 1
           for (int j = 0; j < kTileQ / 32; ++j) {
             uint32_t v[32];
@@ -540,20 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_before();
               mbar_arrive(bar(kSEmpty + kNS * m + slot));
             }
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 c4 = *reinterpret_cast<const float4*>(fac + 32 * j + e);
-              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * j + e);
-              const int4 k4 = *reinterpret_cast<const int4*>(last + 32 * j + e);
-              const float2 t0 = ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                      fmul2(make_float2(c4.x, c4.y), sk2), make_float2(l4.x, l4.y));
-              const float2 t1 = ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                      fmul2(make_float2(c4.z, c4.w), sk2), make_float2(l4.z, l4.w));
-              s0 = fadd2(s0, make_float2(ex2_approx(key <= k4.x ? t0.x : kNegInf),
-                                         ex2_approx(key <= k4.y ? t0.y : kNegInf)));
-              s1 = fadd2(s1, make_float2(ex2_approx(key <= k4.z ? t1.x : kNegInf),
-                                         ex2_approx(key <= k4.w ? t1.y : kNegInf)));
-            }
+            sum32(std::false_type{}, std::false_type{}, v, j);
           }
         }
         slot += slot == 0 ? 2 : -1;  // (slot + 2) % 3
