@@ -473,14 +473,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool one = !til.packed || a.q_gran == 0 || a.G == 1;
     bool ok = true;
     uint32_t qn = 0;
+    bool ahead = false;
+    float old_next = 0.f, sk_next = 1.f;
     int slot = m, lap = 0, third = 0;  // this half's items are every other one of the S ring
     while (ok && take()) {
       const bool stay = w.stay;
       const int key = w.k0 + 128 * m + quad * 32 + lane;
       const size_t o = static_cast<size_t>(w.bkv) * a.cap + key;
       const bool live = key < w.len;
-      const float old = (live && a.base) ? a.base[o] : 0.f;
-      const float sk = a.k_scales ? scale_of(a.k_scales, a.k_gran, w.bkv, nkb, min(w.k0 / 128 + m, nkb - 1)) : 1.f;
+      auto base_of = [&](int k) { return (k < w.len && a.base) ? a.base[static_cast<size_t>(w.bkv) * a.cap + k] : 0.f; };
+      auto key_scale = [&](int k0) {
+        return a.k_scales ? scale_of(a.k_scales, a.k_gran, w.bkv, nkb, min(k0 / 128 + m, nkb - 1)) : 1.f;
+      };
+      // base and scale of a unit that follows in the same head come a unit ahead: their
+      // latency would stand before every unit's first column
+      const float old = ahead ? old_next : base_of(key), sk = ahead ? sk_next : key_scale(w.k0);
+      ahead = w.runs && w.n + 1 < w.count && w.kb + 1 < w.blocks;
+      if (ahead) {
+        old_next = base_of(key + kUnit);
+        sk_next = key_scale(w.k0 + kUnit);
+      }
       const float2 sk2 = make_float2(sk, sk);
       float total = 0.f;
       uint32_t q = qn;
