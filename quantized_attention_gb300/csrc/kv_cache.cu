@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
 // cluster copies the kept rows, each CTA an equal share of the output, 16 bytes a
 // thread, the V codes' channel maxima on the way.  The weights are read once, the
 // kept rows read and written once; a short cache is bound by the rounds' barriers
-// (~1 us each), a long one by the copy.
+// (~1 us each), a long one by the copy.  Measured: 128 heads of ~2K rows cut to 1999
+// (d = 64) 18.3 us = 3.7 TB/s, 8 heads of 32K cut to 4K 18.5 us (64 CTAs); two kernels
+// (select, gather) took 79 and 23.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxCluster = 8;

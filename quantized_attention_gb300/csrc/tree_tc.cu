@@ -13,8 +13,13 @@
 // fp16 into TMEM, O += P V16 (V16 as it lies: the B operand with its N index
 // fastest).  Q and P in TMEM leave shared memory to the codes: 32 KB in, 32 KB
 // read, 64 KB of fp16 written and 64 KB read by the MMAs a step, ~1540 cycles
-// against ~1460 of the step's share of HBM and ~1030 of tensor work.  The
-// reference m moves only when a row's maximum has grown by more than 2^8 (P stays
+// against ~1460 of the step's share of HBM and ~1030 of tensor work.  Measured: ~2500
+// cycles a step, because the converting warps (~1050 a tile, two a step: waits,
+// 180 instructions a thread, the proxy fence), the softmax warps (~2300) and the one
+// issuing thread (~2100) each nearly fill it; 26-node trees over eight caches of 5K
+// to 32K rows 113 us (floor 47), 64 nodes over 32K 67 (floor 18).  Eight converting
+// warps, two issuing threads, and setmaxnreg with more registers for the softmax
+// measured no faster or slower.  The reference m moves only when a row's maximum has grown by more than 2^8 (P stays
 // below 2^8, far inside fp16), so O is rarely rescaled.
 #include <cuda_fp16.h>
 
