@@ -443,9 +443,10 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
  *       c = fp32(fp32(sq * sm_scale) * log2 e)
  *   O = v_chan_scale * sum 2^(t - m) vc / sum 2^(t - m),  m the running max;
  *       lse = natural log of sum e^(t ln 2)
- * The PV product takes P = 2^(t - m) <= 1 rounded to fp16 and the V codes as
- * they are (qattn_decode follows the e4m3 recipe instead); sums and statistics
- * are fp32.  A row that sees nothing gives O = 0 and lse = -inf.
+ * The PV product takes P = 2^(t - m) rounded to fp16 (m a running maximum, at most
+ * 8 behind: P <= 2^8) and the V codes as they are (qattn_decode follows the e4m3
+ * recipe instead); sums and statistics are fp32.  A row that sees nothing gives
+ * O = 0 and lse = -inf.
  *   q_codes/q_scales  as written by qattn_quantize_qk with k_dtype QATTN_I8
  *                     (the cache's K channel scales folded in)
  *   k_codes, v_codes  int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)
@@ -483,7 +484,8 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales,
 
 /* Bytes of workspace qattn_tree_decode accepts for this shape and parameters,
  * with or without drafts (0: none is needed, or the problem is empty or
- * unsupported).  Host only. */
+ * unsupported).  It does not shrink as Nk grows: one for the cache's capacity
+ * serves every shorter one.  Host only. */
 size_t qattn_tree_workspace_size(const qattn_shape* shape, const qattn_params* params);
 
 /* Append the accepted path of a drafted tree to an int8 KV cache: token

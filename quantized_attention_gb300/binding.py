@@ -394,7 +394,19 @@ _current_raw_stream = torch._C._cuda_getCurrentRawStream  # no Stream object on 
 
 
 def _stream_handle(stream, dev: int) -> int:
-    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _current_raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is one of {stream.device}, not of the current device")
+    return stream.cuda_stream
+
+
+def _workspace_ptr(dev: int, t):
+    if t is None:
+        return None
+    if t.get_device() != dev or not t.is_contiguous():
+        _reject("workspace", t, t.dtype, t.shape, dev)
+    return t.data_ptr()
 
 
 def tree_workspace_size(shape: Shape, params: Params) -> int:
@@ -429,7 +441,7 @@ def tree_decode(q_codes, q_scales, k_codes, v_codes, k_chan_scale, v_chan_scale,
         q, _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc, vc, ks, vs, mu,
         _opt_ptr(dev, "lengths", lengths, i32, (B,)), kn, kst, vn, vst,
         _opt_ptr(dev, "tree_mask", tree_mask, i32, (B, T, (T + 31) // 32)), shape, params, o,
-        _opt_ptr(dev, "lse", lse, f32, (B, Hq, T)), None if workspace is None else workspace.data_ptr(),
+        _opt_ptr(dev, "lse", lse, f32, (B, Hq, T)), _workspace_ptr(dev, workspace),
         _nbytes(workspace), _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_tree_decode")

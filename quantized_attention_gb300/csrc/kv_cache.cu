@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
   const int seen = a.seen ? a.seen[b] : len;
   int n = a.n_accept[b];
   const int32_t* path = a.path + static_cast<size_t>(b) * a.T;
-  bool bad = n < 0 || n > a.T || len < 0 || seen < 0 || len + static_cast<long long>(n) > a.cap;
+  bool bad = n < 0 || n > a.T || len < 0 || seen < 0 || seen > 0x7fffffff - max(n, 0) ||
+             len + static_cast<long long>(n) > a.cap;
   if (!bad)
     for (int t = threadIdx.x; t < n; t += kCommitThreads) bad |= path[t] < 0 || path[t] >= a.T;
   bad = __syncthreads_or(bad);

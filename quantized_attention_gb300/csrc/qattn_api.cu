@@ -1111,7 +1111,8 @@ qattn_status qattn_kv_weights(const int8_t* q_codes, const float* q_scales, cons
   qattn_status st = check_shape(shape);
   if (st != QATTN_OK) return st;
   if ((st = check_params(params)) != QATTN_OK) return st;
-  if (shape->d != 64 && shape->d != 128) return QATTN_ERR_UNSUPPORTED;
+  if ((shape->d != 64 && shape->d != 128) || shape->Hkv > 65535 || shape->B * shape->Hkv > 65535)
+    return QATTN_ERR_UNSUPPORTED;
   if (shape->B == 0 || shape->Nk == 0) return QATTN_OK;
   if (params->kv_capacity != 0 &&
       (params->kv_capacity < shape->Nk || params->kv_capacity > (int64_t{1} << 31)))

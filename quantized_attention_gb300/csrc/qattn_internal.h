@@ -254,7 +254,7 @@ inline int tree_tc_cluster(long long heads, long long steps) {
   int c = heads <= 8 ? kTreeCluster : kTreeCluster / 2;
   while (c > 1 && c * heads > kTreeTcCtas) c /= 2;
   const long long waves = (heads * c + kTreeTcCtas - 1) / kTreeTcCtas;
-  const long long extra = steps * waves / c - heads * steps / kTreeTcCtas;
+  const long long extra = steps * (waves * kTreeTcCtas - heads * c) / (c * kTreeTcCtas);
   return extra <= 13 + heads / 26 ? c : 0;
 }
 struct TreeArgs {

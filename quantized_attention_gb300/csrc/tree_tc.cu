@@ -19,8 +19,9 @@
 // issuing thread (~2100) each nearly fill it; 26-node trees over eight caches of 5K
 // to 32K rows 113 us (floor 47), 64 nodes over 32K 67 (floor 18).  Eight converting
 // warps, two issuing threads, and setmaxnreg with more registers for the softmax
-// measured no faster or slower.  The reference m moves only when a row's maximum has grown by more than 2^8 (P stays
-// below 2^8, far inside fp16), so O is rarely rescaled.
+// measured no faster or slower.
+// The reference m moves only when a row's maximum has grown by more than 2^8 (P
+// stays below 2^8, far inside fp16), so O is rarely rescaled.
 #include <cuda_fp16.h>
 
 #include "qattn_check.cuh"

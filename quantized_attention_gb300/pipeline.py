@@ -303,8 +303,10 @@ class TreeCache:
     k_codes, v_codes: int8 [B, Hkv, capacity, d], the cache; k_scale, v_scale: its
     channel scales and k_mean, v_code_amax: its header, fp32 [B, Hkv, d]; lengths:
     int32 [B], rows in use.  The arrays are used and updated in place; ``evict``
-    moves to a second set of the same capacity and back.  All calls go to the
-    current stream (or ``stream``) and none waits for the GPU."""
+    moves to a second set of the same capacity and back (a captured graph keeps the
+    set it was captured with).  max_rows: bound on the rows in use (default: the
+    capacity).  All calls go to the current stream (or ``stream``) and none waits
+    for the GPU; calls on several streams are ordered by the caller."""
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, k_mean, v_code_amax, lengths, Hq, T, *,
                  out_dtype=qb.DT_BF16, sm_scale=0.0, max_rows=None):
@@ -328,6 +330,7 @@ class TreeCache:
         ws = max(qb.tree_workspace_size(self.shape, self.params), qb.workspace_size(*self._q), 256)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
         self._spare = None
+        self._seen = self._all  # params that say which cached rows the last verify's queries saw
 
     def verify(self, Q, K_new=None, V_new=None, tree_mask=None, stream=None):
         """Attention of the T drafted tokens (Q bf16 [B, Hq, T, d]) over the cache and
@@ -339,6 +342,7 @@ class TreeCache:
                        self.v_scale, self.shape, self.params, self.O, self.lse, self.workspace,
                        lengths=self.lengths, K_new=K_new, V_new=V_new, k_mean=self.k_mean,
                        tree_mask=tree_mask, stream=stream)
+        self._seen = self.params if K_new is None else self._all
         return self.O
 
     def weigh(self, lse=None, stream=None):
@@ -346,7 +350,7 @@ class TreeCache:
         ``lse`` with -inf for the drafts that do not count (the rejected ones).
         Call it before ``commit``: it reads the rows in use then."""
         qb.kv_weights(self.q_codes, self.q_scales, self.k_codes, None, self.lse if lse is None else lse,
-                      self.shape, self._all, self.weights, base=self.weights, lengths=self.lengths,
+                      self.shape, self._seen, self.weights, base=self.weights, lengths=self.lengths,
                       stream=stream)
 
     def commit(self, K_new, V_new, path, n_accept, stream=None):
@@ -358,11 +362,12 @@ class TreeCache:
     def evict(self, budget, n_sink=0, n_recent=0, stream=None):
         """Keep the budget rows of most weight per KV head; returns the kept rows'
         former indices, int32 [B, Hkv, budget]."""
-        if self._spare is None:
-            self._spare = [torch.zeros_like(t) for t in (self.k_codes, self.v_codes, self.weights,
-                                                         self.lengths)]
-        k, v, w, n = self._spare
-        kept = torch.empty((*self.weights.shape[:2], budget), dtype=torch.int32, device=w.device)
+        with torch.cuda.stream(stream):  # what is allocated and filled here belongs to the call's stream
+            if self._spare is None:
+                self._spare = [torch.zeros_like(t) for t in (self.k_codes, self.v_codes, self.weights,
+                                                             self.lengths)]
+            k, v, w, n = self._spare
+            kept = torch.empty((*self.weights.shape[:2], budget), dtype=torch.int32, device=w.device)
         qb.kv_evict(self.k_codes, self.v_codes, self.weights, budget, k, v, w, kept, n,
                     self.v_code_amax, lengths=self.lengths, Nk=self.shape.Nk, n_sink=n_sink,
                     n_recent=n_recent, stream=stream)

@@ -326,6 +326,27 @@ def test_two_streams_and_a_captured_graph(T):
     assert qb.get_error() == 0
 
 
+def test_arguments_elsewhere_are_refused():
+    """Tensors that are not on the current device, the workspace among them."""
+    shape, params = qb.make_shape(1, 8, 1, 4, 20000, 64), qb.make_params(kv_capacity=20000)
+    gpu = [torch.zeros(s, dtype=t, device="cuda") for s, t in (
+        ((1, 8, 4, 64), torch.int8), ((8,), torch.float32), ((1, 1, 20000, 64), torch.int8),
+        ((1, 1, 20000, 64), torch.int8), ((1, 1, 64), torch.float32), ((1, 1, 64), torch.float32))]
+    O, lse = torch.zeros(1, 8, 4, 64, device="cuda"), torch.zeros(1, 8, 4, device="cuda")
+    ws = torch.zeros(qb.tree_workspace_size(shape, params), dtype=torch.uint8)
+    assert ws.numel() > 0
+    with pytest.raises((TypeError, ValueError)):
+        qb.tree_decode(*gpu, shape, params, O, lse, ws)
+    with pytest.raises((TypeError, ValueError)):
+        qb.tree_decode(*gpu, shape, params, O, lse, torch.zeros(2 * ws.numel(), dtype=torch.uint8, device="cuda")[::2])
+    for i in (0, 1, 2, 4):
+        args = [t.cpu() if k == i else t for k, t in enumerate(gpu)]
+        if i == 4:  # k_chan_scale is read for drafts only
+            args[5] = args[5].cpu()
+        with pytest.raises((TypeError, ValueError)):
+            qb.tree_decode(*args, shape, params, O, lse, ws.cuda())
+
+
 # ------------------------------------------------------------------ commit
 @pytest.mark.parametrize("B,Hkv,d,T,n", [(1, 1, 64, 1, [1]), (3, 2, 128, 8, [3, 0, 8]), (2, 12, 128, 40, [1, 17]),
                                          (1, 3, 20, 5, [5])])
@@ -403,3 +424,17 @@ def test_commit_refuses_on_the_device(n, p, L):
     assert lens.tolist() == [L, 2]
     assert torch.equal(gk[0], dev(x["kc"])[0]) and torch.equal(mean[0], dev(x["mean"])[0])
     assert not torch.equal(gk[1, :, 1], dev(x["kc"])[1, :, 1])
+
+
+def test_commit_refuses_a_token_count_past_32_bits():
+    x = make(24, 1, 2, 2, 64, 4, [2], cap=8)
+    seen, lens, mean = dev(np.array([2 ** 31 - 2], np.int32)), dev(x["lens"]), dev(x["mean"])
+    am, gk, gv = torch.zeros(1, 2, 64, device="cuda"), dev(x["kc"]), dev(x["vc"])
+    args = (dev(x["K"], torch.bfloat16), dev(x["V"], torch.bfloat16), dev(np.array([[0, 1, 2, 3]], np.int32)))
+    rest = (dev(x["ks"]), dev(x["vs"]), lens, mean, am, gk, gv)
+    qb.tree_commit(*args, dev(np.array([2], np.int32)), *rest, seen=seen)
+    torch.cuda.synchronize()
+    assert qb.get_error() == qb.ERR_INVALID_ARG and lens.tolist() == [2] and seen.tolist() == [2 ** 31 - 2]
+    qb.tree_commit(*args, dev(np.array([1], np.int32)), *rest, seen=seen)
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0 and lens.tolist() == [3] and seen.tolist() == [2 ** 31 - 1]

@@ -352,3 +352,84 @@ def test_serving_loop():
                     assert np.array_equal(C.k_codes[b, h, :m].cpu().numpy(), old["k_codes"][b, h, rows])
                     assert np.array_equal(C.v_codes[b, h, :m].cpu().numpy(), old["v_codes"][b, h, rows])
     assert evicted and qb.get_error() == 0
+
+
+def tree_cache(rng, B, Hq, Hkv, d, T, cap, lens):
+    code = lambda: np.clip(np.rint(rng.normal(size=(B, Hkv, cap, d)) * 28), -127, 127).astype(np.int8)  # noqa: E731
+    scale = lambda: rng.uniform(0.02, 0.06, (B, Hkv, d)).astype(np.float32)  # noqa: E731
+    return TreeCache(dev(code()), dev(code()), dev(scale()), dev(scale()),
+                     dev(rng.normal(size=(B, Hkv, d)).astype(np.float32)), torch.zeros(B, Hkv, d, device="cuda"),
+                     dev(np.asarray(lens, np.int32)), Hq, T, out_dtype=qb.DT_F32)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_weigh_after_a_verify_without_drafts(T):
+    """Queries whose rows are in the cache already see it causally, and so do their
+    weights: each query hands out 1."""
+    rng = np.random.default_rng(61)
+    B, Hq, Hkv, d, cap, lens = 2, 4, 2, 64, 200, [200, 71]
+    C = tree_cache(rng, B, Hq, Hkv, d, T, cap, lens)
+    C.verify(torch.randn(B, Hq, T, d, device="cuda").to(torch.bfloat16))
+    C.weigh()
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0
+    qc, qs, lse = C.q_codes.cpu().numpy(), C.q_scales.cpu().numpy().reshape(B, Hq), C.lse.double().cpu().numpy()
+    for b, L in enumerate(lens):
+        see = np.arange(L)[None, :] <= L - T + np.arange(T)[:, None]
+        for h in range(Hkv):
+            kk = C.k_codes[b, h, :L].cpu().numpy()
+            want = sum(R.weight(qc[b, hq], np.full(T, qs[b, hq]), kk, np.ones(L), lse[b, hq], see, 1 / np.sqrt(d))[0]
+                       for hq in range(2 * h, 2 * h + 2))
+            got = C.weights[b, h].cpu().numpy().astype(np.float64)
+            # as in the serving loop: relative 2^-14
+            np.testing.assert_allclose(got[:L], want, rtol=2.0 ** -14)
+            assert np.all(got[L:] == 0)
+
+
+def test_steps_on_another_stream_and_in_a_graph():
+    """A step of the loop (verify, weigh, commit, evict) on a side stream, its first
+    eviction's second set allocated there, gives the bits of the same step on the
+    current stream; so does a captured step replayed."""
+    B, Hq, Hkv, d, T, cap, lens = 2, 8, 2, 128, 9, 400, [310, 180]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    Q, K, V = (torch.randn(B, h, T, d, device="cuda", generator=gen).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    path = dev(np.tile(np.arange(T, dtype=np.int32), (B, 1)))
+    n = dev(np.array([4, 9], np.int32))
+
+    def state(C):
+        return [getattr(C, k).clone() for k in ("O", "lse", "k_mean", "v_code_amax", "lengths", "seen")] + [
+            t[b, :, :int(C.lengths[b])].clone() for t in (C.k_codes, C.v_codes, C.weights) for b in range(B)]
+
+    def step(C, evict, stream=None):
+        C.verify(Q, K, V, stream=stream)
+        C.weigh(stream=stream)
+        C.commit(K, V, path, n, stream=stream)
+        return C.evict(100, 2, 20, stream=stream) if evict else None
+
+    fresh = lambda: tree_cache(np.random.default_rng(62), B, Hq, Hkv, d, T, cap, lens)  # noqa: E731
+    A = fresh()
+    kept = step(A, True)
+    torch.cuda.synchronize()
+    want = state(A)
+    S, side = fresh(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.empty(1 << 28, device="cuda").fill_(1.0)  # the current stream is busy meanwhile
+    kept_s = step(S, True, side)
+    side.synchronize()
+    assert torch.equal(kept, kept_s)
+    torch.cuda.synchronize()
+    for x, y in zip(want, state(S)):
+        assert torch.equal(x, y)
+    E, C = fresh(), fresh()
+    step(E, False)
+    step(E, False)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(C, False)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(state(E), state(C)):
+        assert torch.equal(x, y)
+    assert qb.get_error() == 0

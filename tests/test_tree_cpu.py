@@ -71,6 +71,15 @@ def test_tree_workspace(L):
     assert size(1, 8, 2, 128, 10 ** 6, 128) == size(1, 8, 2, 128, 8 * 10 ** 6, 128) < 64 << 20
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,T", [(1, 8, 8, 1), (1, 8, 2, 8), (2, 16, 8, 4), (3, 20, 5, 40), (5, 12, 4, 128),
+                                        (19, 32, 8, 16), (64, 8, 1, 2)])
+def test_tree_workspace_grows_with_the_cache(L, B, Hq, Hkv, T):
+    """A workspace for a cache's capacity serves every shorter one."""
+    sizes = [qb.tree_workspace_size(qb.make_shape(B, Hq, Hkv, T, n, 128), qb.make_params())
+             for n in list(range(0, 40000, 97)) + [10 ** 5, 10 ** 6]]
+    assert sizes == sorted(sizes)
+
+
 def commit(L, B=2, Hkv=2, T=4, d=64, cap=32, **kw):
     names = ("K_new", "k_strides", "V_new", "v_strides", "path", "n_accept")
     rest = ("k_chan_scale", "v_chan_scale", "lengths", "seen", "k_mean", "v_code_amax", "lengths_out", "seen_out",
@@ -106,6 +115,7 @@ def test_weights_refusals(L):
     for n in ("q_codes", "k_codes", "k_scales", "lse", "lengths", "base", "weights"):
         assert weights(L, **{n: ODD}) == INVALID, n
     assert weights(L, shape=(2, 8, 2, 4, 100, 32)) == UNSUPPORTED
+    assert weights(L, shape=(2, 0, 40000, 4, 100, 128)) == UNSUPPORTED  # more KV heads than a grid holds
     assert weights(L, params=qb.make_params(kv_capacity=50)) == INVALID
     assert weights(L, params=qb.make_params(causal=True, q_pos0=1 << 40)) == UNSUPPORTED
     assert weights(L, shape=(0, 8, 2, 4, 100, 128)) == OK and weights(L, shape=(2, 8, 2, 4, 0, 128)) == OK
