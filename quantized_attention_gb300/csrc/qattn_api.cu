@@ -301,7 +301,8 @@ struct TreeSplit {
   bool tc;         // the tensor-core kernel
   int cluster;     // CTAs of a head's own cluster; 0: shares and the join
   int step, blocks, rows, drafts, ctas;
-  int64_t steps;  // of all heads, at most
+  int lead;       // steps that a head's start counts for
+  int64_t steps;  // of all heads with their leads, at most
   size_t slots, off_m, off_l, bytes;
 };
 TreeSplit tree_split(const qattn_shape* s, bool drafts) {
@@ -312,7 +313,8 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.rows = t.tc ? qattn::kTreeTcRows : qattn::kTreeRows;
   t.blocks = static_cast<int>((R + t.rows - 1) / t.rows);
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
-  t.steps = s->B * s->Hkv * t.blocks * (t.drafts + (s->Nk + t.step - 1) / t.step);
+  t.lead = t.tc ? qattn::kTreeTcLead : qattn::kTreeWarpLead;
+  t.steps = s->B * s->Hkv * t.blocks * (t.lead + t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
   const int64_t heads = s->B * s->Hkv * t.blocks, head_steps = t.drafts + (s->Nk + t.step - 1) / t.step;
   t.cluster = t.tc ? qattn::tree_tc_cluster(heads, head_steps) : qattn::tree_cluster(heads, head_steps);
@@ -1016,6 +1018,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   a.lse = lse;
   a.cluster = sp.cluster;
   a.ctas = sp.ctas;
+  a.lead = sp.lead;
   a.slots = sp.slots;
   a.rows_total = static_cast<size_t>(shape->B * shape->Hq * shape->Nq);
   char* w = static_cast<char*>(workspace);
@@ -1033,7 +1036,7 @@ qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales, con
   char sb[128];
   QATTN_LOG_LINE("qattn_tree_decode %s drafts=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb),
                  drafts ? a.T : 0,
-                 sp.tc ? (sp.cluster > 0 ? "tree_tc_kernel (clusters)" : "tree_tc_kernel + tree_join_kernel")
+                 sp.tc ? (sp.cluster > 0 ? "tree_tc_kernel (clusters)" : "tree_tc_kernel + tree_join_rows_kernel")
                        : (sp.cluster > 0 ? "tree_warp_kernel (clusters)" : "tree_warp_kernel + tree_join_kernel"),
                  sp.ctas);
   return from_cuda(sp.tc ? qattn::launch_tree_tc(tk, tv, a, s) : qattn::launch_tree_warp(tk, tv, a, s));

@@ -228,6 +228,7 @@ constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
 constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
 constexpr int kTreeTcCtas = 152;     // its CTAs, at most
 constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
+constexpr int kTreeWarpLead = 0, kTreeTcLead = 6;     // steps that a head's start counts for
 constexpr int kTreeCluster = 8;      // most CTAs of a head in the warp-level kernel's clustered form
 // CTAs of the cluster a head gets to itself: as many (a power of two) as fit one
 // wave of two CTAs an SM.  0 -- equal shares of all heads' steps, joined by a second
@@ -283,6 +284,7 @@ struct TreeArgs {
   int cluster;                   // CTAs of the cluster that has a head to itself: no join, no
                                  // workspace (0: shares of all heads' steps, then the join)
   int ctas;
+  int lead;                      // steps that a head's start counts for in the shares
   size_t slots, rows_total;      // 2 ctas; B Hq T
   float* part_o;                 // [slots][block rows][d]
   float* part_m;                 // [slots][block rows]

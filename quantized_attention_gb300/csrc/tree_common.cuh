@@ -36,13 +36,18 @@ __device__ __forceinline__ int tree_length(const TreeArgs& a, int b) {
 __device__ __forceinline__ int tree_steps(const TreeArgs& a, int len, int step) {
   return a.drafts + (len + step - 1) / step;
 }
+// What they count in the division of the work: the head's start (its drafts' codes,
+// the last head's share written out, pipelines filled again) costs as much as
+// a.lead steps.
+__device__ __forceinline__ int tree_cost(const TreeArgs& a, int steps) { return steps > 0 ? a.lead + steps : 0; }
 
-// A CTA's share of the flattened list of W steps (ordered by sequence, KV head,
-// row block, step; W < 2^31): CTA c of G takes W / G of them, the first W % G
-// CTAs one more.  A segment is a run of the share inside one head.
+// A CTA's share of the flattened list of W places (ordered by sequence, KV head,
+// row block; a head's lead, then its steps; W < 2^31): CTA c of G takes W / G of
+// them, the first W % G CTAs one more.  A segment is a run of steps of the share
+// inside one head.
 struct TreeWalk {
-  int p, end;         // the next step of the share in the list, its end
-  int b, head, s0;    // where p lies: sequence, (KV head, row block), step of the head
+  int p, end;         // the next place of the share in the list, its end
+  int b, head, s0;    // where p lies: sequence, (KV head, row block), place in the head less a.lead
   int len, steps;     // the sequence's rows in use, steps of each of its heads
 };
 
@@ -58,7 +63,7 @@ __device__ __forceinline__ void tree_totals(const TreeArgs& a, int step, int b0,
   const int per = a.Hkv * a.blocks, lane = threadIdx.x & 31;
   total = before = 0;
   for (int b = lane; b < a.B; b += 32) {
-    const int n = per * tree_steps(a, tree_length(a, b), step);
+    const int n = per * tree_cost(a, tree_steps(a, tree_length(a, b), step));
     total += n;
     if (b < b0) before += n;
   }
@@ -81,7 +86,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& a, int step) {
       my_len = len;
       my_n = n;
     }
-    total += per * n;
+    total += per * tree_cost(a, n);
   }
 #pragma unroll
   for (int sh = 16; sh > 0; sh >>= 1) total += __shfl_xor_sync(0xffffffffu, total, sh);
@@ -95,7 +100,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& a, int step) {
       my_len = b0 + lane < a.B ? tree_length(a, b0 + lane) : 0;
       my_n = b0 + lane < a.B ? tree_steps(a, my_len, step) : 0;
     }
-    const int n = b0 + lane < a.B ? per * my_n : 0;
+    const int n = b0 + lane < a.B ? per * tree_cost(a, my_n) : 0;
     int inc = n;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
@@ -109,8 +114,8 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& a, int step) {
       w.b = b0 + l;
       w.len = __shfl_sync(0xffffffffu, my_len, l);
       w.steps = __shfl_sync(0xffffffffu, my_n, l);
-      w.head = off / w.steps;
-      w.s0 = off - w.head * w.steps;
+      w.head = off / (a.lead + w.steps);
+      w.s0 = off - w.head * (a.lead + w.steps) - a.lead;
       break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
@@ -122,7 +127,7 @@ __device__ __forceinline__ TreeWalk tree_walk(const TreeArgs& a, int step) {
 __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk& w, TreeSeg& s) {
   if (w.p >= w.end) return false;
   if (w.s0 == w.steps) {  // the next head; the next sequence that has steps
-    w.s0 = 0;
+    w.s0 = -a.lead;
     if (++w.head == a.Hkv * a.blocks) {
       w.head = 0;
       do {
@@ -136,11 +141,13 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk&
   s.rb = a.blocks == 1 ? 0 : w.head - s.hkv * a.blocks;
   s.len = w.len;
   s.steps = w.steps;
-  s.s0 = w.s0;
-  s.s1 = min(w.s0 + (w.end - w.p), w.steps);
-  w.p += s.s1 - s.s0;
-  w.s0 = s.s1;
-  return true;
+  const int n = min(w.end - w.p, w.steps - w.s0);     // places of this head
+  const int skip = w.s0 < 0 ? min(n, -w.s0) : 0;      // of them in its lead
+  s.s0 = w.s0 + skip;
+  s.s1 = w.s0 + n;
+  w.p += n;
+  w.s0 += n;
+  return skip < n;  // a share that ends in a head's lead holds none of its steps
 }
 
 // The clustered form: this CTA's part of its cluster's head (the segment; possibly
@@ -167,7 +174,7 @@ __device__ __forceinline__ bool tree_once(TreeWalk& w, const TreeSeg& s) {
   return s.s0 < s.s1;
 }
 
-// The CTA whose share holds step x of a list of `total`.
+// The CTA whose share holds place x of a list of `total`.
 __device__ __forceinline__ int tree_owner(int x, int total, int G) {
   const int q = total / G, r = total - q * G, big = r * (q + 1);
   return x < big ? x / (q + 1) : r + (x - big) / q;
@@ -196,14 +203,26 @@ __device__ __forceinline__ uint32_t tree_draft_word(const TreeArgs& a, int b, in
   return a.tree_mask[(static_cast<size_t>(b) * a.T + i) * words + s] & real;
 }
 
-// rint(x / s) clamped to +-127, as a byte.  The quotient by the reciprocal is off
+// rint(x / s) clamped to +-127, as bytes.  The quotient by the reciprocal is off
 // by at most 2 ulp (3e-5 below 128), so it rounds as the IEEE quotient does unless
-// it lies next to a half: those few, and anything not finite, are divided.
-__device__ __forceinline__ uint32_t code_byte(float x, float s, float inv) {
-  const float q = x * inv;
-  float r = rintf(q);
-  if (!(fabsf(q - r) <= 0.4999f)) r = rintf(__fdiv_rn(x, s));
+// it lies next to a half: a word with one of those few, or of anything not finite,
+// is divided.
+__device__ __forceinline__ uint32_t code_byte(float r) {
   return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(r, -127.f), 127.f))) & 0xffu;
+}
+__device__ __forceinline__ uint32_t code_word(float4 x, float4 s, float4 inv) {
+  const float4 q = make_float4(x.x * inv.x, x.y * inv.y, x.z * inv.z, x.w * inv.w);
+  float4 r = make_float4(rintf(q.x), rintf(q.y), rintf(q.z), rintf(q.w));
+  const bool near_half = !(fabsf(q.x - r.x) <= 0.4999f) || !(fabsf(q.y - r.y) <= 0.4999f) ||
+                         !(fabsf(q.z - r.z) <= 0.4999f) || !(fabsf(q.w - r.w) <= 0.4999f);
+  if (near_half)
+    r = make_float4(rintf(__fdiv_rn(x.x, s.x)), rintf(__fdiv_rn(x.y, s.y)), rintf(__fdiv_rn(x.z, s.z)),
+                    rintf(__fdiv_rn(x.w, s.w)));
+  return code_byte(r.x) | code_byte(r.y) << 8 | code_byte(r.z) << 16 | code_byte(r.w) << 24;
+}
+__device__ __forceinline__ float4 bf16x4_to_f32(uint2 x) {
+  return make_float4(bf16_bits_to_f32(x.x & 0xffffu), bf16_bits_to_f32(x.x >> 16), bf16_bits_to_f32(x.y & 0xffffu),
+                     bf16_bits_to_f32(x.y >> 16));
 }
 
 // The codes of drafts j0 .. min(j0 + n, T) - 1 of (b, hkv), as qattn_kv_append
@@ -238,20 +257,19 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
         v[i] = *reinterpret_cast<const uint2*>(V + (j0 + r) * a.vsN);
       }
     }
+    // one copy of the code for all of them: it runs once or twice, and fetching its
+    // instructions would take longer than running them
+#pragma unroll 1
+    for (int r = r0; r < min(rows, r0 + U * dr); r += dr) {
+      float4 x = bf16x4_to_f32(k[0]);
+      x = make_float4(__fsub_rn(x.x, mu.x), __fsub_rn(x.y, mu.y), __fsub_rn(x.z, mu.z), __fsub_rn(x.w, mu.w));
+      *reinterpret_cast<uint32_t*>(k_at(r, w >> 2) + 4 * (w & 3)) = code_word(x, ks, ki);
+      *reinterpret_cast<uint32_t*>(v_at(r, w >> 2) + 4 * (w & 3)) = code_word(bf16x4_to_f32(v[0]), vs, vi);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int r = r0 + i * dr;
-      if (r >= rows) break;
-      const uint32_t kc = code_byte(__fsub_rn(bf16_bits_to_f32(k[i].x & 0xffffu), mu.x), ks.x, ki.x) |
-                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].x >> 16), mu.y), ks.y, ki.y) << 8 |
-                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].y & 0xffffu), mu.z), ks.z, ki.z) << 16 |
-                          code_byte(__fsub_rn(bf16_bits_to_f32(k[i].y >> 16), mu.w), ks.w, ki.w) << 24;
-      const uint32_t vc = code_byte(bf16_bits_to_f32(v[i].x & 0xffffu), vs.x, vi.x) |
-                          code_byte(bf16_bits_to_f32(v[i].x >> 16), vs.y, vi.y) << 8 |
-                          code_byte(bf16_bits_to_f32(v[i].y & 0xffffu), vs.z, vi.z) << 16 |
-                          code_byte(bf16_bits_to_f32(v[i].y >> 16), vs.w, vi.w) << 24;
-      *reinterpret_cast<uint32_t*>(k_at(r, w >> 2) + 4 * (w & 3)) = kc;
-      *reinterpret_cast<uint32_t*>(v_at(r, w >> 2) + 4 * (w & 3)) = vc;
+      for (int i = 0; i + 1 < U; ++i) {
+        k[i] = k[i + 1];
+        v[i] = v[i + 1];
+      }
     }
   }
 }
@@ -283,31 +301,42 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
 }
 
 // Joins the shares of the heads that more than one CTA worked on.  A head's steps
-// are [x0, x0 + n) of the flattened list, so its CTAs are the owners of those
-// steps; CTA c left its share in slot 2 c when the head began before it, else in
-// 2 c + 1.  The attention kernel releases this grid after its own dependency wait,
+// are the places [x0, x0 + n) of the flattened list, so its CTAs are their owners;
+// CTA c left its share in slot 2 c when it did not have the head's first step, else
+// in 2 c + 1.  The attention kernel releases this grid after its own dependency wait,
 // so the lengths are final and the division is known before the shares arrive.
-// NW warps work on a row (one CTA, blockIdx.y the row), or one on each of four rows
-// (NW = 1: few shares a head, many rows); a warp takes every NW-th share: the
-// weights 2^(m_c - m) of 32 shares come first, one a lane, then the shares' rows in
-// independent loads.
-template <int D, int ROWS, int STEP, int NW>
-__global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
-  constexpr int CPL = D / 32;  // channels per lane
-  constexpr int RPC = kTreeJoinThreads / 32 / NW;  // rows of a CTA
-  __shared__ float sm[RPC][NW], sl[RPC][NW];
-  __shared__ __align__(16) float so[RPC][NW][D];
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW, rw = (threadIdx.x >> 5) / NW;
-  const int r = blockIdx.y * RPC + rw;
-  const int rb = blockIdx.x % a.blocks, bkv = blockIdx.x / a.blocks;
-  const int b = bkv / a.Hkv, hkv = bkv % a.Hkv;
-  const bool in = rb * ROWS + r < a.G * a.T;
+struct TreeOwners {
+  int b, hkv, rb;  // the head
+  int steps, c0, c1;
+};
+__device__ __forceinline__ TreeOwners tree_owners(const TreeArgs& a, int step, int head) {
+  TreeOwners o;
+  o.rb = head % a.blocks;
+  head /= a.blocks;
+  o.b = head / a.Hkv;
+  o.hkv = head % a.Hkv;
   int tot, x0;
-  tree_totals(a, STEP, b, tot, x0);
-  const int n = tree_steps(a, tree_length(a, b), STEP);
-  x0 += (hkv * a.blocks + rb) * n;
-  const int c0 = n > 0 ? tree_owner(x0, tot, a.ctas) : 0;
-  const int c1 = n > 0 ? tree_owner(x0 + n - 1, tot, a.ctas) : 0;
+  tree_totals(a, step, o.b, tot, x0);
+  o.steps = tree_steps(a, tree_length(a, o.b), step);
+  x0 += (o.hkv * a.blocks + o.rb) * (a.lead + o.steps) + a.lead;  // the head's first step
+  o.c0 = o.steps > 0 ? tree_owner(x0, tot, a.ctas) : 0;
+  o.c1 = o.steps > 0 ? tree_owner(x0 + o.steps - 1, tot, a.ctas) : 0;
+  return o;
+}
+
+// The join for few rows a head and many shares: a CTA for a row (blockIdx.y), whose
+// four warps take every fourth share: the weights 2^(m_c - m) of 32 shares come
+// first, one a lane, then the shares' rows in independent loads.
+template <int D, int ROWS, int STEP>
+__global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
+  constexpr int NW = kTreeJoinThreads / 32;
+  constexpr int CPL = D / 32;  // channels per lane
+  __shared__ float sm[NW], sl[NW];
+  __shared__ __align__(16) float so[NW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  const TreeOwners own = tree_owners(a, STEP, blockIdx.x);
+  const int b = own.b, hkv = own.hkv, rb = own.rb, n = own.steps, c0 = own.c0, c1 = own.c1;
+  const bool in = rb * ROWS + r < a.G * a.T;
   pdl_wait();
   pdl_trigger();
   if (n == 0) {  // no cached row and no draft: nothing is visible
@@ -360,25 +389,24 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
     }
   }
   if (lane == 0) {
-    sm[rw][warp] = m;
-    sl[rw][warp] = l;
+    sm[warp] = m;
+    sl[warp] = l;
   }
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) so[rw][warp][CPL * lane + k] = o[k];
-  if constexpr (NW > 1) __syncthreads();
-  else __syncwarp();
-  const int c = 4 * (NW > 1 ? static_cast<int>(threadIdx.x) : lane);
+  for (int k = 0; k < CPL; ++k) so[warp][CPL * lane + k] = o[k];
+  __syncthreads();
+  const int c = 4 * static_cast<int>(threadIdx.x);
   if (in && c < D) {
     float mx = kNegInf, lt = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[rw][w]);
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (sm[rw][w] == kNegInf) continue;
-      const float f = ex2_approx(sm[rw][w] - mx);
-      lt = fmaf(f, sl[rw][w], lt);
-      const float4 y = *reinterpret_cast<const float4*>(&so[rw][w][c]);
+      if (sm[w] == kNegInf) continue;
+      const float f = ex2_approx(sm[w] - mx);
+      lt = fmaf(f, sl[w], lt);
+      const float4 y = *reinterpret_cast<const float4*>(&so[w][c]);
       x.x = fmaf(f, y.x, x.x);
       x.y = fmaf(f, y.y, x.y);
       x.z = fmaf(f, y.z, x.z);

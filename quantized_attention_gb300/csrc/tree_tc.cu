@@ -351,15 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (s > sg.s0 && __any_sync(0xffffffffu, mn != m)) {
           const float f = mn == m ? 1.f : al;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t x[32];
-            const uint32_t oc = tmem + lane_base + kTmO + (D / 2) * hf + 32 * c;
-            tmem_ld32(oc, x);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[16];
+            const uint32_t oc = tmem + lane_base + kTmO + (D / 2) * hf + 16 * c;
+            tmem_ld16(oc, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-            tmem_st32(oc, x);
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+            tmem_st16(oc, x);
           }
         }
         tmem_st32(tmem + lane_base + kTmP + 32 * hf, pk);
@@ -381,14 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32];
-        const int ch = (D / 2) * hf + 32 * c;
-        tmem_ld32(tmem + lane_base + kTmO + ch, x);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[16];
+        const int ch = (D / 2) * hf + 16 * c;
+        tmem_ld16(tmem + lane_base + kTmO + ch, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
+        for (int k = 0; k < 16; k += 4) {
           const float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
                                        __uint_as_float(x[k + 3]));
           if constexpr (CL) {  // the raw ring is free: every tile has been converted
@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (whole) {
             tree_write_out<D>(a, sg.b, sg.hkv, rr, ch + k, y, m, l);
           } else if (in && QATTN_IN_BOUNDS(slot < a.slots)) {
-            *reinterpret_cast<float4*>(a.part_o + (slot * kRows + r) * D + ch + k) = y;
+            // chunks of four channels, each for all rows: a warp writes 512 consecutive bytes
+            *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + (ch + k) / 4) * kRows + r) * 4) = y;
           }
         }
       }
@@ -524,6 +525,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The join for 128 rows a head and few shares: a lane for a row, a warp for four
+// channels (blockIdx.y: 32 rows, then 16 channels), so that every load of a share
+// takes 512 consecutive bytes; eight shares' loads in flight.
+template <int D>
+__global__ void __launch_bounds__(kTreeJoinThreads) tree_join_rows_kernel(const TreeArgs a) {
+  constexpr int U = 8;
+  const int r = 32 * (blockIdx.y % 4) + (threadIdx.x & 31);
+  const int c = 4 * (4 * (blockIdx.y / 4) + (threadIdx.x >> 5));
+  const TreeOwners own = tree_owners(a, kStep, blockIdx.x);
+  const int rr = own.rb * kRows + r;
+  const bool in = rr < a.G * a.T;
+  pdl_wait();
+  pdl_trigger();
+  float m = kNegInf, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (own.steps > 0) {  // (else nothing is visible: no cached row and no draft)
+    if (own.c0 == own.c1) return;  // written whole
+    for (int cb = own.c0; cb <= own.c1; cb += U) {
+      float mc[U], lc[U], mn = m;
+      float4 y[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int ci = cb + i;
+        const size_t slot = 2 * static_cast<size_t>(ci) + (ci == own.c0 ? 1 : 0);
+        mc[i] = kNegInf;
+        if (in && ci <= own.c1 && QATTN_IN_BOUNDS(slot < a.slots)) {
+          mc[i] = a.part_m[slot * kRows + r];
+          lc[i] = a.part_l[slot * kRows + r];
+          y[i] = *reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + c / 4) * kRows + r) * 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) mn = fmaxf(mn, mc[i]);
+      if (mn == kNegInf) continue;
+      const float f = m == kNegInf ? 0.f : ex2_approx(m - mn);
+      l *= f;
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (mc[i] == kNegInf) continue;
+        const float w = ex2_approx(mc[i] - mn);
+        l = fmaf(w, lc[i], l);
+        o.x = fmaf(w, y[i].x, o.x);
+        o.y = fmaf(w, y[i].y, o.y);
+        o.z = fmaf(w, y[i].z, o.z);
+        o.w = fmaf(w, y[i].w, o.w);
+      }
+      m = mn;
+    }
+  }
+  tree_write_out<D>(a, own.b, own.hkv, rr, c, o, m, l);
+}
+
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, cudaStream_t s) {
   constexpr int smem = Cfg<D>::kBytes;
@@ -537,8 +591,8 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_tc_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_kernel<D, kRows, kStep, 1>, dim3(a.B * a.Hkv * a.blocks, kRows / 4),
-                    dim3(kTreeJoinThreads), 0, s, a);
+  return launch_pdl(tree_join_rows_kernel<D>, dim3(a.B * a.Hkv * a.blocks, 4 * (D / 16)), dim3(kTreeJoinThreads), 0,
+                    s, a);
 }
 
 }  // namespace

@@ -434,7 +434,7 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_warp_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_kernel<D, kTreeRows, kStep, 4>, dim3(a.B * a.Hkv * a.blocks, kTreeRows),
+  return launch_pdl(tree_join_kernel<D, kTreeRows, kStep>, dim3(a.B * a.Hkv * a.blocks, kTreeRows),
                     dim3(kTreeJoinThreads), 0, s, a);
 }
 
