@@ -313,14 +313,17 @@ TreeSplit tree_split(const qattn_shape* s, bool drafts) {
   t.rows = t.tc ? qattn::kTreeTcRows : qattn::kTreeRows;
   t.blocks = static_cast<int>((R + t.rows - 1) / t.rows);
   t.drafts = drafts ? static_cast<int>((s->Nq + t.step - 1) / t.step) : 0;
-  t.lead = t.tc ? qattn::kTreeTcLead : qattn::kTreeWarpLead;
+  t.lead = t.tc ? qattn::kTreeTcLead : qattn::kTreeWarpLead;  // (shares)
   t.steps = s->B * s->Hkv * t.blocks * (t.lead + t.drafts + (s->Nk + t.step - 1) / t.step);
   const int64_t most = t.tc ? qattn::kTreeTcCtas : qattn::kTreeWarpCtas;
   const int64_t heads = s->B * s->Hkv * t.blocks, head_steps = t.drafts + (s->Nk + t.step - 1) / t.step;
   t.cluster = t.tc ? qattn::tree_tc_cluster(heads, head_steps) : qattn::tree_cluster(heads, head_steps);
   // a step per warp of a CTA of four, or per CTA
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
-  if (t.cluster > 0) t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * t.cluster);
+  if (t.cluster > 0) {
+    t.ctas = static_cast<int>(s->B * s->Hkv * t.blocks * t.cluster);
+    t.lead = !drafts ? 0 : t.tc ? qattn::kTreeTcDraftLead : qattn::kTreeWarpDraftLead;
+  }
   t.slots = t.cluster > 0 ? 0 : 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);

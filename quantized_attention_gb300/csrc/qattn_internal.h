@@ -228,35 +228,44 @@ constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
 constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
 constexpr int kTreeTcCtas = 152;     // its CTAs, at most
 constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
-constexpr int kTreeWarpLead = 0, kTreeTcLead = 6;     // steps that a head's start counts for
-constexpr int kTreeCluster = 8;      // most CTAs of a head in the warp-level kernel's clustered form
-// CTAs of the cluster a head gets to itself: as many (a power of two) as fit one
-// wave of two CTAs an SM.  0 -- equal shares of all heads' steps, joined by a second
-// kernel -- where that leaves SMs idle over long caches.  Measured, clusters against
-// shares, us (d = 128): 8 heads of 2K / 8K / 16K / 32K rows 8.5 / 13.9 / 20.8 / 35.6
-// against 12.5 / 15.3 / 20.1 / 25.7; 16 heads of 16K 27.7 / 22.4; 32 of 8K 20.3 / 24.9;
-// 64 of 16K 50.2 / 54.5; 128 of 2K 20.2 / 25.6, of 100 to 8K 47.7 / 56.4; 256 of 300
-// 11.1 / 18.3; 512 of 1K 39.0 / 45.7.  Twice the CTAs (two waves) loses: 64 heads of 1K
-// 16.3 against 10.2.
+// Steps that a head's start counts for in equal shares (the last head's share joined
+// and written, the drafts' codes, the pipeline filled again) and, its drafts alone, in
+// a cluster.  Shares without and with it: 39.4 and 27.8 us (16 sequences of 0.2 to
+// 4.5K rows, four drafts), 114 and 104 (eight of 5K to 32K, 26).
+constexpr int kTreeWarpLead = 18, kTreeTcLead = 6;
+constexpr int kTreeWarpDraftLead = 5, kTreeTcDraftLead = 3;
+constexpr int kTreeCluster = 8;      // most CTAs of a head's own cluster
+// CTAs of the cluster a head gets to itself in the warp-level kernel: as many (a
+// power of two) as are placed at once, two CTAs an SM (38 clusters of 8 are not: 25
+// us against 18 in shares).  0 -- equal shares of all heads' steps, joined by a
+// second kernel, 2.5 us more of host time -- once the busiest CTA would take 10 steps
+// more than its share (the few-head cases that this would take at 4K gain nothing).
+// Measured, clusters against shares, us (d = 128): 8 heads of 2K / 8K / 32K rows 8.0 /
+// 15.2 / 36.4 against 10.1 / 14.1 / 22.7; 16 of 4K / 8K / 16K 12.8 / 18.0 / 28.2 against
+// 14.0 / 18.0 / 22.3; 32 of 8K / 16K 20.9 / 30.9 against 21.9 / 31.7; 64 of 4K 20.8 / 22.3,
+// of 5K to 32K 71.7 / 59.4; 128 of 2K 21.2 / 26.1, of 100 to 4K 27.9 / 25.7, to 8K 47.5 /
+// 36.5; 256 of 300 / 2K 15.1 / 32.9 against 21.5 / 39.6.
 inline int tree_cluster(long long heads, long long steps) {
-  int c = kTreeCluster;
-  while (c > 1 && c * heads > kTreeWarpCtas) c /= 2;
-  return c * heads >= 256 || steps <= 384 ? c : 0;
+  const int c = heads <= 32 ? kTreeCluster : heads <= kTreeWarpCtas / 4 ? 4 : heads <= kTreeWarpCtas / 2 ? 2 : 1;
+  const long long waves = (heads * c + kTreeWarpCtas - 1) / kTreeWarpCtas;
+  const long long extra = steps * (waves * kTreeWarpCtas - heads * c) / (c * kTreeWarpCtas);
+  return extra <= 10 + 80 / heads ? c : 0;
 }
 // The same for the tensor-core kernel (heads: KV heads x row blocks; one CTA an SM).
-// Clusters of 8 are taken for 8 heads at most (16 of them are not placed at once: 105
-// us against 89 in fours).  Equal shares cost a plan and a join, ~18 us of a step's
-// 1.4: they pay once the busiest CTA of a cluster would take 13 steps more than its
-// share.  Measured, clusters against shares, us (d = 128): 8 heads of 300 / 8K / 32K
-// rows 13.5 / 24.3 / 51.9 against 16.4 / 37.5 / 50.5; 16 of 8K / 32K 33.5 / 89.4
-// against 40.1 / 67.2; 32 of 8K 36.2 / 45.7; 64 of 5K to 32K 164 / 113; 128 of 2K 35.8 /
-// 51.8, of 100 to 4K 54 / 115; 256 of 2K 65 / 88.
+// The chip places 32 clusters of 4 at once and 8 of 8, not as many as its SMs would
+// hold (38 in fours: 44 us against 29 in shares).  Equal shares cost a plan, a join
+// and kTreeTcLead steps (of 1.3 us) a head: they pay once the busiest CTA of a
+// cluster would take so many steps more than its share.  Measured, clusters against
+// shares, us (d = 128): 8 heads of 2K / 8K / 32K rows 16.5 / 23.8 / 50.8 against 16.7 /
+// 22.1 / 35.3; 16 of 1K / 4K / 16K 14.7 / 22.3 / 49.0 against 15.9 / 20.5 / 33.8; 32 of
+// 4K / 8K / 16K 23.7 / 32.9 / 51.1 against 25.8 / 34.8 / 51.2; 64 of 4K 33.5 / 40.9, of 5K
+// to 32K 126 / 105; 128 of 2K 35.1 / 52.6, of 100 to 4K 50.5 / 55.7, to 8K 85.2 / 76.7;
+// 256 of 2K 68.5 / 89.1.
 inline int tree_tc_cluster(long long heads, long long steps) {
-  int c = heads <= 8 ? kTreeCluster : kTreeCluster / 2;
-  while (c > 1 && c * heads > kTreeTcCtas) c /= 2;
+  const int c = heads <= 8 ? kTreeCluster : heads <= 32 ? 4 : heads <= kTreeTcCtas / 2 ? 2 : 1;
   const long long waves = (heads * c + kTreeTcCtas - 1) / kTreeTcCtas;
   const long long extra = steps * (waves * kTreeTcCtas - heads * c) / (c * kTreeTcCtas);
-  return extra <= 13 + heads / 26 ? c : 0;
+  return extra <= 3 + heads / 20 ? c : 0;
 }
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use
@@ -284,7 +293,7 @@ struct TreeArgs {
   int cluster;                   // CTAs of the cluster that has a head to itself: no join, no
                                  // workspace (0: shares of all heads' steps, then the join)
   int ctas;
-  int lead;                      // steps that a head's start counts for in the shares
+  int lead;                      // steps that a head's start counts for in the division
   size_t slots, rows_total;      // 2 ctas; B Hq T
   float* part_o;                 // [slots][block rows][d]
   float* part_m;                 // [slots][block rows]

@@ -141,6 +141,8 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk&
   s.rb = a.blocks == 1 ? 0 : w.head - s.hkv * a.blocks;
   s.len = w.len;
   s.steps = w.steps;
+  // (With s0 = max(s0, 0) and s1 = max(min(..), 0) nvcc 13.0 took a caller's
+  // s0 == 0 && s1 == steps for s0 == 0.)
   const int n = min(w.end - w.p, w.steps - w.s0);     // places of this head
   const int skip = w.s0 < 0 ? min(n, -w.s0) : 0;      // of them in its lead
   s.s0 = w.s0 + skip;
@@ -151,7 +153,7 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk&
 }
 
 // The clustered form: this CTA's part of its cluster's head (the segment; possibly
-// no step), and a walk that yields it once.
+// no step: s0 == s1), and a walk that yields it once.
 __device__ __forceinline__ TreeWalk tree_cluster_walk(const TreeArgs& a, int step, TreeSeg& s) {
   const int rank = static_cast<int>(cluster_rank());
   int head = blockIdx.x / a.cluster;
@@ -161,11 +163,14 @@ __device__ __forceinline__ TreeWalk tree_cluster_walk(const TreeArgs& a, int ste
   s.b = head / a.Hkv;
   s.len = tree_length(a, s.b);
   s.steps = tree_steps(a, s.len, step);
-  const int q = s.steps / a.cluster, r = s.steps - q * a.cluster;
-  s.s0 = rank * q + min(rank, r);
-  s.s1 = s.s0 + q + (rank < r ? 1 : 0);
+  const int total = tree_cost(a, s.steps);  // places: the lead, then the steps
+  const int q = total / a.cluster, r = total - q * a.cluster;
+  const int p = rank * q + min(rank, r) - a.lead, n = q + (rank < r ? 1 : 0);
+  const int skip = p < 0 ? min(n, -p) : 0;
+  s.s0 = p + skip;
+  s.s1 = p + n;
   TreeWalk w{};
-  w.end = s.s1 - s.s0;
+  w.end = n - skip;
   return w;
 }
 __device__ __forceinline__ bool tree_once(TreeWalk& w, const TreeSeg& s) {

@@ -17,7 +17,8 @@
 // cycles a step, because the converting warps (~1050 a tile, two a step: waits,
 // 180 instructions a thread, the proxy fence), the softmax warps (~2300) and the one
 // issuing thread (~2100) each nearly fill it; 26-node trees over eight caches of 5K
-// to 32K rows 113 us (floor 47), 64 nodes over 32K 67 (floor 18).  Eight converting
+// to 32K rows 104 us (floor 47), 64 nodes over 32K 53 (floor 18; 37 of it the steps, 6
+// up to the first scores, 5 the join and its launch).  Eight converting
 // warps, two issuing threads, and setmaxnreg with more registers for the softmax
 // measured no faster or slower.
 // The reference m moves only when a row's maximum has grown by more than 2^8 (P

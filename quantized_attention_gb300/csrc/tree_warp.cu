@@ -15,9 +15,9 @@
 // (int8 -> exact fp16, ~10 instructions per 8 codes) and multiplied by
 // mma.m16n8k16: at 16 rows a 128-key tile costs ~510 tensor cycles and ~400
 // issue cycles of an SM against ~1460 cycles of its share of HBM.  Measured: one
-// token over 4K rows of 8 KV heads 10.2 us (launch, first tiles and the cluster's
-// join; floor 1.3), four tokens for 16 sequences of 0.2 to 4.5K rows 31.5 us = 2.5
-// TB/s (floor 11.8; moving the codes without multiplying them takes 26).
+// token over 4K rows of 8 KV heads 9.5 us (launch, first tiles and the cluster's
+// join; floor 1.3), four tokens for 16 sequences of 0.2 to 4.5K rows 27.7 us = 2.8
+// TB/s (floor 11.8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
