@@ -8,11 +8,6 @@
 namespace qattn {
 namespace {
 
-// A 32-bit word of another CTA's shared memory (the same offset as `p` here).
-__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
-  return ld_cluster_u32(cluster_addr(smem_u32(p), rank));
-}
-
 // ------------------------------------------------------------------ commit
 // One cluster per sequence, one thread per (KV head, channel): the accepted
 // tokens pass in order, each quantized against the running mean of the tokens
@@ -79,14 +74,17 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
 // each CTA holds the ordered keys of a contiguous slice of rows in shared memory
 // (re-read from global memory where a slice does not fit); four rounds of 8-bit
 // histograms, summed over the cluster through distributed shared memory, give the
-// budget-th largest key exactly; the rows above it and the first of its ties are
-// kept, in row order, at positions from a prefix sum over the slices.  Then the
+// budget-th largest key exactly, and with it how many rows of the slices before this
+// one lie above it or tie with it; the rows above it and the first of its ties are
+// kept, in row order, at positions from a prefix sum.  (Three rounds of 11 bits read
+// 64 KB of other CTAs' counts each: 22.9 us for 8 heads of 32K rows against 18.4.)  Then the
 // cluster copies the kept rows, each CTA an equal share of the output, 16 bytes a
 // thread, the V codes' channel maxima on the way.  The weights are read once, the
 // kept rows read and written once; a short cache is bound by the rounds' barriers
 // (~1 us each), a long one by the copy.  Measured: 128 heads of ~2K rows cut to 1999
-// (d = 64) 18.3 us = 3.7 TB/s, 8 heads of 32K cut to 4K 18.5 us (64 CTAs); two kernels
-// (select, gather) took 79 and 23.
+// (d = 64) 17.7 us = 3.8 TB/s, 8 heads of 32K cut to 4K 16.2 us (64 CTAs; 17.3 with all
+// weights equal); two kernels (select, gather) took 79 and 23, counting with one
+// addition per distinct bin of a warp 18.5 and 17.5.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -121,8 +119,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
   extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[2][kBins];          // this CTA's counts of a round, alternating
   __shared__ uint32_t wsum[2][kEvictWarps];
-  __shared__ uint32_t pick[2][2];              // a round's bin, rows still wanted in it
-  __shared__ uint32_t mine[2];                 // this slice's rows above / at the threshold
+  __shared__ uint32_t pick[2][4];              // a round's bin, the rows still wanted in it; of the
+                                               // slices before: rows above the bin, rows in it
   __shared__ uint4 red[kEvictWarps][LPR];
   const int NC = a.cluster;
   const uint32_t rank = NC > 1 ? cluster_rank() : 0u;
@@ -156,26 +154,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
 
   uint32_t prefix = 0, left = want;  // the threshold's leading bits; rows wanted among its ties
   const bool all = want == len;      // nothing to choose: every row is above the threshold
+  uint32_t gt0 = all ? r0 : 0, eq0 = 0;  // rows of the slices before above / at the threshold
 #pragma unroll 1
   for (int round = 0; round < 4 && !all; ++round) {
     const int shift = 24 - 8 * round;
     const uint32_t high = round == 0 ? 0u : (0xffffffffu << (shift + 8));
     uint32_t* h = hist[round & 1];
-    for (int i0 = 0; i0 < nr; i0 += kEvictThreads) {
-      const int i = i0 + threadIdx.x;
-      const uint32_t k = i < nr ? key(i) : 0u;
-      const bool live = i < nr && (k & high) == prefix;
-      const uint32_t act = __ballot_sync(0xffffffffu, live);
-      if (live) {  // one addition per distinct bin of the warp
-        const uint32_t bin = (k >> shift) & 255u;
-        const uint32_t same = __match_any_sync(act, bin);
-        if (lane == __ffs(same) - 1) atomicAdd(&h[bin], __popc(same));
-      }
-      __syncwarp();
+    for (int i = threadIdx.x; i < nr; i += kEvictThreads) {
+      const uint32_t k = key(i);
+      if ((k & high) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1u);
     }
     sync();  // the cluster's counts are in
-    // thread i < 256: bin 255 - i, counted from the top
-    uint32_t c = 0;
+    // thread i < 256: bin 255 - i, counted from the top: c, and p in the slices before
+    uint32_t c = 0, p = 0;
     if (threadIdx.x < kBins) {
       hist[(round + 1) & 1][threadIdx.x] = 0u;  // last read a round ago, behind a barrier
       const uint32_t addr = smem_u32(&h[kBins - 1 - threadIdx.x]);
@@ -183,32 +174,49 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         c = h[kBins - 1 - threadIdx.x];
       } else {
 #pragma unroll 8
-        for (int q = 0; q < NC; ++q) c += ld_cluster_u32(cluster_addr(addr, q));
+        for (uint32_t q = 0; q < static_cast<uint32_t>(NC); ++q) {
+          const uint32_t x = ld_cluster_u32(cluster_addr(addr, q));
+          c += x;
+          p += q < rank ? x : 0u;
+        }
       }
     }
-    uint32_t inc = c;
+    uint32_t inc = c, pinc = p;
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, sh);
-      if (lane >= sh) inc += o;
+      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, sh), po = __shfl_up_sync(0xffffffffu, pinc, sh);
+      if (lane >= sh) {
+        inc += o;
+        pinc += po;
+      }
     }
-    if (lane == 31) wsum[0][warp] = inc;
+    if (lane == 31) {
+      wsum[0][warp] = inc;
+      wsum[1][warp] = pinc;
+    }
     __syncthreads();
     if (threadIdx.x < kBins) {
-      uint32_t before = inc - c;
-      for (int q = 0; q < warp; ++q) before += wsum[0][q];
+      uint32_t before = inc - c, pbefore = pinc - p;
+      for (int q = 0; q < warp; ++q) {
+        before += wsum[0][q];
+        pbefore += wsum[1][q];
+      }
       if (before < left && before + c >= left) {
         pick[round & 1][0] = kBins - 1 - threadIdx.x;
         pick[round & 1][1] = left - before;
+        pick[round & 1][2] = pbefore;
+        pick[round & 1][3] = p;
       }
     }
     __syncthreads();
     prefix |= pick[round & 1][0] << shift;
     left = pick[round & 1][1];
+    gt0 += pick[round & 1][2];
+    eq0 = pick[round & 1][3];
   }
   // keep keys above the threshold, and the first `left` of its ties
   const uint32_t thr = all ? 0u : prefix;  // (no key is 0: the lowest is that of -inf)
-  if (all) left = 0;
+  if (all) left = 0;  // (eq0 is 0)
 
   // each thread owns a run of consecutive rows (an odd length: no bank conflicts)
   const int run = ((nr + kEvictThreads - 1) / kEvictThreads) | 1;
@@ -244,19 +252,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
       se += oe;
     }
   }
-  uint32_t pg = __shfl_sync(0xffffffffu, sg - vg, warp) + ig - gt;
-  uint32_t pe = __shfl_sync(0xffffffffu, se - ve, warp) + ie - eq;
-  if (threadIdx.x == kEvictThreads - 1) {
-    mine[0] = sg;
-    mine[1] = se;
-  }
-  if (NC > 1) {
-    cluster_sync();
-    for (uint32_t q = 0; q < rank; ++q) {
-      pg += ld_cluster(&mine[0], q);
-      pe += ld_cluster(&mine[1], q);
-    }
-  }
+  uint32_t pg = gt0 + __shfl_sync(0xffffffffu, sg - vg, warp) + ig - gt;
+  uint32_t pe = eq0 + __shfl_sync(0xffffffffu, se - ve, warp) + ie - eq;
   int32_t* kept = a.kept + static_cast<size_t>(bkv) * a.budget;
   float* wo = a.weights_out + static_cast<size_t>(bkv) * a.out_cap;
   for (int i = i0; i < i1; ++i) {
