@@ -469,7 +469,7 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
  *   workspace         at least qattn_tree_workspace_size() bytes; calls that may
  *                     overlap need one each
  * Limits: d in {64, 128}, Nq <= 128, fewer than 2^31 steps of work (of 32 keys x
- * 16 rows or 128 x 128).  A length outside 0 .. Nk is clamped and
+ * 16 rows or 128 x 128; a head's start counts as up to 18).  A length outside 0 .. Nk is clamped and
  * reported: qattn_get_error() returns QATTN_ERR_INVALID_ARG.
  */
 qattn_status qattn_tree_decode(const int8_t* q_codes, const float* q_scales,
