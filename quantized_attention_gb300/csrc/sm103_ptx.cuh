@@ -254,6 +254,18 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 }
 // Arrives (once) on the mbarrier when every tcgen05 operation this thread
 // issued before it has completed.
+// True in one thread of a whole warp.  A role that issues MMAs branches on this rather
+// than on a lane's number: ptxas then knows that one thread is left (the operands'
+// moves to uniform registers cost 4% of the tree kernel otherwise).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)

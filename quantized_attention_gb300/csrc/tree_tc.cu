@@ -17,7 +17,7 @@
 // cycles a step, because the converting warps (~1050 a tile, two a step: waits,
 // 180 instructions a thread, the proxy fence), the softmax warps (~2300) and the one
 // issuing thread (~2100) each nearly fill it; 26-node trees over eight caches of 5K
-// to 32K rows 104 us (floor 47), 64 nodes over 32K 53 (floor 18; 37 of it the steps, 6
+// to 32K rows 94 us (floor 47), 64 nodes over 32K 49 (floor 18; 33 of it the steps, 6
 // up to the first scores, 5 the join and its launch).  Eight converting
 // warps, two issuing threads, setmaxnreg with more registers for the softmax, and
 // softmax groups that take steps in turn (a thread a row) measured no faster or slower.
@@ -58,17 +58,15 @@ enum {
   kRawFull = 0,    // [kRaw] TMA bytes (a drafted step: the loader's arrival)
   kRawEmpty = 6,   // [kRaw] 128 converting threads
   kKFull = 12,     // [2] 128
-  kKEmpty = 14,    // [2] the step's QK MMAs
-  kVFull = 16,     // [2] 128
-  kVEmpty = 18,    // [2] the step's PV MMAs
+  kVFull = 14,     // [2] 128
+  kSFull = 16,     // [2] the step's QK MMAs: S is there, K16 is free
+  kPvDone = 18,    // [2] the step's PV MMAs: O and P are free, and V16
   kQReady = 20,    // 128 threads wrote Q
-  kSFull = 21,     // [2] QK MMAs
-  kPReady = 23,    // 256
-  kPvDone = 24,    // PV MMAs
-  kXFull = 25,     // [2 buffers][4 quadrants] 64
-  kDrafts = 33,    // kEncode threads wrote a drafted step's codes
-  kDrain = 34,
-  kNumBars = 35
+  kPReady = 21,    // 256
+  kXFull = 22,     // [2 buffers][4 quadrants] 64
+  kDrafts = 30,    // kEncode threads wrote a drafted step's codes
+  kDrain = 31,
+  kNumBars = 32
 };
 
 // Place of 16-byte chunk c of row r of a CTA's O in shared memory (a thread writes a
@@ -181,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ MMA
       constexpr uint32_t idesc_qk = make_idesc(kRows, kStep, 0, 0);
       constexpr uint32_t idesc_pv = make_idesc(kRows, D, 0, 0) | kIdescBMnMajor;
@@ -199,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_f16_ts(tmem + kTmS + 128 * st, tmem + kTmQ + 8 * k, kd + ((k / 4) * (kStep * 128) + 32 * (k % 4)) / 16,
                      idesc_qk, k > 0 ? 1u : 0u);
         mma_commit(bar(kSFull + st));
-        mma_commit(bar(kKEmpty + st));
         return true;
       };
       for (; ok && next_segment(); ++seg) {
@@ -216,8 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kStep / 16; ++k)
             mma_f16_ts(tmem + kTmO, tmem + kTmP + 8 * k, vd + (k * 2048) / 16, idesc_pv,
                        (j > 0 || k > 0) ? 1u : 0u);
-          mma_commit(bar(kPvDone));
-          mma_commit(bar(kVEmpty + st));
+          mma_commit(bar(kPvDone + st));
         }
       }
       mma_commit(bar(kDrain));
@@ -343,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * (mn == m ? 1.f : al) + ((s0.x + s0.y) + (s1.x + s1.y));
         // ---- O and P belong to the previous step's PV until it is done
         if (it > 0) {
-          ok = wait(kPvDone, it - 1);
+          ok = wait(kPvDone + ((it - 1) & 1), (it - 1) >> 1);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -374,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l_other;
       if (!(ok = exchange(l, l_other))) break;
       l += l_other;
-      ok = wait(kPvDone, it - 1);
+      ok = wait(kPvDone + ((it - 1) & 1), (it - 1) >> 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
@@ -464,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait(kRawFull + slot, lap))) break;
             load(slot);
           }
-          if (it >= 2 && !(ok = wait((kv ? kVEmpty : kKEmpty) + st, (it >> 1) - 1))) break;
+          if (it >= 2 && !(ok = wait((kv ? kPvDone : kSFull) + st, (it >> 1) - 1))) break;
           convert(kv ? v16(st) : k16(st));
           mbar_arrive(bar(kRawEmpty + slot));
           if (++slot == kRaw) {
