@@ -329,16 +329,17 @@ __device__ __forceinline__ TreeOwners tree_owners(const TreeArgs& a, int step, i
   return o;
 }
 
-// The join for few rows a head and many shares: a CTA for a row (blockIdx.y), whose
-// four warps take every fourth share: the weights 2^(m_c - m) of 32 shares come
-// first, one a lane, then the shares' rows in independent loads.
-template <int D, int ROWS, int STEP>
+// The join for few rows a head: NW warps for a row (blockIdx.y: 4 / NW rows), which
+// take every NW-th share: the weights 2^(m_c - m) of 32 shares come first, one a
+// lane, then the shares' rows in independent loads.
+template <int D, int ROWS, int STEP, int NW>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
-  constexpr int NW = kTreeJoinThreads / 32;
   constexpr int CPL = D / 32;  // channels per lane
-  __shared__ float sm[NW], sl[NW];
-  __shared__ __align__(16) float so[NW][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+  constexpr int RPC = kTreeJoinThreads / 32 / NW;  // rows of a CTA
+  __shared__ float sm[RPC][NW], sl[RPC][NW];
+  __shared__ __align__(16) float so[RPC][NW][D];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW, rw = (threadIdx.x >> 5) / NW;
+  const int r = blockIdx.y * RPC + rw;
   const TreeOwners own = tree_owners(a, STEP, blockIdx.x);
   const int b = own.b, hkv = own.hkv, rb = own.rb, n = own.steps, c0 = own.c0, c1 = own.c1;
   const bool in = rb * ROWS + r < a.G * a.T;
@@ -394,24 +395,25 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
     }
   }
   if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    sm[rw][warp] = m;
+    sl[rw][warp] = l;
   }
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) so[warp][CPL * lane + k] = o[k];
-  __syncthreads();
-  const int c = 4 * static_cast<int>(threadIdx.x);
+  for (int k = 0; k < CPL; ++k) so[rw][warp][CPL * lane + k] = o[k];
+  if constexpr (NW > 1) __syncthreads();
+  else __syncwarp();
+  const int c = 4 * (NW > 1 ? static_cast<int>(threadIdx.x) : lane);
   if (in && c < D) {
     float mx = kNegInf, lt = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w]);
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[rw][w]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (sm[w] == kNegInf) continue;
-      const float f = ex2_approx(sm[w] - mx);
-      lt = fmaf(f, sl[w], lt);
-      const float4 y = *reinterpret_cast<const float4*>(&so[w][c]);
+      if (sm[rw][w] == kNegInf) continue;
+      const float f = ex2_approx(sm[rw][w] - mx);
+      lt = fmaf(f, sl[rw][w], lt);
+      const float4 y = *reinterpret_cast<const float4*>(&so[rw][w][c]);
       x.x = fmaf(f, y.x, x.x);
       x.y = fmaf(f, y.y, x.y);
       x.z = fmaf(f, y.z, x.z);

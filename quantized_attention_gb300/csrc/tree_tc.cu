@@ -13,14 +13,16 @@
 // fp16 into TMEM, O += P V16 (V16 as it lies: the B operand with its N index
 // fastest).  Q and P in TMEM leave shared memory to the codes: 32 KB in, 32 KB
 // read, 64 KB of fp16 written and 64 KB read by the MMAs a step, ~1540 cycles
-// against ~1460 of the step's share of HBM and ~1030 of tensor work.  Measured: ~2500
-// cycles a step, because the converting warps (~1050 a tile, two a step: waits,
-// 180 instructions a thread, the proxy fence), the softmax warps (~2300) and the one
-// issuing thread (~2100) each nearly fill it; 26-node trees over eight caches of 5K
+// against ~1460 of the step's share of HBM and ~1030 of tensor work.  Measured: ~2250
+// cycles a step: the converting warps (~1050 a tile, two a step: 180 instructions a
+// thread, the proxy fence) and the softmax warps (scores 480, the halves' maxima
+// exchanged 300, exponentials 810, the last PV 380, P 130, loop 140) each nearly fill
+// it, and the issuing thread's K16 comes late; 26-node trees over eight caches of 5K
 // to 32K rows 94 us (floor 47), 64 nodes over 32K 49 (floor 18; 33 of it the steps, 6
-// up to the first scores, 5 the join and its launch).  Eight converting
-// warps, two issuing threads, setmaxnreg with more registers for the softmax, and
-// softmax groups that take steps in turn (a thread a row) measured no faster or slower.
+// up to the first scores, 5 the join and its launch).  Six or eight converting warps,
+// two issuing threads, PV ahead of the next QK, setmaxnreg with more registers for the
+// softmax, and softmax groups that take steps in turn (a thread a row) measured no
+// faster or slower.
 // The reference m moves only when a row's maximum has grown by more than 2^8 (P
 // stays below 2^8, far inside fp16), so O is rarely rescaled.
 #include <cuda_fp16.h>

@@ -16,7 +16,7 @@
 // mma.m16n8k16: at 16 rows a 128-key tile costs ~510 tensor cycles and ~400
 // issue cycles of an SM against ~1460 cycles of its share of HBM.  Measured: one
 // token over 4K rows of 8 KV heads 9.5 us (launch, first tiles and the cluster's
-// join; floor 1.3), four tokens for 16 sequences of 0.2 to 4.5K rows 27.7 us = 2.8
+// join; floor 1.3), four tokens for 16 sequences of 0.2 to 4.5K rows 26.7 us = 2.9
 // TB/s (floor 11.8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,6 +32,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kTreeWarpStep;  // keys per warp step
+// Shares a head, on average, from which four warps join a row.  One against four warps,
+// us: 2.4 shares 26.7 / 27.6 (16 sequences of 0.2 to 4.5K rows), 4.8 shares 61.5 / 59.5
+// (64 heads of 5K to 32K), 38 shares 31.3 / 22.5 (8 heads of 32K).
+constexpr int kJoinShares = 4;
 constexpr int kRing = 3;   // stages of a warp's ring (K and V of one step each)
 
 template <int D>
@@ -434,8 +438,12 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_warp_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_kernel<D, kTreeRows, kStep>, dim3(a.B * a.Hkv * a.blocks, kTreeRows),
-                    dim3(kTreeJoinThreads), 0, s, a);
+  // a head in few shares: a warp for a row
+  const int heads = a.B * a.Hkv * a.blocks;
+  if (a.ctas < kJoinShares * heads)
+    return launch_pdl(tree_join_kernel<D, kTreeRows, kStep, 1>, dim3(heads, kTreeRows / 4), dim3(kTreeJoinThreads), 0,
+                      s, a);
+  return launch_pdl(tree_join_kernel<D, kTreeRows, kStep, 4>, dim3(heads, kTreeRows), dim3(kTreeJoinThreads), 0, s, a);
 }
 
 }  // namespace
