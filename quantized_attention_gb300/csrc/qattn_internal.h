@@ -249,23 +249,25 @@ inline int tree_cluster(long long heads, long long steps) {
   const int c = heads <= 32 ? kTreeCluster : heads <= kTreeWarpCtas / 4 ? 4 : heads <= kTreeWarpCtas / 2 ? 2 : 1;
   const long long waves = (heads * c + kTreeWarpCtas - 1) / kTreeWarpCtas;
   const long long extra = steps * (waves * kTreeWarpCtas - heads * c) / (c * kTreeWarpCtas);
-  return extra <= 10 + 80 / heads ? c : 0;
+  return extra <= 10 + (heads < 8 ? 10 : 80 / heads) ? c : 0;
 }
 // The same for the tensor-core kernel (heads: KV heads x row blocks; one CTA an SM).
 // The chip places 32 clusters of 4 at once and 8 of 8, not as many as its SMs would
 // hold (38 in fours: 44 us against 29 in shares).  Equal shares cost a plan, a join
-// and kTreeTcLead steps (of 1.3 us) a head: they pay once the busiest CTA of a
-// cluster would take so many steps more than its share.  Measured, clusters against
-// shares, us (d = 128): 8 heads of 2K / 8K / 32K rows 16.5 / 23.8 / 50.8 against 16.7 /
-// 22.1 / 35.3; 16 of 1K / 4K / 16K 14.7 / 22.3 / 49.0 against 15.9 / 20.5 / 33.8; 32 of
-// 4K / 8K / 16K 23.7 / 32.9 / 51.1 against 25.8 / 34.8 / 51.2; 64 of 4K 33.5 / 40.9, of 5K
-// to 32K 126 / 105; 128 of 2K 35.1 / 52.6, of 100 to 4K 50.5 / 55.7, to 8K 85.2 / 76.7;
-// 256 of 2K 68.5 / 89.1.
+// and kTreeTcLead steps (of 1.2 us) a head: they pay once the busiest CTA of a
+// cluster would take so many steps more than its share (few for up to 12 heads, whose
+// rows four warps join).  Measured, clusters against shares, us (d = 128): one head of
+// 2K / 8K / 32K rows 14.7 / 19.3 / 44.9 against 11.3 / 12.6 / 22.5; 4 of 8K 19.8 / 17.1; 8
+// of 2K / 8K / 32K 15.5 / 20.9 / 46.5 against 14.6 / 18.7 / 29.9; 16 of 4K / 8K / 16K 19.3 /
+// 27.9 / 45.0 against 20.3 / 24.0 / 30.9; 32 of 4K / 8K / 16K 20.3 / 28.8 / 46.9 against
+// 24.1 / 31.0 / 44.6; 64 of 4K 30.5 / 35.6, of 5K to 32K 119 / 89; 128 of 2K 33.8 / 44.7, of
+// 100 to 4K 48.6 / 51.5, to 8K 81.8 / 68.0; 256 of 2K 66.0 / 74.3.
 inline int tree_tc_cluster(long long heads, long long steps) {
   const int c = heads <= 8 ? kTreeCluster : heads <= 32 ? 4 : heads <= kTreeTcCtas / 2 ? 2 : 1;
   const long long waves = (heads * c + kTreeTcCtas - 1) / kTreeTcCtas;
   const long long extra = steps * (waves * kTreeTcCtas - heads * c) / (c * kTreeTcCtas);
-  return extra <= 3 + heads / 20 ? c : 0;
+  const long long most = heads <= 12 ? 1 : heads < 25 ? 4 : 3 + heads / 25;
+  return extra <= most ? c : 0;
 }
 struct TreeArgs {
   int B, Hq, Hkv, G, T, Nk, d;   // G = Hq / Hkv; Nk: most rows in use

@@ -41,6 +41,10 @@ static_assert(kStep == 128 && kRows == 128, "one TMEM lane per row, one block of
 constexpr int kThreads = 512;
 constexpr int kRaw = 6;      // raw ring: K and V tiles of codes, one after the other
 constexpr int kEncode = 384; // threads that encode a drafted step: softmax and converting warps
+// Shares a head, on average, from which four warps join a row.  One against four warps,
+// us: 9.5 shares (16 heads of 16K rows) 30.9 / 32.3, 19 (8 of 8K) 21.7 / 18.7, 152 (one of
+// 32K) 44.1 / 22.5.
+constexpr int kJoinShares = 12;
 constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;  // TMEM columns
 
@@ -524,14 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The join for 128 rows a head and few shares: a lane for a row, a warp for four
-// channels (blockIdx.y: 32 rows, then 16 channels), so that every load of a share
-// takes 512 consecutive bytes; eight shares' loads in flight.
-template <int D>
+// The join for 128 rows a head: a lane for a row, a warp for four channels of it and
+// every SW-th share (blockIdx.y: 32 rows, then 16 / SW channels), so that every load of
+// a share takes 512 consecutive bytes; eight shares' loads in flight.
+template <int D, int SW>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_rows_kernel(const TreeArgs a) {
-  constexpr int U = 8;
-  const int r = 32 * (blockIdx.y % 4) + (threadIdx.x & 31);
-  const int c = 4 * (4 * (blockIdx.y / 4) + (threadIdx.x >> 5));
+  constexpr int U = 8, W = kTreeJoinThreads / 32;
+  __shared__ float part[SW > 1 ? 6 : 1][W][32];  // m, l and the channels of a warp's shares
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sw = warp % SW;
+  const int r = 32 * (blockIdx.y % 4) + lane;
+  const int c = 4 * ((W / SW) * (blockIdx.y / 4) + warp / SW);
   const TreeOwners own = tree_owners(a, kStep, blockIdx.x);
   const int rr = own.rb * kRows + r;
   const bool in = rr < a.G * a.T;
@@ -539,14 +545,25 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_rows_kernel(const 
   pdl_trigger();
   float m = kNegInf, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto scale = [&](float f) {
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  };
+  auto add = [&](float w, float lw, float4 y) {
+    l = fmaf(w, lw, l);
+    o.x = fmaf(w, y.x, o.x);
+    o.y = fmaf(w, y.y, o.y);
+    o.z = fmaf(w, y.z, o.z);
+    o.w = fmaf(w, y.w, o.w);
+  };
   if (own.steps > 0) {  // (else nothing is visible: no cached row and no draft)
     if (own.c0 == own.c1) return;  // written whole
-    for (int cb = own.c0; cb <= own.c1; cb += U) {
+    for (int cb = own.c0 + sw; cb <= own.c1; cb += SW * U) {
       float mc[U], lc[U], mn = m;
       float4 y[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int ci = cb + i;
+        const int ci = cb + SW * i;
         const size_t slot = 2 * static_cast<size_t>(ci) + (ci == own.c0 ? 1 : 0);
         mc[i] = kNegInf;
         if (in && ci <= own.c1 && QATTN_IN_BOUNDS(slot < a.slots)) {
@@ -558,18 +575,31 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_rows_kernel(const 
 #pragma unroll
       for (int i = 0; i < U; ++i) mn = fmaxf(mn, mc[i]);
       if (mn == kNegInf) continue;
-      const float f = m == kNegInf ? 0.f : ex2_approx(m - mn);
-      l *= f;
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      scale(m == kNegInf ? 0.f : ex2_approx(m - mn));
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (mc[i] == kNegInf) continue;
-        const float w = ex2_approx(mc[i] - mn);
-        l = fmaf(w, lc[i], l);
-        o.x = fmaf(w, y[i].x, o.x);
-        o.y = fmaf(w, y[i].y, o.y);
-        o.z = fmaf(w, y[i].z, o.z);
-        o.w = fmaf(w, y[i].w, o.w);
+      for (int i = 0; i < U; ++i)
+        if (mc[i] != kNegInf) add(ex2_approx(mc[i] - mn), lc[i], y[i]);
+      m = mn;
+    }
+  }
+  if constexpr (SW > 1) {
+    const float mine[6] = {m, l, o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int k = 0; k < 6; ++k) part[k][warp][lane] = mine[k];
+    __syncthreads();
+    if (sw != 0) return;
+    float mn = m;
+#pragma unroll
+    for (int i = 1; i < SW; ++i) mn = fmaxf(mn, part[0][warp + i][lane]);
+    if (mn != kNegInf) {
+      scale(m == kNegInf ? 0.f : ex2_approx(m - mn));
+#pragma unroll
+      for (int i = 1; i < SW; ++i) {
+        const float mw = part[0][warp + i][lane];
+        if (mw != kNegInf)
+          add(ex2_approx(mw - mn), part[1][warp + i][lane],
+              make_float4(part[2][warp + i][lane], part[3][warp + i][lane], part[4][warp + i][lane],
+                          part[5][warp + i][lane]));
       }
       m = mn;
     }
@@ -590,8 +620,10 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   if (e != cudaSuccess) return e;
   e = launch_pdl(tree_tc_kernel<D, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_join_rows_kernel<D>, dim3(a.B * a.Hkv * a.blocks, 4 * (D / 16)), dim3(kTreeJoinThreads), 0,
-                    s, a);
+  const int heads = a.B * a.Hkv * a.blocks;
+  if (a.ctas < kJoinShares * heads)
+    return launch_pdl(tree_join_rows_kernel<D, 1>, dim3(heads, 4 * (D / 16)), dim3(kTreeJoinThreads), 0, s, a);
+  return launch_pdl(tree_join_rows_kernel<D, 4>, dim3(heads, 4 * (D / 4)), dim3(kTreeJoinThreads), 0, s, a);
 }
 
 }  // namespace
