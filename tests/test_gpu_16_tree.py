@@ -207,7 +207,10 @@ def test_granules_and_unused_lengths(T):
 
 
 @pytest.mark.parametrize("T,d,lens", [(1, 128, [20011]), (48, 128, [20011]), (3, 64, [700, 16111, 0]),
-                                      (30, 64, [11, 33333, 0, 20000])])
+                                      (30, 64, [11, 33333, 0, 20000]),
+                                      # many heads, few shares each
+                                      (30, 64, [9000, 11, 4000, 0, 700, 8999, 5000]), (48, 128, [9000, 300, 8000, 1]),
+                                      (4, 64, [(613 * i * i) % 4101 for i in range(40)])])
 def test_tree_decode_long_split(T, d, lens):
     """Long caches in equal shares over every CTA, and their result bit for bit
     whatever the workspace held."""
