@@ -346,7 +346,7 @@ def kv_header_init(v_codes, Nk, v_code_amax, stream=None):
 
 
 def _reject(name: str, t, dtype, shape, dev: int):
-    """Says what is wrong with an argument that failed the tests of _ptrs."""
+    """Says what is wrong with an argument that failed a test of the functions below."""
     if t is None:
         raise ValueError(f"{name} is missing")
     if tuple(t.shape) != tuple(shape):
@@ -355,22 +355,15 @@ def _reject(name: str, t, dtype, shape, dev: int):
     raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _ptrs(dev: int, need: int, *args) -> list:
-    """The addresses of dense tensors of these types and shapes on the current CUDA
-    device `dev`, whose kernels and stream the call uses: (name, tensor, dtype,
-    shape) each, the first `need` of them required, the others None where not
-    given.  A serving step makes these calls between kernels of a few
-    microseconds, so a good argument costs one line of tests."""
-    out = []
-    for name, t, dtype, shape in args:
-        if t is None and len(out) >= need:
-            out.append(None)
-            continue
-        if (t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev
-                or not t.is_contiguous()):
-            _reject(name, t, dtype, shape, dev)
-        out.append(t.data_ptr())
-    return out
+def _ptr(name: str, t, dtype, shape, dev: int) -> int:
+    """The address of a dense tensor of this type and shape on the current CUDA
+    device `dev`, whose kernels and stream the call uses.  A serving step makes its
+    calls between kernels of a few microseconds, so a good argument costs one line
+    of tests."""
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _reject(name, t, dtype, shape, dev)
 
 
 def _input_ptr(dev: int, name: str, t, shape):
@@ -425,26 +418,26 @@ def tree_decode(q_codes, q_scales, k_codes, v_codes, k_chan_scale, v_chan_scale,
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
     dev = torch.cuda.current_device()
     head, cache, rows = (B, Hkv, d), (B, Hkv, params.kv_capacity or Nk, d), (B, Hq, T, d)
-    out = torch.bfloat16 if params.out_dtype == DT_BF16 else f32
     kn = kst = vn = vst = None
     if K_new is not None or V_new is not None:
         if K_new is None or V_new is None:
             raise ValueError("K_new and V_new go together")
         kn, kst = _input_ptr(dev, "K_new", K_new, (B, Hkv, T, d))
         vn, vst = _input_ptr(dev, "V_new", V_new, (B, Hkv, T, d))
-    else:
-        k_chan_scale = k_mean = None  # not read
-    need = 3 if Nk == 0 and k_codes is None else 5 if kn is None else 7
-    q, vs, o, kc, vc, ks, mu, ln, tm, ls = _ptrs(
-        dev, need, ("q_codes", q_codes, i8, rows),
-        ("v_chan_scale", v_chan_scale, f32, head), ("O", O, out, rows), ("k_codes", k_codes, i8, cache),
-        ("v_codes", v_codes, i8, cache), ("k_chan_scale", k_chan_scale, f32, head),
-        ("k_mean", k_mean, f32, head), ("lengths", lengths, i32, (B,)),
-        ("tree_mask", tree_mask, i32, (B, T, (T + 31) // 32)), ("lse", lse, f32, (B, Hq, T)))
+    kc = vc = ks = mu = None
+    if Nk > 0 or k_codes is not None:
+        kc, vc = _ptr("k_codes", k_codes, i8, cache, dev), _ptr("v_codes", v_codes, i8, cache, dev)
+    if kn is not None:  # (not read otherwise)
+        ks, mu = _ptr("k_chan_scale", k_chan_scale, f32, head, dev), _ptr("k_mean", k_mean, f32, head, dev)
     st = lib().qattn_tree_decode(
-        q, _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc, vc, ks, vs, mu, ln, kn, kst,
-        vn, vst, tm, shape, params, o, ls, _workspace_ptr(dev, workspace), _nbytes(workspace),
-        _stream_handle(stream, dev))
+        _ptr("q_codes", q_codes, i8, rows, dev),
+        _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc, vc, ks,
+        _ptr("v_chan_scale", v_chan_scale, f32, head, dev), mu,
+        None if lengths is None else _ptr("lengths", lengths, i32, (B,), dev), kn, kst, vn, vst,
+        None if tree_mask is None else _ptr("tree_mask", tree_mask, i32, (B, T, (T + 31) // 32), dev), shape, params,
+        _ptr("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else f32, rows, dev),
+        None if lse is None else _ptr("lse", lse, f32, (B, Hq, T), dev), _workspace_ptr(dev, workspace),
+        _nbytes(workspace), _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_tree_decode")
 
@@ -460,19 +453,20 @@ def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, length
     cap, i8, f32, i32 = k_codes.shape[2], torch.int8, torch.float32, torch.int32
     dev = torch.cuda.current_device()
     head, cache, seqs = (B, Hkv, d), (B, Hkv, cap, d), (B,)
-    pp, pn, pl, pks, pvs, pm, pa, pkc, pvc, plo, pmo, pao, ps, pso, pw = _ptrs(
-        dev, 9, ("path", path, i32, (B, T)), ("n_accept", n_accept, i32, seqs), ("lengths", lengths, i32, seqs),
-        ("k_chan_scale", k_chan_scale, f32, head), ("v_chan_scale", v_chan_scale, f32, head),
-        ("k_mean", k_mean, f32, head), ("v_code_amax", v_code_amax, f32, head),
-        ("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache), ("lengths_out", lengths_out, i32, seqs),
-        ("k_mean_out", k_mean_out, f32, head), ("v_code_amax_out", v_code_amax_out, f32, head),
-        ("seen", seen, i32, seqs), ("seen_out", seen_out, i32, seqs), ("weights", weights, f32, (B, Hkv, cap)))
+    pl, ps = _ptr("lengths", lengths, i32, seqs, dev), None if seen is None else _ptr("seen", seen, i32, seqs, dev)
+    pm, pa = _ptr("k_mean", k_mean, f32, head, dev), _ptr("v_code_amax", v_code_amax, f32, head, dev)
     kn, kst = _input_ptr(dev, "K_new", K_new, shape)
     vn, vst = _input_ptr(dev, "V_new", V_new, shape)
     st = lib().qattn_tree_commit(
-        kn, kst, vn, vst, pp, pn, B, Hkv, T, d, cap, pks, pvs, pl, ps, pm, pa, pl if lengths_out is None else plo,
-        ps if seen_out is None else pso, pm if k_mean_out is None else pmo, pa if v_code_amax_out is None else pao,
-        pw, pkc, pvc, _stream_handle(stream, dev))
+        kn, kst, vn, vst, _ptr("path", path, i32, (B, T), dev), _ptr("n_accept", n_accept, i32, seqs, dev), B, Hkv, T,
+        d, cap, _ptr("k_chan_scale", k_chan_scale, f32, head, dev), _ptr("v_chan_scale", v_chan_scale, f32, head, dev),
+        pl, ps, pm, pa, pl if lengths_out is None else _ptr("lengths_out", lengths_out, i32, seqs, dev),
+        ps if seen_out is None else _ptr("seen_out", seen_out, i32, seqs, dev),
+        pm if k_mean_out is None else _ptr("k_mean_out", k_mean_out, f32, head, dev),
+        pa if v_code_amax_out is None else _ptr("v_code_amax_out", v_code_amax_out, f32, head, dev),
+        None if weights is None else _ptr("weights", weights, f32, (B, Hkv, cap), dev),
+        _ptr("k_codes", k_codes, i8, cache, dev), _ptr("v_codes", v_codes, i8, cache, dev),
+        _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_tree_commit")
 
@@ -485,14 +479,16 @@ def kv_weights(q_codes, q_scales, k_codes, k_scales, lse, shape, params, weights
     B, Hq, Hkv, T, d, Nk = shape.B, shape.Hq, shape.Hkv, shape.Nq, shape.d, shape.Nk
     cap, i8, f32 = params.kv_capacity or Nk, torch.int8, torch.float32
     dev = torch.cuda.current_device()
-    q, kc, pl, w, ln, pb = _ptrs(
-        dev, 4, ("q_codes", q_codes, i8, (B, Hq, T, d)), ("k_codes", k_codes, i8, (B, Hkv, cap, d)),
-        ("lse", lse, f32, (B, Hq, T)), ("weights", weights, f32, (B, Hkv, cap)),
-        ("lengths", lengths, torch.int32, (B,)), ("base", base, f32, (B, Hkv, cap)))
+    cache = (B, Hkv, cap)
     st = lib().qattn_kv_weights(
-        q, _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T), kc,
-        None if k_scales is None else _scales_ptr(dev, "k_scales", k_scales, params.k_gran, B, Hkv, Nk), pl,
-        ln, shape, params, pb, w, _stream_handle(stream, dev))
+        _ptr("q_codes", q_codes, i8, (B, Hq, T, d), dev),
+        _scales_ptr(dev, "q_scales", q_scales, params.q_gran, B, Hq, T),
+        _ptr("k_codes", k_codes, i8, (B, Hkv, cap, d), dev),
+        None if k_scales is None else _scales_ptr(dev, "k_scales", k_scales, params.k_gran, B, Hkv, Nk),
+        _ptr("lse", lse, f32, (B, Hq, T), dev),
+        None if lengths is None else _ptr("lengths", lengths, torch.int32, (B,), dev), shape, params,
+        None if base is None else _ptr("base", base, f32, cache, dev), _ptr("weights", weights, f32, cache, dev),
+        _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_kv_weights")
 
@@ -506,15 +502,14 @@ def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept,
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
     dev = torch.cuda.current_device()
     out = (B, Hkv, ocap, d)
-    kc, vc, w, ko, vo, wo, kp, lo, am, ln = _ptrs(
-        dev, 9, ("k_codes", k_codes, i8, cache), ("v_codes", v_codes, i8, cache),
-        ("weights", weights, f32, (B, Hkv, cap)), ("k_out", k_out, i8, out), ("v_out", v_out, i8, out),
-        ("weights_out", weights_out, f32, (B, Hkv, ocap)), ("kept", kept, i32, (B, Hkv, budget)),
-        ("lengths_out", lengths_out, i32, (B,)), ("v_code_amax", v_code_amax, f32, (B, Hkv, d)),
-        ("lengths", lengths, i32, (B,)))
-    st = lib().qattn_kv_evict(kc, vc, w, ln, B, Hkv, Nk, d, cap,
-                              budget, int(n_sink), int(n_recent), ko, vo, ocap, wo, kp, lo, am,
-                              _stream_handle(stream, dev))
+    st = lib().qattn_kv_evict(
+        _ptr("k_codes", k_codes, i8, cache, dev), _ptr("v_codes", v_codes, i8, cache, dev),
+        _ptr("weights", weights, f32, (B, Hkv, cap), dev),
+        None if lengths is None else _ptr("lengths", lengths, i32, (B,), dev), B, Hkv, Nk, d, cap, budget, int(n_sink),
+        int(n_recent), _ptr("k_out", k_out, i8, out, dev), _ptr("v_out", v_out, i8, out, dev), ocap,
+        _ptr("weights_out", weights_out, f32, (B, Hkv, ocap), dev), _ptr("kept", kept, i32, (B, Hkv, budget), dev),
+        _ptr("lengths_out", lengths_out, i32, (B,), dev), _ptr("v_code_amax", v_code_amax, f32, (B, Hkv, d), dev),
+        _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_kv_evict")
 
