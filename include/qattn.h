@@ -441,12 +441,15 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
  * accepted path.  Per query row, over its visible keys:
  *   t = S * c,  S the exact int32 score of the codes,
  *       c = fp32(fp32(sq * sm_scale) * log2 e)
- *   O = v_chan_scale * sum 2^(t - m) vc / sum 2^(t - m),  m the running max;
+ *   O = v_chan_scale * sum 2^(t - m) vc / sum 2^(t - m),  m a reference near the
+ *       row's maximum;
  *       lse = natural log of sum e^(t ln 2)
- * The PV product takes P = 2^(t - m) rounded to fp16 (m a running maximum, at most
- * 8 behind: P <= 2^8) and the V codes as they are (qattn_decode follows the e4m3
- * recipe instead); sums and statistics are fp32.  A row that sees nothing gives
- * O = 0 and lse = -inf.
+ * The PV product takes P = 2^(t - m) rounded to fp16 and the V codes as they are
+ * (qattn_decode follows the e4m3 recipe instead); sums and statistics are fp32.  m
+ * lies 15 (more than 16 rows Hq / Hkv * T: 7, and up to 15) below the running
+ * maximum, so that a key down to 2^-29 (2^-21) of the row's largest is off by at
+ * most 2^-11, further down by at most 2^-40 (2^-32) of the largest.  A row that sees
+ * nothing gives O = 0 and lse = -inf.
  *   q_codes/q_scales  as written by qattn_quantize_qk with k_dtype QATTN_I8
  *                     (the cache's K channel scales folded in)
  *   k_codes, v_codes  int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)

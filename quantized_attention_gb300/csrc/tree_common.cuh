@@ -193,6 +193,14 @@ __device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq) {
   return c == 0.f ? 1e-30f : c;
 }
 
+// The exponentials' reference lies below a row's largest t, so that P = 2^(t - m) in
+// fp16 uses the type's range above 1 too: P of a key keeps its 11 bits as long as it is
+// not 2^(14 + head) times smaller than the row's largest.  (P <= 2^15 with every lag of
+// the reference.)  From |t| = 2^20 on, where the difference would round, it is t itself:
+// there the scores are so coarse that the largest alone counts.
+constexpr float kFarScore = 1048576.f;
+__device__ __forceinline__ float tree_head(float top, float head) { return fabsf(top) < kFarScore ? head : 0.f; }
+
 // Cached rows visible to token i: all of them, or (tokens already appended,
 // causal) those up to its own.
 __device__ __forceinline__ int tree_limit(const TreeArgs& a, int len, int i) {
@@ -280,8 +288,10 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
 }
 
 // Four channels c.. of row rr (query head of the group, token) of (b, hkv):
-// O = x s_v / l, 0 for a row that sees nothing; the row's lse with channel 0.
-template <int D>
+// O = x s_v / l, 0 for a row that sees nothing; the row's lse with channel 0.  HEAD: how
+// far the reference m lies below the row's largest t (both shifted back before the
+// logarithm, so that a sum of about 2^HEAD costs lse no bits).
+template <int D, int HEAD>
 __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv, int rr, int c,
                                                float4 x, float m, float l) {
   if (rr >= a.G * a.T) return;
@@ -302,7 +312,8 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
   } else {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * D + c) = x;
   }
-  if (a.lse && c == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : kNegInf;
+  if (a.lse && c == 0)
+    a.lse[row] = l > 0.f ? ((m + HEAD) + log2f(l * (1.f / (1 << HEAD)))) * kLn2 : kNegInf;
 }
 
 // Joins the shares of the heads that more than one CTA worked on.  A head's steps
@@ -332,7 +343,7 @@ __device__ __forceinline__ TreeOwners tree_owners(const TreeArgs& a, int step, i
 // The join for few rows a head: NW warps for a row (blockIdx.y: 4 / NW rows), which
 // take every NW-th share: the weights 2^(m_c - m) of 32 shares come first, one a
 // lane, then the shares' rows in independent loads.
-template <int D, int ROWS, int STEP, int NW>
+template <int D, int HEAD, int ROWS, int STEP, int NW>
 __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeArgs a) {
   constexpr int CPL = D / 32;  // channels per lane
   constexpr int RPC = kTreeJoinThreads / 32 / NW;  // rows of a CTA
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
   pdl_trigger();
   if (n == 0) {  // no cached row and no draft: nothing is visible
     if (in && warp == 0 && lane < D / 4)
-      tree_write_out<D>(a, b, hkv, rb * ROWS + r, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f);
+      tree_write_out<D, HEAD>(a, b, hkv, rb * ROWS + r, 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f);
     return;
   }
   if (c0 == c1) return;  // written whole
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
       x.z = fmaf(f, y.z, x.z);
       x.w = fmaf(f, y.w, x.w);
     }
-    tree_write_out<D>(a, b, hkv, rb * ROWS + r, c, x, mx, lt);
+    tree_write_out<D, HEAD>(a, b, hkv, rb * ROWS + r, c, x, mx, lt);
   }
 }
 

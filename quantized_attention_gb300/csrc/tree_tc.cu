@@ -23,8 +23,10 @@
 // two issuing threads, PV ahead of the next QK, setmaxnreg with more registers for the
 // softmax, and softmax groups that take steps in turn (a thread a row) measured no
 // faster or slower.
-// The reference m moves only when a row's maximum has grown by more than 2^8 (P
-// stays below 2^8, far inside fp16), so O is rarely rescaled.
+// The reference m is set 7 below a row's maximum and moves only when that has grown by
+// another 8 (P stays at or below 2^15, inside fp16), so O is rarely rescaled: a key down
+// to 2^-21 of the row's largest (14.5 nats) is off by at most 2^-11, further down by at
+// most 2^-32 of the largest.
 #include <cuda_fp16.h>
 
 #include "qattn_check.cuh"
@@ -45,7 +47,9 @@ constexpr int kEncode = 384; // threads that encode a drafted step: softmax and 
 // us: 9.5 shares (16 heads of 16K rows) 30.9 / 32.3, 19 (8 of 8K) 21.7 / 18.7, 152 (one of
 // 32K) 44.1 / 22.5.
 constexpr int kJoinShares = 12;
+constexpr int kHead = 7;      // of the exponentials' reference (tree_head)
 constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
+static_assert(kHead + kLazy <= 15.f, "P stays inside fp16");
 constexpr uint32_t kTmS = 0, kTmO = 256, kTmP = 384, kTmQ = 448;  // TMEM columns
 
 template <int D>
@@ -319,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = exchange(mx, other))) break;
         mx = fmaxf(mx, other);
         // max S c = c max S (c > 0); a row that sees nothing stays at -inf
-        const float top = mx * cf;
-        const float mn = top > m + kLazy || m == kNegInf ? top : m;
+        const float top = mx * cf, head = tree_head(top, kHead);
+        const float mn = top > m + (head == 0.f ? 0.f : kHead + kLazy) || m == kNegInf ? top - head : m;
         const float ref = mn == kNegInf ? 0.f : mn;
         const float2 c2 = make_float2(cf, cf), n2 = make_float2(-ref, -ref);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CL) {  // the raw ring is free: every tile has been converted
             *reinterpret_cast<float4*>(smem + 4 * (r * D) + 16 * share_chunk(r, (ch + k) / 4)) = y;
           } else if (whole) {
-            tree_write_out<D>(a, sg.b, sg.hkv, rr, ch + k, y, m, l);
+            tree_write_out<D, kHead>(a, sg.b, sg.hkv, rr, ch + k, y, m, l);
           } else if (in && QATTN_IN_BOUNDS(slot < a.slots)) {
             // chunks of four channels, each for all rows: a warp writes 512 consecutive bytes
             *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + (ch + k) / 4) * kRows + r) * 4) = y;
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.z = fmaf(f, y[q].z, x.z);
         x.w = fmaf(f, y[q].w, x.w);
       }
-      tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kRows + r, c, x, mx, lt);
+      tree_write_out<D, kHead>(a, sg.b, sg.hkv, sg.rb * kRows + r, c, x, mx, lt);
     }
     cluster_sync();  // no CTA leaves while another reads its share
   }
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_rows_kernel(const 
       m = mn;
     }
   }
-  tree_write_out<D>(a, own.b, own.hkv, rr, c, o, m, l);
+  tree_write_out<D, kHead>(a, own.b, own.hkv, rr, c, o, m, l);
 }
 
 template <int D>

@@ -7,8 +7,10 @@
 // keys P = 2^(t - m) with m a running maximum, l = sum P, O = sum P v; the
 // parts of a head (steps of 32 keys dealt to warps, shares of steps dealt to
 // CTAs) are joined by 2^(m_part - m).  P is rounded once, to fp16, for the PV
-// product (11 bits of a number <= 1: half the step of the bf16 output at the
-// most, and independent from key to key); l sums the unrounded P in fp32.
+// product; l sums the unrounded P in fp32.  m lies 15 below the running maximum, so P
+// fills fp16's range: a key down to 2^-29 of the row's largest (20 nats) is off by at
+// most 2^-11, a quarter of the step of the bf16 output, independently from key to key;
+// further down by at most 2^-40 of the largest.
 //
 // What bounds it: the cache's bytes, 2 D per key and KV head.  The rows of one
 // KV head are few, so the codes are converted in registers as they are used
@@ -32,6 +34,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kTreeWarpStep;  // keys per warp step
+constexpr int kHead = 15;             // of the exponentials' reference (tree_head)
 // Shares a head, on average, from which four warps join a row.  One against four warps,
 // us: 2.4 shares 26.7 / 27.6 (16 sequences of 0.2 to 4.5K rows), 4.8 shares 61.5 / 59.5
 // (64 heads of 5K to 32K), 38 shares 31.3 / 22.5 (8 heads of 32K).
@@ -216,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 4; ++e)
             if (!((vis[e >> 1] >> (8 * j + 2 * t4 + (e & 1))) & 1u)) s[j][e] = kNegInf;
       }
-      // running maxima: max S c = c max S (c > 0); -inf stays -inf
+      // running maxima less kHead: max S c = c max S (c > 0); -inf stays -inf
       float al[2], ref[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -225,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; j < 4; ++j) x = fmax3(x, s[j][2 * h], s[j][2 * h + 1]);
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = fmaxf(m[h], x * cf[h]);
+        const float top = x * cf[h];
+        const float mn = fmaxf(m[h], top - tree_head(top, kHead));
         ref[h] = (mn == kNegInf) ? 0.f : mn;
         al[h] = (m[h] == kNegInf) ? 0.f : ex2_approx(m[h] - ref[h]);
         m[h] = mn;
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           cl_l[r] = lt;
         }
       } else if (whole) {
-        tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
+        tree_write_out<D, kHead>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
       } else if (QATTN_IN_BOUNDS(slot < a.slots)) {
         *reinterpret_cast<float4*>(a.part_o + (slot * kTreeRows + r) * D + c) = x;
         if (c == 0) {
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         x.z = fmaf(f, y[q].z, x.z);
         x.w = fmaf(f, y[q].w, x.w);
       }
-      tree_write_out<D>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
+      tree_write_out<D, kHead>(a, sg.b, sg.hkv, sg.rb * kTreeRows + r, c, x, mx, lt);
     }
     cluster_sync();  // no CTA leaves while another reads its share
   }
@@ -441,9 +445,10 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArg
   // a head in few shares: a warp for a row
   const int heads = a.B * a.Hkv * a.blocks;
   if (a.ctas < kJoinShares * heads)
-    return launch_pdl(tree_join_kernel<D, kTreeRows, kStep, 1>, dim3(heads, kTreeRows / 4), dim3(kTreeJoinThreads), 0,
-                      s, a);
-  return launch_pdl(tree_join_kernel<D, kTreeRows, kStep, 4>, dim3(heads, kTreeRows), dim3(kTreeJoinThreads), 0, s, a);
+    return launch_pdl(tree_join_kernel<D, kHead, kTreeRows, kStep, 1>, dim3(heads, kTreeRows / 4),
+                      dim3(kTreeJoinThreads), 0, s, a);
+  return launch_pdl(tree_join_kernel<D, kHead, kTreeRows, kStep, 4>, dim3(heads, kTreeRows), dim3(kTreeJoinThreads), 0,
+                    s, a);
 }
 
 }  // namespace
