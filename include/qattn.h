@@ -449,7 +449,8 @@ qattn_status qattn_kv_header_init(const int8_t* v_codes, int64_t B, int64_t Hkv,
  * lies 15 (more than 16 rows Hq / Hkv * T: 7, and up to 15) below the running
  * maximum, so that a key down to 2^-29 (2^-21) of the row's largest is off by at
  * most 2^-11, further down by at most 2^-40 (2^-32) of the largest.  A row that sees
- * nothing gives O = 0 and lse = -inf.
+ * nothing gives O = 0 and lse = -inf, whatever its scale; one that sees keys through
+ * a scale that is not finite gives NaN for both.
  *   q_codes/q_scales  as written by qattn_quantize_qk with k_dtype QATTN_I8
  *                     (the cache's K channel scales folded in)
  *   k_codes, v_codes  int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)

@@ -186,11 +186,18 @@ __device__ __forceinline__ int tree_owner(int x, int total, int G) {
 }
 // c = fp32(fp32(sq * sm_scale) * log2 e) of a query head's tokens (T <= 128: one
 // scale block).  A factor of 0 (all the head's codes 0) becomes 1e-30: 2^(S c) is
-// 1 all the same for every |S| < 2^21, and a hidden key's -inf stays -inf.
-__device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq) {
+// 1 all the same for every |S| < 2^21, and a hidden key's -inf stays -inf.  So does
+// one that is not finite, for the sake of the row's hidden keys; tree_sum makes up for it.
+__device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq, bool& finite) {
   const float sq = a.q_gran == 0 ? a.q_scales[0] : a.q_scales[b * a.Hq + hq];
   const float c = __fmul_rn(__fmul_rn(sq, a.sm_scale), kLog2e);
-  return c == 0.f ? 1e-30f : c;
+  finite = fabsf(c) < -kNegInf;
+  return c == 0.f || !finite ? 1e-30f : c;
+}
+// A share's sum of P: NaN if its row saw keys through a factor that is not finite (and
+// with it O and lse, through every join).
+__device__ __forceinline__ float tree_sum(float l, bool finite) {
+  return l > 0.f && !finite ? __int_as_float(0x7fffffff) : l;
 }
 
 // The exponentials' reference lies below a row's largest t, so that P = 2^(t - m) in
@@ -288,9 +295,9 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
 }
 
 // Four channels c.. of row rr (query head of the group, token) of (b, hkv):
-// O = x s_v / l, 0 for a row that sees nothing; the row's lse with channel 0.  HEAD: how
-// far the reference m lies below the row's largest t (both shifted back before the
-// logarithm, so that a sum of about 2^HEAD costs lse no bits).
+// O = x s_v / l, 0 for a row that sees nothing (l = 0), NaN if l is; the row's lse with
+// channel 0.  HEAD: how far the reference m lies below the row's largest t (both shifted
+// back before the logarithm, so that a sum of about 2^HEAD costs lse no bits).
 template <int D, int HEAD>
 __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv, int rr, int c,
                                                float4 x, float m, float l) {
@@ -300,7 +307,7 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
   if (!QATTN_IN_BOUNDS(row < a.rows_total)) return;
   const float4 sv =
       *reinterpret_cast<const float4*>(a.v_chan_scale + (static_cast<size_t>(b) * a.Hkv + hkv) * D + c);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   x.x *= sv.x * inv;
   x.y *= sv.y * inv;
   x.z *= sv.z * inv;
@@ -313,7 +320,7 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * D + c) = x;
   }
   if (a.lse && c == 0)
-    a.lse[row] = l > 0.f ? ((m + HEAD) + log2f(l * (1.f / (1 << HEAD)))) * kLn2 : kNegInf;
+    a.lse[row] = l == 0.f ? kNegInf : ((m + HEAD) + log2f(l * (1.f / (1 << HEAD)))) * kLn2;
 }
 
 // Joins the shares of the heads that more than one CTA worked on.  A head's steps

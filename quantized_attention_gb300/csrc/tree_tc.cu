@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(bar(kQReady));
       }
-      const float cf = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq) : 1.f;
+      bool fin = true;
+      const float cf = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq, fin) : 1.f;
       const int lim = tree_limit(a, sg.len, tok);
       float m = kNegInf, l = 0.f;  // the row's reference; this half's share of the sum
       for (int s = sg.s0; s < sg.s1; ++s, ++it) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the segment's share: O from TMEM, l of both halves
       float l_other;
       if (!(ok = exchange(l, l_other))) break;
-      l += l_other;
+      l = tree_sum(l + l_other, fin);
       ok = wait(kPvDone + ((it - 1) & 1), (it - 1) >> 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;

@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- this lane's rows g and g + 8 of the block: codes, factor, key limit
     uint32_t qa[KS][4];
     float cf[2];
+    bool fin[2] = {true, true};
     int lim[2];
     uint32_t tok[2];
 #pragma unroll
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         codes4_to_f16x2(x.z, qa[4 * w4 + 2][h], qa[4 * w4 + 2][2 + h]);
         codes4_to_f16x2(x.w, qa[4 * w4 + 3][h], qa[4 * w4 + 3][2 + h]);
       }
-      cf[h] = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq) : 1.f;
+      cf[h] = in ? tree_factor(a, sg.b, sg.hkv * a.G + hq, fin[h]) : 1.f;
       lim[h] = tree_limit(a, sg.len, i);
       tok[h] = i;
     }
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      l[h] = tree_sum(l[h], fin[h]);
       if (t4 == 0) {
         red_m[warp][g + 8 * h] = m[h];
         red_l[warp][g + 8 * h] = l[h];

@@ -7,7 +7,7 @@ import torch
 from quantized_attention_gb300 import binding as qb
 from tests import tree_ref as R
 from tests.gpu_common import ensure_library
-from tests.test_gpu_16_tree import make, run
+from tests.test_gpu_16_tree import make, run, words_of
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,31 @@ def test_scores_past_the_lowered_reference(name, big):
             # ex2, 1 / l and V s: 2^-20
             torch.testing.assert_close(got, want.expand_as(got), rtol=2.0 ** -11 + 2.0 ** -20, atol=0)
         assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("name", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_scale_that_is_not_finite(name, bad):
+    """NaN for the query head it belongs to, in O and in lse, whatever the division of
+    the work; the other heads keep their bits."""
+    x = form(name)
+    want_o, want_z = run(x, "chain")
+    x["qs"][0, 1] = x["qs"][1, 6] = bad
+    O, lse = run(x, "chain")
+    hit = torch.zeros(2, 8, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[1, 6] = True
+    assert torch.isnan(O[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(O[~hit], want_o[~hit]) and torch.equal(lse[~hit], want_z[~hit])
+
+
+@pytest.mark.parametrize("T,lens,cap", [(6, [0, 0], 50), (40, [0, 0], 50), (6, [0, 0], 20011), (40, [0, 0], 20011),
+                                        (6, [0, 20011], 20011), (40, [0, 20011], 20011)])
+def test_padding_rows_with_scales_that_are_not_finite(T, lens, cap):
+    """A row that sees nothing gives O = 0 and lse = -inf whatever its scale."""
+    x = make(18, 2, 4, 2, 64, T, lens, cap=cap)
+    see = np.zeros((2, T, T), bool)
+    see[1] = np.tril(np.ones((T, T), bool))
+    x["qs"][0] = [np.nan, np.inf, np.nan, 0.0]
+    O, lse = run(x, "tree", words_of(see), Nk=cap)
+    assert torch.all(O[0] == 0) and torch.all(lse[0] == -float("inf"))
+    assert torch.isfinite(O[1]).all() and torch.isfinite(lse[1]).all()
