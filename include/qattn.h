@@ -534,7 +534,7 @@ qattn_status qattn_tree_commit(const uint16_t* K_new, const int64_t* k_strides,
  * qattn_fwd, qattn_decode or qattn_tree_decode wrote it: each query hands out a
  * total of 1 per head, less what its drafts took.  Accumulated over decode steps,
  * or taken over a prompt's last tokens, it says which rows qattn_kv_evict keeps.
- * A query with lse = -inf gives nothing.
+ * A query with lse = -inf gives nothing, whatever its scale.
  *   q_codes/q_scales, k_codes/k_scales  as for qattn_fwd (k_scales NULL: all 1);
  *       k_codes int8 [B][Hkv][cap][d], cap = params->kv_capacity (or Nk)
  *   lse       fp32 [B][Hq][Nq]

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
       const float s = scale_of(a.q_scales, a.q_gran, b * a.Hq + hkv * a.G + hq, nqb, i / 128);
       const float e = a.lse[row0 + r];
       // a query that saw nothing (lse = -inf) gives nothing
-      f = make_float2(__fmul_rn(__fmul_rn(s, a.sm_scale), kLog2e), e == kNegInf ? -kNegInf : e * kLog2e);
+      f = make_float2(weight_factor(s, a.sm_scale, e), e == kNegInf ? -kNegInf : e * kLog2e);
     }
     rowc[r] = f;
     rowi[r] = i;

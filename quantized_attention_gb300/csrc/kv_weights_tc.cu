@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // row tid's constants: {factor sq sm log2 e, -lse2, last visible key}; a row
           // past the end, or one that saw nothing, gives 2^-inf = 0
           float* fac = reinterpret_cast<float*>(smem + C::kOffF + st * C::kFac);
-          fac[tid] = __fmul_rn(__fmul_rn(s_next, a.sm_scale), kLog2e);
+          fac[tid] = weight_factor(s_next, a.sm_scale, e_next);
           fac[128 + tid] = e_next == kNegInf ? kNegInf : -e_next * kLog2e;
           reinterpret_cast<int*>(fac)[256 + tid] = a.causal ? w.pos0 + i_next : 0x7fffffff;
           fence_proxy_async_smem();

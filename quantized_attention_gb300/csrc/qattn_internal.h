@@ -327,6 +327,12 @@ struct WeightArgs {
   float* weights;            // [B][Hkv][cap]
   unsigned int* err;
 };
+// A query row's factor sq sm log2 e; 0 for a query that gives nothing (lse = -inf) if
+// its scale is not finite: 0 S - inf is -inf, where NaN would hide every other query.
+__device__ __forceinline__ float weight_factor(float sq, float sm_scale, float lse) {
+  const float c = __fmul_rn(__fmul_rn(sq, sm_scale), 1.44269502162933349609375f);  // fp32(log2 e)
+  return fabsf(c) < __builtin_huge_valf() || lse != -__builtin_huge_valf() ? c : 0.f;
+}
 // Query rows (query heads of the group x tokens) up to which the warp-level kernel
 // runs; above, the tensor-core one, which works in tiles of 128.  Measured on 8
 // heads of 32K rows, warp-level against tensor cores, us: 16 rows 13.8 / 22.8, 32

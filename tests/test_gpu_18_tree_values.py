@@ -7,7 +7,7 @@ import torch
 from quantized_attention_gb300 import binding as qb
 from tests import tree_ref as R
 from tests.gpu_common import ensure_library
-from tests.test_gpu_16_tree import make, run, words_of
+from tests.test_gpu_16_tree import dev, make, run, words_of
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,30 @@ def test_padding_rows_with_scales_that_are_not_finite(T, lens, cap):
     O, lse = run(x, "tree", words_of(see), Nk=cap)
     assert torch.all(O[0] == 0) and torch.all(lse[0] == -float("inf"))
     assert torch.isfinite(O[1]).all() and torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("T,G", [(3, 2), (40, 4), (70, 1), (300, 2)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_weights_of_masked_queries_with_scales_that_are_not_finite(T, G, bad):
+    """A query with lse = -inf gives nothing, whatever its scale: a sequence of
+    queries that do not count, and one head's among others that do."""
+    rng = np.random.default_rng(19)
+    B, Hkv, d, N = 2, 2, 64, 700
+    Hq, nb = Hkv * G, (T + 127) // 128
+    qc = dev(rng.integers(-127, 128, (B, Hq, T, d)).astype(np.int8))
+    kc = dev(rng.integers(-127, 128, (B, Hkv, N, d)).astype(np.int8))
+    qs = torch.full((B, Hq, nb), 1e-4, device="cuda")
+    lse = torch.full((B, Hq, T), 6.0, device="cuda")
+    lse[0] = -float("inf")
+    lse[1, 0] = -float("inf")
+    base = torch.rand(B, Hkv, N, device="cuda")
+    shape, params = qb.make_shape(B, Hq, Hkv, T, N, d), qb.make_params()
+    want, got = torch.zeros_like(base), torch.zeros_like(base)
+    qb.kv_weights(qc, qs, kc, None, lse, shape, params, want, base=base)
+    qs[0] = bad
+    qs[1, 0] = bad
+    qb.kv_weights(qc, qs, kc, None, lse, shape, params, got, base=base)
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0
+    assert torch.equal(want[0], base[0])
+    assert torch.equal(got, want)
