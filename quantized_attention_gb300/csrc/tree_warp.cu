@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();  // the abort flag is set
   const int R = a.G * a.T;
   uint32_t used = 0;  // tiles this warp has taken through its ring
+  uint32_t sent = 0;  // lane 0: those it has issued
 
   TreeSeg sg;
   if constexpr (CL) walk = tree_cluster_walk(a, kStep, sg);
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t q = used + i, slot = q % kRing;
       const uint32_t bar = smem_u32(&full[warp][slot]);
       const int key = (first + i * kWarps - nd) * kStep;
+      sent = q + 1;
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(SM::kStage));
       tma_load_3d(smem_u32(ring + slot * SM::kStage), &tmK, bar, 0, key, bkv);
       tma_load_3d(smem_u32(ring + slot * SM::kStage + SM::kTile), &tmV, bar, 0, key, bkv);
@@ -331,7 +333,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncthreads();
-    if (abort_flag) break;  // a wait ran out (every thread sees it here)
+    if (abort_flag) {  // a wait ran out (every thread sees it here)
+      // every load this warp issued lands before the CTA may exit
+      if (lane == 0)
+        for (uint32_t back = 1; back <= min(sent, static_cast<uint32_t>(kRing)); ++back) {
+          const uint32_t q = sent - back;
+          volatile int never = 0;
+          mbar_wait(smem_u32(&full[warp][q % kRing]), (q / kRing) & 1, &never, a.err, kErrTimeout);
+        }
+      break;
+    }
     float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
