@@ -306,7 +306,13 @@ class TreeCache:
     moves to a second set of the same capacity and back (a captured graph keeps the
     set it was captured with).  max_rows: bound on the rows in use (default: the
     capacity).  All calls go to the current stream (or ``stream``) and none waits
-    for the GPU; calls on several streams are ordered by the caller."""
+    for the GPU; calls on several streams are ordered by the caller.
+
+    Rows enter through ``commit`` and ``append``, which keep ``lengths``, ``seen`` (int32
+    [B]: the tokens behind k_mean, more than the rows in use once rows have been
+    evicted) and the new rows' ``weights`` (0) in step.  Code that writes rows by other
+    means advances ``lengths`` and ``seen`` itself; the weights behind the rows in use
+    are 0."""
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, k_mean, v_code_amax, lengths, Hq, T, *,
                  out_dtype=qb.DT_BF16, sm_scale=0.0, max_rows=None):
@@ -330,12 +336,13 @@ class TreeCache:
         ws = max(qb.tree_workspace_size(self.shape, self.params), qb.workspace_size(*self._q), 256)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
         self._spare = None
+        self._whole = self._every(T)
         self._seen = self._all  # params that say which cached rows the last verify's queries saw
 
     def verify(self, Q, K_new=None, V_new=None, tree_mask=None, stream=None):
         """Attention of the T drafted tokens (Q bf16 [B, Hq, T, d]) over the cache and
         the drafts' own K_new, V_new (bf16 [B, Hkv, T, d]); tree_mask None: a chain.
-        K_new None: the T last rows in use are the tokens' own."""
+        K_new None: the T last rows in use are the tokens' own (``append`` them first)."""
         qb.quantize_qk(Q, None, qb.DT_I8, None, self.k_scale, *self._q, self.q_codes, self.q_scales,
                        None, None, self.workspace, stream)
         qb.tree_decode(self.q_codes, self.q_scales, self.k_codes, self.v_codes, self.k_scale,
@@ -346,7 +353,8 @@ class TreeCache:
         return self.O
 
     def weigh(self, lse=None, stream=None):
-        """Add the weight the last ``verify``'s drafts gave each cached row.  lse: its
+        """Add the weight the drafts of the last ``verify`` (the last called, not one
+        replayed from a graph) gave each cached row.  lse: its
         ``lse`` with -inf for the drafts that do not count (the rejected ones).
         Call it before ``commit``: it reads the rows in use then."""
         qb.kv_weights(self.q_codes, self.q_scales, self.k_codes, None, self.lse if lse is None else lse,
@@ -359,6 +367,19 @@ class TreeCache:
                        self.k_mean, self.v_code_amax, self.k_codes, self.v_codes, seen=self.seen,
                        weights=self.weights, stream=stream)
 
+    def append(self, K_new, V_new, stream=None):
+        """Append every token of K_new, V_new (bf16 [B, Hkv, n, d], any n) to each sequence."""
+        n = K_new.shape[2]
+        with torch.cuda.stream(stream):
+            path, count = self._whole if n == self.shape.Nq else self._every(n)
+        self.commit(K_new, V_new, path, count, stream)
+
+    def _every(self, n):
+        """The path of all n tokens, and its length, for each sequence."""
+        B, dev = self.lengths.shape[0], self.lengths.device
+        return (torch.arange(n, dtype=torch.int32, device=dev).repeat(B, 1),
+                torch.full((B,), n, dtype=torch.int32, device=dev))
+
     def evict(self, budget, n_sink=0, n_recent=0, stream=None):
         """Keep the budget rows of most weight per KV head; returns the kept rows'
         former indices, int32 [B, Hkv, budget]."""
@@ -366,6 +387,8 @@ class TreeCache:
             if self._spare is None:
                 self._spare = [torch.zeros_like(t) for t in (self.k_codes, self.v_codes, self.weights,
                                                              self.lengths)]
+            else:
+                self._spare[2].zero_()  # what the rows behind the kept ones weighed there last
             k, v, w, n = self._spare
             kept = torch.empty((*self.weights.shape[:2], budget), dtype=torch.int32, device=w.device)
         qb.kv_evict(self.k_codes, self.v_codes, self.weights, budget, k, v, w, kept, n,
