@@ -382,7 +382,7 @@ class TreeCache:
 
     def evict(self, budget, n_sink=0, n_recent=0, stream=None):
         """Keep the budget rows of most weight per KV head; returns the kept rows'
-        former indices, int32 [B, Hkv, budget]."""
+        former indices, int32 [B, Hkv, budget], -1 behind them where there are fewer."""
         with torch.cuda.stream(stream):  # what is allocated and filled here belongs to the call's stream
             if self._spare is None:
                 self._spare = [torch.zeros_like(t) for t in (self.k_codes, self.v_codes, self.weights,
@@ -390,7 +390,7 @@ class TreeCache:
             else:
                 self._spare[2].zero_()  # what the rows behind the kept ones weighed there last
             k, v, w, n = self._spare
-            kept = torch.empty((*self.weights.shape[:2], budget), dtype=torch.int32, device=w.device)
+            kept = torch.full((*self.weights.shape[:2], budget), -1, dtype=torch.int32, device=w.device)
         qb.kv_evict(self.k_codes, self.v_codes, self.weights, budget, k, v, w, kept, n,
                     self.v_code_amax, lengths=self.lengths, Nk=self.shape.Nk, n_sink=n_sink,
                     n_recent=n_recent, stream=stream)

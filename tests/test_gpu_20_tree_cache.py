@@ -1,4 +1,5 @@
-"""pipeline.TreeCache: rows that enter by another way than an accepted path."""
+"""pipeline.TreeCache: rows that enter by another way than an accepted path, and
+what an eviction returns."""
 import numpy as np
 import pytest
 import torch
@@ -100,3 +101,14 @@ def test_rows_written_from_outside_start_with_no_weight():
     torch.cuda.synchronize()
     assert qb.get_error() == 0
     check_weights(C, before, C.lse)
+
+
+def test_evict_marks_the_entries_without_a_row():
+    """kept is -1 behind the rows kept, whatever its memory held."""
+    C = tree_cache(np.random.default_rng(85), 2, 4, 2, 64, 3, 90, [40, 9])
+    torch.full((2, 2, 30), 7, dtype=torch.int32, device="cuda")  # freed: the next of this size lies there
+    kept = C.evict(30, 2, 5)
+    torch.cuda.synchronize()
+    assert qb.get_error() == 0
+    assert torch.all(kept[0] >= 0) and torch.all(kept[1, :, :9] >= 0)
+    assert torch.all(kept[1, :, 9:] == -1)
