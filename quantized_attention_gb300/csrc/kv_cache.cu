@@ -30,7 +30,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
   bool bad = n < 0 || n > a.T || len < 0 || seen < 0 || seen > 0x7fffffff - max(n, 0) ||
              len + static_cast<long long>(n) > a.cap;
   if (!bad)
-    for (int t = threadIdx.x; t < n; t += kCommitThreads) bad |= path[t] < 0 || path[t] >= a.T;
+    for (int t = threadIdx.x; t < n; t += kCommitThreads)
+      bad |= !QATTN_IN_BOUNDS(t < a.T) || path[t] < 0 || path[t] >= a.T;
   bad = __syncthreads_or(bad);
   if (bad) {  // nothing of this sequence is appended
     n = 0;
@@ -46,6 +47,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     const size_t row0 = (static_cast<size_t>(b) * a.Hkv + h) * a.cap + len;
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
+      if (!QATTN_IN_BOUNDS(t < a.T && path[t] >= 0 && path[t] < a.T)) continue;
       const long long j = path[t];
       const float k = bf16_bits_to_f32(K[j * a.ksN]), v = bf16_bits_to_f32(V[j * a.vsN]);
       const float diff = __fsub_rn(k, mu);
@@ -139,7 +141,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
   const float* w = a.weights + static_cast<size_t>(bkv) * a.cap;
   const bool fits = slice <= kSelRows;
   auto fresh = [&](int r) {
-    return (r < a.n_sink || r >= len - a.n_recent) ? 0xffffffffu : weight_key(w[r]);
+    if (r < a.n_sink || r >= len - a.n_recent || !QATTN_IN_BOUNDS(r < a.cap)) return 0xffffffffu;
+    return weight_key(w[r]);
   };
   auto key = [&](int i) { return fits ? keys[i] : fresh(r0 + i); };
   if (fits)
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     const uint32_t k = key(i);
     if (k > thr || (k == thr && pe < left)) {
       const uint32_t pos = pg + min(pe, left);
-      if (QATTN_IN_BOUNDS(pos < static_cast<uint32_t>(want))) {
+      if (QATTN_IN_BOUNDS(pos < static_cast<uint32_t>(want) && r0 + i < a.cap)) {
         kept[pos] = r0 + i;
         wo[pos] = w[r0 + i];
       }
@@ -283,7 +286,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
     int row[U];
     uint4 kx[U], vx[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) row[i] = p + i * RPI < p1 ? kept[p + i * RPI] : -1;
+    for (int i = 0; i < U; ++i)
+      row[i] = p + i * RPI < p1 && QATTN_IN_BOUNDS(p + i * RPI < a.budget) ? kept[p + i * RPI] : -1;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);

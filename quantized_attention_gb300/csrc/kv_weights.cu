@@ -26,6 +26,7 @@ static_assert(kRows % 8 == 0, "rows come in fragments of 8");
 
 __device__ __forceinline__ int row_count(const WeightArgs& a, int b) {
   if (!a.lengths) return a.Nk;
+  if (!QATTN_IN_BOUNDS(b >= 0 && b < a.B)) return 0;
   const int n = a.lengths[b];
   if (n < 0 || n > a.Nk) {
     atomicOr(a.err, kErrDomain);
@@ -34,8 +35,10 @@ __device__ __forceinline__ int row_count(const WeightArgs& a, int b) {
   return n;
 }
 
-__device__ __forceinline__ float scale_of(const float* s, int gran, int bh, int nblk, int blk) {
+// nbh: (batch, head) pairs of the scales
+__device__ __forceinline__ float scale_of(const float* s, int gran, int bh, int nbh, int nblk, int blk) {
   if (gran == 0) return s[0];
+  if (!QATTN_IN_BOUNDS(bh < nbh && (gran == 1 || (blk >= 0 && blk < nblk)))) return 0.f;
   if (gran == 1) return s[bh];
   return s[static_cast<size_t>(bh) * nblk + blk];
 }
@@ -94,9 +97,10 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
     }
   }
   const int nkb = (a.Nk + 127) / 128, nqb = (a.Nq + 127) / 128;
-  const float sk = a.k_scales ? scale_of(a.k_scales, a.k_gran, bkv, nkb, min(kw, a.Nk - 1) / 128) : 1.f;
+  const float sk = a.k_scales ? scale_of(a.k_scales, a.k_gran, bkv, a.B * a.Hkv, nkb, min(kw, a.Nk - 1) / 128) : 1.f;
   const int pos0 = a.pos0_len ? len - a.Nq : a.pos0;
   const size_t row0 = (static_cast<size_t>(b) * a.Hq + hkv * a.G) * a.Nq;
+  const size_t rows_total = static_cast<size_t>(a.B) * a.Hq * a.Nq;
   // rows, widened once: chunk c of row r at 32 (r NC + c), its two 16-byte halves
   // exchanged in odd rows (eight lanes of a read, four chunks of two rows, hit
   // eight bank groups)
@@ -104,7 +108,8 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
   for (int x = threadIdx.x; x < rows8 * NC; x += kThreads) {
     const int r = x / NC, c = x % NC;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < R) v = *reinterpret_cast<const uint4*>(a.q_codes + (row0 + r) * D + 16 * c);
+    if (r < R && QATTN_IN_BOUNDS(row0 + r < rows_total))
+      v = *reinterpret_cast<const uint4*>(a.q_codes + (row0 + r) * D + 16 * c);
     uint32_t h[8];
     codes4_to_f16x2(v.x, h[0], h[1]);
     codes4_to_f16x2(v.y, h[2], h[3]);
@@ -118,10 +123,10 @@ __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightA
     const int r = threadIdx.x;
     float2 f = make_float2(0.f, -kNegInf);  // a row past the end: 2^(0 - inf) = 0
     int i = 0;
-    if (r < R) {
+    if (r < R && QATTN_IN_BOUNDS(row0 + r < rows_total)) {
       const int hq = r / a.Nq;
       i = r - hq * a.Nq;
-      const float s = scale_of(a.q_scales, a.q_gran, b * a.Hq + hkv * a.G + hq, nqb, i / 128);
+      const float s = scale_of(a.q_scales, a.q_gran, b * a.Hq + hkv * a.G + hq, a.B * a.Hq, nqb, i / 128);
       const float e = a.lse[row0 + r];
       // a query that saw nothing (lse = -inf) gives nothing
       f = make_float2(weight_factor(s, a.sm_scale, e), e == kNegInf ? -kNegInf : e * kLog2e);

@@ -87,6 +87,7 @@ struct Tile {
 
 __device__ __forceinline__ int row_count(const WeightArgs& a, int b) {
   if (!a.lengths) return a.Nk;
+  if (!QATTN_IN_BOUNDS(b >= 0 && b < a.B)) return 0;
   const int n = a.lengths[b];
   if (n < 0 || n > a.Nk) {
     atomicOr(a.err, kErrDomain);
@@ -95,8 +96,10 @@ __device__ __forceinline__ int row_count(const WeightArgs& a, int b) {
   return n;
 }
 
-__device__ __forceinline__ float scale_of(const float* s, int gran, int bh, int nblk, int blk) {
+// nbh: (batch, head) pairs of the scales
+__device__ __forceinline__ float scale_of(const float* s, int gran, int bh, int nbh, int nblk, int blk) {
   if (gran == 0) return s[0];
+  if (!QATTN_IN_BOUNDS(bh < nbh && (gran == 1 || (blk >= 0 && blk < nblk)))) return 0.f;
   if (gran == 1) return s[bh];
   return s[static_cast<size_t>(bh) * nblk + blk];
 }
@@ -287,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && take(); ++cnt) {
         const int st = cnt & 1;
         if (cnt >= 2 && !(ok = wait(kRawEmpty + st, (cnt >> 1) - 1))) break;
+        (void)QATTN_IN_BOUNDS(w.k0 < a.Nk && w.bkv < a.B * a.Hkv);  // TMA coordinates
         mbar_arrive_expect_tx(bar(kRawFull + st), C::kRaw);
         for (int m = 0; m < 2; ++m)
           tma_load_3d(base + st * C::kRaw + m * (C::kRaw / 2), &tmK, bar(kRawFull + st), 0, w.k0 + 128 * m, w.bkv);
@@ -406,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t q = qn;
       if (!kept) {
         const size_t row0 = (static_cast<size_t>(w.b) * a.Hq + w.hkv * a.G) * a.Nq;
+        const size_t rows_total = static_cast<size_t>(a.B) * a.Hq * a.Nq;
         uint4 v[CH];
         float s_next = 0.f, e_next = kNegInf;
         int i_next = 0;
@@ -416,14 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
             v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (rw + RS * i < n_rows) v[i] = src[RS * i * (D / 16)];
+            if (rw + RS * i < n_rows && QATTN_IN_BOUNDS(row0 + r0 + rw + RS * i < rows_total))
+              v[i] = src[RS * i * (D / 16)];
           }
           s_next = 0.f;
           e_next = kNegInf;
-          if (tid < n_rows) {
+          if (tid < n_rows && QATTN_IN_BOUNDS(row0 + r0 + tid < rows_total)) {
             const int hq = til.packed ? (r0 + tid) / a.Nq : t.h;
             i_next = r0 + tid - hq * a.Nq;
-            s_next = scale_of(a.q_scales, a.q_gran, w.b * a.Hq + w.hkv * a.G + hq, nqb, i_next / 128);
+            s_next = scale_of(a.q_scales, a.q_gran, w.b * a.Hq + w.hkv * a.G + hq, a.B * a.Hq, nqb, i_next / 128);
             e_next = a.lse[row0 + r0 + tid];
           }
         };
@@ -484,9 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = w.k0 + 128 * m + quad * 32 + lane;
       const size_t o = static_cast<size_t>(w.bkv) * a.cap + key;
       const bool live = key < w.len;
-      auto base_of = [&](int k) { return (k < w.len && a.base) ? a.base[static_cast<size_t>(w.bkv) * a.cap + k] : 0.f; };
+      auto base_of = [&](int k) {
+        if (k >= w.len || !a.base || !QATTN_IN_BOUNDS(k < a.cap)) return 0.f;
+        return a.base[static_cast<size_t>(w.bkv) * a.cap + k];
+      };
       auto key_scale = [&](int k0) {
-        return a.k_scales ? scale_of(a.k_scales, a.k_gran, w.bkv, nkb, min(k0 / 128 + m, nkb - 1)) : 1.f;
+        return a.k_scales ? scale_of(a.k_scales, a.k_gran, w.bkv, a.B * a.Hkv, nkb, min(k0 / 128 + m, nkb - 1)) : 1.f;
       };
       // base and scale of a unit that follows in the same head come a unit ahead: their
       // latency would stand before every unit's first column

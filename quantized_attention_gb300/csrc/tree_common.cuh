@@ -24,6 +24,7 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
 // it is clamped (no access leaves the cache) and reported by the error word.
 __device__ __forceinline__ int tree_length(const TreeArgs& a, int b) {
   if (!a.lengths) return a.Nk;
+  if (!QATTN_IN_BOUNDS(b >= 0 && b < a.B)) return 0;
   const int n = a.lengths[b];
   if (n < 0 || n > a.Nk) {
     atomicOr(a.err, kErrDomain);
@@ -133,7 +134,7 @@ __device__ __forceinline__ bool tree_next(const TreeArgs& a, int step, TreeWalk&
       do {
         w.len = tree_length(a, ++w.b);
         w.steps = tree_steps(a, w.len, step);
-      } while (w.steps == 0);
+      } while (w.steps == 0 && QATTN_IN_BOUNDS(w.b < a.B));
     }
   }
   s.b = w.b;
@@ -189,7 +190,8 @@ __device__ __forceinline__ int tree_owner(int x, int total, int G) {
 // 1 all the same for every |S| < 2^21, and a hidden key's -inf stays -inf.  So does
 // one that is not finite, for the sake of the row's hidden keys; tree_sum makes up for it.
 __device__ __forceinline__ float tree_factor(const TreeArgs& a, int b, int hq, bool& finite) {
-  const float sq = a.q_gran == 0 ? a.q_scales[0] : a.q_scales[b * a.Hq + hq];
+  const int i = a.q_gran == 0 ? 0 : b * a.Hq + hq;
+  const float sq = QATTN_IN_BOUNDS(i >= 0 && i < a.B * a.Hq) ? a.q_scales[i] : 0.f;
   const float c = __fmul_rn(__fmul_rn(sq, a.sm_scale), kLog2e);
   finite = fabsf(c) < -kNegInf;
   return c == 0.f || !finite ? 1e-30f : c;
@@ -220,6 +222,7 @@ __device__ __forceinline__ uint32_t tree_draft_word(const TreeArgs& a, int b, in
   if (real == 0u) return 0u;  // past the mask's words
   if (!a.tree_mask) return a.draft_causal ? first_bits(i + 1 - 32 * s) & real : real;
   const int words = (a.T + 31) / 32;
+  if (!QATTN_IN_BOUNDS(b < a.B && i >= 0 && i < a.T && s < words)) return 0u;
   return a.tree_mask[(static_cast<size_t>(b) * a.T + i) * words + s] & real;
 }
 
@@ -257,6 +260,7 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
   constexpr int W = D / 4;  // words of a row
   constexpr int U = 4;      // rows in flight
   const int w = tid % W;    // W <= 32 divides nthr
+  if (!QATTN_IN_BOUNDS(b < a.B && hkv < a.Hkv)) return;
   const size_t ch = (static_cast<size_t>(b) * a.Hkv + hkv) * D + 4 * w;
   const float4 ks = *reinterpret_cast<const float4*>(a.k_chan_scale + ch);
   const float4 mu = *reinterpret_cast<const float4*>(a.k_mean + ch);
@@ -272,7 +276,7 @@ __device__ __forceinline__ void tree_encode_drafts(const TreeArgs& a, int b, int
     for (int i = 0; i < U; ++i) {
       const int r = r0 + i * dr;
       k[i] = v[i] = make_uint2(0u, 0u);
-      if (r < rows) {
+      if (r < rows && QATTN_IN_BOUNDS(j0 + r < a.T)) {
         k[i] = *reinterpret_cast<const uint2*>(K + (j0 + r) * a.ksN);
         v[i] = *reinterpret_cast<const uint2*>(V + (j0 + r) * a.vsN);
       }
@@ -304,7 +308,7 @@ __device__ __forceinline__ void tree_write_out(const TreeArgs& a, int b, int hkv
   if (rr >= a.G * a.T) return;
   const int hq = rr / a.T, i = rr % a.T;
   const size_t row = (static_cast<size_t>(b) * a.Hq + hkv * a.G + hq) * a.T + i;
-  if (!QATTN_IN_BOUNDS(row < a.rows_total)) return;
+  if (!QATTN_IN_BOUNDS(row < a.rows_total && b < a.B && hkv < a.Hkv)) return;
   const float4 sv =
       *reinterpret_cast<const float4*>(a.v_chan_scale + (static_cast<size_t>(b) * a.Hkv + hkv) * D + c);
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -398,6 +402,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads) tree_join_kernel(const TreeA
       const int ci = cb + i * NW;
       const size_t si = 2 * static_cast<size_t>(ci) + (ci == c0 ? 1 : 0);
       const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (!QATTN_IN_BOUNDS(si < a.slots)) continue;
       const float* po = a.part_o + (si * ROWS + r) * D + CPL * lane;
       if constexpr (CPL == 4) {
         const float4 y = *reinterpret_cast<const float4*>(po);

@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (s < a.drafts) {
               mbar_arrive(bar(kRawFull + slot));
             } else {
+              (void)QATTN_IN_BOUNDS((s - a.drafts) * kStep < a.Nk && bkv < a.B * a.Hkv);  // TMA coordinates
               mbar_arrive_expect_tx(bar(kRawFull + slot), C::kRawTile);
               tma_load_3d(raw(slot), kv ? &tmV : &tmK, bar(kRawFull + slot), 0, (s - a.drafts) * kStep, bkv);
             }

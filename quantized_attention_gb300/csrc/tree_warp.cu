@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t bar = smem_u32(&full[warp][slot]);
       const int key = (first + i * kWarps - nd) * kStep;
       sent = q + 1;
+      (void)QATTN_IN_BOUNDS(key >= 0 && key < a.Nk && bkv < a.B * a.Hkv);  // TMA coordinates
       mbar_arrive_expect_tx(bar, static_cast<uint32_t>(SM::kStage));
       tma_load_3d(smem_u32(ring + slot * SM::kStage), &tmK, bar, 0, key, bkv);
       tma_load_3d(smem_u32(ring + slot * SM::kStage + SM::kTile), &tmV, bar, 0, key, bkv);
