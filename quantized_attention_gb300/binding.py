@@ -368,16 +368,16 @@ def _ptr(name: str, t, dtype, shape, dev: int) -> int:
 
 def _input_ptr(dev: int, name: str, t, shape):
     """A bf16 input at any strides (see _input): its address and strides."""
-    if t.dtype is not torch.bfloat16:
+    if t is not None and t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.shape != shape or t.get_device() != dev:
+    if t is None or t.shape != shape or t.get_device() != dev:
         _reject(name, t, torch.bfloat16, shape, dev)
     return t.data_ptr(), None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
 
 
 def _scales_ptr(dev: int, name: str, t, gran: int, B: int, H: int, N: int) -> int:
-    if t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
-        _reject(name, t, torch.float32, t.shape, dev)
+    if t is None or t.dtype is not torch.float32 or t.get_device() != dev or not t.is_contiguous():
+        _reject(name, t, torch.float32, None if t is None else t.shape, dev)
     if t.numel() < (1 if gran == GRAN_TENSOR else B * H * (1 if gran == GRAN_HEAD else (N + 127) // 128)):
         raise ValueError(f"{name}: too few for the granularity")
     return t.data_ptr()
@@ -449,6 +449,8 @@ def tree_commit(K_new, V_new, path, n_accept, k_chan_scale, v_chan_scale, length
     T, d]) to the cache (see qattn_tree_commit in include/qattn.h).  path: int32
     [B, T] draft indices, n_accept: int32 [B].  An output not given is written
     over the array it is computed from."""
+    if K_new is None or k_codes is None:
+        _reject("K_new" if K_new is None else "k_codes", None, None, None, None)
     shape = B, Hkv, T, d = K_new.shape
     cap, i8, f32, i32 = k_codes.shape[2], torch.int8, torch.float32, torch.int32
     dev = torch.cuda.current_device()
@@ -497,6 +499,8 @@ def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept,
              v_code_amax, *, lengths=None, Nk=None, n_sink=0, n_recent=0, stream=None):
     """Keep the budget rows of most weight per KV head (see qattn_kv_evict in
     include/qattn.h).  Nk: most rows in use (default: the capacity)."""
+    if k_codes is None or k_out is None:
+        _reject("k_codes" if k_codes is None else "k_out", None, None, None, None)
     cache = B, Hkv, cap, d = k_codes.shape
     Nk, budget, ocap = cap if Nk is None else int(Nk), int(budget), k_out.shape[2]
     i8, f32, i32 = torch.int8, torch.float32, torch.int32
