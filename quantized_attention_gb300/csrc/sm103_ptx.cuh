@@ -406,9 +406,13 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16) {
 // Programmatic dependent launch.  pdl_trigger lets the next kernel of the
 // stream start launching (its CTAs are placed once every CTA of this grid has
 // triggered or exited); pdl_wait blocks until the previous grid of the stream
-// has completed and its writes are visible.  Every kernel here triggers at
-// entry and waits before it reads any input, so the overlap is limited to
-// launch latency and set-up.  Both are no-ops without the launch attribute.
+// has completed and its writes are visible.  Kernels trigger at entry and wait
+// before they read any input, so the overlap is limited to launch latency and
+// set-up -- but a kernel whose dependent reads inputs ahead of its own wait
+// triggers only after its own: the joins of the tree kernels (tree_join_kernel,
+// tree_join_rows_kernel) read the lengths before their wait, so tree_warp_kernel
+// and tree_tc_kernel trigger after theirs, when whatever wrote the lengths is
+// done.  Both are no-ops without the launch attribute.
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
