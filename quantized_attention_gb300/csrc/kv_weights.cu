@@ -57,11 +57,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // memory); the rows wait in shared memory as fp16 B fragments with their
 // constants.  Lane (g, t) takes 16-byte chunks t and t + 4 of its keys and rows
 // (four lanes read 64 consecutive bytes), so a k-step's fragment is one word of
-// each.  A step over 32K rows of 8 KV heads takes 12.7 us = 2.8 TB/s (floor 5.4).
+// each.  A step over 32K rows of 8 KV heads takes 12.8 us = 2.8 TB/s (floor 5.4).
 // Bound by the latency of a warp's chain (load, widen, eight dependent MMAs,
 // exponentials) at 16 warps an SM.  A CTA walking over several key blocks with the
-// next block's loads in flight measured no faster (17.8 against 16.1 us for a step
-// over 32K rows of 8 heads): fewer warps fit.
+// next block's loads in flight measured no faster (17.8 against 16.1 us, both before
+// the rows waited as ready fragments): fewer warps fit.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_weights_warp_kernel(const WeightArgs a) {
   constexpr int KS = D / 16;

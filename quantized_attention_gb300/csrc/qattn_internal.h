@@ -223,8 +223,16 @@ cudaError_t launch_kv_append(const uint16_t* K_new, const uint16_t* V_new, int B
 
 // ---- tree_warp.cu, tree_tc.cu (tree_common.cuh): qattn_tree_decode
 constexpr int kTreeMaxTokens = 128;  // drafted tokens of a sequence
-constexpr int kTreeRows = 16;        // query rows of the warp-level kernel's block
-constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each)
+// Query rows of the warp-level kernel's block, and the most of a KV head that it takes:
+// beyond them the tensor-core kernel runs, which reads the cache once for up to 128.
+// Measured, warp-level against tensor cores, us (d = 128, four query heads a KV head; 8
+// heads of 4K, 8 of 32K, 128 of 0.1 to 4K, 64 of 5K to 32K rows): 16 rows 10.0 / 13.4,
+// 23.0 / 27.4, 27.9 / 43.7, 61 / 90; 20 rows 11.6 / 13.5, 30.1 / 27.8, 36.2 / 44.0, 110 /
+// 90; 32 rows 11.8 / 13.6, 30.7 / 27.8, 38.3 / 44.3, 108 / 90; 64 rows 12.5 / 14.7, 47.8 /
+// 28.7, 63.6 / 46.4, 195 / 92.
+constexpr int kTreeRows = 16;
+constexpr int kTreeWarpCtas = 304;   // its CTAs, at most (152 SMs, two each; the workspace's size
+                                     // is asked for without a device, so not num_sms())
 constexpr int kTreeTcRows = 128;     // query rows of the tensor-core kernel's block
 constexpr int kTreeTcCtas = 152;     // its CTAs, at most
 constexpr int kTreeWarpStep = 32, kTreeTcStep = 128;  // keys of a step
@@ -244,7 +252,10 @@ constexpr int kTreeCluster = 8;      // most CTAs of a head's own cluster
 // 15.2 / 36.4 against 10.1 / 14.1 / 22.7; 16 of 4K / 8K / 16K 12.8 / 18.0 / 28.2 against
 // 14.0 / 18.0 / 22.3; 32 of 8K / 16K 20.9 / 30.9 against 21.9 / 31.7; 64 of 4K 20.8 / 22.3,
 // of 5K to 32K 71.7 / 59.4; 128 of 2K 21.2 / 26.1, of 100 to 4K 27.9 / 25.7, to 8K 47.5 /
-// 36.5; 256 of 300 / 2K 15.1 / 32.9 against 21.5 / 39.6.
+// 36.5; 256 of 300 / 2K 15.1 / 32.9 against 21.5 / 39.6.  The same rule serves d = 64: 8 of
+// 2K / 8K / 32K 6.6 / 10.9 / 27.9 against 8.7 / 11.2 / 17.5; 32 of 4K / 16K 11.4 / 24.9
+// against 13.0 / 21.9; 64 of 5K to 32K 63.5 / 40.0; 128 of 2K 16.8 / 17.4, of 100 to 4K 21.9 /
+// 18.1 (taken as clusters); 256 of 300 / 2K 10.1 / 26.3 against 12.2 / 25.2.
 inline int tree_cluster(long long heads, long long steps) {
   const int c = heads <= 32 ? kTreeCluster : heads <= kTreeWarpCtas / 4 ? 4 : heads <= kTreeWarpCtas / 2 ? 2 : 1;
   const long long waves = (heads * c + kTreeWarpCtas - 1) / kTreeWarpCtas;
@@ -261,7 +272,10 @@ inline int tree_cluster(long long heads, long long steps) {
 // of 2K / 8K / 32K 15.5 / 20.9 / 46.5 against 14.6 / 18.7 / 29.9; 16 of 4K / 8K / 16K 19.3 /
 // 27.9 / 45.0 against 20.3 / 24.0 / 30.9; 32 of 4K / 8K / 16K 20.3 / 28.8 / 46.9 against
 // 24.1 / 31.0 / 44.6; 64 of 4K 30.5 / 35.6, of 5K to 32K 119 / 89; 128 of 2K 33.8 / 44.7, of
-// 100 to 4K 48.6 / 51.5, to 8K 81.8 / 68.0; 256 of 2K 66.0 / 74.3.
+// 100 to 4K 48.6 / 51.5, to 8K 81.8 / 68.0; 256 of 2K 66.0 / 74.3.  At d = 64: 8 of 2K / 8K /
+// 32K 12.1 / 16.4 / 39.6 against 11.8 / 14.3 / 24.5; 32 of 4K / 16K 16.5 / 39.1 against 20.1 /
+// 38.3; 64 of 4K 25.1 / 27.3, of 5K to 32K 129 / 78; 128 of 2K 27.5 / 31.7, of 100 to 4K
+// 41.7 / 33.9 (taken as clusters); 256 of 300 / 2K 29.7 / 53.8 against 31.7 / 54.1.
 inline int tree_tc_cluster(long long heads, long long steps) {
   const int c = heads <= 8 ? kTreeCluster : heads <= 32 ? 4 : heads <= kTreeTcCtas / 2 ? 2 : 1;
   const long long waves = (heads * c + kTreeTcCtas - 1) / kTreeTcCtas;

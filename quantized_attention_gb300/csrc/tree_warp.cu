@@ -9,17 +9,18 @@
 // CTAs) are joined by 2^(m_part - m).  P is rounded once, to fp16, for the PV
 // product; l sums the unrounded P in fp32.  m lies 15 below the running maximum, so P
 // fills fp16's range: a key down to 2^-29 of the row's largest (20 nats) is off by at
-// most 2^-11, a quarter of the step of the bf16 output, independently from key to key;
+// most 2^-11, an eighth of a step of the bf16 output, independently from key to key;
 // further down by at most 2^-40 of the largest.
 //
-// What bounds it: the cache's bytes, 2 D per key and KV head.  The rows of one
-// KV head are few, so the codes are converted in registers as they are used
+// What it cannot do without: the cache's bytes, 2 D per key and KV head.  The rows
+// of one KV head are few, so the codes are converted in registers as they are used
 // (int8 -> exact fp16, ~10 instructions per 8 codes) and multiplied by
 // mma.m16n8k16: at 16 rows a 128-key tile costs ~510 tensor cycles and ~400
-// issue cycles of an SM against ~1460 cycles of its share of HBM.  Measured: one
-// token over 4K rows of 8 KV heads 9.5 us (launch, first tiles and the cluster's
-// join; floor 1.3), four tokens for 16 sequences of 0.2 to 4.5K rows 26.7 us = 2.9
-// TB/s (floor 11.8).
+// issue cycles of an SM against ~1460 cycles of its share of HBM.  What bounds it:
+// a warp's chain (scores, maximum, exponentials, PV) a step of 32 keys at two warps a
+// scheduler.  Measured: one token over 4K rows of 8 KV heads 9.6 us (launch, first
+// tiles and the cluster's join; floor 1.3), four tokens for 16 sequences of 0.2 to
+// 4.5K rows 27.0 us = 2.9 TB/s (floor 11.8, 42% of DRAM's time).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,7 +37,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kTreeWarpStep;  // keys per warp step
 constexpr int kHead = 15;             // of the exponentials' reference (tree_head)
 // Shares a head, on average, from which four warps join a row.  One against four warps,
-// us: 2.4 shares 26.7 / 27.6 (16 sequences of 0.2 to 4.5K rows), 4.8 shares 61.5 / 59.5
+// us: 2.4 shares 26.7 / 27.6 (d = 128; 16 sequences of 0.2 to 4.5K rows), 4.8 shares 61.5 / 59.5
 // (64 heads of 5K to 32K), 38 shares 31.3 / 22.5 (8 heads of 32K).
 constexpr int kJoinShares = 4;
 constexpr int kRing = 3;   // stages of a warp's ring (K and V of one step each)

@@ -272,7 +272,10 @@ def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     trees given by their parents: parents[b, j] is the draft that j continues
     (any i < j), -1 if j continues the last cached token, -2 for a padding entry,
     which sees nothing and is seen by no other draft.  Set-up in plain tensor
-    operations, on the parents' device."""
+    operations, on the parents' device: it reads two truth values back to refuse bad
+    parents, so on a GPU it waits for them and cannot be captured in a graph.  A loop
+    whose trees keep their shape calls it once; one whose trees change gives it the
+    parents on the CPU and copies the words (at most 2 KB a sequence)."""
     B, T = parents.shape
     j = torch.arange(T, device=parents.device)
     if bool(((parents < -2) | (parents >= j)).any()):
