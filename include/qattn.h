@@ -581,6 +581,130 @@ qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const 
                             float* weights_out, int32_t* kept, int32_t* lengths_out,
                             float* v_code_amax, qattn_stream_t stream);
 
+/* Rotary positions, and serving from a paged 8-bit KV cache (the pages have no
+ * counterpart).  A pair of channels (x1, x2) of a token at position p turns by the
+ * angles of the table's row p:
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s   (fp32, each product and sum rounded)
+ * The table is made once, in 64 bits; what a long context asks of the angles
+ * (interpolation, a ramp over the wavelengths, a factor on both) is in its values. */
+typedef enum {
+  QATTN_ROPE_HALF = 0,        /* channel i pairs with i + rot_dim / 2             */
+  QATTN_ROPE_INTERLEAVED = 1  /* channel 2 i pairs with 2 i + 1                   */
+} qattn_rope_layout;
+
+typedef struct {
+  const float* table;   /* device, 16-byte aligned: [n_positions][rot_dim], the
+                           rot_dim / 2 cosines, then the sines                    */
+  int64_t n_positions;  /* rows of the table                                      */
+  int32_t rot_dim;      /* leading channels that turn: a multiple of 8, <= d; the
+                           others stay as they are                                */
+  int32_t layout;       /* qattn_rope_layout                                      */
+  int32_t inverse;      /* 1: turn back (the gradient of the rotation)            */
+} qattn_rope;
+
+/* Rotate X into Y.  The gradient of the rotated tensor is rotated back by the same
+ * call with rope->inverse = 1.
+ *   X, x_strides  [B][H][T][d], QATTN_BF16 or QATTN_F32 (dtype); strides as in the
+ *                 conventions (NULL = dense)
+ *   positions     NULL (token t at position t), or int32 [B][T], device
+ *   Y (out)       [B][H][T][d], the same type, dense; X itself if X is dense
+ * A token whose position is outside the table is not written and reported:
+ * qattn_get_error() returns QATTN_ERR_INVALID_ARG.  Limits: d in {32, 64, 128},
+ * B <= 65535, H <= 65535, B * T < 2^31. */
+qattn_status qattn_rotate(const void* X, const int64_t* x_strides, qattn_dtype dtype, int64_t B,
+                          int64_t H, int64_t T, int64_t d, const int32_t* positions,
+                          const qattn_rope* rope, void* Y, qattn_stream_t stream);
+
+/* A paged 8-bit KV cache: a pool of pages of page_size rows that sequences share,
+ *   k_pages, v_pages    [n_pages][Hkv][page_size][d] codes (16-byte aligned)
+ *   k_scales, v_scales  fp32 [n_pages][Hkv]: the value of a code is code * scale
+ *   page_table          int32 [B][max_pages]: row r of sequence b lies in page
+ *                       page_table[b][r / page_size], row r % page_size; entries past
+ *                       the rows in use are not read */
+typedef struct {
+  int64_t n_pages;
+  int64_t page_size;   /* 32, 64 or 128                                           */
+  int64_t max_pages;   /* entries of a sequence in the page table                 */
+  int32_t code_dtype;  /* QATTN_I8 or QATTN_E4M3                                  */
+} qattn_paging;
+
+/* Enter new tokens in a paged cache, K rotated on the way; their Q rotated beside
+ * them (Q and Q_out both or neither).  Token t < n_new[b] of sequence b becomes row
+ * lengths[b] - n_new[b] + t, so `lengths` counts the new tokens already.  Per page
+ * and KV head, with a = the largest magnitude of the new rows (K's rotated) and
+ * top = 127 or 448:
+ *   a page without rows of the sequence before these:  s = fp32(a * fp32(1 / top)),
+ *          0 if a < 2^-64
+ *   else:  s = its scale, doubled as often as a > fp32(top s) asks (a scale of 0 or
+ *          below 2^-100 starts anew, its rows' codes 0); the codes of the rows that were there are divided
+ *          along and rounded (half to even; e4m3 as the type rounds)
+ *   code = clamp(rint(x inv), -127, 127), or e4m3(x inv) saturated;  inv = fp32(1 / s)
+ * Doublings keep what an old row loses to rounding below one step in all, however
+ * often its page's scale grows.  A page that meets a value that is not finite gets
+ * the scale NaN for good (codes of 0); qattn_paged_fwd then gives NaN to every row
+ * that sees one of the page's keys.
+ *   Q, K, V        bf16 [B][Hq or Hkv][T][d], strides as in the conventions
+ *   shape          Nq = T, Nk = most rows in use (<= max_pages * page_size)
+ *   lengths        int32 [B], device: rows in use, the new ones among them
+ *   n_new          NULL (T everywhere), or int32 [B], device, 0 .. T
+ *   positions      NULL (token's row), or int32 [B][T], device
+ *   rope           NULL (K and Q as they are), or the rotation
+ *   Q_out (out)    bf16 [B][Hq][T][d]; rows t >= n_new[b] are left as they were
+ * The pages that a call writes belong to one sequence each (a page shared with
+ * another is copied first).  A sequence whose length or n_new is out of range is left
+ * as it is; so are the rows of a page that is not in 0 .. n_pages - 1 and tokens
+ * whose position is outside the table.  Each is reported: qattn_get_error() returns
+ * QATTN_ERR_INVALID_ARG.  Limits: d in {64, 128}, n_pages * Hkv <= 2^31 - 1, T <=
+ * 65534 * page_size.  No workspace. */
+qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, const uint16_t* K,
+                                const int64_t* k_strides, const uint16_t* V,
+                                const int64_t* v_strides, const qattn_shape* shape,
+                                const int32_t* lengths, const int32_t* n_new,
+                                const int32_t* positions, const qattn_rope* rope,
+                                const qattn_paging* paging, const int32_t* page_table,
+                                uint16_t* Q_out, void* k_pages, void* v_pages, float* k_scales,
+                                float* v_scales, qattn_stream_t stream);
+
+/* Attention over a paged cache: single tokens, a few, a prompt's chunk or a whole
+ * prompt, whose rows are in the cache (qattn_paged_append first).  Token t < n_new[b]
+ * of sequence b stands at row p = lengths[b] - n_new[b] + t and sees every row in
+ * use, or (params->causal) the rows up to p:
+ *   t = sm_scale * s_k * (q . kc);  O = sum e^t s_v vc / sum e^t;  lse = log sum e^t
+ * q is taken as it is, the codes as they are, sums and statistics are fp32; e^t s_v
+ * is rounded once, to fp16, relative to the row's largest (11 bits down to 2^-29 of
+ * it, absolute beyond).  V scales lie within 2^-48 and 2^48: a smaller one counts as 0.
+ * A row that sees nothing gives O = 0 and lse = -inf; one that sees a key through a
+ * scale that is negative or not finite or a V scale above 2^48, or whose q is not
+ * finite, gives NaN for both.
+ *   Q              bf16 [B][Hq][T][d], strides as in the conventions
+ *   shape          Nq = T, Nk = most rows in use (<= max_pages * page_size)
+ *   params         causal, out_dtype, sm_scale (0 -> 1 / sqrt(d)); q_pos0 must be
+ *                  QATTN_POS0_BOTTOM_RIGHT, pv_mode 0, kv_capacity 0
+ *   lengths        int32 [B], device, 0 .. Nk
+ *   n_new          NULL (T everywhere), or int32 [B], device, 0 .. T
+ *   O, lse (out)   [B][Hq][T][d] and (nullable) fp32 [B][Hq][T]; rows t >= n_new[b]
+ *                  are left as they were
+ *   workspace      at least qattn_paged_workspace_size() bytes; calls that may
+ *                  overlap need one each
+ * The order of the additions depends on the shape and the lengths alone: equal calls
+ * give equal bits.  A length or n_new out of range is clamped and a page that is not
+ * in 0 .. n_pages - 1 hidden; both are reported: qattn_get_error() returns
+ * QATTN_ERR_INVALID_ARG.  Codes of rows in use are numbers (e4m3: no NaN).  Limits: d
+ * in {64, 128}, n_pages * Hkv <= 2^31 - 1, T * Hq / Hkv < 2^31 - 256, fewer than 2^31
+ * steps of work (of 32 keys x 16 rows or 128 x 128; a block of rows starts as up to 18). */
+qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const qattn_shape* shape,
+                             const qattn_params* params, const int32_t* lengths,
+                             const int32_t* n_new, const qattn_paging* paging,
+                             const int32_t* page_table, const void* k_pages, const void* v_pages,
+                             const float* k_scales, const float* v_scales, void* O, float* lse,
+                             void* workspace, size_t workspace_bytes, qattn_stream_t stream);
+
+/* Bytes of workspace qattn_paged_fwd accepts for this shape and parameters (0: none is
+ * needed, or the problem is empty or unsupported).  It does not shrink as Nk grows.
+ * Host only. */
+size_t qattn_paged_workspace_size(const qattn_shape* shape, const qattn_params* params,
+                                  const qattn_paging* paging);
+
 /* a4 alone (debug) -- the int32 score tiles S = q_codes . k_codes^T
  * ("QFlash", eq. (3)), through the same tensor-core path as qattn_fwd.
  *   S (out) int32 [B][Hq][Nq][Nk]
@@ -615,8 +739,8 @@ qattn_status qattn_debug_bounds_probe(qattn_stream_t stream);
 
 /* Synchronises `stream`, then returns and clears the device error word of
  * the current device (QATTN_ERR_TIMEOUT if a kernel gave up on a wait,
- * QATTN_ERR_INVALID_ARG if a kernel found device-held scales, lengths or paths
- * outside its domain). */
+ * QATTN_ERR_INVALID_ARG if a kernel found device-held scales, lengths, paths, pages
+ * or positions outside its domain). */
 qattn_status qattn_get_error(qattn_stream_t stream);
 
 /* Failure-path check (debug; no counterpart on the pages): one thread runs

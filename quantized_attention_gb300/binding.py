@@ -23,6 +23,7 @@ FWD_AUTO, FWD_TC, FWD_SHORT = 0, 1, 2
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_BOUNDS = 1, 2, 3, 4, 5, 6
 GRAN_TENSOR, GRAN_HEAD, GRAN_BLOCK = 0, 1, 2
 DT_BF16, DT_F32, DT_I8, DT_E4M3 = 0, 1, 2, 3
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 POS0_BOTTOM_RIGHT = -(2 ** 63)
 PV_E4M3, PV_INT8 = 0, 1
 
@@ -34,7 +35,8 @@ EXPORTED = (
     "qattn_fwd_kernel_choice", "qattn_prepare_launches", "qattn_debug_wait_timeout",
     "qattn_peak_loop", "qattn_kv_header_init", "qattn_checked", "qattn_debug_bounds_probe",
     "qattn_tree_decode", "qattn_tree_workspace_size", "qattn_tree_commit", "qattn_kv_weights",
-    "qattn_kv_evict",
+    "qattn_kv_evict", "qattn_rotate", "qattn_paged_append", "qattn_paged_fwd",
+    "qattn_paged_workspace_size",
 )
 
 
@@ -55,6 +57,18 @@ class Params(ctypes.Structure):
                 ("q_pos0", ctypes.c_int64), ("sm_scale", ctypes.c_float),
                 ("pv_mode", ctypes.c_int32), ("bias_head_stride", ctypes.c_int64),
                 ("kv_capacity", ctypes.c_int64), ("fwd_kernel", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    """qattn_rope; keeps its table alive (make_rope)."""
+    _fields_ = [("table", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("inverse", ctypes.c_int32)]
+
+
+class Paging(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("code_dtype", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -98,6 +112,12 @@ def lib() -> ctypes.CDLL:
     L.qattn_tree_commit.argtypes = [vp] * 6 + [i64] * 5 + [vp] * 14
     L.qattn_kv_weights.argtypes = [vp] * 6 + [PS, PP, vp, vp, vp]
     L.qattn_kv_evict.argtypes = [vp] * 4 + [i64] * 8 + [vp, vp, i64, vp, vp, vp, vp, vp]
+    PR, PG = ctypes.POINTER(Rope), ctypes.POINTER(Paging)
+    L.qattn_rotate.argtypes = [vp, vp, ctypes.c_int, i64, i64, i64, i64, vp, PR, vp, vp]
+    L.qattn_paged_append.argtypes = [vp] * 6 + [PS] + [vp] * 3 + [PR, PG] + [vp] * 7
+    L.qattn_paged_fwd.argtypes = [vp, vp, PS, PP, vp, vp, PG] + [vp] * 8 + [sz, vp]
+    L.qattn_paged_workspace_size.argtypes = [PS, PP, PG]
+    L.qattn_paged_workspace_size.restype = sz
     L.qattn_get_error.argtypes = [vp]
     L.qattn_debug_wait_timeout.argtypes = [vp, vp]
     L.qattn_fwd_kernel_choice.argtypes = [PS, PP]
@@ -115,7 +135,8 @@ def lib() -> ctypes.CDLL:
                  "qattn_debug_qk_scores", "qattn_get_error", "qattn_quantize_v_noalloc",
                  "qattn_prepare", "qattn_debug_wait_timeout", "qattn_kv_header_init",
                  "qattn_debug_bounds_probe", "qattn_tree_decode", "qattn_tree_commit",
-                 "qattn_kv_weights", "qattn_kv_evict"):
+                 "qattn_kv_weights", "qattn_kv_evict", "qattn_rotate", "qattn_paged_append",
+                 "qattn_paged_fwd"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -516,6 +537,123 @@ def kv_evict(k_codes, v_codes, weights, budget, k_out, v_out, weights_out, kept,
         _stream_handle(stream, dev))
     if st != OK:
         raise QattnError(st, "qattn_kv_evict")
+
+
+def make_rope(table, *, interleaved=False, inverse=False) -> Rope:
+    """A rotation by a table fp32 [positions, rot_dim] (rot_dim / 2 cosines, then the
+    sines; pipeline.rope_table makes one): pairs rot_dim / 2 apart, or neighbours."""
+    _dense(table, torch.float32, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D [positions, rot_dim]")
+    r = Rope(table.data_ptr(), table.shape[0], table.shape[1],
+             ROPE_INTERLEAVED if interleaved else ROPE_HALF, int(bool(inverse)))
+    r.tensor, r.device = table, table.get_device()
+    return r
+
+
+def make_paging(n_pages, page_size, max_pages, code_dtype=DT_I8) -> Paging:
+    return Paging(int(n_pages), int(page_size), int(max_pages), code_dtype)
+
+
+def _rope_on(rope, dev: int):
+    if rope is not None and rope.device != dev:
+        raise ValueError(f"the rope's table is on cuda:{rope.device}, not on the current device")
+    return rope
+
+
+def _strided_ptr(dev: int, name: str, t, dtype, shape):
+    """_input_ptr for an input of this type."""
+    if t is None or t.shape != shape or t.get_device() != dev:
+        _reject(name, t, dtype, shape, dev)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    return t.data_ptr(), None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
+
+
+def rotate(X, Y, rope, *, positions=None, stream=None):
+    """Rotary positions: X [B, H, T, d] (bf16 or fp32, any strides) rotated into the
+    dense Y (see qattn_rotate in include/qattn.h).  positions: int32 [B, T] (None:
+    token t at t).  With an inverse rope: the gradient of the rotation."""
+    if X is None or X.dim() != 4:
+        raise ValueError("X must be 4-D [B, H, T, d]")
+    if X.dtype is not torch.bfloat16 and X.dtype is not torch.float32:
+        raise TypeError(f"X: expected torch.bfloat16 or torch.float32, got {X.dtype}")
+    if rope is None:
+        raise ValueError("rope is missing")
+    shape = B, H, T, d = X.shape
+    dev = torch.cuda.current_device()
+    x, xst = _strided_ptr(dev, "X", X, X.dtype, shape)
+    st = lib().qattn_rotate(
+        x, xst, DT_BF16 if X.dtype is torch.bfloat16 else DT_F32, B, H, T, d,
+        None if positions is None else _ptr("positions", positions, torch.int32, (B, T), dev),
+        _rope_on(rope, dev), _ptr("Y", Y, X.dtype, shape, dev), _stream_handle(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_rotate")
+
+
+def _pool_ptrs(dev: int, shape: Shape, paging: Paging, page_table, lengths, n_new, k_pages, v_pages,
+               k_scales, v_scales):
+    """Addresses of a paged cache's arrays, in the C calls' order."""
+    B, i32, f32 = shape.B, torch.int32, torch.float32
+    code = torch.int8 if paging.code_dtype == DT_I8 else torch.uint8
+    pool, heads = (paging.n_pages, shape.Hkv, paging.page_size, shape.d), (paging.n_pages, shape.Hkv)
+    return (_ptr("lengths", lengths, i32, (B,), dev),
+            None if n_new is None else _ptr("n_new", n_new, i32, (B,), dev),
+            _ptr("page_table", page_table, i32, (B, paging.max_pages), dev),
+            _ptr("k_pages", k_pages, code, pool, dev), _ptr("v_pages", v_pages, code, pool, dev),
+            _ptr("k_scales", k_scales, f32, heads, dev), _ptr("v_scales", v_scales, f32, heads, dev))
+
+
+def paged_append(K, V, shape, paging, page_table, lengths, k_pages, v_pages, k_scales, v_scales, *,
+                 n_new=None, positions=None, rope=None, Q=None, Q_out=None, stream=None):
+    """New tokens entered in a paged cache, K rotated on the way and Q (if given)
+    rotated into Q_out (see qattn_paged_append in include/qattn.h).  K, V: bf16 [B,
+    Hkv, T, d], Q: bf16 [B, Hq, T, d], any strides; lengths: int32 [B], rows in use
+    with the new ones; pages: int8 (DT_I8) or uint8 (DT_E4M3) [n_pages, Hkv, page, d],
+    scales fp32 [n_pages, Hkv]; page_table: int32 [B, max_pages]."""
+    B, Hkv, T, d = shape.B, shape.Hkv, shape.Nq, shape.d
+    dev = torch.cuda.current_device()
+    bf16 = torch.bfloat16
+    k, kst = _strided_ptr(dev, "K", K, bf16, (B, Hkv, T, d))
+    v, vst = _strided_ptr(dev, "V", V, bf16, (B, Hkv, T, d))
+    q = qst = qo = None
+    if Q is not None or Q_out is not None:
+        if Q is None or Q_out is None:
+            raise ValueError("Q and Q_out go together")
+        q, qst = _strided_ptr(dev, "Q", Q, bf16, (B, shape.Hq, T, d))
+        qo = _ptr("Q_out", Q_out, bf16, (B, shape.Hq, T, d), dev)
+    n, nn, pt, kp, vp, ks, vs = _pool_ptrs(dev, shape, paging, page_table, lengths, n_new, k_pages, v_pages,
+                                           k_scales, v_scales)
+    st = lib().qattn_paged_append(
+        q, qst, k, kst, v, vst, shape, n, nn,
+        None if positions is None else _ptr("positions", positions, torch.int32, (B, T), dev),
+        _rope_on(rope, dev), paging, pt, qo, kp, vp, ks, vs, _stream_handle(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_paged_append")
+
+
+def paged_workspace_size(shape: Shape, params: Params, paging: Paging) -> int:
+    return lib().qattn_paged_workspace_size(ctypes.byref(shape), ctypes.byref(params), ctypes.byref(paging))
+
+
+def paged_fwd(Q, shape, params, paging, page_table, lengths, k_pages, v_pages, k_scales, v_scales, O, lse,
+              workspace, *, n_new=None, stream=None):
+    """Attention of the last n_new[b] (None: T) rows of each sequence over a paged
+    cache (see qattn_paged_fwd in include/qattn.h).  Q: bf16 [B, Hq, T, d], any
+    strides; the cache as for paged_append."""
+    B, Hq, T, d = shape.B, shape.Hq, shape.Nq, shape.d
+    dev = torch.cuda.current_device()
+    rows = (B, Hq, T, d)
+    q, qst = _strided_ptr(dev, "Q", Q, torch.bfloat16, rows)
+    n, nn, pt, kp, vp, ks, vs = _pool_ptrs(dev, shape, paging, page_table, lengths, n_new, k_pages, v_pages,
+                                           k_scales, v_scales)
+    st = lib().qattn_paged_fwd(
+        q, qst, shape, params, n, nn, paging, pt, kp, vp, ks, vs,
+        _ptr("O", O, torch.bfloat16 if params.out_dtype == DT_BF16 else torch.float32, rows, dev),
+        None if lse is None else _ptr("lse", lse, torch.float32, (B, Hq, T), dev),
+        _workspace_ptr(dev, workspace), _nbytes(workspace), _stream_handle(stream, dev))
+    if st != OK:
+        raise QattnError(st, "qattn_paged_fwd")
 
 
 def debug_qk_scores(q_codes, k_codes, shape, S, workspace, stream=None):

@@ -1,0 +1,520 @@
+// Attention over a paged 8-bit KV cache (qattn_paged_fwd), warp-level kernel: 16
+// query rows (token, query head of the KV group) at a time against the cached codes.
+//
+// Mathematics.  Q's rows are brought to fp16 by a power of two each (exact, see
+// pg_row_shift), the codes of K and V are exact in fp16 (|int8| <= 127, e4m3 <= 448),
+// so S = q . k is a sum of exact products in fp32.  With a page's scales s_k, s_v:
+//   t = S c + log2 s_v,  c = row factor * s_k  (row factor: sm_scale log2 e and the
+//       row's power of two)
+//   P = 2^(t - m),  m a reference 15 below the running maximum of t
+//   O = sum P vc,   l = sum P / s_v,   out = O / l,   lse = ln 2 (m + log2 l)
+// The V scale rides in the exponent: P, rounded once to fp16 for the PV product, keeps
+// its eleven bits where P s_v, the key's part in O, is down to 2^-29 of the row's
+// largest, and no key costs an instruction more than with one scale for all.  l sums
+// the unrounded P in fp32.  Parts of a row (steps of 32 keys dealt to warps, shares of
+// steps dealt to CTAs) are joined by 2^(m_part - m).
+//
+// What it cannot do without: the cache's bytes, 2 D per key and KV head.  A step lies in
+// one page (pages of 32, 64 or 128 rows): one TMA box each for K and V at the page's
+// plane of the pool.  A warp looks up the pages and scales of its next 32 steps at once,
+// one a lane, ahead of their use.
+#include "paged_common.cuh"
+
+namespace qattn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = kPagedWarpStep;
+constexpr int kRows = kPagedRows;
+constexpr int kHead = 15;  // of the exponentials' reference (pg_head)
+constexpr int kRing = 3;   // stages of a warp's ring (K and V of one step each)
+// Shares a block, on average, from which four warps join a row.
+constexpr int kJoinShares = 4;
+
+template <int D>
+struct WarpSmem {
+  static constexpr int kTile = kStep * D;  // bytes of a step's K (or V) codes
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kWarp = kRing * kStage;   // one warp's ring
+  static constexpr int kShare = kWarps * kWarp;  // a CTA's O for its cluster
+  static constexpr int kBytes = kShare + kRows * D * 4 + 1024;
+  static_assert(kRows * D * 4 <= kWarp, "a warp's O does not fit its ring");
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile stored with the 128-byte
+// (D = 128) or 64-byte (D = 64) swizzle.
+template <int D>
+__device__ __forceinline__ int swz(int r, int c) {
+  return r * D + 16 * (c ^ ((D == 128) ? (r & 7) : ((r >> 1) & 3)));
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes of a word -> two f16x2, exact.
+template <bool E4M3>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E4M3) {
+    lo = e4m3x2_to_f16x2(w & 0xffffu);
+    hi = e4m3x2_to_f16x2(w >> 16);
+  } else {
+    codes4_to_f16x2(w, lo, hi);
+  }
+}
+// Words x, y (four channels of two keys) -> four f16x2 {x_e, y_e}, exact.
+template <bool E4M3>
+__device__ __forceinline__ void widen_pair(uint32_t x, uint32_t y, uint32_t (&o)[4]) {
+  widen4<E4M3>(__byte_perm(x, y, 0x5140u), o[0], o[1]);
+  widen4<E4M3>(__byte_perm(x, y, 0x7362u), o[2], o[3]);
+}
+
+// Place of 16-byte chunk c of row r of a warp's O in shared memory.
+template <int D>
+__device__ __forceinline__ int join_chunk(int r, int c) {
+  return c ^ (((c >> ((D == 128) ? 3 : 2)) & 3) + 4 * (r & 1));
+}
+
+// Pages and scales of a warp's next 32 steps, one a lane.
+struct Window {
+  int page;      // -1: no such page, its keys are hidden
+  float ks, vs;
+};
+
+// ------------------------------------------------------------------ attention
+// Each CTA takes an equal share of the flattened list of steps (sequence, KV head,
+// 16-row block, step), or (CL) its part of its cluster's block.  Each run of steps
+// inside one block is a segment; its steps go round the four warps, each with its own
+// ring of TMA tiles and its own (m, l, O), so the main loop has no CTA barrier.
+template <int D, bool E4M3, bool CL>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_warp_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const PagedArgs a) {
+  using SM = WarpSmem<D>;
+  constexpr int KS = D / 16;   // k-steps of QK^T = words of K a lane holds per key
+  constexpr int NT = D / 8;    // n-tiles of PV
+  constexpr int VW = NT / 4;   // V words a lane reads per key
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t full[kWarps][kRing];
+  __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
+  __shared__ float cl_m[kRows], cl_l[kRows];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  uint8_t* ring = smem + warp * SM::kWarp;
+  if (lane == 0) {
+    for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&full[warp][s]), 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      abort_flag = 0;
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
+  pdl_wait();
+  pdl_trigger();  // after the wait: the join reads the lengths before its own
+  PagedWalk walk;
+  PagedSeg sg;
+  bool some = true;  // CL: the block has rows
+  if constexpr (CL) some = pg_cluster_seg<kRows, kStep>(a, sg);
+  else walk = pg_walk<kRows, kStep>(a);
+  __syncthreads();  // the abort flag is set
+  uint32_t used = 0;  // tiles this warp has taken through its ring
+  uint32_t sent = 0;  // lane 0: those it has issued
+
+  while (CL ? some : pg_next<kRows, kStep>(a, walk, sg)) {
+    const int len = sg.seq.len;
+    // this warp's steps: sg.s0 + warp, + kWarps, ...
+    const int first = sg.s0 + warp;
+    const int ntile = first < sg.s1 ? (sg.s1 - first + kWarps - 1) / kWarps : 0;
+    auto key_of = [&](int i) { return (first + i * kWarps) * kStep; };
+    auto look_up = [&](int i0) {  // the window of tiles i0 .. i0 + 31
+      Window w{-1, 0.f, 0.f};
+      const int i = i0 + lane;
+      if (i < ntile) {
+        const int key = key_of(i), j = key >> a.page_shift;
+        if (key < len && QATTN_IN_BOUNDS(j < a.max_pages && sg.b < a.B)) {
+          const int p = a.page_table[static_cast<size_t>(sg.b) * a.max_pages + j];
+          if (p >= 0 && p < a.n_pages) {
+            const size_t sc = static_cast<size_t>(p) * a.Hkv + sg.hkv;
+            w.page = p;
+            w.ks = a.k_scales[sc];
+            w.vs = a.v_scales[sc];
+          } else {
+            atomicOr(a.err, kErrDomain);
+          }
+        }
+      }
+      return w;
+    };
+    Window cur = look_up(0), nxt{-1, 0.f, 0.f};
+    if (ntile > 32) nxt = look_up(32);
+    int base = 0;  // tile of cur's first lane
+    auto issue = [&](int i) {  // tile i of this warp (the whole warp calls)
+      const uint32_t q = used + i, slot = q % kRing;
+      const int pc = __shfl_sync(0xffffffffu, cur.page, (i - base) & 31);
+      const int pn = __shfl_sync(0xffffffffu, nxt.page, (i - base) & 31);
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&full[warp][slot]);
+        // a page that does not exist: any page of the pool stands in, its keys are hidden
+        const int page = max(i - base < 32 ? pc : pn, 0);
+        const int row = key_of(i) & ((1 << a.page_shift) - 1);
+        const int plane = page * a.Hkv + sg.hkv;
+        sent = q + 1;
+        (void)QATTN_IN_BOUNDS(page < a.n_pages && row >= 0 && row + kStep <= (1 << a.page_shift));  // TMA coordinates
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(SM::kStage));
+        tma_load_3d(smem_u32(ring + slot * SM::kStage), &tmK, bar, 0, row, plane);
+        tma_load_3d(smem_u32(ring + slot * SM::kStage + SM::kTile), &tmV, bar, 0, row, plane);
+      }
+    };
+    for (int i = 0; i < min(kRing - 1, ntile); ++i) issue(i);
+
+    // ---- this lane's rows g and g + 8 of the block: fp16 values, factor, key limit
+    uint32_t qa[KS][4];
+    float rf[2];
+    bool fin[2];
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rr = sg.rb * kRows + g + 8 * h;
+      const int tok = rr / a.G;
+      const bool in = tok < sg.seq.n;
+      const int hq = sg.hkv * a.G + rr - tok * a.G;
+      const uint16_t* src = a.q + sg.b * a.qsB + hq * a.qsH + tok * a.qsN + (D / 4) * t4;
+      uint4 x[D / 32];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && QATTN_IN_BOUNDS(sg.b < a.B && hq < a.Hq && tok < a.T))
+          x[k] = *reinterpret_cast<const uint4*>(src + 8 * k);
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      fin[h] = top < 0x7f800000u;  // else the row is NaN once it sees a key
+      float up, down;
+      pg_row_shift(top, up, down);
+      rf[h] = __fmul_rn(__fmul_rn(a.sm_scale, kPgLog2e), down);
+      lim[h] = in ? min(pg_limit(a, sg.seq, tok), len) : 0;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = fin[h] ? bf16_bits_to_f32(w[e] & 0xffffu) * up : 0.f;
+          const float hi = fin[h] ? __uint_as_float(w[e] & 0xffff0000u) * up : 0.f;
+          f[e] = pack_half2(lo, hi);
+        }
+        qa[2 * k][h] = f[0];
+        qa[2 * k][2 + h] = f[1];
+        qa[2 * k + 1][h] = f[2];
+        qa[2 * k + 1][2 + h] = f[3];
+      }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m[2] = {-kPgInf, -kPgInf}, l[2] = {0.f, 0.f};
+
+    for (int i = 0; i < ntile; ++i) {
+      if (i - base == 32) {
+        base = i;
+        cur = nxt;
+        if (i + 32 < ntile) nxt = look_up(i + 32);
+      }
+      if (i + kRing - 1 < ntile) issue(i + kRing - 1);
+      const int page = __shfl_sync(0xffffffffu, cur.page, i - base);
+      const PageScale ps = pg_scale(__shfl_sync(0xffffffffu, cur.ks, i - base),
+                                    __shfl_sync(0xffffffffu, cur.vs, i - base));
+      const uint32_t q = used + i, slot = q % kRing;
+      const bool ok = mbar_wait(smem_u32(&full[warp][slot]), (q / kRing) & 1, &abort_flag, a.err, kErrTimeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t* st = ring + slot * SM::kStage;
+      const int key = key_of(i);
+      int room[2];  // visible keys of the step
+      float cf[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        room[h] = page < 0 ? 0 : lim[h] - key;
+        bool f;
+        cf[h] = pg_factor(rf[h], ps.k, f);
+        if (room[h] > 0 && (ps.nan || !f)) fin[h] = false;
+      }
+      const bool masked = __any_sync(0xffffffffu, room[0] < kStep || room[1] < kStep);
+      // ---- scores
+      float s[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+        for (int w4 = 0; w4 < KS / 4; ++w4) {
+          const uint4 kw = *reinterpret_cast<const uint4*>(st + swz<D>(8 * j + g, (KS / 4) * t4 + w4));
+          const uint32_t kx[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1;
+            widen4<E4M3>(kx[e], b0, b1);
+            const uint32_t(&qv)[4] = qa[4 * w4 + e];
+            mma16816(s[j], qv[0], qv[1], qv[2], qv[3], b0, b1);
+          }
+        }
+      }
+      if (masked) {
+        const uint32_t vis[2] = {pg_first_bits(room[0]), pg_first_bits(room[1])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((vis[e >> 1] >> (8 * j + 2 * t4 + (e & 1))) & 1u)) s[j][e] = -kPgInf;
+      }
+      // ---- running maxima less kHead: max t = c max S + e (c > 0); -inf stays -inf
+      float al[2], ref[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = -kPgInf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x = fmax3(x, s[j][2 * h], s[j][2 * h + 1]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float top = fmaf(x, cf[h], ps.e_max);
+        const float mn = fmaxf(m[h], top - pg_head(top, kHead));
+        ref[h] = (mn == -kPgInf) ? 0.f : mn;
+        al[h] = (m[h] == -kPgInf) ? 0.f : ex2_approx(m[h] - ref[h]);
+        m[h] = mn;
+      }
+      if (!__all_sync(0xffffffffu, al[0] == 1.f && al[1] == 1.f)) {
+        l[0] *= al[0];
+        l[1] *= al[1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[n][0] *= al[0];
+          o[n][1] *= al[0];
+          o[n][2] *= al[1];
+          o[n][3] *= al[1];
+        }
+      }
+      uint32_t pa[4][2];
+      float sum[2] = {0.f, 0.f};
+      const float off[2] = {ps.e - ref[0], ps.e - ref[1]};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float pr[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(s[j][e], cf[e >> 1], off[e >> 1]));
+        sum[0] += pr[0] + pr[1];
+        sum[1] += pr[2] + pr[3];
+        pa[j][0] = pack_half2(pr[0], pr[1]) & ps.keep;
+        pa[j][1] = pack_half2(pr[2], pr[3]) & ps.keep;
+      }
+      l[0] = fmaf(sum[0], ps.inv, l[0]);
+      l[1] = fmaf(sum[1], ps.inv, l[1]);
+      // ---- O += P V
+      const uint8_t* sv = st + SM::kTile;
+      // rows behind the sequence may hold any byte: an e4m3 NaN there must not meet P = 0
+      const int rows = E4M3 && masked ? (page < 0 ? 0 : len - key) : kStep;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int kx = 16 * kk + 2 * t4 + (u & 1) + 8 * (u >> 1);
+          const uint8_t* src = sv + swz<D>(kx, (4 * VW * g) >> 4) + ((4 * VW * g) & 15);
+          if constexpr (VW == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src);
+            vw[u][0] = x.x;
+            vw[u][1] = x.y;
+            vw[u][2] = x.z;
+            vw[u][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(src);
+            vw[u][0] = x.x;
+            vw[u][1] = x.y;
+          }
+          if (E4M3 && kx >= rows) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vw[u][w] = 0u;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t b0[4], b1[4];
+          widen_pair<E4M3>(vw[0][w], vw[1][w], b0);
+          widen_pair<E4M3>(vw[2][w], vw[3][w], b1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mma16816(o[4 * w + e], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1],
+                     b0[e], b1[e]);
+        }
+      }
+      __syncwarp();  // the stage is read
+    }
+    used += ntile;
+
+    // ---- join the four warps (their rings are free)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // a row that saw a key through something not finite is NaN.  (The four lanes of a
+      // row agree: what they looked at is the same for all.)
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (!fin[h] && m[h] > -kPgInf) l[h] = __uint_as_float(0x7fffffffu);
+      if (t4 == 0) {
+        red_m[warp][g + 8 * h] = m[h];
+        red_l[warp][g + 8 * h] = l[h];
+      }
+    }
+    __syncthreads();
+    if (abort_flag) {  // a wait ran out (every thread sees it here)
+      // every load this warp issued lands before the CTA may exit
+      if (lane == 0)
+        for (uint32_t back = 1; back <= min(sent, static_cast<uint32_t>(kRing)); ++back) {
+          const uint32_t q = sent - back;
+          volatile int never = 0;
+          mbar_wait(smem_u32(&full[warp][q % kRing]), (q / kRing) & 1, &never, a.err, kErrTimeout);
+        }
+      break;
+    }
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = -kPgInf;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w][g + 8 * h]);
+      const float f = (m[h] == -kPgInf) ? 0.f : ex2_approx(m[h] - mx);
+      // n-tile n, column 2 t4 (+ 1) is channel NT * column + n; 16-byte chunks XORed
+      // so that the eight lanes of a store hit eight bank groups
+#pragma unroll
+      for (int cl = 0; cl < 2; ++cl) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+          const int ch = (NT * (2 * t4 + cl) + n) / 4;
+          *reinterpret_cast<float4*>(mine + (g + 8 * h) * D + 4 * join_chunk<D>(g, ch)) =
+              make_float4(o[n][2 * h + cl] * f, o[n + 1][2 * h + cl] * f, o[n + 2][2 * h + cl] * f,
+                          o[n + 3][2 * h + cl] * f);
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
+    float* share = reinterpret_cast<float*>(smem + SM::kShare);  // CL: this CTA's O, for the cluster
+    for (int idx = threadIdx.x; idx < kRows * (D / 4); idx += kThreads) {
+      const int r = idx / (D / 4), c = 4 * (idx % (D / 4));
+      float mx = -kPgInf, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w][r]);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = red_m[w][r];
+        lt += (mw == -kPgInf) ? 0.f : red_l[w][r] * ex2_approx(mw - mx);
+        const float4 y =
+            *reinterpret_cast<const float4*>(smem + w * SM::kWarp + 4 * (r * D + 4 * join_chunk<D>(r, c / 4)));
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      if constexpr (CL) {
+        *reinterpret_cast<float4*>(share + r * D + c) = x;
+        if (c == 0) {
+          cl_m[r] = mx;
+          cl_l[r] = lt;
+        }
+      } else if (whole) {
+        pg_write_out<D, kHead>(a, sg.b, sg.hkv, sg.seq.n, sg.rb * kRows + r, c, x, mx, lt);
+      } else if (QATTN_IN_BOUNDS(slot < a.slots)) {
+        *reinterpret_cast<float4*>(a.part_o + (slot * kRows + r) * D + c) = x;
+        if (c == 0) {
+          a.part_m[slot * kRows + r] = mx;
+          a.part_l[slot * kRows + r] = lt;
+        }
+      }
+    }
+    if constexpr (CL) break;
+    fence_proxy_async_smem();  // the rings go back to the TMA engine
+    __syncthreads();
+  }
+  if constexpr (CL) {
+    // ---- join the cluster: CTA `rank` writes rows rank, rank + cluster, ...  Every
+    // CTA reaches both barriers, one that gave up on a wait too
+    cluster_sync();
+    const int rank = static_cast<int>(cluster_rank());
+    for (int idx = threadIdx.x; some && idx < (kRows / a.cluster) * (D / 4); idx += kThreads) {
+      const int r = rank + a.cluster * (idx / (D / 4)), c = 4 * (idx % (D / 4));
+      if ((sg.rb * kRows + r) / a.G >= sg.seq.n) continue;
+      float mc[kPagedCluster], lc[kPagedCluster], mx = -kPgInf, lt = 0.f;
+      float4 y[kPagedCluster], x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kPagedCluster; ++q) {
+        mc[q] = -kPgInf;
+        if (q < a.cluster) {
+          mc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_m[r]), q)));
+          lc[q] = __uint_as_float(ld_cluster_u32(cluster_addr(smem_u32(&cl_l[r]), q)));
+          y[q] = ld_cluster_f4(cluster_addr(smem_u32(smem + SM::kShare) + 4 * (r * D + c), q));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kPagedCluster; ++q) mx = fmaxf(mx, mc[q]);
+#pragma unroll
+      for (int q = 0; q < kPagedCluster; ++q) {
+        if (mc[q] == -kPgInf) continue;
+        const float f = ex2_approx(mc[q] - mx);
+        lt = fmaf(f, lc[q], lt);
+        x.x = fmaf(f, y[q].x, x.x);
+        x.y = fmaf(f, y[q].y, x.y);
+        x.z = fmaf(f, y[q].z, x.z);
+        x.w = fmaf(f, y[q].w, x.w);
+      }
+      pg_write_out<D, kHead>(a, sg.b, sg.hkv, sg.seq.n, sg.rb * kRows + r, c, x, mx, lt);
+    }
+    cluster_sync();  // no CTA leaves while another reads its share
+  }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {
+  constexpr int smem = WarpSmem<D>::kBytes;
+  cudaError_t e;
+  if (a.cluster > 0) {
+    e = cudaFuncSetAttribute(paged_warp_kernel<D, E4M3, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_cluster(paged_warp_kernel<D, E4M3, true>, dim3(a.ctas), dim3(kThreads), a.cluster, smem, s, tk,
+                              tv, a);
+  }
+  e = cudaFuncSetAttribute(paged_warp_kernel<D, E4M3, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_warp_kernel<D, E4M3, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  const int blocks = a.B * a.Hkv * a.blocks;
+  if (a.ctas < kJoinShares * blocks)  // a block in few shares: a warp for a row
+    return launch_pdl(paged_join_kernel<D, kHead, kRows, kStep, 1>, dim3(blocks, kRows / 4), dim3(kPgJoinThreads), 0,
+                      s, a);
+  return launch_pdl(paged_join_kernel<D, kHead, kRows, kStep, 4>, dim3(blocks, kRows), dim3(kPgJoinThreads), 0, s, a);
+}
+
+}  // namespace
+
+unsigned int check_take_paged_warp() { return check_take_local(); }
+
+cudaError_t launch_paged_warp(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {
+  if (a.e4m3) return a.d == 64 ? launch_d<64, true>(tk, tv, a, s) : launch_d<128, true>(tk, tv, a, s);
+  return a.d == 64 ? launch_d<64, false>(tk, tv, a, s) : launch_d<128, false>(tk, tv, a, s);
+}
+
+}  // namespace qattn

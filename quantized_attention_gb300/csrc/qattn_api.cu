@@ -339,6 +339,63 @@ qattn_status tree_shape_ok(const qattn_shape* shape) {
   return QATTN_OK;
 }
 
+// qattn_paged_fwd's split, as TreeSplit.
+struct PagedSplit {
+  int cluster, step, rows, blocks, ctas, lead;
+  int64_t steps;
+  size_t slots, off_m, off_l, bytes;
+};
+PagedSplit paged_split(const qattn_shape* s) {
+  PagedSplit t{};
+  const int64_t R = s->Hq / s->Hkv * s->Nq;
+  t.step = qattn::kPagedWarpStep;
+  t.rows = qattn::kPagedRows;
+  const int64_t blocks = (R + t.rows - 1) / t.rows, heads = s->B * s->Hkv * blocks;
+  const int64_t head_steps = std::max<int64_t>(1, (s->Nk + t.step - 1) / t.step);
+  t.blocks = static_cast<int>(blocks);
+  t.lead = qattn::kPagedWarpLead;
+  t.steps = heads * (t.lead + head_steps);
+  t.cluster = qattn::tree_cluster(heads, head_steps);
+  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(qattn::kPagedWarpCtas, (t.steps + 3) / 4)));
+  if (t.cluster > 0 && heads * t.cluster >= (int64_t{1} << 31)) t.cluster = 0;
+  if (t.cluster > 0) {
+    t.ctas = static_cast<int>(heads * t.cluster);
+    t.lead = 0;
+  }
+  t.slots = t.cluster > 0 ? 0 : 2 * static_cast<size_t>(t.ctas);
+  t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
+  t.off_l = t.off_m + align256(t.slots * t.rows * 4);
+  t.bytes = t.off_l + align256(t.slots * t.rows * 4);
+  return t;
+}
+
+// The shape of a paged cache's calls: a bad pool is an invalid argument.
+qattn_status paged_ok(const qattn_shape* shape, const qattn_paging* g) {
+  const qattn_status st = check_shape(shape);
+  if (st != QATTN_OK) return st;
+  if (!g || g->n_pages < 1 || g->max_pages < 0 || g->max_pages > (int64_t{1} << 30)) return QATTN_ERR_INVALID_ARG;
+  if (g->code_dtype != QATTN_I8 && g->code_dtype != QATTN_E4M3) return QATTN_ERR_INVALID_ARG;
+  if (g->page_size != 32 && g->page_size != 64 && g->page_size != 128) return QATTN_ERR_UNSUPPORTED;
+  if (shape->d != 64 && shape->d != 128) return QATTN_ERR_UNSUPPORTED;
+  if (shape->Nk > g->max_pages * g->page_size) return QATTN_ERR_INVALID_ARG;
+  if (g->n_pages > ((int64_t{1} << 31) - 1) / shape->Hkv) return QATTN_ERR_UNSUPPORTED;
+  if (shape->Hq / shape->Hkv * shape->Nq >= (int64_t{1} << 31) - 256) return QATTN_ERR_UNSUPPORTED;
+  return QATTN_OK;
+}
+int page_shift_of(const qattn_paging* g) { return g->page_size == 32 ? 5 : g->page_size == 64 ? 6 : 7; }
+
+// A rotation of heads of d channels (rope not null).
+qattn_status rope_args(const qattn_rope* r, int64_t d, qattn::RopeArgs* out) {
+  if (!r->table || !aligned16(r->table) || r->n_positions < 0 || r->rot_dim < 8 || r->rot_dim % 8 != 0 ||
+      r->rot_dim > d || (r->layout != QATTN_ROPE_HALF && r->layout != QATTN_ROPE_INTERLEAVED) ||
+      (r->inverse != 0 && r->inverse != 1))
+    return QATTN_ERR_INVALID_ARG;
+  if (r->n_positions >= (int64_t{1} << 31)) return QATTN_ERR_UNSUPPORTED;
+  *out = qattn::RopeArgs{r->table, static_cast<int>(r->n_positions), r->rot_dim, r->layout == QATTN_ROPE_INTERLEAVED,
+                         r->inverse};
+  return QATTN_OK;
+}
+
 // Map over int8 cache codes [planes][cap][d], rows 0 .. rows-1 in use, boxes of
 // box_rows rows; 128-byte swizzle for d = 128, 64-byte for d = 64.
 bool encode_cache(CUtensorMap* map, const void* ptr, int64_t planes, int64_t rows, int64_t cap,
@@ -1215,6 +1272,186 @@ qattn_status qattn_kv_evict(const int8_t* k_codes, const int8_t* v_codes, const 
   return from_cuda(qattn::launch_kv_evict(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+qattn_status qattn_rotate(const void* X, const int64_t* x_strides, qattn_dtype dtype, int64_t B,
+                          int64_t H, int64_t T, int64_t d, const int32_t* positions,
+                          const qattn_rope* rope, void* Y, qattn_stream_t stream) {
+  if (B < 0 || H < 0 || T < 0 || d <= 0 || !rope || (dtype != QATTN_BF16 && dtype != QATTN_F32))
+    return QATTN_ERR_INVALID_ARG;
+  if (!valid_d(d) || B > 65535 || H > 65535 || T >= (int64_t{1} << 31) || B * T >= (int64_t{1} << 31))
+    return QATTN_ERR_UNSUPPORTED;
+  qattn::RotateArgs a{};
+  const qattn_status st = rope_args(rope, d, &a.rope);
+  if (st != QATTN_OK) return st;
+  if (B == 0 || H == 0 || T == 0) return QATTN_OK;
+  if (!X || !aligned16(X) || !Y || !aligned16(Y) || !aligned_to(positions, 4)) return QATTN_ERR_INVALID_ARG;
+  qattn::Src xs;
+  if (!make_src(X, x_strides, H, T, d, dtype == QATTN_BF16 ? 2 : 4, &xs)) return QATTN_ERR_INVALID_ARG;
+  if (X == Y && !is_dense(x_strides, H, T, d)) return QATTN_ERR_INVALID_ARG;
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(B);
+  a.H = static_cast<int>(H);
+  a.T = static_cast<int>(T);
+  a.d = static_cast<int>(d);
+  a.f32 = dtype == QATTN_F32;
+  a.x = X;
+  a.xsB = xs.sB;
+  a.xsH = xs.sH;
+  a.xsN = xs.sN;
+  a.y = Y;
+  a.positions = positions;
+  QATTN_LOG_LINE("qattn_rotate B=%d H=%d T=%d d=%d rot=%d: rotate_kernel", a.B, a.H, a.T, a.d, a.rope.rot);
+  return from_cuda(qattn::launch_rotate(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, const uint16_t* K,
+                                const int64_t* k_strides, const uint16_t* V,
+                                const int64_t* v_strides, const qattn_shape* shape,
+                                const int32_t* lengths, const int32_t* n_new,
+                                const int32_t* positions, const qattn_rope* rope,
+                                const qattn_paging* paging, const int32_t* page_table,
+                                uint16_t* Q_out, void* k_pages, void* v_pages, float* k_scales,
+                                float* v_scales, qattn_stream_t stream) {
+  qattn_status st = paged_ok(shape, paging);
+  if (st != QATTN_OK) return st;
+  if ((shape->Nq + paging->page_size - 2) / paging->page_size + 1 > 65535) return QATTN_ERR_UNSUPPORTED;
+  qattn::PagedAppendArgs a{};
+  if (rope && (st = rope_args(rope, shape->d, &a.rope)) != QATTN_OK) return st;
+  if ((Q == nullptr) != (Q_out == nullptr)) return QATTN_ERR_INVALID_ARG;
+  if (shape->B == 0 || shape->Nq == 0) return QATTN_OK;
+  if (!K || !aligned16(K) || !V || !aligned16(V) || !aligned16(Q) || !aligned16(Q_out) || !lengths ||
+      !aligned_to(lengths, 4) || !aligned_to(n_new, 4) || !aligned_to(positions, 4) || !page_table ||
+      !aligned_to(page_table, 4) || !k_pages || !aligned16(k_pages) || !v_pages || !aligned16(v_pages) ||
+      !k_scales || !aligned_to(k_scales, 4) || !v_scales || !aligned_to(v_scales, 4))
+    return QATTN_ERR_INVALID_ARG;
+  qattn::Src qs{}, ks, vs;
+  if (!make_src(K, k_strides, shape->Hkv, shape->Nq, shape->d, 2, &ks) ||
+      !make_src(V, v_strides, shape->Hkv, shape->Nq, shape->d, 2, &vs) ||
+      (Q && !make_src(Q, q_strides, shape->Hq, shape->Nq, shape->d, 2, &qs)))
+    return QATTN_ERR_INVALID_ARG;
+  if (Q == Q_out && Q && !is_dense(q_strides, shape->Hq, shape->Nq, shape->d)) return QATTN_ERR_INVALID_ARG;
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(shape->B);
+  a.Hq = static_cast<int>(shape->Hq);
+  a.Hkv = static_cast<int>(shape->Hkv);
+  a.T = static_cast<int>(shape->Nq);
+  a.Nk = static_cast<int>(shape->Nk);
+  a.d = static_cast<int>(shape->d);
+  a.n_pages = static_cast<int>(paging->n_pages);
+  a.page_shift = page_shift_of(paging);
+  a.max_pages = static_cast<int>(paging->max_pages);
+  a.e4m3 = paging->code_dtype == QATTN_E4M3;
+  a.q = Q;
+  a.k = K;
+  a.v = V;
+  a.qsB = qs.sB;
+  a.qsH = qs.sH;
+  a.qsN = qs.sN;
+  a.ksB = ks.sB;
+  a.ksH = ks.sH;
+  a.ksN = ks.sN;
+  a.vsB = vs.sB;
+  a.vsH = vs.sH;
+  a.vsN = vs.sN;
+  a.lengths = lengths;
+  a.n_new = n_new;
+  a.positions = positions;
+  a.page_table = page_table;
+  a.q_out = Q_out;
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  char sb[128];
+  QATTN_LOG_LINE("qattn_paged_append %s page=%d rot=%d: paged_append_kernel", shape_str(shape, sb, sizeof sb),
+                 1 << a.page_shift, a.rope.rot);
+  return from_cuda(qattn::launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qattn_paged_workspace_size(const qattn_shape* shape, const qattn_params* params,
+                                  const qattn_paging* paging) {
+  if (paged_ok(shape, paging) != QATTN_OK || check_params(params) != QATTN_OK || empty_problem(shape)) return 0;
+  return paged_split(shape).bytes;
+}
+
+qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const qattn_shape* shape,
+                             const qattn_params* params, const int32_t* lengths,
+                             const int32_t* n_new, const qattn_paging* paging,
+                             const int32_t* page_table, const void* k_pages, const void* v_pages,
+                             const float* k_scales, const float* v_scales, void* O, float* lse,
+                             void* workspace, size_t workspace_bytes, qattn_stream_t stream) {
+  qattn_status st = paged_ok(shape, paging);
+  if (st != QATTN_OK) return st;
+  if ((st = check_params(params)) != QATTN_OK) return st;
+  if (empty_problem(shape)) return QATTN_OK;
+  if (params->pv_mode != QATTN_PV_E4M3 || params->q_pos0 != QATTN_POS0_BOTTOM_RIGHT || params->kv_capacity != 0)
+    return QATTN_ERR_UNSUPPORTED;
+  if (!Q || !aligned16(Q) || !lengths || !aligned_to(lengths, 4) || !aligned_to(n_new, 4) || !O || !aligned16(O) ||
+      !aligned_to(lse, 4))
+    return QATTN_ERR_INVALID_ARG;
+  if ((shape->Nk > 0 && !page_table) || !aligned_to(page_table, 4) || !k_pages || !aligned16(k_pages) || !v_pages ||
+      !aligned16(v_pages) || !k_scales || !aligned_to(k_scales, 4) || !v_scales || !aligned_to(v_scales, 4))
+    return QATTN_ERR_INVALID_ARG;
+  qattn::Src qs;
+  if (!make_src(Q, q_strides, shape->Hq, shape->Nq, shape->d, 2, &qs)) return QATTN_ERR_INVALID_ARG;
+  const PagedSplit sp = paged_split(shape);
+  if (sp.steps >= (int64_t{1} << 31)) return QATTN_ERR_UNSUPPORTED;  // counted in 32 bits
+  if (sp.bytes > 0 && (!workspace || workspace_bytes < sp.bytes || !aligned16(workspace)))
+    return QATTN_ERR_WORKSPACE;
+  qattn::PagedArgs a{};
+  a.err = error_word();
+  if (!a.err) return QATTN_ERR_CUDA;
+  a.B = static_cast<int>(shape->B);
+  a.Hq = static_cast<int>(shape->Hq);
+  a.Hkv = static_cast<int>(shape->Hkv);
+  a.G = a.Hq / a.Hkv;
+  a.T = static_cast<int>(shape->Nq);
+  a.Nk = static_cast<int>(shape->Nk);
+  a.d = static_cast<int>(shape->d);
+  a.n_pages = static_cast<int>(paging->n_pages);
+  a.page_shift = page_shift_of(paging);
+  a.max_pages = static_cast<int>(paging->max_pages);
+  a.e4m3 = paging->code_dtype == QATTN_E4M3;
+  a.blocks = sp.blocks;
+  a.causal = params->causal;
+  a.sm_scale = sm_scale_of(shape, params);
+  a.q = Q;
+  a.qsB = qs.sB;
+  a.qsH = qs.sH;
+  a.qsN = qs.sN;
+  a.lengths = lengths;
+  a.n_new = n_new;
+  a.page_table = page_table;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.k_pages = static_cast<const uint8_t*>(k_pages);
+  a.v_pages = static_cast<const uint8_t*>(v_pages);
+  a.out = O;
+  a.out_bf16 = params->out_dtype == QATTN_BF16;
+  a.lse = lse;
+  a.cluster = sp.cluster;
+  a.ctas = sp.ctas;
+  a.lead = sp.lead;
+  a.slots = sp.slots;
+  a.rows_total = static_cast<size_t>(shape->B * shape->Hq * shape->Nq);
+  char* w = static_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_m = reinterpret_cast<float*>(w + sp.off_m);
+  a.part_l = reinterpret_cast<float*>(w + sp.off_l);
+  CUtensorMap tk, tv;
+  const int64_t planes = paging->n_pages * shape->Hkv;
+  if (!encode_cache(&tk, k_pages, planes, paging->page_size, paging->page_size, shape->d,
+                    static_cast<uint32_t>(sp.step)) ||
+      !encode_cache(&tv, v_pages, planes, paging->page_size, paging->page_size, shape->d,
+                    static_cast<uint32_t>(sp.step)))
+    return QATTN_ERR_CUDA;
+  char sb[128];
+  QATTN_LOG_LINE("qattn_paged_fwd %s page=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb), 1 << a.page_shift,
+                 sp.cluster > 0 ? "paged_warp_kernel (clusters)" : "paged_warp_kernel + paged_join_kernel", sp.ctas);
+  return from_cuda(qattn::launch_paged_warp(tk, tv, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int qattn_fwd_kernel_choice(const qattn_shape* shape, const qattn_params* params) {
   if (check_shape(shape) != QATTN_OK || check_params(params) != QATTN_OK) return -1;
   const int c = fwd_choice(shape, params);
@@ -1266,7 +1503,9 @@ qattn_status qattn_get_error(qattn_stream_t stream) {
                               qattn::check_take_tree_warp() | qattn::check_take_tree_tc() |
                               qattn::check_take_kv_weights() |
                               qattn::check_take_kv_weights_tc() |
-                              qattn::check_take_kv_cache();
+                              qattn::check_take_kv_cache() |
+                              qattn::check_take_paged_cache() |
+                              qattn::check_take_paged_warp();
   if (v & qattn::kErrTimeout) return QATTN_ERR_TIMEOUT;
   if (checks != 0) return QATTN_ERR_BOUNDS;
   return (v & qattn::kErrDomain) ? QATTN_ERR_INVALID_ARG : QATTN_OK;

@@ -81,6 +81,8 @@ unsigned int check_take_tree_tc();
 unsigned int check_take_kv_weights();
 unsigned int check_take_kv_weights_tc();
 unsigned int check_take_kv_cache();
+unsigned int check_take_paged_cache();
+unsigned int check_take_paged_warp();
 // One guard that fails for 16 of 32 threads, touching no memory (quant_kernels.cu).
 cudaError_t launch_bounds_probe(cudaStream_t s);
 
@@ -390,6 +392,74 @@ struct EvictArgs {
   int cluster;          // CTAs per (sequence, KV head); set by launch_kv_evict
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t s);
+
+// ---- paged_cache.cu: rotary positions, and a paged 8-bit KV cache's new tokens
+struct RopeArgs {
+  const float* table;   // [n][rot]: rot / 2 cosines, then rot / 2 sines; null: no rotation
+  int n, rot;
+  int inter;            // pairs are neighbours (else rot / 2 apart)
+  int inverse;
+};
+struct RotateArgs {
+  int B, H, T, d, f32;
+  const void* x;        // bf16 or fp32, element strides
+  long long xsB, xsH, xsN;
+  void* y;              // [B][H][T][d]
+  const int32_t* positions;  // [B][T] or null (t)
+  RopeArgs rope;
+  unsigned int* err;
+  int heads;            // set by launch_rotate: heads of a CTA
+};
+cudaError_t launch_rotate(RotateArgs a, cudaStream_t s);
+
+struct PagedAppendArgs {
+  int B, Hq, Hkv, T, Nk, d;       // Nk: most rows in use
+  int n_pages, page_shift, max_pages, e4m3;
+  const uint16_t *q, *k, *v;      // bf16, element strides; q null: no queries
+  long long qsB, qsH, qsN, ksB, ksH, ksN, vsB, vsH, vsN;
+  const int32_t *lengths, *n_new; // [B]; rows in use with the new ones; n_new null: T
+  const int32_t* positions;       // [B][T] or null (the rows)
+  const int32_t* page_table;      // [B][max_pages]
+  RopeArgs rope;
+  uint16_t* q_out;                // [B][Hq][T][d]
+  uint8_t *k_pages, *v_pages;     // [n_pages][Hkv][page][d]
+  float *k_scales, *v_scales;     // [n_pages][Hkv]
+  unsigned int* err;
+  int heads;                      // set by launch_paged_append: heads of a CTA
+};
+cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s);
+
+// ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
+constexpr int kPagedRows = 16;                // query rows of the warp-level kernel's block
+constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
+constexpr int kPagedWarpStep = 32;            // keys of a step
+constexpr int kPagedWarpLead = 10;            // steps that a block's start counts for in equal shares
+constexpr int kPagedCluster = 8;              // most CTAs of a block's own cluster
+struct PagedArgs {
+  int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
+  int n_pages, page_shift, max_pages, e4m3;
+  int blocks;                     // row blocks of a KV head, at most
+  int causal;
+  float sm_scale;
+  const uint16_t* q;              // bf16, element strides
+  long long qsB, qsH, qsN;
+  const int32_t *lengths, *n_new; // [B]; n_new null: T
+  const int32_t* page_table;      // [B][max_pages]
+  const float *k_scales, *v_scales;  // [n_pages][Hkv]
+  const uint8_t *k_pages, *v_pages;  // [n_pages][Hkv][page][d]
+  void* out;                      // [B][Hq][T][d]
+  int out_bf16;
+  float* lse;                     // [B][Hq][T] or null
+  unsigned int* err;
+  // the split and its workspace (see TreeArgs)
+  int cluster, ctas, lead;
+  size_t slots, rows_total;
+  float *part_o, *part_m, *part_l;
+};
+// tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x (keys of a step) x 1
+// (128-byte swizzle for d = 128, 64-byte for d = 64).
+cudaError_t launch_paged_warp(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                              cudaStream_t s);
 
 // ---- exact24.cu
 struct Exact24Args {

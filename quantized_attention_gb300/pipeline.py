@@ -7,6 +7,7 @@ reused across calls.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -400,6 +401,160 @@ class TreeCache:
         self._spare = [self.k_codes, self.v_codes, self.weights, self.lengths]
         self.k_codes, self.v_codes, self.weights, self.lengths = k, v, w, n
         return kept
+
+
+def rope_table(n_positions, rot_dim, *, base=10000.0, scaling="none", factor=1.0, trained=4096, slow=1.0,
+               fast=32.0, mscale=1.0, device="cuda") -> torch.Tensor:
+    """The table of qb.make_rope, fp32 [n_positions, rot_dim]: cosines, then sines of
+    the positions' angles, times mscale.  Pair i turns by f_i = base^(-2 i / rot_dim)
+    a position.  For contexts `factor` times as long as the `trained` one, scaling is
+      "linear"  every f_i / factor (positions interpolated),
+      "base"    base * factor^(rot_dim / (rot_dim - 2)): the slowest pair as in
+                "linear", the fastest as it was,
+      "ramp"    by how often a pair turns over the trained context: `fast` times or
+                more: f_i as it was; `slow` times or fewer: f_i / factor; a linear
+                mixture between.
+    Computed in 64 bits and rounded once: set-up in plain tensor operations."""
+    if rot_dim < 8 or rot_dim % 8:
+        raise ValueError("rot_dim must be a multiple of 8")
+    if scaling not in ("none", "linear", "base", "ramp"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    if scaling == "base":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        keep = ((f * (trained / (2.0 * math.pi)) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    a = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * f
+    return (torch.cat([a.cos(), a.sin()], dim=1) * mscale).to(torch.float32).contiguous()
+
+
+class PagedCache:
+    """A paged 8-bit KV cache shared by up to B sequences, and a serving step on it:
+    ``step(Q, K, V, n_new)`` takes pages for the new tokens, enters them (K and Q
+    rotated) and attends.  The tokens of a step may be a prompt, a chunk of one, or
+    one each, and another number for each sequence.
+
+    n_pages pages of page_size rows; max_rows: most rows of a sequence; rope: the
+    rotation (None: none), its table for max_rows positions.  Pages are dealt on the
+    host: ``grow`` and ``release`` keep ``page_table``, ``lengths`` and ``n_new`` on
+    the device in step by one copy (which waits until the host's numbers are read);
+    ``append`` and ``attend`` wait for nothing and can be captured in a graph, replayed
+    after each ``grow`` (grow is not captured).  All calls go to the current stream
+    (or ``stream``)."""
+
+    def __init__(self, n_pages, page_size, Hq, Hkv, d, B, max_rows, *, code_dtype=qb.DT_I8, rope=None,
+                 out_dtype=qb.DT_BF16, sm_scale=0.0, device="cuda"):
+        dev = torch.device(device)
+        width = max(1, -(-max_rows // page_size))
+        self.paging = qb.make_paging(n_pages, page_size, width, code_dtype)
+        self.rope, self.max_rows = rope, max_rows
+        if rope is not None and rope.n_positions < max_rows:
+            raise ValueError("the rope's table is shorter than max_rows")
+        self._dims, self._out_dtype = (B, Hq, Hkv, d), out_dtype
+        self.params = qb.make_params(causal=True, out_dtype=out_dtype, sm_scale=sm_scale)
+        code = torch.int8 if code_dtype == qb.DT_I8 else torch.uint8
+        pool = (n_pages, Hkv, page_size, d)
+        self.k_pages, self.v_pages = (torch.zeros(pool, dtype=code, device=dev) for _ in range(2))
+        self.k_scales, self.v_scales = (torch.zeros(pool[:2], dtype=torch.float32, device=dev) for _ in range(2))
+        # page table, lengths and n_new: one array here and one on the device
+        self._host = torch.zeros(B * (width + 2), dtype=torch.int32)
+        self._meta = torch.zeros_like(self._host, device=dev)
+        self.page_table, self.lengths, self.n_new = self._views(self._meta)
+        self._pt, self._len, self._new = self._views(self._host)
+        self._pt.fill_(-1)
+        self._meta.copy_(self._host)
+        self._free = list(range(n_pages - 1, -1, -1))
+        self._steps = {}
+
+    def _views(self, t):
+        B, width = self._dims[0], self.paging.max_pages
+        return t[:B * width].view(B, width), t[B * width:B * (width + 1)], t[B * (width + 1):]
+
+    def _upload(self, stream):
+        with torch.cuda.stream(stream):
+            self._meta.copy_(self._host)
+
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def rows(self, b) -> int:
+        """Rows in use of sequence b, on the host."""
+        return int(self._len[b])
+
+    def grow(self, n_new, stream=None):
+        """Pages for n_new[b] (host numbers) more rows of each sequence; ValueError, and
+        nothing changed, where a sequence would pass max_rows or the pool runs out."""
+        B, page = self._dims[0], self.paging.page_size
+        n = [int(x) for x in n_new]
+        if len(n) != B or min(n, default=0) < 0:
+            raise ValueError(f"n_new: expected {B} numbers of new tokens")
+        have = self._len.tolist()
+        if any(h + x > self.max_rows for h, x in zip(have, n)):
+            raise ValueError("a sequence would pass max_rows")
+        want = [(-(-h // page), -(-(h + x) // page)) for h, x in zip(have, n)]
+        if sum(e - s for s, e in want) > len(self._free):
+            raise ValueError("the pool has too few free pages")
+        for b, (s, e) in enumerate(want):
+            for j in range(s, e):
+                self._pt[b, j] = self._free.pop()
+        self._len += torch.tensor(n, dtype=torch.int32)
+        self._new.copy_(torch.tensor(n, dtype=torch.int32))
+        self._upload(stream)
+
+    def release(self, b, stream=None):
+        """Sequence b is done: its pages go back to the pool."""
+        used = -(-int(self._len[b]) // self.paging.page_size)
+        self._free.extend(reversed(self._pt[b, :used].tolist()))
+        self._pt[b].fill_(-1)
+        self._len[b] = 0
+        self._new[b] = 0
+        self._upload(stream)
+
+    def _buffers(self, T):
+        """Shape, output buffers and workspace of steps of up to T tokens."""
+        if T not in self._steps:
+            B, Hq, Hkv, d = self._dims
+            dev = self._meta.device
+            shape = qb.make_shape(B, Hq, Hkv, T, self.max_rows, d)
+            ws = max(qb.paged_workspace_size(shape, self.params, self.paging), 256)
+            dt = torch.bfloat16 if self._out_dtype == qb.DT_BF16 else torch.float32
+            self._steps[T] = (shape, torch.zeros((B, Hq, T, d), dtype=torch.bfloat16, device=dev),
+                              torch.zeros((B, Hq, T, d), dtype=dt, device=dev),
+                              torch.zeros((B, Hq, T), dtype=torch.float32, device=dev),
+                              torch.empty(ws, dtype=torch.uint8, device=dev))
+        return self._steps[T]
+
+    def append(self, Q, K, V, stream=None):
+        """Enter the tokens that the last ``grow`` made room for; returns Q rotated
+        (Q itself without a rope)."""
+        shape, q_out = self._buffers(Q.shape[2])[:2]
+        turn = self.rope is not None
+        qb.paged_append(K, V, shape, self.paging, self.page_table, self.lengths, self.k_pages, self.v_pages,
+                        self.k_scales, self.v_scales, n_new=self.n_new, rope=self.rope, Q=Q if turn else None,
+                        Q_out=q_out if turn else None, stream=stream)
+        return q_out if turn else Q
+
+    def attend(self, Q, stream=None):
+        """Attention of the last n_new[b] rows of each sequence; Q as ``append`` gave it.
+        Returns O; ``lse(T)`` has the rows' lse."""
+        shape, _, O, lse, ws = self._buffers(Q.shape[2])
+        qb.paged_fwd(Q, shape, self.params, self.paging, self.page_table, self.lengths, self.k_pages,
+                     self.v_pages, self.k_scales, self.v_scales, O, lse, ws, n_new=self.n_new, stream=stream)
+        return O
+
+    def lse(self, T):
+        return self._buffers(T)[3]
+
+    def step(self, Q, K, V, n_new=None, stream=None):
+        """grow, append and attend: Q bf16 [B, Hq, T, d], K, V bf16 [B, Hkv, T, d] (any
+        strides), n_new: tokens of each sequence (host numbers; None: T each).  Rows
+        behind a sequence's tokens in the returned O are left as they were."""
+        self.grow([Q.shape[2]] * self._dims[0] if n_new is None else n_new, stream)
+        return self.attend(self.append(Q, K, V, stream), stream)
 
 
 def problem_for(wl, **kw) -> Problem:
