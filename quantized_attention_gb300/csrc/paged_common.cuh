@@ -91,6 +91,7 @@ struct PagedWalk {
   int b, hkv, rb;    // where p lies
   int s0;            // place in the block less a.lead
   int steps;         // of the block
+  int total;         // W
   PagedSeq seq;
 };
 // A run of steps of a share inside one block.
@@ -124,14 +125,15 @@ __device__ __forceinline__ void pg_totals(const PagedArgs& a, int b0, int& total
   }
 }
 
-// Where this CTA's share begins.  Called by whole warps, each for itself.
+// Where the share of CTA c of G begins.  Called by whole warps, each for itself.
 template <int ROWS, int STEP>
-__device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a) {
+__device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a, int c, int G) {
   const int lane = threadIdx.x & 31;
   PagedWalk w{};
   int total, none;
   pg_totals<ROWS, STEP>(a, 0, total, none);
-  const int G = gridDim.x, c = blockIdx.x, q = total / G, r = total - q * G;
+  const int q = total / G, r = total - q * G;
+  w.total = total;
   w.p = c * q + min(c, r);
   w.end = w.p + q + (c < r ? 1 : 0);
   if (w.p >= w.end) return w;

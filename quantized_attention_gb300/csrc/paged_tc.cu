@@ -1,0 +1,678 @@
+// Attention over a paged 8-bit KV cache (qattn_paged_fwd), for more than 16 query rows
+// of a KV head: on the 5th-generation tensor cores.  Mathematics as in paged_warp.cu.
+//
+// A CTA works on a block of 256 query rows (two tiles of 128) in steps of 128 keys:
+//   warp 0       issues the MMAs
+//   warps 4-7    codes -> fp16 tiles K16, V16 [key][channel] in shared memory, straight
+//                from the pages: a warp takes 32 rows of every tile (they lie in one
+//                page), the next step's loads in flight
+//   warps 8-11   softmax of tile 0, warps 12-15 of tile 1: a thread a row
+// Per tile and step: S = Q K16^T (both in shared memory), P = 2^(t - m) rounded to fp16
+// in place of S, O += P V16 (P in TMEM, V16 as it lies: the B operand with its N index
+// fastest).  TMEM: S0, S1 and O0, O1, 512 columns at d = 128, so P lies in S's columns
+// and a tile's QK follows its PV; the other tile's MMAs run under a tile's softmax.  The
+// issuing order PV(0, j), QK(0, j + 1), PV(1, j), QK(1, j + 1) makes one barrier do for
+// "S is there", "O is done" and "P has been read".
+// A block of at most 128 rows gives both tiles the same rows and every other step each
+// (dual); their parts are joined from TMEM at the end.
+// Codes widened once serve 256 rows: 64 KB written and 192 KB read by the MMAs a step,
+// ~2050 cycles of shared memory against as many of tensor work.
+// The reference m is set 7 below a row's maximum and moves only when that has grown by
+// another 8 (P stays at or below 2^15), so O is rarely rescaled: P keeps its eleven bits
+// where P s_v is down to 2^-21 of the row's largest, and is off by at most 2^-32 of it.
+#include "paged_common.cuh"
+
+namespace qattn {
+namespace {
+
+constexpr int kStep = kPagedTcStep;
+constexpr int kRows = kPagedTcRows;
+static_assert(kStep == 128 && kRows == 256, "two tiles of 128 TMEM lanes, one block of keys per step");
+constexpr int kThreads = 512;
+constexpr int kHead = 7;      // of the exponentials' reference (pg_head)
+constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
+static_assert(kHead + kLazy <= 15.f, "P stays inside fp16");
+constexpr uint32_t kTmS = 0, kTmO = 256;  // TMEM columns (tile t: + 128 t, + D t)
+constexpr int kGroups = kStep / 32;       // groups of keys that lie in one page
+constexpr int kWinSteps = 32 / kGroups;   // steps of a warp's window of scales
+
+// A group's scales for the softmax (PageScale), and what is rare.
+struct GroupScale {
+  float k, e_max, e, inv;
+};
+constexpr uint32_t kFlagHidden = 1, kFlagZeroV = 2, kFlagNaN = 4;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = 128 * D * 2;  // fp16 Q, K16 or V16: D / 64 blocks of [128][128 B]
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + 2 * kTile;
+  static constexpr int kOffScale = kOffV + 2 * kTile;              // [8 warps][32] GroupScale
+  static constexpr int kOffFlags = kOffScale + 8 * 32 * 16;        // [8 warps][32]
+  static constexpr int kOffML = kOffFlags + 8 * 32 * 4;            // m and l of both tiles (dual)
+  static constexpr int kOffBar = kOffML + 2 * 2 * 128 * 4;
+  static constexpr int kBytes = kOffBar + 256;
+  static_assert(kBytes <= 227 * 1024, "shared memory budget");
+};
+
+enum {
+  kKFull = 0,   // [2] 128 converting threads
+  kKEmpty = 2,  // [2] the step's QK MMAs
+  kVFull = 4,   // [2] 128 converting threads
+  kVEmpty = 6,  // [2] the step's PV MMAs
+  kSFull = 8,   // [2 tiles] QK (and every MMA before it) is done
+  kPFull = 10,  // [2 tiles] 128 threads: P is there, O rescaled
+  kQFull = 12,  // [2 tiles] 128 threads wrote Q
+  kOFull = 14,  // [2 tiles] a segment's last PV is done
+  kMerge = 16,  // [2] 256 threads: m and l are there; O has been read (dual)
+  kDrain = 18,
+  kNumBars = 19
+};
+
+// Steps of a segment that a tile takes part in.
+__device__ __forceinline__ int tile_steps(int n, bool dual, int t) { return dual ? (n + 1 - t) / 2 : n; }
+__device__ __forceinline__ bool is_dual(const PagedArgs& a, const PagedSeg& s) {
+  return s.seq.n * a.G - s.rb * kRows <= 128;
+}
+
+// 16 codes -> 16 fp16, exact.
+template <bool E4M3>
+__device__ __forceinline__ void widen16(const uint4& v, uint32_t (&h)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (E4M3) {
+      h[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
+      h[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
+    } else {
+      codes4_to_f16x2(w[e], h[2 * e], h[2 * e + 1]);
+    }
+  }
+}
+
+// 32 channels ch .. of a row, times inv, to the output.
+__device__ __forceinline__ void write_out32(const PagedArgs& a, size_t row, int ch, const float (&x)[32], float inv) {
+  if (!QATTN_IN_BOUNDS(row < a.rows_total && ch + 32 <= a.d)) return;
+  if (a.out_bf16) {
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.d + ch);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * k + 2 * e] * inv, x[8 * k + 2 * e + 1] * inv);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * a.d + ch);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      dst[k] = make_float4(x[4 * k] * inv, x[4 * k + 1] * inv, x[4 * k + 2] * inv, x[4 * k + 3] * inv);
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
+    return mbar_wait_fast(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t n = 1;
+      if ((i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 2) ||
+          (i >= kQFull && i < kQFull + 2))
+        n = 128;
+      if (i >= kMerge && i < kMerge + 2) n = 256;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();  // after the wait: the join reads the lengths before its own
+  PagedWalk walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
+  PagedSeg sg;
+  auto next_segment = [&] {
+    // (a share may hold the lead of a block and none of its steps, and end with it)
+    return pg_next<kRows, kStep>(a, walk, sg);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // ------------------------------------------------------------ MMA
+      constexpr uint32_t idesc_qk = make_idesc(128, kStep, 0, 0);
+      constexpr uint32_t idesc_pv = make_idesc(128, D, 0, 0) | kIdescBMnMajor;
+      const uint64_t qd0 = smem_desc(base + C::kOffQ, 1024, kSwizzle128B);
+      const uint64_t kd0 = smem_desc(base + C::kOffK, 1024, kSwizzle128B);
+      const uint64_t vd0 = smem_desc_mn(base + C::kOffV, kStep * 128, 1024);
+      bool ok = true;
+      uint32_t it = 0, seg = 0;        // steps and segments done
+      uint32_t np[2] = {0, 0};         // PVs issued for each tile
+      auto qk = [&](int t, uint32_t step) {
+        const uint64_t qd = qd0 + t * (C::kTile >> 4), kd = kd0 + (step & 1) * (C::kTile >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k / 4) * (128 * 128) + 32 * (k % 4)) >> 4;
+          mma_f16(tmem + kTmS + 128 * t, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(kSFull + t));
+      };
+      auto pv = [&](int t, uint32_t step, bool first) {
+        const uint64_t vd = vd0 + (step & 1) * (C::kTile >> 4);
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+          mma_f16_ts(tmem + kTmO + D * t, tmem + kTmS + 128 * t + 8 * k, vd + (k * 2048) / 16, idesc_pv,
+                     (!first || k > 0) ? 1u : 0u);
+      };
+      for (; ok && next_segment(); ++seg) {
+        const int n = sg.s1 - sg.s0;
+        const bool dual = is_dual(a, sg);
+        // the first QK of each tile
+        for (int t = 0; ok && t < 2; ++t) {
+          if (!(ok = wait(kQFull + t, seg))) break;
+          if (tile_steps(n, dual, t) == 0) continue;
+          const uint32_t step = it + (dual ? t : 0);
+          if ((dual || t == 0) && !(ok = wait(kKFull + (step & 1), step >> 1))) break;
+          tc_fence_after();
+          qk(t, step);
+          if (dual || t == 1) mma_commit(bar(kKEmpty + (step & 1)));
+        }
+        for (int j = 0; ok && j < n; ++j, ++it) {
+          if (!(ok = wait(kVFull + (it & 1), it >> 1))) break;
+          const int t0 = dual ? (j & 1) : 0, t1 = dual ? t0 + 1 : 2;
+          const int ahead = dual ? 2 : 1;   // the tile's next step
+          for (int t = t0; t < t1; ++t) {
+            if (!(ok = wait(kPFull + t, np[t]))) break;
+            tc_fence_after();
+            pv(t, it, j < ahead);
+            ++np[t];
+            if (t == t1 - 1) mma_commit(bar(kVEmpty + (it & 1)));
+            if (j + ahead < n) {
+              const uint32_t step = it + ahead;
+              if (t == t0) {
+                if (!(ok = wait(kKFull + (step & 1), step >> 1))) break;
+                tc_fence_after();
+              }
+              qk(t, step);
+              if (t == t1 - 1) mma_commit(bar(kKEmpty + (step & 1)));
+            } else {
+              mma_commit(bar(kOFull + t));
+            }
+          }
+        }
+      }
+      mma_commit(bar(kDrain));
+      volatile int never = 0;
+      mbar_wait(bar(kDrain), 0, &never, a.err, kErrTimeout);
+      if (!ok) *abort_flag = 1;
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    // -------------------------------------------------------------- codes -> fp16
+    // Warp w takes rows 32 w .. 32 w + 31 of every tile, K and V of a step in turn, so that
+    // each waits for every stage in order.  The eight lanes of a store take four chunks of
+    // rows r and r ^ 5, which differ in the swizzle's low and high bit: eight bank groups.
+    constexpr int NB = D / 64, NL = 4 * NB;  // 64-channel blocks; 16-byte loads of a batch a lane
+    const int w = warp - 4;
+    const int cc = lane & 3, u = (lane >> 3) ^ (((lane >> 2) & 1) * 5);  // chunk of a block, row of eight
+    const uint32_t dst = base + (32 * w + u) * 128;
+    const uint32_t c0 = ((2 * cc) ^ u) << 4, c1 = ((2 * cc + 1) ^ u) << 4;
+    bool ok = true;
+    uint32_t it = 0;  // steps done
+    while (ok && next_segment()) {
+      const int n = sg.s1 - sg.s0, len = sg.seq.len;
+      // pages of this warp's rows in the next 32 steps, one a lane, and in the 32 after
+      auto look_up = [&](int j0) {
+        const int key = (sg.s0 + j0 + lane) * kStep + 32 * w;
+        int p = -1;
+        if (j0 + lane < n && key < len && QATTN_IN_BOUNDS((key >> a.page_shift) < a.max_pages && sg.b < a.B)) {
+          p = a.page_table[static_cast<size_t>(sg.b) * a.max_pages + (key >> a.page_shift)];
+          if (p < 0 || p >= a.n_pages) p = -1;  // (the softmax warps report it)
+        }
+        return p;
+      };
+      int cur = look_up(0), nxt = n > 32 ? look_up(32) : -1;
+      uint4 vk[NL], vv[NL];
+      // where step j's rows start in the pool (in bytes), or -1
+      auto place = [&](int j) -> long long {
+        if (j > 0 && j % 32 == 0) {
+          cur = nxt;
+          if (j + 32 < n) nxt = look_up(j + 32);
+        }
+        const int p = __shfl_sync(0xffffffffu, cur, j & 31);
+        if (p < 0) return -1;
+        const int key = (sg.s0 + j) * kStep + 32 * w;
+        const long long row = ((static_cast<long long>(p) * a.Hkv + sg.hkv) << a.page_shift) +
+                              (key & ((1 << a.page_shift) - 1)) + u;
+        return row * D + 16 * cc;
+      };
+      auto load = [&](uint4 (&x)[NL], const uint8_t* pages, long long at, int j) {
+        const int left = len - (sg.s0 + j) * kStep - 32 * w - u;
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+          x[k] = make_uint4(0u, 0u, 0u, 0u);
+          // rows behind the sequence may hold any byte: zeros stand in
+          if (at >= 0 && 8 * (k / NB) < left)
+            x[k] = *reinterpret_cast<const uint4*>(pages + at + 8 * (k / NB) * D + 64 * (k % NB));
+        }
+      };
+      auto convert = [&](const uint4 (&x)[NL], uint32_t tile) {
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+          uint32_t h[8];
+          widen16<E4M3>(x[k], h);
+          const uint32_t d = dst + tile + (k % NB) * (128 * 128) + 8 * (k / NB) * 128;
+          sts128(d + c0, h[0], h[1], h[2], h[3]);
+          sts128(d + c1, h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+      };
+      long long at = place(0);
+      load(vk, a.k_pages, at, 0);
+      load(vv, a.v_pages, at, 0);
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t st = it & 1;
+        const bool more = j + 1 < n;
+        if (more) at = place(j + 1);
+        ok = it < 2 || wait(kKEmpty + st, (it >> 1) - 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        convert(vk, C::kOffK + st * C::kTile);
+        mbar_arrive(bar(kKFull + st));
+        if (more) load(vk, a.k_pages, at, j + 1);
+        ok = it < 2 || wait(kVEmpty + st, (it >> 1) - 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        convert(vv, C::kOffV + st * C::kTile);
+        mbar_arrive(bar(kVFull + st));
+        if (more) load(vv, a.v_pages, at, j + 1);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- softmax
+    const int t = (warp - 8) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;  // TMEM lane, row of the tile
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_base + kTmS + 128 * t, tO = tmem + lane_base + kTmO + D * t;
+    GroupScale* win = reinterpret_cast<GroupScale*>(smem + C::kOffScale) + 32 * (warp - 8);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kOffFlags) + 32 * (warp - 8);
+    float* ml = reinterpret_cast<float*>(smem + C::kOffML);  // [tile][m, l][128]
+    uint32_t ns = 0, shares = 0, merges = 0;  // this tile's steps, segments that had some; dual segments
+    bool ok = true;
+    while (ok && next_segment()) {
+      const int n = sg.s1 - sg.s0, len = sg.seq.len;
+      const bool dual = is_dual(a, sg);
+      const int rr = sg.rb * kRows + (dual ? 0 : 128 * t) + r;
+      const int tok = rr / a.G, hq = sg.hkv * a.G + rr - tok * a.G;
+      const bool in = tok < sg.seq.n;
+      // ---- the scales' windows, one group a lane: pages two windows ahead, scales one
+      auto page_of = [&](int w) {
+        const int key = sg.s0 * kStep + 32 * (32 * w + lane);
+        int p = -1;
+        if (32 * w + lane < kGroups * n && key < len &&
+            QATTN_IN_BOUNDS((key >> a.page_shift) < a.max_pages && sg.b < a.B)) {
+          p = a.page_table[static_cast<size_t>(sg.b) * a.max_pages + (key >> a.page_shift)];
+          if (p < 0 || p >= a.n_pages) {
+            atomicOr(a.err, kErrDomain);
+            p = -1;
+          }
+        }
+        return p;
+      };
+      auto scales_of = [&](int p, float& ks, float& vs) {
+        ks = vs = 0.f;
+        if (p < 0) return;
+        const size_t sc = static_cast<size_t>(p) * a.Hkv + sg.hkv;
+        ks = a.k_scales[sc];
+        vs = a.v_scales[sc];
+      };
+      int p1 = page_of(0), p2 = page_of(1);
+      float ks1, vs1;
+      scales_of(p1, ks1, vs1);
+      // ---- Q's row -> fp16 in shared memory
+      float rf;
+      bool fin;
+      {
+        const uint16_t* src = a.q + sg.b * a.qsB + hq * a.qsH + tok * a.qsN;
+        uint4 x[D / 8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          x[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (in && QATTN_IN_BOUNDS(sg.b < a.B && hq < a.Hq && tok < a.T)) x[k] = *reinterpret_cast<const uint4*>(src + 8 * k);
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+        }
+        fin = top < 0x7f800000u;  // else the row is NaN once it sees a key
+        float up, down;
+        pg_row_shift(top, up, down);
+        rf = __fmul_rn(__fmul_rn(a.sm_scale, kPgLog2e), down);
+        const uint32_t row = base + C::kOffQ + t * C::kTile + r * 128;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(fin ? bf16_bits_to_f32(w[e] & 0xffffu) * up : 0.f,
+                                                fin ? __uint_as_float(w[e] & 0xffff0000u) * up : 0.f);
+            f[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          sts128(row + (k / 8) * (128 * 128) + (((k % 8) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kQFull + t));
+      const int lim = in ? min(pg_limit(a, sg.seq, tok), len) : 0;
+      float m = -kPgInf, l = 0.f;  // the row's reference and its sum
+      const int first = dual ? t : 0, pace = dual ? 2 : 1;
+      for (int j = first; j < n; j += pace, ++ns) {
+        if (j % kWinSteps == first) {  // a new window
+          const int w = j / kWinSteps;
+          __syncwarp();
+          const PageScale ps = pg_scale(ks1, vs1);
+          win[lane] = GroupScale{ps.k, ps.e_max, ps.e, ps.inv};
+          flags[lane] = (p1 < 0 ? kFlagHidden : 0u) | (ps.keep == 0u ? kFlagZeroV : 0u) | (ps.nan ? kFlagNaN : 0u);
+          __syncwarp();
+          p1 = p2;
+          scales_of(p1, ks1, vs1);
+          p2 = page_of(w + 2);
+        }
+        ok = wait(kSFull + t, ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // S in two halves, the upper one for its maxima alone: it is read again where it is
+        // used, which leaves 64 registers for scores
+        uint32_t v0[32], v1[32];
+        float mx[kGroups];
+        const int q0 = kGroups * (j % kWinSteps);
+        const uint4 fl = *reinterpret_cast<const uint4*>(&flags[q0]);
+        const uint32_t f4[kGroups] = {fl.x, fl.y, fl.z, fl.w};
+        const int room = lim - (sg.s0 + j) * kStep;  // visible keys of the step
+        const uint32_t rare = fl.x | fl.y | fl.z | fl.w;
+        const bool masked = __any_sync(0xffffffffu, room < kStep || rare != 0u);
+        auto hide = [&](uint32_t (&v)[32], int g) {  // (masked) hidden keys' scores to -inf
+          const uint32_t vis = pg_first_bits((f4[g] & kFlagHidden) ? 0 : room - 32 * g);
+          if (vis != 0u && (f4[g] & kFlagNaN)) fin = false;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (!((vis >> k) & 1u)) v[k] = __float_as_uint(-kPgInf);
+        };
+        auto largest = [&](const uint32_t (&v)[32]) {
+          float x[4] = {-kPgInf, -kPgInf, -kPgInf, -kPgInf};
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              x[q] = fmax3(x[q], __uint_as_float(v[k + 2 * q]), __uint_as_float(v[k + 2 * q + 1]));
+          return fmax3(x[0], x[1], fmaxf(x[2], x[3]));
+        };
+        tmem_ld32_max(tS + 64, v0, mx[2]);
+        tmem_ld32_max(tS + 96, v1, mx[3]);
+        tmem_wait_ld();
+        if (masked) {
+          hide(v0, 2);
+          hide(v1, 3);
+          mx[2] = largest(v0);
+          mx[3] = largest(v1);
+        }
+        tmem_ld32_max(tS, v0, mx[0]);
+        tmem_ld32_max(tS + 32, v1, mx[1]);
+        tmem_wait_ld();
+        if (masked) {
+          hide(v0, 0);
+          hide(v1, 1);
+          mx[0] = largest(v0);
+          mx[1] = largest(v1);
+        }
+        float top = -kPgInf;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const GroupScale gs = win[q0 + g];
+          const float c = fmaxf(rf * gs.k, 1e-30f);
+          if (c == kPgInf && mx[g] > -kPgInf) fin = false;
+          top = fmaxf(top, fmaf(mx[g], c, gs.e_max));
+        }
+        const float head = pg_head(top, kHead);
+        const float mn = top > m + (head == 0.f ? 0.f : kHead + kLazy) || m == -kPgInf ? top - head : m;
+        const float ref = mn == -kPgInf ? 0.f : mn;
+        const float al = m == -kPgInf ? 0.f : ex2_approx(m - ref);
+        const bool moved = mn != m;
+        if (moved) l *= al;
+        auto weigh = [&](const uint32_t (&v)[32], int g) {  // P of a group, in place of S
+          const GroupScale gs = win[q0 + g];
+          const float c = fmaxf(rf * gs.k, 1e-30f), off = gs.e - ref;
+          const float2 c2 = make_float2(c, c), n2 = make_float2(off, off);
+          float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float2 x0 = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, n2);
+            float2 x1 = ffma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), c2, n2);
+            x0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+            x1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+            s0 = fadd2(s0, x0);
+            s1 = fadd2(s1, x1);
+            const __half2 h0 = __floats2half2_rn(x0.x, x0.y), h1 = __floats2half2_rn(x1.x, x1.y);
+            pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+            pk[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          }
+          l = fmaf((s0.x + s0.y) + (s1.x + s1.y), gs.inv, l);
+          if (f4[g] & kFlagZeroV) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pk[k] = 0u;
+          }
+          tmem_st16(tS + 16 * g, pk);  // (groups 0 to 3: the columns of S's lower half)
+        };
+        weigh(v0, 0);
+        tmem_ld32(tS + 64, v0);
+        weigh(v1, 1);
+        tmem_wait_ld();
+        if (masked) hide(v0, 2);
+        tmem_ld32(tS + 96, v1);
+        weigh(v0, 2);
+        tmem_wait_ld();
+        if (masked) hide(v1, 3);
+        weigh(v1, 3);
+        if (j > first && __any_sync(0xffffffffu, moved)) {  // (O of the step before is done: S came after it)
+          const float f = moved ? al : 1.f;
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t x[32];
+            tmem_ld32(tO + 32 * k, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * f);
+            tmem_st32(tO + 32 * k, x);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + t));
+        m = mn;
+      }
+      if (!ok) break;
+      // ---- the segment's share
+      if (!fin && m > -kPgInf) l = __uint_as_float(0x7fffffffu);  // saw a key through something not finite
+      if (first < n) {
+        ok = wait(kOFull + t, shares);
+        ++shares;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+      }
+      float fa = 1.f, fb = 0.f;  // weights of this tile's O and (dual) the other's
+      if (dual) {
+        ml[(2 * t) * 128 + r] = m;
+        ml[(2 * t + 1) * 128 + r] = l;
+        tc_fence_before();
+        mbar_arrive(bar(kMerge));
+        ok = wait(kMerge, merges);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const float mo = ml[(2 * (1 - t)) * 128 + r], lo = ml[(2 * (1 - t) + 1) * 128 + r];
+        const float mm = fmaxf(m, mo);
+        fa = m == -kPgInf ? 0.f : ex2_approx(m - mm);
+        fb = mo == -kPgInf ? 0.f : ex2_approx(mo - mm);
+        l = fa * l + fb * lo;
+        m = mm;
+      }
+      tc_fence_after();
+      const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
+      const size_t row = (static_cast<size_t>(sg.b) * a.Hq + hq) * a.T + tok;
+      const int pr = (dual ? 0 : 128 * t) + r;  // row of the block
+      const float rl = l == 0.f ? 0.f : 1.f / l;
+      const uint32_t tOther = tmem + lane_base + kTmO + D * (1 - t);
+#pragma unroll 1
+      for (int k = dual ? t * (D / 64) : 0; k < (dual ? (t + 1) * (D / 64) : D / 32); ++k) {
+        uint32_t x[32];
+        float y[32];
+        tmem_ld32(tO + 32 * k, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 32; ++q) y[q] = fa == 0.f ? 0.f : __uint_as_float(x[q]) * fa;
+        if (dual) {
+          tmem_ld32(tOther + 32 * k, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) y[q] = fb == 0.f ? y[q] : fmaf(__uint_as_float(x[q]), fb, y[q]);
+        }
+        if (whole) {
+          if (in) write_out32(a, row, 32 * k, y, rl);
+        } else if (in && QATTN_IN_BOUNDS(slot < a.slots)) {
+          // chunks of four channels, each for all rows: a warp writes 512 consecutive bytes
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + 8 * k + q / 4) * kRows + pr) * 4) =
+                make_float4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+        }
+      }
+      if (in && (!dual || t == 0)) {
+        if (whole) {
+          if (a.lse && QATTN_IN_BOUNDS(row < a.rows_total))
+            a.lse[row] = l == 0.f ? -kPgInf : ((m + kHead) + log2f(l * (1.f / (1 << kHead)))) * kPgLn2;
+        } else if (QATTN_IN_BOUNDS(slot < a.slots)) {
+          a.part_m[slot * kRows + pr] = m;
+          a.part_l[slot * kRows + pr] = l;
+        }
+      }
+      tc_fence_before();  // the next segment's MMAs overwrite O
+      if (dual) {
+        mbar_arrive(bar(kMerge + 1));
+        ok = wait(kMerge + 1, merges);  // the other tile's threads have read this one's O
+        ++merges;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The join: CTAs (c, y) work for the boundary between the shares of CTAs c and c + 1, if
+// it is the first one inside a block.  A lane for a row, a warp for four channels of it
+// (blockIdx.y: 32 rows, then 16 channels), so that every load of a share takes 512
+// consecutive bytes; eight shares' loads in flight.
+template <int D>
+__global__ void __launch_bounds__(kPgJoinThreads) paged_join_rows_kernel(const PagedArgs a) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PagedWalk w = pg_walk<kRows, kStep>(a, blockIdx.x + 1, a.ctas);
+  const int r = 32 * (blockIdx.y % (kRows / 32)) + lane;
+  const int c = 4 * (4 * (blockIdx.y / (kRows / 32)) + warp);
+  const bool inside = w.p < w.end && w.s0 > 0 && w.s0 < w.steps;
+  const int c0 = inside ? pg_owner(w.p - w.s0, w.total, a.ctas) : 0;
+  const int c1 = inside ? pg_owner(w.p - w.s0 + w.steps - 1, w.total, a.ctas) : 0;
+  const int rr = w.rb * kRows + r;
+  pdl_wait();
+  pdl_trigger();
+  if (!inside || c0 != static_cast<int>(blockIdx.x) || rr / a.G >= w.seq.n) return;
+  float m = -kPgInf, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int cb = c0; cb <= c1; cb += U) {
+    float mc[U], lc[U], mn = m;
+    float4 y[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int ci = cb + i;
+      const size_t slot = 2 * static_cast<size_t>(ci) + (ci == c0 ? 1 : 0);
+      mc[i] = -kPgInf;
+      if (ci <= c1 && QATTN_IN_BOUNDS(slot < a.slots)) {
+        mc[i] = a.part_m[slot * kRows + r];
+        lc[i] = a.part_l[slot * kRows + r];
+        y[i] = *reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + c / 4) * kRows + r) * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) mn = fmaxf(mn, mc[i]);
+    if (mn == -kPgInf) continue;
+    const float f = m == -kPgInf ? 0.f : ex2_approx(m - mn);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (mc[i] == -kPgInf) continue;
+      const float g = ex2_approx(mc[i] - mn);
+      l = fmaf(g, lc[i], l);
+      o.x = fmaf(g, y[i].x, o.x);
+      o.y = fmaf(g, y[i].y, o.y);
+      o.z = fmaf(g, y[i].z, o.z);
+      o.w = fmaf(g, y[i].w, o.w);
+    }
+    m = mn;
+  }
+  pg_write_out<D, kHead>(a, w.b, w.hkv, w.seq.n, rr, c, o, m, l);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
+  constexpr int smem = Cfg<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_tc_kernel<D, E4M3>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  if (e != cudaSuccess || a.ctas == 1) return e;
+  return launch_pdl(paged_join_rows_kernel<D>, dim3(a.ctas - 1, (kRows / 32) * (D / 16)), dim3(kPgJoinThreads), 0, s, a);
+}
+
+}  // namespace
+
+unsigned int check_take_paged_tc() { return check_take_local(); }
+
+cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s) {
+  if (a.e4m3) return a.d == 64 ? launch_d<64, true>(a, s) : launch_d<128, true>(a, s);
+  return a.d == 64 ? launch_d<64, false>(a, s) : launch_d<128, false>(a, s);
+}
+
+}  // namespace qattn

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   PagedSeg sg;
   bool some = true;  // CL: the block has rows
   if constexpr (CL) some = pg_cluster_seg<kRows, kStep>(a, sg);
-  else walk = pg_walk<kRows, kStep>(a);
+  else walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
   __syncthreads();  // the abort flag is set
   uint32_t used = 0;  // tiles this warp has taken through its ring
   uint32_t sent = 0;  // lane 0: those it has issued

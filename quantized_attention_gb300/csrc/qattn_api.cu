@@ -341,6 +341,7 @@ qattn_status tree_shape_ok(const qattn_shape* shape) {
 
 // qattn_paged_fwd's split, as TreeSplit.
 struct PagedSplit {
+  bool tc;
   int cluster, step, rows, blocks, ctas, lead;
   int64_t steps;
   size_t slots, off_m, off_l, bytes;
@@ -348,16 +349,17 @@ struct PagedSplit {
 PagedSplit paged_split(const qattn_shape* s) {
   PagedSplit t{};
   const int64_t R = s->Hq / s->Hkv * s->Nq;
-  t.step = qattn::kPagedWarpStep;
-  t.rows = qattn::kPagedRows;
+  t.tc = R > qattn::kPagedRows;
+  t.step = t.tc ? qattn::kPagedTcStep : qattn::kPagedWarpStep;
+  t.rows = t.tc ? qattn::kPagedTcRows : qattn::kPagedRows;
   const int64_t blocks = (R + t.rows - 1) / t.rows, heads = s->B * s->Hkv * blocks;
   const int64_t head_steps = std::max<int64_t>(1, (s->Nk + t.step - 1) / t.step);
   t.blocks = static_cast<int>(blocks);
-  t.lead = qattn::kPagedWarpLead;
+  t.lead = t.tc ? qattn::kPagedTcLead : qattn::kPagedWarpLead;
   t.steps = heads * (t.lead + head_steps);
-  t.cluster = qattn::tree_cluster(heads, head_steps);
-  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(qattn::kPagedWarpCtas, (t.steps + 3) / 4)));
-  if (t.cluster > 0 && heads * t.cluster >= (int64_t{1} << 31)) t.cluster = 0;
+  t.cluster = t.tc ? 0 : qattn::tree_cluster(heads, head_steps);
+  const int64_t most = t.tc ? qattn::kPagedTcCtas : qattn::kPagedWarpCtas;
+  t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
   if (t.cluster > 0) {
     t.ctas = static_cast<int>(heads * t.cluster);
     t.lead = 0;
@@ -1439,6 +1441,13 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   a.part_o = reinterpret_cast<float*>(w);
   a.part_m = reinterpret_cast<float*>(w + sp.off_m);
   a.part_l = reinterpret_cast<float*>(w + sp.off_l);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  char sb[128];
+  QATTN_LOG_LINE("qattn_paged_fwd %s page=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb), 1 << a.page_shift,
+                 sp.tc ? "paged_tc_kernel + paged_join_rows_kernel"
+                       : sp.cluster > 0 ? "paged_warp_kernel (clusters)" : "paged_warp_kernel + paged_join_kernel",
+                 sp.ctas);
+  if (sp.tc) return from_cuda(qattn::launch_paged_tc(a, cs));
   CUtensorMap tk, tv;
   const int64_t planes = paging->n_pages * shape->Hkv;
   if (!encode_cache(&tk, k_pages, planes, paging->page_size, paging->page_size, shape->d,
@@ -1446,10 +1455,7 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
       !encode_cache(&tv, v_pages, planes, paging->page_size, paging->page_size, shape->d,
                     static_cast<uint32_t>(sp.step)))
     return QATTN_ERR_CUDA;
-  char sb[128];
-  QATTN_LOG_LINE("qattn_paged_fwd %s page=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb), 1 << a.page_shift,
-                 sp.cluster > 0 ? "paged_warp_kernel (clusters)" : "paged_warp_kernel + paged_join_kernel", sp.ctas);
-  return from_cuda(qattn::launch_paged_warp(tk, tv, a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(qattn::launch_paged_warp(tk, tv, a, cs));
 }
 
 int qattn_fwd_kernel_choice(const qattn_shape* shape, const qattn_params* params) {
@@ -1505,7 +1511,8 @@ qattn_status qattn_get_error(qattn_stream_t stream) {
                               qattn::check_take_kv_weights_tc() |
                               qattn::check_take_kv_cache() |
                               qattn::check_take_paged_cache() |
-                              qattn::check_take_paged_warp();
+                              qattn::check_take_paged_warp() |
+                              qattn::check_take_paged_tc();
   if (v & qattn::kErrTimeout) return QATTN_ERR_TIMEOUT;
   if (checks != 0) return QATTN_ERR_BOUNDS;
   return (v & qattn::kErrDomain) ? QATTN_ERR_INVALID_ARG : QATTN_OK;

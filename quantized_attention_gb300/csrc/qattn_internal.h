@@ -83,6 +83,7 @@ unsigned int check_take_kv_weights_tc();
 unsigned int check_take_kv_cache();
 unsigned int check_take_paged_cache();
 unsigned int check_take_paged_warp();
+unsigned int check_take_paged_tc();
 // One guard that fails for 16 of 32 threads, touching no memory (quant_kernels.cu).
 cudaError_t launch_bounds_probe(cudaStream_t s);
 
@@ -435,6 +436,12 @@ constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
 constexpr int kPagedWarpStep = 32;            // keys of a step
 constexpr int kPagedWarpLead = 10;            // steps that a block's start counts for in equal shares
 constexpr int kPagedCluster = 8;              // most CTAs of a block's own cluster
+// More than kPagedRows query rows of a KV head (query heads of the group x tokens): the
+// tensor-core kernel.
+constexpr int kPagedTcRows = 256;             // query rows of its block
+constexpr int kPagedTcStep = 128;
+constexpr int kPagedTcCtas = 152;             // one an SM
+constexpr int kPagedTcLead = 4;
 struct PagedArgs {
   int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
   int n_pages, page_shift, max_pages, e4m3;
@@ -460,6 +467,8 @@ struct PagedArgs {
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
 cudaError_t launch_paged_warp(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                               cudaStream_t s);
+// ---- paged_tc.cu
+cudaError_t launch_paged_tc(const PagedArgs& a, cudaStream_t s);
 
 // ---- exact24.cu
 struct Exact24Args {

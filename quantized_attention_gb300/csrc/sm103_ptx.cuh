@@ -402,6 +402,18 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 
+// Registers a thread of this warpgroup (four warps, all of which call) keeps, or asks
+// for: what a block's warpgroups ask for together may not be more than it was launched
+// with, or the asking waits forever.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------- launches
 // Programmatic dependent launch.  pdl_trigger lets the next kernel of the
 // stream start launching (its CTAs are placed once every CTA of this grid has

@@ -346,6 +346,15 @@ SHAPES = [
     (5, 4, 2, 128, 32, "int8", 2, [4173, 0, 17, 1, 900], [1, 2, 2, 0, 2]),
     (40, 2, 1, 64, 32, "e4m3", 1, list(range(0, 1200, 30)), None),  # more sequences than a warp has lanes
     (1, 5, 5, 64, 64, "int8", 1, [9001], None),
+    (1, 4, 1, 128, 64, "int8", 200, [5000], None),            # 800 rows over 40 blocks of keys
+    (3, 2, 1, 64, 32, "e4m3", 100, [3000, 100, 2049], [100, 65, 30]),  # row blocks of one tile and of two
+    (2, 8, 1, 128, 128, "e4m3", 40, [6000, 333], [40, 9]),
+    (1, 1, 1, 64, 128, "int8", 700, [2300], None),
+    # shares of many steps, blocks of one tile and of two
+    (8, 16, 8, 64, 32, "int8", 9, [3000, 2999, 1700, 2100, 40, 3100, 2500, 2000], [9, 9, 8, 9, 9, 9, 1, 9]),
+    (3, 12, 12, 64, 64, "e4m3", 515, [1500, 2000, 1030], [515, 260, 300]),
+    (2, 32, 8, 128, 64, "int8", 70, [2500, 4000], [70, 20]),
+    (7, 4, 4, 128, 32, "int8", 130, [131, 130, 700, 0, 1500, 260, 128], [130, 129, 128, 0, 127, 1, 128]),
 ]
 
 
