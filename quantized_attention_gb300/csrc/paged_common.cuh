@@ -284,7 +284,7 @@ __device__ __forceinline__ void pg_row_shift(uint32_t amax, float& up, float& do
 // 2^-48 and 2^48 (96 powers of two, 30 left for the weights).  A smaller one counts as
 // 0: the page adds 2^(t - m) to l and nothing to O.  A larger one, and scales that are
 // negative or not finite, give NaN to every row that sees a key of the page.
-constexpr float kPgMinV = 0x1p-48f, kPgMaxV = 0x1p48f;
+constexpr float kPgMinV = 0x1p-48f, kPgMaxV = 0x1p48f, kPgZeroE = -48.f;
 struct PageScale {
   float k;       // K scale (0 for a page that counts as NaN)
   float e_max;   // the exponent's part in the maximum,
@@ -299,7 +299,7 @@ __device__ __forceinline__ PageScale pg_scale(float ks, float vs) {
   const bool zero = p.nan || vs < kPgMinV;
   p.k = p.nan ? 0.f : ks;
   p.e = zero ? 0.f : log2f(vs);
-  p.e_max = zero ? -48.f : p.e;
+  p.e_max = zero ? kPgZeroE : p.e;
   p.inv = zero ? 1.f : 1.f / vs;
   p.keep = zero ? 0u : 0xffffffffu;
   return p;

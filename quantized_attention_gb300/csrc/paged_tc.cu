@@ -3,6 +3,7 @@
 //
 // A CTA works on a block of 256 query rows (two tiles of 128) in steps of 128 keys:
 //   warp 0       issues the MMAs
+//   warp 2       walks the share: its segments go to the others through shared memory
 //   warps 4-7    codes -> fp16 tiles K16, V16 [key][channel] in shared memory, straight
 //                from the pages: a warp takes 32 rows of every tile (they lie in one
 //                page), the next step's loads in flight
@@ -28,7 +29,11 @@ namespace {
 constexpr int kStep = kPagedTcStep;
 constexpr int kRows = kPagedTcRows;
 static_assert(kStep == 128 && kRows == 256, "two tiles of 128 TMEM lanes, one block of keys per step");
+// Four warpgroups: the issuing and the planning warp's, the converting one, softmax of
+// tile 0 and of tile 1.  Registers a thread: 128 at launch, shared out.
 constexpr int kThreads = 512;
+constexpr int kIssueRegs = 48, kConvRegs = 80, kSoftRegs = 192;
+static_assert(kIssueRegs + kConvRegs + 2 * kSoftRegs == 4 * 128, "the split takes what the launch holds");
 constexpr int kHead = 7;      // of the exponentials' reference (pg_head)
 constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
 static_assert(kHead + kLazy <= 15.f, "P stays inside fp16");
@@ -36,23 +41,16 @@ constexpr uint32_t kTmS = 0, kTmO = 256;  // TMEM columns (tile t: + 128 t, + D 
 constexpr int kGroups = kStep / 32;       // groups of keys that lie in one page
 constexpr int kWinSteps = 32 / kGroups;   // steps of a warp's window of scales
 
-// A group's scales for the softmax (PageScale), and what is rare.
-struct GroupScale {
-  float k, e_max, e, inv;
-};
-constexpr uint32_t kFlagHidden = 1, kFlagZeroV = 2, kFlagNaN = 4;
-
 template <int D>
 struct Cfg {
   static constexpr int kTile = 128 * D * 2;  // fp16 Q, K16 or V16: D / 64 blocks of [128][128 B]
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = 2 * kTile;
   static constexpr int kOffV = kOffK + 2 * kTile;
-  static constexpr int kOffScale = kOffV + 2 * kTile;              // [8 warps][32] GroupScale
-  static constexpr int kOffFlags = kOffScale + 8 * 32 * 16;        // [8 warps][32]
-  static constexpr int kOffML = kOffFlags + 8 * 32 * 4;            // m and l of both tiles (dual)
+  static constexpr int kOffML = kOffV + 2 * kTile;                 // m and l of both tiles (dual)
   static constexpr int kOffBar = kOffML + 2 * 2 * 128 * 4;
-  static constexpr int kBytes = kOffBar + 256;
+  static constexpr int kOffSeg = kOffBar + 256;                    // [2] PagedSeg
+  static constexpr int kBytes = kOffSeg + 2 * 64;
   static_assert(kBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -61,17 +59,31 @@ enum {
   kKEmpty = 2,  // [2] the step's QK MMAs
   kVFull = 4,   // [2] 128 converting threads
   kVEmpty = 6,  // [2] the step's PV MMAs
-  kSFull = 8,   // [2 tiles] QK (and every MMA before it) is done
-  kPFull = 10,  // [2 tiles] 128 threads: P is there, O rescaled
-  kQFull = 12,  // [2 tiles] 128 threads wrote Q
-  kOFull = 14,  // [2 tiles] a segment's last PV is done
-  kMerge = 16,  // [2] 256 threads: m and l are there; O has been read (dual)
-  kDrain = 18,
-  kNumBars = 19
+  kSFull = 8,   // [2 tiles] QK (and every MMA of the tile before it) is done
+  kPFull = 10,  // [2 tiles][2 halves] 128 threads: P is there, O rescaled
+  kQFull = 14,  // [2 tiles] 128 threads wrote Q
+  kOFull = 16,  // [2 tiles] a segment's last PV is done
+  kMerge = 18,  // [2] 256 threads: m and l are there; O has been read (dual)
+  kDrain = 20,
+  kSegFull = 21,   // [2] the planning thread
+  kSegEmpty = 23,  // [2] every other thread that works: 1 + 128 + 256
+  kNumBars = 25
 };
 
-// Steps of a segment that a tile takes part in.
-__device__ __forceinline__ int tile_steps(int n, bool dual, int t) { return dual ? (n + 1 - t) / 2 : n; }
+// f(constant 0), f(constant 1), ...
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unroll(F f) {
+  if constexpr (I < N) {
+    f(Const<I>{});
+    unroll<N, I + 1>(f);
+  }
+}
+
+// Whether both tiles hold the block's rows and take its steps in turn.
 __device__ __forceinline__ bool is_dual(const PagedArgs& a, const PagedSeg& s) {
   return s.seq.n * a.G - s.rb * kRows <= 128;
 }
@@ -124,17 +136,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 8 * kNumBars + 4);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
-    return mbar_wait_fast(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
+    return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
   };
+  auto poll = [&](int i, uint32_t n) { return mbar_poll(bar(i), n & 1, abort_flag, a.err, kErrTimeout); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
-      if ((i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 2) ||
+      if ((i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 4) ||
           (i >= kQFull && i < kQFull + 2))
         n = 128;
       if (i >= kMerge && i < kMerge + 2) n = 256;
+      if (i >= kSegEmpty && i < kSegEmpty + 2) n = 1 + 128 + 256;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -150,67 +164,100 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();  // after the wait: the join reads the lengths before its own
-  PagedWalk walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
-  PagedSeg sg;
-  auto next_segment = [&] {
-    // (a share may hold the lead of a block and none of its steps, and end with it)
-    return pg_next<kRows, kStep>(a, walk, sg);
+  // Segment `seg` (from 0) of this CTA's share; n() == 0: there is none.
+  PagedSeg* const slots = reinterpret_cast<PagedSeg*>(smem + C::kOffSeg);
+  auto fetch = [&](uint32_t seg, const PagedSeg*& sg) {
+    sg = &slots[seg & 1];
+    return wait(kSegFull + (seg & 1), seg >> 1);
   };
 
-  if (warp == 0) {
-    if (elect_one()) {
+  if (warp < 4) {
+    reg_dec<kIssueRegs>();
+    if (warp == 2) {
+      // ------------------------------------------------------------ segments
+      PagedWalk walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
+      if (lane == 0) {
+        bool ok = true, some = true;
+        for (uint32_t seg = 0; ok && some; ++seg) {
+          PagedSeg sg{};
+          some = pg_next<kRows, kStep>(a, walk, sg);
+          if (!some) sg.s0 = sg.s1 = 0;
+          if (seg >= 2 && !(ok = wait(kSegEmpty + (seg & 1), (seg >> 1) - 1))) break;
+          slots[seg & 1] = sg;
+          mbar_arrive(bar(kSegFull + (seg & 1)));
+        }
+        if (!ok) *abort_flag = 1;
+      }
+      __syncwarp();
+    } else if (warp == 0 && elect_one()) {
       // ------------------------------------------------------------ MMA
+      // One thread for both tiles: its order keeps them half a step apart, so that one
+      // tile's MMAs run under the other's softmax.  (A thread for each lets both wait and
+      // then contend: 1021 us against 910 for 2048 tokens over 32K.)
       constexpr uint32_t idesc_qk = make_idesc(128, kStep, 0, 0);
       constexpr uint32_t idesc_pv = make_idesc(128, D, 0, 0) | kIdescBMnMajor;
-      const uint64_t qd0 = smem_desc(base + C::kOffQ, 1024, kSwizzle128B);
-      const uint64_t kd0 = smem_desc(base + C::kOffK, 1024, kSwizzle128B);
-      const uint64_t vd0 = smem_desc_mn(base + C::kOffV, kStep * 128, 1024);
+      constexpr uint32_t high = desc_high(1024, kSwizzle128B);  // of Q, K16 and V16
+      const uint32_t q0 = static_cast<uint32_t>(smem_desc(base + C::kOffQ, 1024, kSwizzle128B));
+      const uint32_t k0 = static_cast<uint32_t>(smem_desc(base + C::kOffK, 1024, kSwizzle128B));
+      const uint32_t v0 = static_cast<uint32_t>(smem_desc_mn(base + C::kOffV, kStep * 128, 1024));
+      constexpr uint32_t tile = C::kTile >> 4;
       bool ok = true;
-      uint32_t it = 0, seg = 0;        // steps and segments done
-      uint32_t np[2] = {0, 0};         // PVs issued for each tile
+      uint32_t it = 0;         // steps done
+      uint32_t np[2] = {0, 0}; // PVs of each tile
       auto qk = [&](int t, uint32_t step) {
-        const uint64_t qd = qd0 + t * (C::kTile >> 4), kd = kd0 + (step & 1) * (C::kTile >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k / 4) * (128 * 128) + 32 * (k % 4)) >> 4;
-          mma_f16(tmem + kTmS + 128 * t, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
-        }
+        const uint32_t qd = q0 + t * tile, kd = k0 + (step & 1) * tile, d = tmem + kTmS + 128 * t;
+        unroll<D / 16>([&](auto k) {
+          constexpr int i = decltype(k)::value;
+          mma_f16_at<((i / 4) * (128 * 128) + 32 * (i % 4)) / 16, high, idesc_qk>(d, qd, kd, i > 0 ? 1u : 0u);
+        });
         mma_commit(bar(kSFull + t));
       };
-      auto pv = [&](int t, uint32_t step, bool first) {
-        const uint64_t vd = vd0 + (step & 1) * (C::kTile >> 4);
-#pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
-          mma_f16_ts(tmem + kTmO + D * t, tmem + kTmS + 128 * t + 8 * k, vd + (k * 2048) / 16, idesc_pv,
-                     (!first || k > 0) ? 1u : 0u);
-      };
-      for (; ok && next_segment(); ++seg) {
-        const int n = sg.s1 - sg.s0;
-        const bool dual = is_dual(a, sg);
+      for (uint32_t seg = 0;; ++seg) {
+        const PagedSeg* sg;
+        if (!(ok = fetch(seg, sg))) break;
+        const int n = sg->s1 - sg->s0;
+        const bool dual = is_dual(a, *sg);
+        mbar_arrive(bar(kSegEmpty + (seg & 1)));
+        if (n == 0) break;
         // the first QK of each tile
         for (int t = 0; ok && t < 2; ++t) {
           if (!(ok = wait(kQFull + t, seg))) break;
-          if (tile_steps(n, dual, t) == 0) continue;
+          if (dual && t >= n) {  // no step for this tile
+            mbar_arrive(bar(kOFull + t));
+            continue;
+          }
           const uint32_t step = it + (dual ? t : 0);
           if ((dual || t == 0) && !(ok = wait(kKFull + (step & 1), step >> 1))) break;
           tc_fence_after();
           qk(t, step);
           if (dual || t == 1) mma_commit(bar(kKEmpty + (step & 1)));
         }
+        const int ahead = dual ? 2 : 1;  // to a tile's next step
         for (int j = 0; ok && j < n; ++j, ++it) {
-          if (!(ok = wait(kVFull + (it & 1), it >> 1))) break;
+          const uint32_t st = it & 1;
+          if (!(ok = poll(kVFull + st, it >> 1))) break;
+          const uint32_t vd = v0 + st * tile;
           const int t0 = dual ? (j & 1) : 0, t1 = dual ? t0 + 1 : 2;
-          const int ahead = dual ? 2 : 1;   // the tile's next step
           for (int t = t0; t < t1; ++t) {
-            if (!(ok = wait(kPFull + t, np[t]))) break;
+            const uint32_t o = tmem + kTmO + D * t, p = tmem + kTmS + 128 * t, more = j >= ahead ? 1u : 0u;
+            if (!(ok = poll(kPFull + 2 * t, np[t]))) break;  // keys 0 - 63
             tc_fence_after();
-            pv(t, it, j < ahead);
+            unroll<4>([&](auto k) {
+              constexpr int i = decltype(k)::value;
+              mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
+            });
+            if (!(ok = poll(kPFull + 2 * t + 1, np[t]))) break;  // keys 64 - 127
+            tc_fence_after();
+            unroll<4>([&](auto k) {
+              constexpr int i = 4 + decltype(k)::value;
+              mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, 1u);
+            });
             ++np[t];
-            if (t == t1 - 1) mma_commit(bar(kVEmpty + (it & 1)));
+            if (t == t1 - 1) mma_commit(bar(kVEmpty + st));
             if (j + ahead < n) {
               const uint32_t step = it + ahead;
               if (t == t0) {
-                if (!(ok = wait(kKFull + (step & 1), step >> 1))) break;
+                if (!(ok = poll(kKFull + (step & 1), step >> 1))) break;
                 tc_fence_after();
               }
               qk(t, step);
@@ -220,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
             }
           }
         }
+        if (!ok) break;
       }
       mma_commit(bar(kDrain));
       volatile int never = 0;
@@ -227,8 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       if (!ok) *abort_flag = 1;
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp < 8) {
     // -------------------------------------------------------------- codes -> fp16
+    reg_dec<kConvRegs>();
     // Warp w takes rows 32 w .. 32 w + 31 of every tile, K and V of a step in turn, so that
     // each waits for every stage in order.  The eight lanes of a store take four chunks of
     // rows r and r ^ 5, which differ in the swizzle's low and high bit: eight bank groups.
@@ -239,8 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
     const uint32_t c0 = ((2 * cc) ^ u) << 4, c1 = ((2 * cc + 1) ^ u) << 4;
     bool ok = true;
     uint32_t it = 0;  // steps done
-    while (ok && next_segment()) {
+    for (uint32_t seg = 0;; ++seg) {
+      const PagedSeg* at_seg;
+      if (!(ok = __all_sync(0xffffffffu, fetch(seg, at_seg)))) break;
+      const PagedSeg sg = *at_seg;
+      mbar_arrive(bar(kSegEmpty + (seg & 1)));
       const int n = sg.s1 - sg.s0, len = sg.seq.len;
+      if (n == 0) break;
       // pages of this warp's rows in the next 32 steps, one a lane, and in the 32 after
       auto look_up = [&](int j0) {
         const int key = (sg.s0 + j0 + lane) * kStep + 32 * w;
@@ -252,7 +306,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         return p;
       };
       int cur = look_up(0), nxt = n > 32 ? look_up(32) : -1;
-      uint4 vk[NL], vv[NL];
       // where step j's rows start in the pool (in bytes), or -1
       auto place = [&](int j) -> long long {
         if (j > 0 && j % 32 == 0) {
@@ -266,71 +319,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
                               (key & ((1 << a.page_shift) - 1)) + u;
         return row * D + 16 * cc;
       };
-      auto load = [&](uint4 (&x)[NL], const uint8_t* pages, long long at, int j) {
+      uint4 x[2][NL / 2];  // a tile's rows in two halves of 16
+      auto load = [&](int h, const uint8_t* pages, long long at, int j) {
         const int left = len - (sg.s0 + j) * kStep - 32 * w - u;
 #pragma unroll
-        for (int k = 0; k < NL; ++k) {
-          x[k] = make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < NL / 2; ++k) {
+          const int r = 16 * h + 8 * (k / NB);
+          x[h][k] = make_uint4(0u, 0u, 0u, 0u);
           // rows behind the sequence may hold any byte: zeros stand in
-          if (at >= 0 && 8 * (k / NB) < left)
-            x[k] = *reinterpret_cast<const uint4*>(pages + at + 8 * (k / NB) * D + 64 * (k % NB));
+          if (at >= 0 && r < left) x[h][k] = *reinterpret_cast<const uint4*>(pages + at + r * D + 64 * (k % NB));
         }
       };
-      auto convert = [&](const uint4 (&x)[NL], uint32_t tile) {
+      auto convert = [&](int h, uint32_t tile) {
 #pragma unroll
-        for (int k = 0; k < NL; ++k) {
-          uint32_t h[8];
-          widen16<E4M3>(x[k], h);
-          const uint32_t d = dst + tile + (k % NB) * (128 * 128) + 8 * (k / NB) * 128;
-          sts128(d + c0, h[0], h[1], h[2], h[3]);
-          sts128(d + c1, h[4], h[5], h[6], h[7]);
+        for (int k = 0; k < NL / 2; ++k) {
+          uint32_t y[8];
+          widen16<E4M3>(x[h][k], y);
+          const uint32_t d = dst + tile + (k % NB) * (128 * 128) + (16 * h + 8 * (k / NB)) * 128;
+          sts128(d + c0, y[0], y[1], y[2], y[3]);
+          sts128(d + c1, y[4], y[5], y[6], y[7]);
         }
-        fence_proxy_async_smem();
       };
       long long at = place(0);
-      load(vk, a.k_pages, at, 0);
-      load(vv, a.v_pages, at, 0);
+      load(0, a.k_pages, at, 0);
+      load(1, a.k_pages, at, 0);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t st = it & 1;
-        const bool more = j + 1 < n;
-        if (more) at = place(j + 1);
         ok = it < 2 || wait(kKEmpty + st, (it >> 1) - 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        convert(vk, C::kOffK + st * C::kTile);
+        const uint32_t tk = C::kOffK + st * C::kTile, tv = C::kOffV + st * C::kTile;
+        convert(0, tk);
+        load(0, a.v_pages, at, j);
+        convert(1, tk);
+        load(1, a.v_pages, at, j);
+        fence_proxy_async_smem();
         mbar_arrive(bar(kKFull + st));
-        if (more) load(vk, a.k_pages, at, j + 1);
+        const bool more = j + 1 < n;
+        if (more) at = place(j + 1);
         ok = it < 2 || wait(kVEmpty + st, (it >> 1) - 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        convert(vv, C::kOffV + st * C::kTile);
+        convert(0, tv);
+        if (more) load(0, a.k_pages, at, j + 1);
+        convert(1, tv);
+        if (more) load(1, a.k_pages, at, j + 1);
+        fence_proxy_async_smem();
         mbar_arrive(bar(kVFull + st));
-        if (more) load(vv, a.v_pages, at, j + 1);
       }
+      if (!ok) break;
     }
     if (!ok) *abort_flag = 1;
-  } else if (warp >= 8) {
+  } else {
     // -------------------------------------------------------------- softmax
+    reg_inc<kSoftRegs>();
     const int t = (warp - 8) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;  // TMEM lane, row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_base + kTmS + 128 * t, tO = tmem + lane_base + kTmO + D * t;
-    GroupScale* win = reinterpret_cast<GroupScale*>(smem + C::kOffScale) + 32 * (warp - 8);
-    uint32_t* flags = reinterpret_cast<uint32_t*>(smem + C::kOffFlags) + 32 * (warp - 8);
     float* ml = reinterpret_cast<float*>(smem + C::kOffML);  // [tile][m, l][128]
-    uint32_t ns = 0, shares = 0, merges = 0;  // this tile's steps, segments that had some; dual segments
+    uint32_t ns = 0, merges = 0;  // this tile's steps, dual segments
     bool ok = true;
-    while (ok && next_segment()) {
-      const int n = sg.s1 - sg.s0, len = sg.seq.len;
-      const bool dual = is_dual(a, sg);
-      const int rr = sg.rb * kRows + (dual ? 0 : 128 * t) + r;
-      const int tok = rr / a.G, hq = sg.hkv * a.G + rr - tok * a.G;
-      const bool in = tok < sg.seq.n;
+    for (uint32_t seg = 0;; ++seg) {
+      const PagedSeg* at_seg;
+      if (!(ok = __all_sync(0xffffffffu, fetch(seg, at_seg)))) break;
+      const int n = at_seg->s1 - at_seg->s0;
+      if (n == 0) break;
+      const bool dual = is_dual(a, *at_seg);
+      const int s0 = at_seg->s0;
       // ---- the scales' windows, one group a lane: pages two windows ahead, scales one
       auto page_of = [&](int w) {
-        const int key = sg.s0 * kStep + 32 * (32 * w + lane);
+        const int key = s0 * kStep + 32 * (32 * w + lane);
         int p = -1;
-        if (32 * w + lane < kGroups * n && key < len &&
-            QATTN_IN_BOUNDS((key >> a.page_shift) < a.max_pages && sg.b < a.B)) {
-          p = a.page_table[static_cast<size_t>(sg.b) * a.max_pages + (key >> a.page_shift)];
+        if (32 * w + lane < kGroups * n && key < at_seg->seq.len &&
+            QATTN_IN_BOUNDS((key >> a.page_shift) < a.max_pages && at_seg->b < a.B)) {
+          p = a.page_table[static_cast<size_t>(at_seg->b) * a.max_pages + (key >> a.page_shift)];
           if (p < 0 || p >= a.n_pages) {
             atomicOr(a.err, kErrDomain);
             p = -1;
@@ -341,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       auto scales_of = [&](int p, float& ks, float& vs) {
         ks = vs = 0.f;
         if (p < 0) return;
-        const size_t sc = static_cast<size_t>(p) * a.Hkv + sg.hkv;
+        const size_t sc = static_cast<size_t>(p) * a.Hkv + at_seg->hkv;
         ks = a.k_scales[sc];
         vs = a.v_scales[sc];
       };
@@ -351,7 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       // ---- Q's row -> fp16 in shared memory
       float rf;
       bool fin;
+      int lim;
       {
+        const PagedSeg sg = *at_seg;
+        const int rr = sg.rb * kRows + (dual ? 0 : 128 * t) + r;
+        const int tok = rr / a.G, hq = sg.hkv * a.G + rr - tok * a.G;
+        const bool in = tok < sg.seq.n;
+        // (a row that is none sees everything: its scores are 0, and it asks for no mask)
+        lim = in ? min(pg_limit(a, sg.seq, tok), sg.seq.len) : 0x7fffffff;
         const uint16_t* src = a.q + sg.b * a.qsB + hq * a.qsH + tok * a.qsN;
         uint4 x[D / 8];
         uint32_t top = 0;
@@ -383,148 +451,165 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull + t));
-      const int lim = in ? min(pg_limit(a, sg.seq, tok), len) : 0;
       float m = -kPgInf, l = 0.f;  // the row's reference and its sum
       const int first = dual ? t : 0, pace = dual ? 2 : 1;
-      for (int j = first; j < n; j += pace, ++ns) {
+      float c[kGroups], e[kGroups], inv[kGroups];  // the step's scales
+      uint32_t rare = 0;
+      // a window's scales, a lane for a group, and its groups that are out of the ordinary
+      // (kept from shared memory: the MMAs' reads leave a load there waiting for ~1500 cycles)
+      float wk = 0.f, we = 0.f, winv = 1.f;
+      uint32_t hidden = 0, zero_v = 0, bad = 0;
+      auto scales = [&](int j) {
         if (j % kWinSteps == first) {  // a new window
-          const int w = j / kWinSteps;
-          __syncwarp();
           const PageScale ps = pg_scale(ks1, vs1);
-          win[lane] = GroupScale{ps.k, ps.e_max, ps.e, ps.inv};
-          flags[lane] = (p1 < 0 ? kFlagHidden : 0u) | (ps.keep == 0u ? kFlagZeroV : 0u) | (ps.nan ? kFlagNaN : 0u);
-          __syncwarp();
+          wk = ps.k;
+          we = ps.e;
+          winv = ps.inv;
+          hidden = __ballot_sync(0xffffffffu, p1 < 0);
+          zero_v = __ballot_sync(0xffffffffu, ps.keep == 0u);
+          bad = __ballot_sync(0xffffffffu, ps.nan);
           p1 = p2;
           scales_of(p1, ks1, vs1);
-          p2 = page_of(w + 2);
+          p2 = page_of(j / kWinSteps + 2);
         }
-        ok = wait(kSFull + t, ns);
+        const int q0 = kGroups * (j % kWinSteps);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          c[g] = fmaxf(rf * __shfl_sync(0xffffffffu, wk, q0 + g), 1e-30f);
+          e[g] = __shfl_sync(0xffffffffu, we, q0 + g);
+          inv[g] = __shfl_sync(0xffffffffu, winv, q0 + g);
+        }
+        rare = ((hidden | zero_v | bad) >> q0) & ((1u << kGroups) - 1u);
+      };
+      if (first < n) scales(first);
+      for (int j = first; j < n; j += pace, ++ns) {
+        const int q0 = kGroups * (j % kWinSteps);
+        const int room = lim - (s0 + j) * kStep;  // visible keys of the step
+        const bool masked = __any_sync(0xffffffffu, room < kStep || rare != 0u);
+        // The reference seldom moves, so the exponentials begin with the one that stands
+        // while the other scores are on their way; should the maxima ask for another, S is
+        // read again.  0: try; 1: settle the reference first; 2: settled.
+        int mode = masked || __any_sync(0xffffffffu, m == -kPgInf) ? 1 : 0;
+        ok = poll(kSFull + t, ns);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // S in two halves, the upper one for its maxima alone: it is read again where it is
-        // used, which leaves 64 registers for scores
-        uint32_t v0[32], v1[32];
-        float mx[kGroups];
-        const int q0 = kGroups * (j % kWinSteps);
-        const uint4 fl = *reinterpret_cast<const uint4*>(&flags[q0]);
-        const uint32_t f4[kGroups] = {fl.x, fl.y, fl.z, fl.w};
-        const int room = lim - (sg.s0 + j) * kStep;  // visible keys of the step
-        const uint32_t rare = fl.x | fl.y | fl.z | fl.w;
-        const bool masked = __any_sync(0xffffffffu, room < kStep || rare != 0u);
-        auto hide = [&](uint32_t (&v)[32], int g) {  // (masked) hidden keys' scores to -inf
-          const uint32_t vis = pg_first_bits((f4[g] & kFlagHidden) ? 0 : room - 32 * g);
-          if (vis != 0u && (f4[g] & kFlagNaN)) fin = false;
+        for (;;) {
+          uint32_t v[kGroups][32];
+          float mx[kGroups];
+          tmem_ld32_max(tS, v[0], mx[0]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!((vis >> k) & 1u)) v[k] = __float_as_uint(-kPgInf);
-        };
-        auto largest = [&](const uint32_t (&v)[32]) {
-          float x[4] = {-kPgInf, -kPgInf, -kPgInf, -kPgInf};
+          for (int g = 1; g < kGroups; ++g) tmem_ld32_max(tS + 32 * g, v[g], mx[g]);
+          if (mode != 0) tmem_wait_ld();
+          if (masked) {  // hidden keys' scores to -inf
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
+            for (int g = 0; g < kGroups; ++g) {
+              const uint32_t vis = pg_first_bits(((hidden >> (q0 + g)) & 1u) ? 0 : room - 32 * g);
+              if (vis != 0u && ((bad >> (q0 + g)) & 1u)) fin = false;
+              mx[g] = -kPgInf;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x[q] = fmax3(x[q], __uint_as_float(v[k + 2 * q]), __uint_as_float(v[k + 2 * q + 1]));
-          return fmax3(x[0], x[1], fmaxf(x[2], x[3]));
-        };
-        tmem_ld32_max(tS + 64, v0, mx[2]);
-        tmem_ld32_max(tS + 96, v1, mx[3]);
-        tmem_wait_ld();
-        if (masked) {
-          hide(v0, 2);
-          hide(v1, 3);
-          mx[2] = largest(v0);
-          mx[3] = largest(v1);
-        }
-        tmem_ld32_max(tS, v0, mx[0]);
-        tmem_ld32_max(tS + 32, v1, mx[1]);
-        tmem_wait_ld();
-        if (masked) {
-          hide(v0, 0);
-          hide(v1, 1);
-          mx[0] = largest(v0);
-          mx[1] = largest(v1);
-        }
-        float top = -kPgInf;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const GroupScale gs = win[q0 + g];
-          const float c = fmaxf(rf * gs.k, 1e-30f);
-          if (c == kPgInf && mx[g] > -kPgInf) fin = false;
-          top = fmaxf(top, fmaf(mx[g], c, gs.e_max));
-        }
-        const float head = pg_head(top, kHead);
-        const float mn = top > m + (head == 0.f ? 0.f : kHead + kLazy) || m == -kPgInf ? top - head : m;
-        const float ref = mn == -kPgInf ? 0.f : mn;
-        const float al = m == -kPgInf ? 0.f : ex2_approx(m - ref);
-        const bool moved = mn != m;
-        if (moved) l *= al;
-        auto weigh = [&](const uint32_t (&v)[32], int g) {  // P of a group, in place of S
-          const GroupScale gs = win[q0 + g];
-          const float c = fmaxf(rf * gs.k, 1e-30f), off = gs.e - ref;
-          const float2 c2 = make_float2(c, c), n2 = make_float2(off, off);
-          float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float2 x0 = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), c2, n2);
-            float2 x1 = ffma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), c2, n2);
-            x0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-            x1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-            s0 = fadd2(s0, x0);
-            s1 = fadd2(s1, x1);
-            const __half2 h0 = __floats2half2_rn(x0.x, x0.y), h1 = __floats2half2_rn(x1.x, x1.y);
-            pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-            pk[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+              for (int k = 0; k < 32; ++k) {
+                if (!((vis >> k) & 1u)) v[g][k] = __float_as_uint(-kPgInf);
+                mx[g] = fmaxf(mx[g], __uint_as_float(v[g][k]));
+              }
+            }
           }
-          l = fmaf((s0.x + s0.y) + (s1.x + s1.y), gs.inv, l);
-          if (f4[g] & kFlagZeroV) {
+          auto largest = [&] {
+            float top = -kPgInf;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) pk[k] = 0u;
-          }
-          tmem_st16(tS + 16 * g, pk);  // (groups 0 to 3: the columns of S's lower half)
-        };
-        weigh(v0, 0);
-        tmem_ld32(tS + 64, v0);
-        weigh(v1, 1);
-        tmem_wait_ld();
-        if (masked) hide(v0, 2);
-        tmem_ld32(tS + 96, v1);
-        weigh(v0, 2);
-        tmem_wait_ld();
-        if (masked) hide(v1, 3);
-        weigh(v1, 3);
-        if (j > first && __any_sync(0xffffffffu, moved)) {  // (O of the step before is done: S came after it)
-          const float f = moved ? al : 1.f;
+            for (int g = 0; g < kGroups; ++g) {
+              float x = fmaf(mx[g], c[g], e[g]);
+              if ((zero_v >> (q0 + g)) & 1u) x = fmaf(mx[g], c[g], kPgZeroE);
+              top = fmaxf(top, x);
+            }
+            return top;
+          };
+          auto moves = [&](float top, float head) {
+            return top > m + (head == 0.f ? 0.f : kHead + kLazy) || (m == -kPgInf && top > -kPgInf);
+          };
+          if (mode == 1) {
+            const float top = largest(), head = pg_head(top, kHead);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+              if (c[g] == kPgInf && mx[g] > -kPgInf) fin = false;
+            const bool moved = moves(top, head);
+            const float mn = moved ? top - head : m;
+            const float al = !moved ? 1.f : m == -kPgInf ? 0.f : ex2_approx(m - mn);
+            l *= al;
+            m = mn;
+            if (j > first && __any_sync(0xffffffffu, moved)) {  // (O is done: S came after it)
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t x[32];
-            tmem_ld32(tO + 32 * k, x);
-            tmem_wait_ld();
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t x[32];
+                tmem_ld32(tO + 32 * k, x);
+                tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * f);
-            tmem_st32(tO + 32 * k, x);
+                for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * al);
+                tmem_st32(tO + 32 * k, x);
+              }
+              tmem_wait_st();
+            }
+            mode = 2;
+            continue;
           }
+          const float ref = m == -kPgInf ? 0.f : m;
+          float add = 0.f;
+          uint32_t pk[2][32];
+          auto weigh = [&](int g) {
+            const float off = e[g] - ref;
+            const float2 c2 = make_float2(c[g], c[g]), n2 = make_float2(off, off);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float2 x0 = ffma2(make_float2(__uint_as_float(v[g][k]), __uint_as_float(v[g][k + 1])), c2, n2);
+              float2 x1 = ffma2(make_float2(__uint_as_float(v[g][k + 2]), __uint_as_float(v[g][k + 3])), c2, n2);
+              x0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+              x1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+              sum0 = fadd2(sum0, x0);
+              sum1 = fadd2(sum1, x1);
+              const __half2 h0 = __floats2half2_rn(x0.x, x0.y), h1 = __floats2half2_rn(x1.x, x1.y);
+              pk[g / 2][16 * (g % 2) + k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+              pk[g / 2][16 * (g % 2) + k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+            }
+            add = fmaf((sum0.x + sum0.y) + (sum1.x + sum1.y), inv[g], add);
+            if ((zero_v >> (q0 + g)) & 1u) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) pk[g / 2][16 * (g % 2) + k] = 0u;
+            }
+          };
+          weigh(0);
+          if (mode == 0) {
+            tmem_wait_ld();
+            const float top = largest();
+            if (__any_sync(0xffffffffu, moves(top, pg_head(top, kHead)))) {
+              mode = 1;
+              continue;
+            }
+          }
+          weigh(1);
+          tmem_st32(tS, pk[0]);  // P in place of S (its columns are in registers)
+          weigh(2);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + 2 * t));
+          weigh(3);
+          tmem_st32(tS + 32, pk[1]);
+          l += add;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + 2 * t + 1));
+          break;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kPFull + t));
-        m = mn;
+        if (j + pace < n) scales(j + pace);
       }
       if (!ok) break;
       // ---- the segment's share
       if (!fin && m > -kPgInf) l = __uint_as_float(0x7fffffffu);  // saw a key through something not finite
-      if (first < n) {
-        ok = wait(kOFull + t, shares);
-        ++shares;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-      }
+      ok = __all_sync(0xffffffffu, wait(kOFull + t, seg));
+      if (!ok) break;
       float fa = 1.f, fb = 0.f;  // weights of this tile's O and (dual) the other's
       if (dual) {
         ml[(2 * t) * 128 + r] = m;
@@ -544,10 +629,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         m = mm;
       }
       tc_fence_after();
+      const PagedSeg sg = *at_seg;
+      mbar_arrive(bar(kSegEmpty + (seg & 1)));
+      const int pr = (dual ? 0 : 128 * t) + r;  // row of the block
+      const int rr = sg.rb * kRows + pr, tok = rr / a.G, hq = sg.hkv * a.G + rr - tok * a.G;
+      const bool in = tok < sg.seq.n;
       const bool whole = sg.s0 == 0 && sg.s1 == sg.steps;
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
       const size_t row = (static_cast<size_t>(sg.b) * a.Hq + hq) * a.T + tok;
-      const int pr = (dual ? 0 : 128 * t) + r;  // row of the block
       const float rl = l == 0.f ? 0.f : 1.f / l;
       const uint32_t tOther = tmem + lane_base + kTmO + D * (1 - t);
 #pragma unroll 1
@@ -588,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         mbar_arrive(bar(kMerge + 1));
         ok = wait(kMerge + 1, merges);  // the other tile's threads have read this one's O
         ++merges;
-        ok = __all_sync(0xffffffffu, ok);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
       }
     }
     if (!ok) *abort_flag = 1;

@@ -94,6 +94,25 @@ __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, vo
   return mbar_wait_slow(bar, parity, abort_flag, err, code);
 }
 
+// The same without suspending: for a wait that a pipeline's period hangs on (a suspended
+// thread was seen to go on ~550 cycles after the last arrival, a polling one ~50).
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* err, unsigned int code) {
+  if (mbar_test(bar, parity)) return true;
+  const unsigned long long t0 = cycles();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_test(bar, parity)) return true;
+    if ((n & 255u) == 0) {
+      if (*abort_flag) return false;
+      if (cycles() - t0 > kWaitTimeoutCycles) {
+        *abort_flag = 1;
+        atomicOr(err, code);
+        return false;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -241,6 +260,32 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same two with descriptors whose low words are given a constant further (in units of
+// 16 bytes) and whose high word is a constant: an unrolled loop over k then keeps no
+// descriptor of its own in registers.
+constexpr uint32_t desc_high(uint32_t sbo_bytes, uint32_t swz) { return (sbo_bytes >> 4) | (1u << 14) | (swz << 29); }
+template <uint32_t more, uint32_t high, uint32_t idesc>
+__device__ __forceinline__ void mma_f16_at(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "add.u32 x, %1, %3;\n\tadd.u32 y, %2, %3;\n\t"
+      "mov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "n"(more), "n"(high), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <uint32_t a_more, uint32_t more, uint32_t high, uint32_t idesc>
+__device__ __forceinline__ void mma_f16_ts_at(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "add.u32 x, %1, %3;\n\tadd.u32 y, %2, %4;\n\t"
+      "mov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %6, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "n"(a_more), "n"(more), "n"(high), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
