@@ -347,36 +347,34 @@ __device__ __forceinline__ int pg_owner(int x, int total, int G) {
   const int q = total / G, r = total - q * G, big = r * (q + 1);
   return x < big ? x / (q + 1) : r + (x - big) / q;
 }
-// The CTAs that a block's steps were dealt to.  CTA c left its share in slot 2 c when it
-// did not have the block's first step, else in 2 c + 1.
-struct PagedOwners {
+// What the join has to know, left by each CTA of the attention kernel about the place
+// where its share begins: the block that lies across it, if that is the block's first
+// such place, and the CTAs c0 .. c1 that its steps were dealt to (else c1 = -1).  CTA c left
+// its share in slot 2 c when it did not have the block's first step, else in 2 c + 1.
+struct __align__(16) PagedPlan {
   int b, hkv, rb, n;  // n: the sequence's new tokens
-  int c0, c1;         // c0 == c1: written whole, or no such block
+  int c0, c1, pad0, pad1;
 };
-template <int ROWS, int STEP>
-__device__ __forceinline__ PagedOwners pg_owners(const PagedArgs& a, int x) {
-  PagedOwners o;
-  o.rb = x % a.blocks;
-  x /= a.blocks;
-  o.b = x / a.Hkv;
-  o.hkv = x % a.Hkv;
-  o.c0 = o.c1 = 0;
-  const PagedSeq s = pg_seq(a, o.b);
-  o.n = s.n;
-  if (o.rb >= pg_blocks<ROWS>(a, s)) return o;
-  int total, x0, pre;
-  pg_totals<ROWS, STEP>(a, o.b, total, x0);
-  const int head = pg_head_places<ROWS, STEP>(a, s, o.rb, pre);
-  x0 += o.hkv * head + pre + a.lead;  // the block's first step
-  o.c0 = pg_owner(x0, total, a.ctas);
-  o.c1 = pg_owner(x0 + pg_steps<ROWS, STEP>(a, s, o.rb) - 1, total, a.ctas);
-  return o;
+__device__ __forceinline__ void pg_put_plan(const PagedArgs& a, const PagedWalk& w) {
+  const int c = blockIdx.x;
+  PagedPlan p{w.b, w.hkv, w.rb, w.seq.n, 0, -1, 0, 0};
+  if (w.p < w.end && w.s0 > 0 && w.s0 < w.steps) {
+    p.c0 = pg_owner(w.p - w.s0, w.total, a.ctas);
+    if (p.c0 == c - 1) p.c1 = pg_owner(w.p - w.s0 + w.steps - 1, w.total, a.ctas);
+  }
+  if (a.plan && QATTN_IN_BOUNDS(c < a.ctas)) a.plan[c] = p;
+}
+__device__ __forceinline__ PagedPlan pg_get_plan(const PagedArgs& a, int c) {
+  PagedPlan p{0, 0, 0, 0, 0, -1, 0, 0};
+  if (QATTN_IN_BOUNDS(c < a.ctas)) p = a.plan[c];
+  return p;
 }
 
-// The join for few rows a block: NW warps for a row (blockIdx.y: 4 / NW rows), which
+// The join for few rows a block (blockIdx.x: a boundary between shares, as PagedPlan has
+// it): NW warps for a row (blockIdx.y: 4 / NW rows), which
 // take every NW-th share: the weights 2^(m_c - m) of 32 shares come first, one a
 // lane, then the shares' rows in independent loads.
-template <int D, int HEAD, int ROWS, int STEP, int NW>
+template <int D, int HEAD, int ROWS, int NW>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedArgs a) {
   constexpr int CPL = D / 32;                    // channels per lane
   constexpr int RPC = kPgJoinThreads / 32 / NW;  // rows of a CTA
@@ -384,14 +382,12 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
   __shared__ __align__(16) float so[RPC][NW][D];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW, rw = (threadIdx.x >> 5) / NW;
   const int r = blockIdx.y * RPC + rw;
-  // (the attention kernel releases this grid after its own dependency wait, so the
-  // lengths are final and the division is known before the shares arrive)
-  const PagedOwners own = pg_owners<ROWS, STEP>(a, blockIdx.x);
-  const int c0 = own.c0, c1 = own.c1;
-  const bool in = own.rb * ROWS + r < own.n * a.G;
   pdl_wait();
   pdl_trigger();
-  if (c0 == c1) return;
+  const PagedPlan own = pg_get_plan(a, blockIdx.x + 1);
+  const int c0 = own.c0, c1 = own.c1;
+  const bool in = own.rb * ROWS + r < own.n * a.G;
+  if (c1 < 0) return;
   float m = -kPgInf, l = 0.f, o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = 0.f;

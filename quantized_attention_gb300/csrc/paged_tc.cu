@@ -37,13 +37,16 @@ static_assert(kIssueRegs + kConvRegs + 2 * kSoftRegs == 4 * 128, "the split take
 constexpr int kHead = 7;      // of the exponentials' reference (pg_head)
 constexpr float kLazy = 8.f;  // log2 growth of a row's maximum that moves its reference
 static_assert(kHead + kLazy <= 15.f, "P stays inside fp16");
-constexpr uint32_t kTmS = 0, kTmO = 256;  // TMEM columns (tile t: + 128 t, + D t)
 constexpr int kGroups = kStep / 32;       // groups of keys that lie in one page
 constexpr int kWinSteps = 32 / kGroups;   // steps of a warp's window of scales
 
 template <int D>
 struct Cfg {
   static constexpr int kTile = 128 * D * 2;  // fp16 Q, K16 or V16: D / 64 blocks of [128][128 B]
+  // TMEM columns of tile t: S at 128 t, P at kTmP + kTmPStep t, O at kTmO + D t.  d = 64
+  // leaves room for a P of its own: the next QK then follows the moment S has been read.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kTmP = kOwnP ? 256 : 0, kTmPStep = kOwnP ? 64 : 128, kTmO = kOwnP ? 384 : 256;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = 2 * kTile;
   static constexpr int kOffV = kOffK + 2 * kTile;
@@ -67,7 +70,9 @@ enum {
   kDrain = 20,
   kSegFull = 21,   // [2] the planning thread
   kSegEmpty = 23,  // [2] every other thread that works: 1 + 128 + 256
-  kNumBars = 25
+  kSFree = 25,     // [2 tiles] 128 threads have S in registers (kOwnP)
+  kPvDone = 27,    // [2 tiles] a step's PV: P and O are free (kOwnP)
+  kNumBars = 29
 };
 
 // f(constant 0), f(constant 1), ...
@@ -145,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t n = 1;
       if ((i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 4) ||
-          (i >= kQFull && i < kQFull + 2))
+          (i >= kQFull && i < kQFull + 2) || (i >= kSFree && i < kSFree + 2))
         n = 128;
       if (i >= kMerge && i < kMerge + 2) n = 256;
       if (i >= kSegEmpty && i < kSegEmpty + 2) n = 1 + 128 + 256;
@@ -177,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       // ------------------------------------------------------------ segments
       PagedWalk walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
       if (lane == 0) {
+        pg_put_plan(a, walk);
         bool ok = true, some = true;
         for (uint32_t seg = 0; ok && some; ++seg) {
           PagedSeg sg{};
@@ -203,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       constexpr uint32_t tile = C::kTile >> 4;
       bool ok = true;
       uint32_t it = 0;         // steps done
-      uint32_t np[2] = {0, 0}; // PVs of each tile
+      uint32_t np0 = 0, np1 = 0;  // PVs of each tile
       auto qk = [&](int t, uint32_t step) {
-        const uint32_t qd = q0 + t * tile, kd = k0 + (step & 1) * tile, d = tmem + kTmS + 128 * t;
+        const uint32_t qd = q0 + t * tile, kd = k0 + (step & 1) * tile, d = tmem + 128 * t;
         unroll<D / 16>([&](auto k) {
           constexpr int i = decltype(k)::value;
           mma_f16_at<((i / 4) * (128 * 128) + 32 * (i % 4)) / 16, high, idesc_qk>(d, qd, kd, i > 0 ? 1u : 0u);
@@ -235,36 +241,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         const int ahead = dual ? 2 : 1;  // to a tile's next step
         for (int j = 0; ok && j < n; ++j, ++it) {
           const uint32_t st = it & 1;
-          if (!(ok = poll(kVFull + st, it >> 1))) break;
-          const uint32_t vd = v0 + st * tile;
           const int t0 = dual ? (j & 1) : 0, t1 = dual ? t0 + 1 : 2;
-          for (int t = t0; t < t1; ++t) {
-            const uint32_t o = tmem + kTmO + D * t, p = tmem + kTmS + 128 * t, more = j >= ahead ? 1u : 0u;
-            if (!(ok = poll(kPFull + 2 * t, np[t]))) break;  // keys 0 - 63
+          for (int t = t0; ok && t < t1; ++t) {
+            const uint32_t np = t == 0 ? np0 : np1;
+            auto next_qk = [&] {
+              if (j + ahead >= n) return true;
+              const uint32_t step = it + ahead;
+              if (t == t0 && !poll(kKFull + (step & 1), step >> 1)) return false;
+              if (C::kOwnP && !poll(kSFree + t, np)) return false;
+              tc_fence_after();
+              qk(t, step);
+              if (t == t1 - 1) mma_commit(bar(kKEmpty + (step & 1)));
+              return true;
+            };
+            if (C::kOwnP && !(ok = next_qk())) break;
+            if (t == t0 && !(ok = poll(kVFull + st, it >> 1))) break;
+            const uint32_t vd = v0 + st * tile;
+            const uint32_t o = tmem + C::kTmO + D * t, p = tmem + C::kTmP + C::kTmPStep * t, more = j >= ahead ? 1u : 0u;
+            if (!(ok = poll(kPFull + 2 * t, np))) break;  // keys 0 - 63
             tc_fence_after();
             unroll<4>([&](auto k) {
               constexpr int i = decltype(k)::value;
               mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
             });
-            if (!(ok = poll(kPFull + 2 * t + 1, np[t]))) break;  // keys 64 - 127
+            if (!(ok = poll(kPFull + 2 * t + 1, np))) break;  // keys 64 - 127
             tc_fence_after();
             unroll<4>([&](auto k) {
               constexpr int i = 4 + decltype(k)::value;
               mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, 1u);
             });
-            ++np[t];
+            if (t == 0) ++np0;
+            else ++np1;
+            if (C::kOwnP) mma_commit(bar(kPvDone + t));
             if (t == t1 - 1) mma_commit(bar(kVEmpty + st));
-            if (j + ahead < n) {
-              const uint32_t step = it + ahead;
-              if (t == t0) {
-                if (!(ok = poll(kKFull + (step & 1), step >> 1))) break;
-                tc_fence_after();
-              }
-              qk(t, step);
-              if (t == t1 - 1) mma_commit(bar(kKEmpty + (step & 1)));
-            } else {
-              mma_commit(bar(kOFull + t));
-            }
+            if (j + ahead >= n) mma_commit(bar(kOFull + t));
+            if (!C::kOwnP) ok = next_qk();
           }
         }
         if (!ok) break;
@@ -374,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
     const int t = (warp - 8) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;  // TMEM lane, row of the tile
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kTmS + 128 * t, tO = tmem + lane_base + kTmO + D * t;
+    const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + C::kTmO + D * t;
+    const uint32_t tP = tmem + lane_base + C::kTmP + C::kTmPStep * t;
     float* ml = reinterpret_cast<float*>(smem + C::kOffML);  // [tile][m, l][128]
     uint32_t ns = 0, merges = 0;  // this tile's steps, dual segments
     bool ok = true;
@@ -408,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       };
       int p1 = page_of(0), p2 = page_of(1);
       float ks1, vs1;
-      scales_of(p1, ks1, vs1);
       // ---- Q's row -> fp16 in shared memory
       float rf;
       bool fin;
@@ -427,6 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         for (int k = 0; k < D / 8; ++k) {
           x[k] = make_uint4(0u, 0u, 0u, 0u);
           if (in && QATTN_IN_BOUNDS(sg.b < a.B && hq < a.Hq && tok < a.T)) x[k] = *reinterpret_cast<const uint4*>(src + 8 * k);
+        }
+        scales_of(p1, ks1, vs1);  // (behind Q's loads)
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
@@ -496,6 +511,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
           break;
         }
         tc_fence_after();
+        bool pv_over = false;  // the tile's PV before this step is done (else S comes after it)
+        auto pv_done = [&] {
+          if (!C::kOwnP || pv_over || j == first) return true;
+          pv_over = true;
+          if (!__all_sync(0xffffffffu, poll(kPvDone + t, ns - 1))) return false;
+          tc_fence_after();
+          return true;
+        };
         for (;;) {
           uint32_t v[kGroups][32];
           float mx[kGroups];
@@ -509,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
             for (int g = 0; g < kGroups; ++g) {
               const uint32_t vis = pg_first_bits(((hidden >> (q0 + g)) & 1u) ? 0 : room - 32 * g);
               if (vis != 0u && ((bad >> (q0 + g)) & 1u)) fin = false;
+              if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
               mx[g] = -kPgInf;
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
@@ -540,7 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
             const float al = !moved ? 1.f : m == -kPgInf ? 0.f : ex2_approx(m - mn);
             l *= al;
             m = mn;
-            if (j > first && __any_sync(0xffffffffu, moved)) {  // (O is done: S came after it)
+            if (j > first && __any_sync(0xffffffffu, moved)) {
+              ok = pv_done();
+              if (!ok) break;
 #pragma unroll 1
               for (int k = 0; k < D / 32; ++k) {
                 uint32_t x[32];
@@ -551,9 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
                 tmem_st32(tO + 32 * k, x);
               }
               tmem_wait_st();
+              mode = 2;
+              continue;  // (the scores made room for O)
             }
-            mode = 2;
-            continue;
           }
           const float ref = m == -kPgInf ? 0.f : m;
           float add = 0.f;
@@ -589,20 +615,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
               continue;
             }
           }
+          if (C::kOwnP) {  // S may be overwritten
+            tc_fence_before();
+            mbar_arrive(bar(kSFree + t));
+          }
           weigh(1);
-          tmem_st32(tS, pk[0]);  // P in place of S (its columns are in registers)
+          ok = pv_done();
+          if (!ok) break;
+          tmem_st32(tP, pk[0]);
           weigh(2);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(kPFull + 2 * t));
           weigh(3);
-          tmem_st32(tS + 32, pk[1]);
+          tmem_st32(tP + 32, pk[1]);
           l += add;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(kPFull + 2 * t + 1));
           break;
         }
+        if (!ok) break;
         if (j + pace < n) scales(j + pace);
       }
       if (!ok) break;
@@ -638,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (sg.s0 > 0 ? 0 : 1);
       const size_t row = (static_cast<size_t>(sg.b) * a.Hq + hq) * a.T + tok;
       const float rl = l == 0.f ? 0.f : 1.f / l;
-      const uint32_t tOther = tmem + lane_base + kTmO + D * (1 - t);
+      const uint32_t tOther = tmem + lane_base + C::kTmO + D * (1 - t);
 #pragma unroll 1
       for (int k = dual ? t * (D / 64) : 0; k < (dual ? (t + 1) * (D / 64) : D / 32); ++k) {
         uint32_t x[32];
@@ -691,23 +724,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
 }
 
 // The join: CTAs (c, y) work for the boundary between the shares of CTAs c and c + 1, if
-// it is the first one inside a block.  A lane for a row, a warp for four channels of it
+// it is the first one inside a block (PagedPlan).  A lane for a row, a warp for four channels of it
 // (blockIdx.y: 32 rows, then 16 channels), so that every load of a share takes 512
 // consecutive bytes; eight shares' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_rows_kernel(const PagedArgs a) {
   constexpr int U = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PagedWalk w = pg_walk<kRows, kStep>(a, blockIdx.x + 1, a.ctas);
   const int r = 32 * (blockIdx.y % (kRows / 32)) + lane;
   const int c = 4 * (4 * (blockIdx.y / (kRows / 32)) + warp);
-  const bool inside = w.p < w.end && w.s0 > 0 && w.s0 < w.steps;
-  const int c0 = inside ? pg_owner(w.p - w.s0, w.total, a.ctas) : 0;
-  const int c1 = inside ? pg_owner(w.p - w.s0 + w.steps - 1, w.total, a.ctas) : 0;
-  const int rr = w.rb * kRows + r;
   pdl_wait();
   pdl_trigger();
-  if (!inside || c0 != static_cast<int>(blockIdx.x) || rr / a.G >= w.seq.n) return;
+  const PagedPlan w = pg_get_plan(a, blockIdx.x + 1);
+  const int rr = w.rb * kRows + r, c0 = w.c0, c1 = w.c1;
+  if (c1 < 0 || rr / a.G >= w.n) return;
   float m = -kPgInf, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int cb = c0; cb <= c1; cb += U) {
@@ -742,7 +772,7 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_rows_kernel(const P
     }
     m = mn;
   }
-  pg_write_out<D, kHead>(a, w.b, w.hkv, w.seq.n, rr, c, o, m, l);
+  pg_write_out<D, kHead>(a, w.b, w.hkv, w.n, rr, c, o, m, l);
 }
 
 template <int D, bool E4M3>

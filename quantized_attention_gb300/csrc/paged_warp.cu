@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool some = true;  // CL: the block has rows
   if constexpr (CL) some = pg_cluster_seg<kRows, kStep>(a, sg);
   else walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
+  if (!CL && threadIdx.x == 0) pg_put_plan(a, walk);
   __syncthreads();  // the abort flag is set
   uint32_t used = 0;  // tiles this warp has taken through its ring
   uint32_t sent = 0;  // lane 0: those it has issued
@@ -501,11 +502,11 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAr
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_warp_kernel<D, E4M3, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess) return e;
+  if (a.ctas == 1) return e;
   const int blocks = a.B * a.Hkv * a.blocks;
   if (a.ctas < kJoinShares * blocks)  // a block in few shares: a warp for a row
-    return launch_pdl(paged_join_kernel<D, kHead, kRows, kStep, 1>, dim3(blocks, kRows / 4), dim3(kPgJoinThreads), 0,
-                      s, a);
-  return launch_pdl(paged_join_kernel<D, kHead, kRows, kStep, 4>, dim3(blocks, kRows), dim3(kPgJoinThreads), 0, s, a);
+    return launch_pdl(paged_join_kernel<D, kHead, kRows, 1>, dim3(a.ctas - 1, kRows / 4), dim3(kPgJoinThreads), 0, s, a);
+  return launch_pdl(paged_join_kernel<D, kHead, kRows, 4>, dim3(a.ctas - 1, kRows), dim3(kPgJoinThreads), 0, s, a);
 }
 
 }  // namespace

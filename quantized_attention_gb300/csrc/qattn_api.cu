@@ -344,7 +344,7 @@ struct PagedSplit {
   bool tc;
   int cluster, step, rows, blocks, ctas, lead;
   int64_t steps;
-  size_t slots, off_m, off_l, bytes;
+  size_t slots, off_m, off_l, off_plan, bytes;
 };
 PagedSplit paged_split(const qattn_shape* s) {
   PagedSplit t{};
@@ -367,7 +367,8 @@ PagedSplit paged_split(const qattn_shape* s) {
   t.slots = t.cluster > 0 ? 0 : 2 * static_cast<size_t>(t.ctas);
   t.off_m = align256(t.slots * t.rows * static_cast<size_t>(s->d) * 4);
   t.off_l = t.off_m + align256(t.slots * t.rows * 4);
-  t.bytes = t.off_l + align256(t.slots * t.rows * 4);
+  t.off_plan = t.off_l + align256(t.slots * t.rows * 4);
+  t.bytes = t.off_plan + (t.slots > 0 ? align256(static_cast<size_t>(t.ctas) * 32) : 0);
   return t;
 }
 
@@ -1441,6 +1442,7 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   a.part_o = reinterpret_cast<float*>(w);
   a.part_m = reinterpret_cast<float*>(w + sp.off_m);
   a.part_l = reinterpret_cast<float*>(w + sp.off_l);
+  a.plan = sp.slots > 0 ? reinterpret_cast<qattn::PagedPlan*>(w + sp.off_plan) : nullptr;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   char sb[128];
   QATTN_LOG_LINE("qattn_paged_fwd %s page=%d: %s, %d CTAs", shape_str(shape, sb, sizeof sb), 1 << a.page_shift,

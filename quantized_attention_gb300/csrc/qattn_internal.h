@@ -442,6 +442,7 @@ constexpr int kPagedTcRows = 256;             // query rows of its block
 constexpr int kPagedTcStep = 128;
 constexpr int kPagedTcCtas = 152;             // one an SM
 constexpr int kPagedTcLead = 4;
+struct PagedPlan;
 struct PagedArgs {
   int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
   int n_pages, page_shift, max_pages, e4m3;
@@ -462,6 +463,7 @@ struct PagedArgs {
   int cluster, ctas, lead;
   size_t slots, rows_total;
   float *part_o, *part_m, *part_l;
+  PagedPlan* plan;         // [ctas]
 };
 // tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x (keys of a step) x 1
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
