@@ -10,9 +10,10 @@
 // codes as often: doublings keep what an old row loses below one step in all,
 // however often the page's scale grows.
 //
-// Work item: eight channels of a row.  In the half layout those are channels
-// 4 i .. 4 i + 3 and their partners rot / 2 further, else eight neighbours, so
-// that an item needs four cosines and four sines either way.
+// Work item: W channels of a row (8, or 16 where the rotated and the other channels are
+// multiples of it).  In the half layout those are W / 2 channels and their partners
+// rot / 2 further, else W neighbours, so that an item needs W / 2 cosines and as many
+// sines either way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,93 +25,141 @@ namespace qattn {
 namespace {
 
 // ------------------------------------------------------------------ items
-struct Item8 {
-  float v[8];
+template <int W>
+struct Place {  // first channels of an item's halves
+  int c0, c1;
+  bool turned;
 };
-
-// First channels of an item's two quads: `i` of the row's d / 8 items.
-__device__ __forceinline__ void item_channels(int i, int rot, bool inter, int& c0, int& c1, bool& turned) {
-  turned = 8 * i < rot;
-  const bool split = turned && !inter;
-  c0 = split ? 4 * i : 8 * i;
-  c1 = split ? rot / 2 + 4 * i : 8 * i + 4;
+template <int W>
+__device__ __forceinline__ Place<W> item_place(int i, int rot, bool inter) {
+  Place<W> p;
+  p.turned = W * i < rot;
+  const bool split = p.turned && !inter;
+  p.c0 = split ? (W / 2) * i : W * i;
+  p.c1 = split ? rot / 2 + (W / 2) * i : W * i + W / 2;
+  return p;
 }
-__device__ __forceinline__ Item8 load_item(const uint16_t* row, int c0, int c1) {
-  Item8 x;
-  uint2 a, b;
-  if (c1 == c0 + 4) {
-    const uint4 w = *reinterpret_cast<const uint4*>(row + c0);
-    a = make_uint2(w.x, w.y);
-    b = make_uint2(w.z, w.w);
+template <int W>
+struct Item {
+  float v[W];
+};
+template <int W>
+struct Raw {  // an item as it lies: bf16 pairs
+  uint32_t w[W / 2];
+};
+template <int W>
+__device__ __forceinline__ Raw<W> load_raw(const uint16_t* row, const Place<W>& p) {
+  Raw<W> x;
+  if constexpr (W == 8) {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + p.c0), b = *reinterpret_cast<const uint2*>(row + p.c1);
+    x.w[0] = a.x;
+    x.w[1] = a.y;
+    x.w[2] = b.x;
+    x.w[3] = b.y;
   } else {
-    a = *reinterpret_cast<const uint2*>(row + c0);
-    b = *reinterpret_cast<const uint2*>(row + c1);
-  }
-  const uint32_t w[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x.v[2 * k] = bf16_bits_to_f32(w[k] & 0xffffu);
-    x.v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    const uint4 a = *reinterpret_cast<const uint4*>(row + p.c0), b = *reinterpret_cast<const uint4*>(row + p.c1);
+    x.w[0] = a.x;
+    x.w[1] = a.y;
+    x.w[2] = a.z;
+    x.w[3] = a.w;
+    x.w[4] = b.x;
+    x.w[5] = b.y;
+    x.w[6] = b.z;
+    x.w[7] = b.w;
   }
   return x;
 }
-__device__ __forceinline__ Item8 load_item(const float* row, int c0, int c1) {
-  const float4 a = *reinterpret_cast<const float4*>(row + c0), b = *reinterpret_cast<const float4*>(row + c1);
-  return Item8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+template <int W>
+__device__ __forceinline__ Item<W> values(const Raw<W>& r) {
+  Item<W> x;
+#pragma unroll
+  for (int k = 0; k < W / 2; ++k) {
+    x.v[2 * k] = bf16_bits_to_f32(r.w[k] & 0xffffu);
+    x.v[2 * k + 1] = __uint_as_float(r.w[k] & 0xffff0000u);
+  }
+  return x;
+}
+__device__ __forceinline__ Item<8> load_item(const float* row, const Place<8>& p) {
+  const float4 a = *reinterpret_cast<const float4*>(row + p.c0), b = *reinterpret_cast<const float4*>(row + p.c1);
+  return Item<8>{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+template <int W>
+__device__ __forceinline__ Item<W> load_item(const uint16_t* row, const Place<W>& p) {
+  return values<W>(load_raw<W>(row, p));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store_item(uint16_t* row, int c0, int c1, const Item8& x) {
-  const uint2 a = make_uint2(pack_bf16(x.v[0], x.v[1]), pack_bf16(x.v[2], x.v[3]));
-  const uint2 b = make_uint2(pack_bf16(x.v[4], x.v[5]), pack_bf16(x.v[6], x.v[7]));
-  if (c1 == c0 + 4) {
-    *reinterpret_cast<uint4*>(row + c0) = make_uint4(a.x, a.y, b.x, b.y);
+template <int W>
+__device__ __forceinline__ void store_item(uint16_t* row, const Place<W>& p, const Item<W>& x) {
+  uint32_t w[W / 2];
+#pragma unroll
+  for (int k = 0; k < W / 2; ++k) w[k] = pack_bf16(x.v[2 * k], x.v[2 * k + 1]);
+  if constexpr (W == 8) {
+    *reinterpret_cast<uint2*>(row + p.c0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + p.c1) = make_uint2(w[2], w[3]);
   } else {
-    *reinterpret_cast<uint2*>(row + c0) = a;
-    *reinterpret_cast<uint2*>(row + c1) = b;
+    *reinterpret_cast<uint4*>(row + p.c0) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(row + p.c1) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
-__device__ __forceinline__ void store_item(float* row, int c0, int c1, const Item8& x) {
-  *reinterpret_cast<float4*>(row + c0) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
-  *reinterpret_cast<float4*>(row + c1) = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+__device__ __forceinline__ void store_item(float* row, const Place<8>& p, const Item<8>& x) {
+  *reinterpret_cast<float4*>(row + p.c0) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+  *reinterpret_cast<float4*>(row + p.c1) = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
 }
 
-// Four cosines and sines of item i of a position's row of the table.
-__device__ __forceinline__ void load_angles(const RopeArgs& r, int pos, int i, float4& c, float4& s) {
-  const float* row = r.table + static_cast<size_t>(pos) * r.rot + 4 * i;
-  c = __ldg(reinterpret_cast<const float4*>(row));
-  s = __ldg(reinterpret_cast<const float4*>(row + r.rot / 2));
-  if (r.inverse) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-}
-__device__ __forceinline__ void turn(Item8& x, float4 c4, float4 s4, bool inter) {
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-  Item8 y;
+template <int W>
+struct Angles {
+  float c[W / 2], s[W / 2];
+};
+// Cosines and sines of item i of a position's row of the table.
+template <int W>
+__device__ __forceinline__ Angles<W> load_angles(const RopeArgs& r, int pos, int i) {
+  Angles<W> a;
+  const float* row = r.table + static_cast<size_t>(pos) * r.rot + (W / 2) * i;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float a = inter ? x.v[2 * k] : x.v[k], b = inter ? x.v[2 * k + 1] : x.v[4 + k];
-    const float u = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
-    const float w = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
+  for (int k = 0; k < W / 2; k += 4) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(row + k));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(row + r.rot / 2 + k));
+    a.c[k] = c.x;
+    a.c[k + 1] = c.y;
+    a.c[k + 2] = c.z;
+    a.c[k + 3] = c.w;
+    a.s[k] = r.inverse ? -s.x : s.x;
+    a.s[k + 1] = r.inverse ? -s.y : s.y;
+    a.s[k + 2] = r.inverse ? -s.z : s.z;
+    a.s[k + 3] = r.inverse ? -s.w : s.w;
+  }
+  return a;
+}
+template <int W>
+__device__ __forceinline__ Item<W> turn(const Item<W>& x, const Angles<W>& a, bool inter) {
+  Item<W> y;
+#pragma unroll
+  for (int k = 0; k < W / 2; ++k) {
+    const float p = inter ? x.v[2 * k] : x.v[k], q = inter ? x.v[2 * k + 1] : x.v[W / 2 + k];
+    const float u = __fsub_rn(__fmul_rn(p, a.c[k]), __fmul_rn(q, a.s[k]));
+    const float w = __fadd_rn(__fmul_rn(q, a.c[k]), __fmul_rn(p, a.s[k]));
     if (inter) {
       y.v[2 * k] = u;
       y.v[2 * k + 1] = w;
     } else {
       y.v[k] = u;
-      y.v[4 + k] = w;
+      y.v[W / 2 + k] = w;
     }
   }
-  x = y;
+  return y;
 }
 
 // ------------------------------------------------------------------ rotate
 constexpr int kRotateThreads = 256;
-constexpr int kRotateHeads = 8;  // heads a thread turns by the same angles
 
-template <typename T>
+// A thread turns one item of a token in `heads` heads by the same angles.
+template <typename T, int W>
 __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateArgs a) {
-  const int items = a.d / 8;
-  const int i = threadIdx.x % items, per = kRotateThreads / items;
+  const int items = a.d / W, per = kRotateThreads / items;
+  const int i = threadIdx.x % items;
   const long long tok = static_cast<long long>(blockIdx.x) * per + threadIdx.x / items;
   const int h0 = blockIdx.y * a.heads, h1 = min(a.H, h0 + a.heads);
   pdl_trigger();
@@ -122,28 +171,21 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateArgs
     if (i == 0 && h0 == 0) atomicOr(a.err, kErrDomain);
     return;
   }
-  int c0, c1;
-  bool turned;
-  item_channels(i, a.rope.rot, a.rope.inter, c0, c1, turned);
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (turned) load_angles(a.rope, pos, i, c, s);
+  const Place<W> p = item_place<W>(i, a.rope.rot, a.rope.inter);
+  Angles<W> ang{};
+  if (p.turned) ang = load_angles<W>(a.rope, pos, i);
   const T* X = static_cast<const T*>(a.x) + b * a.xsB + t * a.xsN;
   T* Y = static_cast<T*>(a.y) + (static_cast<size_t>(b) * a.H * a.T + t) * a.d;
 #pragma unroll 4
   for (int h = h0; h < h1; ++h) {
-    if (!QATTN_IN_BOUNDS(b < a.B && h < a.H && c1 + 4 <= a.d)) continue;
-    Item8 x = load_item(X + h * a.xsH, c0, c1);
-    if (turned) turn(x, c, s, a.rope.inter);
-    store_item(Y + static_cast<size_t>(h) * a.T * a.d, c0, c1, x);
+    if (!QATTN_IN_BOUNDS(b < a.B && h < a.H && p.c1 + W / 2 <= a.d)) continue;
+    Item<W> x = load_item(X + h * a.xsH, p);
+    if (p.turned) x = turn(x, ang, a.rope.inter);
+    store_item(Y + static_cast<size_t>(h) * a.T * a.d, p, x);
   }
 }
 
 // ------------------------------------------------------------------ append
-// A CTA takes one page of one sequence and some heads of one kind (K, V or Q): its
-// threads hold the page's new rows in registers (NIT items each), reduce the largest
-// magnitude, settle the scale and write the codes.
-constexpr int kItems = 8;  // rows' items a thread holds
-
 template <bool E4M3>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   if constexpr (E4M3) {
@@ -174,139 +216,138 @@ __device__ __forceinline__ uint32_t divide4(uint32_t w, float mul) {
   return encode4<E4M3>(__fmul_rn(x[0], mul), __fmul_rn(x[1], mul), __fmul_rn(x[2], mul), __fmul_rn(x[3], mul));
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppendArgs a) {
-  constexpr float kTop = E4M3 ? 448.f : 127.f;
-  __shared__ uint32_t red[2][8];
-  const int b = blockIdx.z;
-  // heads of this CTA: K's groups, then V's, then Q's
-  int kind = 0, grp = blockIdx.x;
-  const int gkv = (a.Hkv + a.heads - 1) / a.heads;
-  while (kind < 2 && grp >= gkv) {
-    grp -= gkv;
-    ++kind;
+// The new rows of a sequence, checked.
+struct NewRows {
+  int first, len, n;  // the row of token 0, rows in use, new ones (0: nothing to do)
+};
+__device__ __forceinline__ NewRows new_rows(const PagedAppendArgs& a, int b, bool report) {
+  NewRows s{0, a.lengths[b], a.n_new ? a.n_new[b] : a.T};
+  if (s.n < 0 || s.n > a.T || s.len > a.Nk || s.len < s.n) {  // the sequence is left as it is
+    if (report) atomicOr(a.err, kErrDomain);
+    s.n = 0;
   }
-  const int H = kind == 2 ? a.Hq : a.Hkv;
-  const int h0 = grp * a.heads, h1 = min(H, h0 + a.heads);
-  const int items = a.d / 8, per = blockDim.x / items;
-  const int i = threadIdx.x % items, rw = threadIdx.x / items;
-  pdl_trigger();
-  pdl_wait();
-  const int len = a.lengths[b], n = a.n_new ? a.n_new[b] : a.T;
-  if (n < 0 || n > a.T || len > a.Nk || len < n) {  // the sequence is left as it is
-    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.err, kErrDomain);
-    return;
-  }
-  const int first = len - n;  // the row of token 0
-  const int j = (first >> a.page_shift) + blockIdx.y, row0 = j << a.page_shift;
-  if (n == 0 || row0 >= len) return;
-  const bool held = row0 < first;  // rows of the page that were there before
-  int page = -1;
-  if (kind < 2 && QATTN_IN_BOUNDS(j < a.max_pages)) {
-    page = a.page_table[static_cast<size_t>(b) * a.max_pages + j];
-    if (page < 0 || page >= a.n_pages) {  // no such page: its rows are not written
-      if (threadIdx.x == 0) atomicOr(a.err, kErrDomain);
-      return;
+  s.first = s.len - s.n;
+  return s;
+}
+__device__ __forceinline__ int position(const PagedAppendArgs& a, int b, int first, int t) {
+  return a.positions ? a.positions[static_cast<size_t>(b) * a.T + t] : first + t;
+}
+
+// Whose threads hold a page's new rows: a warp or a CTA.
+template <bool CTA>
+struct Team {
+  uint32_t (*red)[32];  // [2][warps] (CTA)
+  __device__ __forceinline__ int size() const { return CTA ? blockDim.x : 32; }
+  __device__ __forceinline__ int rank() const { return CTA ? threadIdx.x : threadIdx.x & 31; }
+  // The largest x of the team; between what its threads did before and do after it.
+  __device__ __forceinline__ uint32_t largest(uint32_t x, int turn) const {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if constexpr (CTA) {
+      if ((threadIdx.x & 31) == 0) red[turn & 1][threadIdx.x >> 5] = x;
+      __syncthreads();
+      x = 0;
+      for (unsigned w = 0; w < blockDim.x / 32; ++w) x = max(x, red[turn & 1][w]);
     }
+    return x;
   }
-  const bool rotated = kind != 1 && a.rope.table != nullptr;
-  int c0, c1;
-  bool turned;
-  item_channels(i, rotated ? a.rope.rot : 0, a.rope.inter, c0, c1, turned);
-  const uint16_t* X = kind == 0 ? a.k : kind == 1 ? a.v : a.q;
-  const long long sB = kind == 0 ? a.ksB : kind == 1 ? a.vsB : a.qsB;
-  const long long sH = kind == 0 ? a.ksH : kind == 1 ? a.vsH : a.qsH;
-  const long long sN = kind == 0 ? a.ksN : kind == 1 ? a.vsN : a.qsN;
-  X += b * sB;
-  uint8_t* pages = kind == 0 ? a.k_pages : a.v_pages;
-  float* scales = kind == 0 ? a.k_scales : a.v_scales;
-  // this thread's rows of the page: rw + per k, their tokens' positions
-  auto token = [&](int k) { return row0 + rw + per * k - first; };
-  auto live = [&](int k) {
-    const int r = rw + per * k, t = token(k);
-    return r < (1 << a.page_shift) && t >= 0 && t < n;
-  };
-  auto position = [&](int t) {
-    return a.positions ? a.positions[static_cast<size_t>(b) * a.T + t] : first + t;
-  };
+};
+
+// One page of a sequence and heads h0 .. h1 - 1 of K or V, by a team: the new rows of a
+// head (NP items a thread, rows rw + per k) are held as they came, the next head's loads
+// on their way; their largest magnitude settles the scale; the codes follow.  K's rows
+// are turned twice, for the maximum and for the codes: angles come from L1 and the
+// registers stay few.
+template <bool E4M3, int NP, bool CTA>
+__device__ __forceinline__ void append_page(const PagedAppendArgs& a, const Team<CTA> team, int b, const NewRows& s,
+                                            int j, bool is_v, int h0, int h1) {
+  constexpr float kTop = E4M3 ? 448.f : 127.f;
+  const int row0 = j << a.page_shift;
+  const bool held = row0 < s.first;  // rows of the page that were there before
+  if (!QATTN_IN_BOUNDS(j < a.max_pages)) return;
+  const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + j];
+  const int items = a.d / 8, per = team.size() / items;
+  const int i = team.rank() % items, rw = team.rank() / items;
+  const bool rotated = !is_v && a.rope.table != nullptr;
+  const Place<8> pl = item_place<8>(i, rotated ? a.rope.rot : 0, a.rope.inter);
+  const uint16_t* X = (is_v ? a.v + b * a.vsB : a.k + b * a.ksB);
+  const long long sH = is_v ? a.vsH : a.ksH, sN = is_v ? a.vsN : a.ksN;
+  // rows of the page in turn from the first new one: `shift` + rw + per k
+  const int shift = held ? s.first - row0 : 0, t0 = row0 + shift - s.first;  // its token
+  const int rows = min(min(1 << a.page_shift, s.len - row0) - shift, s.n - t0);
   uint32_t ok = 0;  // bit k: row k is written
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    if (!live(k)) continue;
+  for (int k = 0; k < NP; ++k) {
+    if (rw + per * k >= rows) continue;
     if (rotated) {
-      const int p = position(token(k));
-      if (p < 0 || p >= a.rope.n) {  // outside the table: the token is not written
+      const int pos = position(a, b, s.first, t0 + rw + per * k);
+      if (pos < 0 || pos >= a.rope.n) {  // outside the table: the token is not written
         if (i == 0) atomicOr(a.err, kErrDomain);
         continue;
       }
     }
     ok |= 1u << k;
   }
+  if (page < 0 || page >= a.n_pages) {  // no such page: its rows are not written
+    if (team.rank() == 0) atomicOr(a.err, kErrDomain);
+    return;
+  }
+  uint8_t* const pages = is_v ? a.v_pages : a.k_pages;
+  float* const scales = is_v ? a.v_scales : a.k_scales;
+  Raw<8> x[NP], y[NP];
+  auto fetch = [&](Raw<8> (&z)[NP], int h) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      z[k] = Raw<8>{};
+      if (((ok >> k) & 1u) && QATTN_IN_BOUNDS(t0 + rw + per * k < a.T && h < a.Hkv))
+        z[k] = load_raw<8>(X + h * sH + (t0 + rw + per * k) * sN, pl);
+    }
+  };
+  auto value = [&](int k) {
+    Item<8> v = values<8>(x[k]);
+    if (pl.turned) v = turn(v, load_angles<8>(a.rope, position(a, b, s.first, t0 + rw + per * k), i), a.rope.inter);
+    return v;
+  };
+  fetch(x, h0);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
-    Item8 x[kItems];
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      if (!((ok >> k) & 1u) || !QATTN_IN_BOUNDS(token(k) < a.T && h < H)) continue;
-      x[k] = load_item(X + h * sH + token(k) * sN, c0, c1);
-    }
-    if (turned) {
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if (!((ok >> k) & 1u)) continue;
-        float4 c, s;
-        load_angles(a.rope, position(token(k)), i, c, s);
-        turn(x[k], c, s, a.rope.inter);
-      }
-    }
-    if (kind == 2) {
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        if (!((ok >> k) & 1u)) continue;
-        const size_t row = (static_cast<size_t>(b) * a.Hq + h) * a.T + token(k);
-        store_item(a.q_out + row * a.d, c0, c1, x[k]);
-      }
-      continue;
-    }
+    const size_t sc = static_cast<size_t>(page) * a.Hkv + h;
+    const float was = held ? scales[sc] : 0.f;
+    if (h + 1 < h1) fetch(y, h + 1);
     // the largest magnitude, as bits: NaN lies above infinity, infinity above every number
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < NP; ++k) {
       if (!((ok >> k) & 1u)) continue;
+      const Item<8> v = value(k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[k].v[e]) & 0x7fffffffu);
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v.v[e]) & 0x7fffffffu);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) red[h & 1][threadIdx.x >> 5] = top;
-    const size_t sc = static_cast<size_t>(page) * a.Hkv + h;
-    const float was = held ? scales[sc] : 0.f;
-    __syncthreads();  // also: every thread has the old scale
-    top = 0;
-    for (unsigned w = 0; w < blockDim.x / 32; ++w) top = max(top, red[h & 1][w]);
+    top = team.largest(top, h);  // (every thread has the old scale)
     const float amax = __uint_as_float(top);
     // the page's scale, and the doublings of the old one
-    float s;
+    float sc_new;
     int up = 0;
     const bool finite = top < 0x7f800000u;
     if (!finite || !(was >= 0.f && was < __builtin_huge_valf())) {
-      s = __uint_as_float(0x7fffffffu);
+      sc_new = __uint_as_float(0x7fffffffu);
     } else if (was >= 0x1p-100f) {
       const float fit = __fmul_rn(was, kTop);
       if (amax > fit) {
         const uint32_t f = __float_as_uint(fit);
         up = static_cast<int>(top >> 23) - static_cast<int>(f >> 23) + ((top & 0x7fffffu) > (f & 0x7fffffu) ? 1 : 0);
       }
-      s = ldexpf(was, up);
+      sc_new = ldexpf(was, up);
     } else {
-      s = amax < 0x1p-64f ? 0.f : __fmul_rn(amax, 1.f / kTop);
-      up = held && s > 0.f ? 127 : 0;  // rows held with no scale are zeros, and stay so
+      sc_new = amax < 0x1p-64f ? 0.f : __fmul_rn(amax, 1.f / kTop);
+      up = held && sc_new > 0.f ? 127 : 0;  // rows held with no scale are zeros, and stay so
     }
-    if (threadIdx.x == 0 && QATTN_IN_BOUNDS(page >= 0 && page < a.n_pages)) scales[sc] = s;
+    if (team.rank() == 0 && rows > 0 && QATTN_IN_BOUNDS(page >= 0 && page < a.n_pages)) scales[sc] = sc_new;
     uint8_t* P = pages + (sc << a.page_shift) * a.d;
     if (up > 0) {  // the rows that were there: their codes halved as often
       const float mul = up > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-      const int words = (first - row0) * a.d / 16;
-      for (int w = threadIdx.x; w < words; w += blockDim.x) {
+      const int words = shift * a.d / 16;
+#pragma unroll 4
+      for (int w = team.rank(); w < words; w += team.size()) {
         if (!QATTN_IN_BOUNDS(16 * w < (a.d << a.page_shift))) continue;
         uint4 v = *reinterpret_cast<const uint4*>(P + 16 * w);
         v = make_uint4(divide4<E4M3>(v.x, mul), divide4<E4M3>(v.y, mul), divide4<E4M3>(v.z, mul),
@@ -314,23 +355,105 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppendArgs
         *reinterpret_cast<uint4*>(P + 16 * w) = v;
       }
     }
-    const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;  // (0 for NaN: codes of zero)
+    const float inv = finite && sc_new > 0.f ? __fdiv_rn(1.f, sc_new) : 0.f;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
+    for (int k = 0; k < NP; ++k) {
       if (!((ok >> k) & 1u)) continue;
-      float y[8];
+      const Item<8> v = value(k);
+      float q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = finite && inv > 0.f ? __fmul_rn(x[k].v[e], inv) : 0.f;
-      const uint32_t lo = encode4<E4M3>(y[0], y[1], y[2], y[3]), hi = encode4<E4M3>(y[4], y[5], y[6], y[7]);
-      uint8_t* row = P + (rw + per * k) * a.d;
-      if (c1 == c0 + 4) {
-        *reinterpret_cast<uint2*>(row + c0) = make_uint2(lo, hi);
-      } else {
-        *reinterpret_cast<uint32_t*>(row + c0) = lo;
-        *reinterpret_cast<uint32_t*>(row + c1) = hi;
-      }
+      for (int e = 0; e < 8; ++e) q[e] = inv > 0.f ? __fmul_rn(v.v[e], inv) : 0.f;  // (codes of zero beside NaN)
+      uint8_t* row = P + (shift + rw + per * k) * a.d;
+      *reinterpret_cast<uint32_t*>(row + pl.c0) = encode4<E4M3>(q[0], q[1], q[2], q[3]);
+      *reinterpret_cast<uint32_t*>(row + pl.c1) = encode4<E4M3>(q[4], q[5], q[6], q[7]);
     }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) x[k] = y[k];
   }
+}
+
+// Q rotated: item i of token t in heads h0 .. h1 - 1.
+template <int W>
+__device__ __forceinline__ void append_q(const PagedAppendArgs& a, int b, const NewRows& s, int t, int i, int h0, int h1) {
+  if (t >= s.n) return;
+  const bool rotated = a.rope.table != nullptr;
+  const Place<W> p = item_place<W>(i, rotated ? a.rope.rot : 0, a.rope.inter);
+  Angles<W> ang{};
+  if (rotated) {
+    const int pos = position(a, b, s.first, t);
+    if (pos < 0 || pos >= a.rope.n) {
+      if (i == 0) atomicOr(a.err, kErrDomain);
+      return;
+    }
+    if (p.turned) ang = load_angles<W>(a.rope, pos, i);
+  }
+  const uint16_t* X = a.q + b * a.qsB + t * a.qsN;
+  uint16_t* Y = a.q_out + (static_cast<size_t>(b) * a.Hq * a.T + t) * a.d;
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    if (!QATTN_IN_BOUNDS(b < a.B && t < a.T && h < a.Hq)) continue;
+    Item<W> x = load_item<W>(X + h * a.qsH, p);
+    if (p.turned) x = turn(x, ang, a.rope.inter);
+    store_item(Y + static_cast<size_t>(h) * a.T * a.d, p, x);
+  }
+}
+
+// Many tokens: a CTA a page (x: kind and head group, y: page, z: sequence); then, behind
+// a.kv_groups, CTAs that rotate Q, 256 items (tokens x channels) and a head group each.
+constexpr int kPageThreads = 256;
+template <bool E4M3, int NP, int WQ>
+__global__ void __launch_bounds__(kPageThreads, NP == 8 ? 2 : 3) paged_append_kernel(const PagedAppendArgs a) {
+  __shared__ uint32_t red[2][32];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.z;
+  const NewRows s = new_rows(a, b, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
+  if (s.n == 0) return;
+  int g = blockIdx.x;
+  if (g < 2 * a.kv_groups) {
+    const bool is_v = g >= a.kv_groups;
+    if (is_v) g -= a.kv_groups;
+    const int j = (s.first >> a.page_shift) + blockIdx.y;
+    if ((j << a.page_shift) >= s.len) return;
+    append_page<E4M3, NP, true>(a, Team<true>{red}, b, s, j, is_v, g * a.heads, min(a.Hkv, (g + 1) * a.heads));
+    return;
+  }
+  g -= 2 * a.kv_groups;
+  const int items = a.d / WQ, per = kPageThreads / items;
+  // a page's tokens in as many rounds as it takes
+  const int t0 = blockIdx.y << a.page_shift, t1 = min(s.n, t0 + (1 << a.page_shift));
+  for (int t = t0 + threadIdx.x / items; t < t1; t += per)
+    append_q<WQ>(a, b, s, t, threadIdx.x % items, g * a.q_heads, min(a.Hq, (g + 1) * a.q_heads));
+}
+
+// A few tokens: a warp a page and head of K or V; then warps that rotate Q, a token and a
+// head group each.  x: units of a sequence, 8 a CTA; y: sequence.
+constexpr int kFewWarps = 8;
+template <bool E4M3, int NP>
+__global__ void __launch_bounds__(32 * kFewWarps) paged_append_few_kernel(const PagedAppendArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y;
+  int u = blockIdx.x * kFewWarps + (threadIdx.x >> 5);
+  const NewRows s = new_rows(a, b, (threadIdx.x & 31) == 0 && u == 0);
+  if (s.n == 0) return;
+  const int kv = 2 * a.Hkv * a.touched;
+  if (u < kv) {
+    const int h = u % a.Hkv;
+    u /= a.Hkv;
+    const int j = (s.first >> a.page_shift) + (u >> 1);
+    if ((j << a.page_shift) >= s.len) return;
+    append_page<E4M3, NP, false>(a, Team<false>{}, b, s, j, u & 1, h, h + 1);
+    return;
+  }
+  u -= kv;
+  const int groups = (a.Hq + a.q_heads - 1) / a.q_heads;
+  const int t = u / groups, g = u % groups;
+  if (a.q == nullptr || t >= a.T) return;
+  // 32 lanes: items of `per` heads at once
+  const int items = a.d / 8, per = 32 / items, sub = (threadIdx.x & 31) / items;
+  const int h0 = g * a.q_heads, h1 = min(a.Hq, h0 + a.q_heads), each = (h1 - h0 + per - 1) / per;
+  append_q<8>(a, b, s, t, (threadIdx.x & 31) % items, min(h1, h0 + sub * each), min(h1, h0 + (sub + 1) * each));
 }
 
 }  // namespace
@@ -338,24 +461,48 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppendArgs
 unsigned int check_take_paged_cache() { return check_take_local(); }
 
 cudaError_t launch_rotate(RotateArgs a, cudaStream_t s) {
-  const int per = kRotateThreads / (a.d / 8);
-  const long long tokens = static_cast<long long>(a.B) * a.T;
+  const bool wide = !a.f32 && a.rope.rot % 16 == 0 && a.d % 16 == 0;
+  const int per = kRotateThreads / (a.d / (wide ? 16 : 8));
+  const long long tokens = static_cast<long long>(a.B) * a.T, blocks = (tokens + per - 1) / per;
   a.heads = kRotateHeads;
-  const dim3 grid(static_cast<unsigned int>((tokens + per - 1) / per), static_cast<unsigned int>((a.H + a.heads - 1) / a.heads));
-  return a.f32 ? launch_pdl(rotate_kernel<float>, grid, dim3(kRotateThreads), 0, s, a)
-               : launch_pdl(rotate_kernel<uint16_t>, grid, dim3(kRotateThreads), 0, s, a);
+  const dim3 grid(static_cast<unsigned int>(blocks), static_cast<unsigned int>((a.H + a.heads - 1) / a.heads));
+  if (a.f32) return launch_pdl(rotate_kernel<float, 8>, grid, dim3(kRotateThreads), 0, s, a);
+  return wide ? launch_pdl(rotate_kernel<uint16_t, 16>, grid, dim3(kRotateThreads), 0, s, a)
+              : launch_pdl(rotate_kernel<uint16_t, 8>, grid, dim3(kRotateThreads), 0, s, a);
 }
 
-cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s) {
+namespace {
+template <bool E4M3, int NP>
+cudaError_t launch_pages(const PagedAppendArgs& a, dim3 grid, cudaStream_t s) {
+  const bool wide = a.rope.rot % 16 == 0;
+  return wide ? launch_pdl(paged_append_kernel<E4M3, NP, 16>, grid, dim3(kPageThreads), 0, s, a)
+              : launch_pdl(paged_append_kernel<E4M3, NP, 8>, grid, dim3(kPageThreads), 0, s, a);
+}
+template <bool E4M3>
+cudaError_t launch_append(PagedAppendArgs a, cudaStream_t s) {
   const int page = 1 << a.page_shift;
-  const int threads = page * (a.d / 8) / kItems;
-  // pages that a sequence's new rows touch, at most
-  const int touched = (a.T + page - 2) / page + 1;
-  a.heads = 1;
-  const int groups = 2 * ((a.Hkv + a.heads - 1) / a.heads) + (a.q ? (a.Hq + a.heads - 1) / a.heads : 0);
-  const dim3 grid(groups, touched, a.B);
-  return a.e4m3 ? launch_pdl(paged_append_kernel<true>, grid, dim3(threads), 0, s, a)
-                : launch_pdl(paged_append_kernel<false>, grid, dim3(threads), 0, s, a);
+  a.touched = (a.T + page - 2) / page + 1;  // pages that a sequence's new rows touch, at most
+  if (a.T <= kAppendFew) {
+    a.q_heads = kFewQHeads;
+    const long long units = 2LL * a.Hkv * a.touched + (a.q ? static_cast<long long>(a.T) * ((a.Hq + a.q_heads - 1) / a.q_heads) : 0);
+    const dim3 grid(static_cast<unsigned int>((units + kFewWarps - 1) / kFewWarps), a.B);
+    constexpr int kRows = 8;  // items a lane holds: 16 rows of 128 channels, 32 of 64
+    static_assert(kAppendFew <= kRows * 2, "a warp holds a page's new rows");
+    return launch_pdl(paged_append_few_kernel<E4M3, kRows>, grid, dim3(32 * kFewWarps), 0, s, a);
+  }
+  a.heads = kAppendHeads;
+  a.q_heads = kAppendQHeads;
+  a.kv_groups = (a.Hkv + a.heads - 1) / a.heads;
+  const dim3 grid(2 * a.kv_groups + (a.q ? (a.Hq + a.q_heads - 1) / a.q_heads : 0), a.touched, a.B);
+  const int np = page * (a.d / 8) / kPageThreads;
+  return np == 8 ? launch_pages<E4M3, 8>(a, grid, s)
+       : np == 4 ? launch_pages<E4M3, 4>(a, grid, s)
+       : np == 2 ? launch_pages<E4M3, 2>(a, grid, s) : launch_pages<E4M3, 1>(a, grid, s);
+}
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
+  return a.e4m3 ? launch_append<true>(a, s) : launch_append<false>(a, s);
 }
 
 }  // namespace qattn

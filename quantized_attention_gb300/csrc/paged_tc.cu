@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
   auto wait = [&](int i, uint32_t n) {  // the n-th completion (from 0) of barrier i
     return mbar_wait(bar(i), n & 1, abort_flag, a.err, kErrTimeout);
   };
-  auto poll = [&](int i, uint32_t n) { return mbar_poll(bar(i), n & 1, abort_flag, a.err, kErrTimeout); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       __syncwarp();
     } else if (warp == 0 && elect_one()) {
       // ------------------------------------------------------------ MMA
-      // One thread for both tiles: its order keeps them half a step apart, so that one
+      // One thread for both tiles.  With P in S's place its order keeps them half a step apart, so that one
       // tile's MMAs run under the other's softmax.  (A thread for each lets both wait and
       // then contend: 1021 us against 910 for 2048 tokens over 32K.)
       constexpr uint32_t idesc_qk = make_idesc(128, kStep, 0, 0);
@@ -209,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       constexpr uint32_t tile = C::kTile >> 4;
       bool ok = true;
       uint32_t it = 0;         // steps done
-      uint32_t np0 = 0, np1 = 0;  // PVs of each tile
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // PVs and (kOwnP) QKs of each tile
+      auto ready = [&](int i, uint32_t k) { return mbar_test(bar(i), k & 1); };  // its k-th completion
       auto qk = [&](int t, uint32_t step) {
         const uint32_t qd = q0 + t * tile, kd = k0 + (step & 1) * tile, d = tmem + 128 * t;
         unroll<D / 16>([&](auto k) {
@@ -225,57 +225,120 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         const bool dual = is_dual(a, *sg);
         mbar_arrive(bar(kSegEmpty + (seg & 1)));
         if (n == 0) break;
-        // the first QK of each tile
-        for (int t = 0; ok && t < 2; ++t) {
-          if (!(ok = wait(kQFull + t, seg))) break;
-          if (dual && t >= n) {  // no step for this tile
-            mbar_arrive(bar(kOFull + t));
-            continue;
+        if constexpr (C::kOwnP) {
+          // Whatever is ready first: a tile's QK once S has been read, its PV once P is there
+          ok = wait(kQFull, seg) && wait(kQFull + 1, seg);
+          const int ahead = dual ? 2 : 1;  // to a tile's next step
+          int q[2] = {0, dual ? 1 : 0}, p[2] = {0, dual ? 1 : 0};  // the tiles' next QK and PV
+          bool half[2] = {false, false};                           // PV's first half is issued
+          if (dual && n == 1) mbar_arrive(bar(kOFull + 1));         // no step for tile 1
+          uint32_t idle = 0;
+          unsigned long long since = 0;
+          while (ok && (p[0] < n || p[1] < n)) {
+            bool any = false;
+            unroll<2>([&](auto tile_no) {
+              constexpr int t = decltype(tile_no)::value;
+              const uint32_t qs = it + q[t], ps = it + p[t];
+              if (q[t] < n && q[t] - p[t] < 2 * ahead && ready(kKFull + (qs & 1), qs >> 1) &&
+                  (q[t] < ahead || ready(kSFree + t, nq[t] - 1))) {
+                tc_fence_after();
+                qk(t, qs);
+                if (dual || q[1 - t] > q[t]) mma_commit(bar(kKEmpty + (qs & 1)));
+                q[t] += ahead;
+                ++nq[t];
+                any = true;
+              }
+              if (p[t] < q[t] && p[t] < n) {
+                const uint32_t vd = v0 + (ps & 1) * tile, o = tmem + C::kTmO + D * t,
+                               pc = tmem + C::kTmP + C::kTmPStep * t;
+                if (!half[t] && ready(kVFull + (ps & 1), ps >> 1) && ready(kPFull + 2 * t, np[t])) {
+                  tc_fence_after();
+                  const uint32_t more = p[t] >= ahead ? 1u : 0u;
+                  unroll<4>([&](auto k) {
+                    constexpr int i = decltype(k)::value;
+                    mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, pc, vd, i > 0 ? 1u : more);
+                  });
+                  half[t] = any = true;
+                }
+                if (half[t] && ready(kPFull + 2 * t + 1, np[t])) {
+                  tc_fence_after();
+                  unroll<4>([&](auto k) {
+                    constexpr int i = 4 + decltype(k)::value;
+                    mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, pc, vd, 1u);
+                  });
+                  mma_commit(bar(kPvDone + t));
+                  if (dual || p[1 - t] > p[t]) mma_commit(bar(kVEmpty + (ps & 1)));
+                  p[t] += ahead;
+                  if (p[t] >= n) mma_commit(bar(kOFull + t));
+                  ++np[t];
+                  half[t] = false;
+                  any = true;
+                }
+              }
+            });
+            if (any) {
+              idle = 0;
+            } else if ((++idle & 255u) == 0) {
+              if (idle == 256u) since = cycles();
+              if (*abort_flag) ok = false;
+              if (cycles() - since > kWaitTimeoutCycles) {
+                atomicOr(a.err, kErrTimeout);
+                ok = false;
+              }
+            }
           }
-          const uint32_t step = it + (dual ? t : 0);
-          if ((dual || t == 0) && !(ok = wait(kKFull + (step & 1), step >> 1))) break;
-          tc_fence_after();
-          qk(t, step);
-          if (dual || t == 1) mma_commit(bar(kKEmpty + (step & 1)));
-        }
-        const int ahead = dual ? 2 : 1;  // to a tile's next step
-        for (int j = 0; ok && j < n; ++j, ++it) {
-          const uint32_t st = it & 1;
-          const int t0 = dual ? (j & 1) : 0, t1 = dual ? t0 + 1 : 2;
-          for (int t = t0; ok && t < t1; ++t) {
-            const uint32_t np = t == 0 ? np0 : np1;
-            auto next_qk = [&] {
-              if (j + ahead >= n) return true;
-              const uint32_t step = it + ahead;
-              if (t == t0 && !poll(kKFull + (step & 1), step >> 1)) return false;
-              if (C::kOwnP && !poll(kSFree + t, np)) return false;
+          it += n;
+        } else {
+          // In turn, which keeps the tiles half a step apart
+          // the first QK of each tile
+          for (int t = 0; ok && t < 2; ++t) {
+            if (!(ok = wait(kQFull + t, seg))) break;
+            if (dual && t >= n) {  // no step for this tile
+              mbar_arrive(bar(kOFull + t));
+              continue;
+            }
+            const uint32_t step = it + (dual ? t : 0);
+            if ((dual || t == 0) && !(ok = wait(kKFull + (step & 1), step >> 1))) break;
+            tc_fence_after();
+            qk(t, step);
+            if (dual || t == 1) mma_commit(bar(kKEmpty + (step & 1)));
+          }
+          const int ahead = dual ? 2 : 1;  // to a tile's next step
+          for (int j = 0; ok && j < n; ++j, ++it) {
+            const uint32_t st = it & 1;
+            const int t0 = dual ? (j & 1) : 0, t1 = dual ? t0 + 1 : 2;
+            for (int t = t0; ok && t < t1; ++t) {
+              const uint32_t done = t == 0 ? np[0] : np[1];
+              auto next_qk = [&] {
+                if (j + ahead >= n) return true;
+                const uint32_t step = it + ahead;
+                if (t == t0 && !wait(kKFull + (step & 1), step >> 1)) return false;
+                tc_fence_after();
+                qk(t, step);
+                if (t == t1 - 1) mma_commit(bar(kKEmpty + (step & 1)));
+                return true;
+              };
+              if (t == t0 && !(ok = wait(kVFull + st, it >> 1))) break;
+              const uint32_t vd = v0 + st * tile;
+              const uint32_t o = tmem + C::kTmO + D * t, p = tmem + C::kTmP + C::kTmPStep * t, more = j >= ahead ? 1u : 0u;
+              if (!(ok = wait(kPFull + 2 * t, done))) break;  // keys 0 - 63
               tc_fence_after();
-              qk(t, step);
-              if (t == t1 - 1) mma_commit(bar(kKEmpty + (step & 1)));
-              return true;
-            };
-            if (C::kOwnP && !(ok = next_qk())) break;
-            if (t == t0 && !(ok = poll(kVFull + st, it >> 1))) break;
-            const uint32_t vd = v0 + st * tile;
-            const uint32_t o = tmem + C::kTmO + D * t, p = tmem + C::kTmP + C::kTmPStep * t, more = j >= ahead ? 1u : 0u;
-            if (!(ok = poll(kPFull + 2 * t, np))) break;  // keys 0 - 63
-            tc_fence_after();
-            unroll<4>([&](auto k) {
-              constexpr int i = decltype(k)::value;
-              mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
-            });
-            if (!(ok = poll(kPFull + 2 * t + 1, np))) break;  // keys 64 - 127
-            tc_fence_after();
-            unroll<4>([&](auto k) {
-              constexpr int i = 4 + decltype(k)::value;
-              mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, 1u);
-            });
-            if (t == 0) ++np0;
-            else ++np1;
-            if (C::kOwnP) mma_commit(bar(kPvDone + t));
-            if (t == t1 - 1) mma_commit(bar(kVEmpty + st));
-            if (j + ahead >= n) mma_commit(bar(kOFull + t));
-            if (!C::kOwnP) ok = next_qk();
+              unroll<4>([&](auto k) {
+                constexpr int i = decltype(k)::value;
+                mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
+              });
+              if (!(ok = wait(kPFull + 2 * t + 1, done))) break;  // keys 64 - 127
+              tc_fence_after();
+              unroll<4>([&](auto k) {
+                constexpr int i = 4 + decltype(k)::value;
+                mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, 1u);
+              });
+              if (t == 0) ++np[0];
+              else ++np[1];
+              if (t == t1 - 1) mma_commit(bar(kVEmpty + st));
+              if (j + ahead >= n) mma_commit(bar(kOFull + t));
+              ok = next_qk();
+            }
           }
         }
         if (!ok) break;
@@ -505,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         // while the other scores are on their way; should the maxima ask for another, S is
         // read again.  0: try; 1: settle the reference first; 2: settled.
         int mode = masked || __any_sync(0xffffffffu, m == -kPgInf) ? 1 : 0;
-        ok = poll(kSFull + t, ns);
+        ok = wait(kSFull + t, ns);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -515,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         auto pv_done = [&] {
           if (!C::kOwnP || pv_over || j == first) return true;
           pv_over = true;
-          if (!__all_sync(0xffffffffu, poll(kPvDone + t, ns - 1))) return false;
+          if (!__all_sync(0xffffffffu, wait(kPvDone + t, ns - 1))) return false;
           tc_fence_after();
           return true;
         };

@@ -426,9 +426,14 @@ struct PagedAppendArgs {
   uint8_t *k_pages, *v_pages;     // [n_pages][Hkv][page][d]
   float *k_scales, *v_scales;     // [n_pages][Hkv]
   unsigned int* err;
-  int heads;                      // set by launch_paged_append: heads of a CTA
+  // set by launch_paged_append: K or V heads of a CTA and their groups, Q heads of a CTA
+  // (or warp), pages that a sequence's new rows touch at most
+  int heads, kv_groups, q_heads, touched;
 };
-cudaError_t launch_paged_append(PagedAppendArgs a, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+constexpr int kRotateHeads = 8;   // heads a thread turns by the same angles
+constexpr int kAppendFew = 16;    // new tokens of a sequence up to which a warp takes a page
+constexpr int kFewQHeads = 8, kAppendHeads = 2, kAppendQHeads = 8;
 
 // ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
 constexpr int kPagedRows = 16;                // query rows of the warp-level kernel's block

@@ -94,25 +94,6 @@ __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, vo
   return mbar_wait_slow(bar, parity, abort_flag, err, code);
 }
 
-// The same without suspending: for a wait that a pipeline's period hangs on (a suspended
-// thread was seen to go on ~550 cycles after the last arrival, a polling one ~50).
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned int* err, unsigned int code) {
-  if (mbar_test(bar, parity)) return true;
-  const unsigned long long t0 = cycles();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_test(bar, parity)) return true;
-    if ((n & 255u) == 0) {
-      if (*abort_flag) return false;
-      if (cycles() - t0 > kWaitTimeoutCycles) {
-        *abort_flag = 1;
-        atomicOr(err, code);
-        return false;
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
