@@ -157,7 +157,7 @@ constexpr int kRotateThreads = 256;
 
 // A thread turns one item of a token in `heads` heads by the same angles.
 template <typename T, int W>
-__global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kRotateThreads, 4) rotate_kernel(const RotateArgs a) {
   const int items = a.d / W, per = kRotateThreads / items;
   const int i = threadIdx.x % items;
   const long long tok = static_cast<long long>(blockIdx.x) * per + threadIdx.x / items;
@@ -253,8 +253,8 @@ struct Team {
 };
 
 // One page of a sequence and heads h0 .. h1 - 1 of K or V, by a team: the new rows of a
-// head (NP items a thread, rows rw + per k) are held as they came, the next head's loads
-// on their way; their largest magnitude settles the scale; the codes follow.  K's rows
+// head (NP items a thread, rows rw + per k) are held as they came; their largest magnitude
+// settles the scale; the codes follow.  K's rows
 // are turned twice, for the maximum and for the codes: angles come from L1 and the
 // registers stay few.
 template <bool E4M3, int NP, bool CTA>
@@ -293,26 +293,22 @@ __device__ __forceinline__ void append_page(const PagedAppendArgs& a, const Team
   }
   uint8_t* const pages = is_v ? a.v_pages : a.k_pages;
   float* const scales = is_v ? a.v_scales : a.k_scales;
-  Raw<8> x[NP], y[NP];
-  auto fetch = [&](Raw<8> (&z)[NP], int h) {
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      z[k] = Raw<8>{};
-      if (((ok >> k) & 1u) && QATTN_IN_BOUNDS(t0 + rw + per * k < a.T && h < a.Hkv))
-        z[k] = load_raw<8>(X + h * sH + (t0 + rw + per * k) * sN, pl);
-    }
-  };
+  Raw<8> x[NP];
   auto value = [&](int k) {
     Item<8> v = values<8>(x[k]);
     if (pl.turned) v = turn(v, load_angles<8>(a.rope, position(a, b, s.first, t0 + rw + per * k), i), a.rope.inter);
     return v;
   };
-  fetch(x, h0);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     const size_t sc = static_cast<size_t>(page) * a.Hkv + h;
     const float was = held ? scales[sc] : 0.f;
-    if (h + 1 < h1) fetch(y, h + 1);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      x[k] = Raw<8>{};
+      if (((ok >> k) & 1u) && QATTN_IN_BOUNDS(t0 + rw + per * k < a.T && h < a.Hkv))
+        x[k] = load_raw<8>(X + h * sH + (t0 + rw + per * k) * sN, pl);
+    }
     // the largest magnitude, as bits: NaN lies above infinity, infinity above every number
     uint32_t top = 0;
 #pragma unroll
@@ -367,8 +363,6 @@ __device__ __forceinline__ void append_page(const PagedAppendArgs& a, const Team
       *reinterpret_cast<uint32_t*>(row + pl.c0) = encode4<E4M3>(q[0], q[1], q[2], q[3]);
       *reinterpret_cast<uint32_t*>(row + pl.c1) = encode4<E4M3>(q[4], q[5], q[6], q[7]);
     }
-#pragma unroll
-    for (int k = 0; k < NP; ++k) x[k] = y[k];
   }
 }
 
@@ -399,10 +393,10 @@ __device__ __forceinline__ void append_q(const PagedAppendArgs& a, int b, const 
 }
 
 // Many tokens: a CTA a page (x: kind and head group, y: page, z: sequence); then, behind
-// a.kv_groups, CTAs that rotate Q, 256 items (tokens x channels) and a head group each.
-constexpr int kPageThreads = 256;
-template <bool E4M3, int NP, int WQ>
-__global__ void __launch_bounds__(kPageThreads, NP == 8 ? 2 : 3) paged_append_kernel(const PagedAppendArgs a) {
+// a.kv_groups, CTAs that rotate Q, a page's tokens and a head group each.
+constexpr int kPageItems = 4;  // items of a page that a thread holds
+template <bool E4M3, int WQ>
+__global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendArgs a) {
   __shared__ uint32_t red[2][32];
   pdl_trigger();
   pdl_wait();
@@ -415,11 +409,11 @@ __global__ void __launch_bounds__(kPageThreads, NP == 8 ? 2 : 3) paged_append_ke
     if (is_v) g -= a.kv_groups;
     const int j = (s.first >> a.page_shift) + blockIdx.y;
     if ((j << a.page_shift) >= s.len) return;
-    append_page<E4M3, NP, true>(a, Team<true>{red}, b, s, j, is_v, g * a.heads, min(a.Hkv, (g + 1) * a.heads));
+    append_page<E4M3, kPageItems, true>(a, Team<true>{red}, b, s, j, is_v, g * a.heads, min(a.Hkv, (g + 1) * a.heads));
     return;
   }
   g -= 2 * a.kv_groups;
-  const int items = a.d / WQ, per = kPageThreads / items;
+  const int items = a.d / WQ, per = blockDim.x / items;
   // a page's tokens in as many rounds as it takes
   const int t0 = blockIdx.y << a.page_shift, t1 = min(s.n, t0 + (1 << a.page_shift));
   for (int t = t0 + threadIdx.x / items; t < t1; t += per)
@@ -472,12 +466,6 @@ cudaError_t launch_rotate(RotateArgs a, cudaStream_t s) {
 }
 
 namespace {
-template <bool E4M3, int NP>
-cudaError_t launch_pages(const PagedAppendArgs& a, dim3 grid, cudaStream_t s) {
-  const bool wide = a.rope.rot % 16 == 0;
-  return wide ? launch_pdl(paged_append_kernel<E4M3, NP, 16>, grid, dim3(kPageThreads), 0, s, a)
-              : launch_pdl(paged_append_kernel<E4M3, NP, 8>, grid, dim3(kPageThreads), 0, s, a);
-}
 template <bool E4M3>
 cudaError_t launch_append(PagedAppendArgs a, cudaStream_t s) {
   const int page = 1 << a.page_shift;
@@ -494,10 +482,9 @@ cudaError_t launch_append(PagedAppendArgs a, cudaStream_t s) {
   a.q_heads = kAppendQHeads;
   a.kv_groups = (a.Hkv + a.heads - 1) / a.heads;
   const dim3 grid(2 * a.kv_groups + (a.q ? (a.Hq + a.q_heads - 1) / a.q_heads : 0), a.touched, a.B);
-  const int np = page * (a.d / 8) / kPageThreads;
-  return np == 8 ? launch_pages<E4M3, 8>(a, grid, s)
-       : np == 4 ? launch_pages<E4M3, 4>(a, grid, s)
-       : np == 2 ? launch_pages<E4M3, 2>(a, grid, s) : launch_pages<E4M3, 1>(a, grid, s);
+  const dim3 block(page * (a.d / 8) / kPageItems);
+  return a.rope.rot % 16 == 0 ? launch_pdl(paged_append_kernel<E4M3, 16>, grid, block, 0, s, a)
+                              : launch_pdl(paged_append_kernel<E4M3, 8>, grid, block, 0, s, a);
 }
 }  // namespace
 

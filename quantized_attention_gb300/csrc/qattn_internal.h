@@ -431,9 +431,9 @@ struct PagedAppendArgs {
   int heads, kv_groups, q_heads, touched;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
-constexpr int kRotateHeads = 8;   // heads a thread turns by the same angles
+constexpr int kRotateHeads = 4;   // heads a thread turns by the same angles
 constexpr int kAppendFew = 16;    // new tokens of a sequence up to which a warp takes a page
-constexpr int kFewQHeads = 8, kAppendHeads = 2, kAppendQHeads = 8;
+constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
 
 // ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
 constexpr int kPagedRows = 16;                // query rows of the warp-level kernel's block
