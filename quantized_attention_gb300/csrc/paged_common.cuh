@@ -286,7 +286,8 @@ __device__ __forceinline__ void pg_row_shift(uint32_t amax, float& up, float& do
 // negative or not finite, give NaN to every row that sees a key of the page.
 constexpr float kPgMinV = 0x1p-48f, kPgMaxV = 0x1p48f, kPgZeroE = -48.f;
 struct PageScale {
-  float k;       // K scale (0 for a page that counts as NaN)
+  float k;       // K scale (0 for a page that counts as NaN).  A row's factor times it is held
+                 // at 1e-30 or more (2^(S c) is 1 all the same), so that a hidden key's -inf stays -inf
   float e_max;   // the exponent's part in the maximum,
   float e;       // and in the exponential
   float inv;     // 1 / V scale (1 where that counts as 0)
@@ -304,14 +305,6 @@ __device__ __forceinline__ PageScale pg_scale(float ks, float vs) {
   p.keep = zero ? 0u : 0xffffffffu;
   return p;
 }
-// The factor of a row's scores in a page.  At least 1e-30 (2^(S c) is 1 all the same),
-// so that a hidden key's -inf stays -inf; one that is not finite is the row's NaN.
-__device__ __forceinline__ float pg_factor(float row, float k, bool& finite) {
-  const float c = row * k;
-  finite = c < kPgInf;
-  return finite ? fmaxf(c, 1e-30f) : 1e-30f;
-}
-
 // The exponentials' reference lies below a row's largest t, so that P in fp16 uses the
 // type's range above 1 too; from |t| = 2^20 on, where the difference would round, it is
 // t itself.

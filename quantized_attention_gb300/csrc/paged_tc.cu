@@ -619,9 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
           };
           if (mode == 1) {
             const float top = largest(), head = pg_head(top, kHead);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-              if (c[g] == kPgInf && mx[g] > -kPgInf) fin = false;
             const bool moved = moves(top, head);
             const float mn = moved ? top - head : m;
             const float al = !moved ? 1.f : m == -kPgInf ? 0.f : ex2_approx(m - mn);

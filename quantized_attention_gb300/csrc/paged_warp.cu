@@ -11,13 +11,13 @@
 // The V scale rides in the exponent: P, rounded once to fp16 for the PV product, keeps
 // its eleven bits where P s_v, the key's part in O, is down to 2^-29 of the row's
 // largest, and no key costs an instruction more than with one scale for all.  l sums
-// the unrounded P in fp32.  Parts of a row (steps of 32 keys dealt to warps, shares of
+// the unrounded P in fp32.  Parts of a row (steps of 64 keys dealt to warps, shares of
 // steps dealt to CTAs) are joined by 2^(m_part - m).
 //
-// What it cannot do without: the cache's bytes, 2 D per key and KV head.  A step lies in
-// one page (pages of 32, 64 or 128 rows): one TMA box each for K and V at the page's
-// plane of the pool.  A warp looks up the pages and scales of its next 32 steps at once,
-// one a lane, ahead of their use.
+// What it cannot do without: the cache's bytes, 2 D per key and KV head.  A step's K and
+// V come as a tile each, one TMA box at the page's plane of the pool (pages of 32 rows:
+// two).  A warp looks up the pages and scales of its next 16 steps at once, one half step
+// (which lies in one page) a lane, ahead of their use.
 #include "paged_common.cuh"
 
 namespace qattn {
@@ -28,15 +28,14 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kPagedWarpStep;
 constexpr int kRows = kPagedRows;
 constexpr int kHead = 15;  // of the exponentials' reference (pg_head)
-constexpr int kRing = 3;   // stages of a warp's ring (K and V of one step each)
+constexpr int kRing = 3;   // tiles of a warp's ring (K or V of a step)
 // Shares a block, on average, from which four warps join a row.
 constexpr int kJoinShares = 4;
 
 template <int D>
 struct WarpSmem {
   static constexpr int kTile = kStep * D;  // bytes of a step's K (or V) codes
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kWarp = kRing * kStage;   // one warp's ring
+  static constexpr int kWarp = kRing * kTile;    // one warp's ring
   static constexpr int kShare = kWarps * kWarp;  // a CTA's O for its cluster
   static constexpr int kBytes = kShare + kRows * D * 4 + 1024;
   static_assert(kRows * D * 4 <= kWarp, "a warp's O does not fit its ring");
@@ -85,7 +84,7 @@ __device__ __forceinline__ int join_chunk(int r, int c) {
   return c ^ (((c >> ((D == 128) ? 3 : 2)) & 3) + 4 * (r & 1));
 }
 
-// Pages and scales of a warp's next 32 steps, one a lane.
+// Pages and scales of a warp's 16 steps from `base` on, one half step a lane.
 struct Window {
   int page;      // -1: no such page, its keys are hidden
   float ks, vs;
@@ -132,19 +131,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!CL && threadIdx.x == 0) pg_put_plan(a, walk);
   __syncthreads();  // the abort flag is set
   uint32_t used = 0;  // tiles this warp has taken through its ring
-  uint32_t sent = 0;  // lane 0: those it has issued
+  uint32_t sent = 0;  // and issued
 
   while (CL ? some : pg_next<kRows, kStep>(a, walk, sg)) {
     const int len = sg.seq.len;
     // this warp's steps: sg.s0 + warp, + kWarps, ...
     const int first = sg.s0 + warp;
-    const int ntile = first < sg.s1 ? (sg.s1 - first + kWarps - 1) / kWarps : 0;
+    const int nstep = first < sg.s1 ? (sg.s1 - first + kWarps - 1) / kWarps : 0;
     auto key_of = [&](int i) { return (first + i * kWarps) * kStep; };
-    auto look_up = [&](int i0) {  // the window of tiles i0 .. i0 + 31
+    auto look_up = [&](int i0) {  // the window of steps i0 .. i0 + 15
       Window w{-1, 0.f, 0.f};
-      const int i = i0 + lane;
-      if (i < ntile) {
-        const int key = key_of(i), j = key >> a.page_shift;
+      const int i = i0 + (lane >> 1);
+      if (i < nstep) {
+        const int key = key_of(i) + 32 * (lane & 1), j = key >> a.page_shift;
         if (key < len && QATTN_IN_BOUNDS(j < a.max_pages && sg.b < a.B)) {
           const int p = a.page_table[static_cast<size_t>(sg.b) * a.max_pages + j];
           if (p >= 0 && p < a.n_pages) {
@@ -159,30 +158,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       return w;
     };
-    Window cur = look_up(0), nxt{-1, 0.f, 0.f};
-    if (ntile > 32) nxt = look_up(32);
-    int base = 0;  // tile of cur's first lane
-    auto issue = [&](int i) {  // tile i of this warp (the whole warp calls)
-      const uint32_t q = used + i, slot = q % kRing;
-      const int pc = __shfl_sync(0xffffffffu, cur.page, (i - base) & 31);
-      const int pn = __shfl_sync(0xffffffffu, nxt.page, (i - base) & 31);
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&full[warp][slot]);
-        // a page that does not exist: any page of the pool stands in, its keys are hidden
-        const int page = max(i - base < 32 ? pc : pn, 0);
-        const int row = key_of(i) & ((1 << a.page_shift) - 1);
-        const int plane = page * a.Hkv + sg.hkv;
-        sent = q + 1;
-        (void)QATTN_IN_BOUNDS(page < a.n_pages && row >= 0 && row + kStep <= (1 << a.page_shift));  // TMA coordinates
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(SM::kStage));
-        tma_load_3d(smem_u32(ring + slot * SM::kStage), &tmK, bar, 0, row, plane);
-        tma_load_3d(smem_u32(ring + slot * SM::kStage + SM::kTile), &tmV, bar, 0, row, plane);
-      }
-    };
-    for (int i = 0; i < min(kRing - 1, ntile); ++i) issue(i);
-
-    // ---- this lane's rows g and g + 8 of the block: fp16 values, factor, key limit
-    uint32_t qa[KS][4];
+    // ---- this lane's rows g and g + 8 of the block: loads first, then the pages, then the
+    // first tiles, so that one latency covers another
+    uint4 xq[2][D / 32];
     float rf[2];
     bool fin[2];
     int lim[2];
@@ -193,14 +171,46 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool in = tok < sg.seq.n;
       const int hq = sg.hkv * a.G + rr - tok * a.G;
       const uint16_t* src = a.q + sg.b * a.qsB + hq * a.qsH + tok * a.qsN + (D / 4) * t4;
-      uint4 x[D / 32];
+      // (a row that is none sees everything: its scores are 0, and it asks for no mask)
+      lim[h] = in ? min(pg_limit(a, sg.seq, tok), len) : 0x7fffffff;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        xq[h][k] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && QATTN_IN_BOUNDS(sg.b < a.B && hq < a.Hq && tok < a.T))
+          xq[h][k] = *reinterpret_cast<const uint4*>(src + 8 * k);
+      }
+    }
+    Window raw = look_up(0), nxt{-1, 0.f, 0.f};
+    int base = 0;            // the first step of the current window,
+    int pages = raw.page;    // its pages
+    auto issue = [&](int n) {  // tile n (the whole warp calls)
+      const int i = n >> 1, o = 2 * (i - base);
+      const int c0 = __shfl_sync(0xffffffffu, pages, o & 31), c1 = __shfl_sync(0xffffffffu, pages, (o + 1) & 31);
+      const int n0 = __shfl_sync(0xffffffffu, nxt.page, o & 31), n1 = __shfl_sync(0xffffffffu, nxt.page, (o + 1) & 31);
+      if (lane == 0) {
+        const uint32_t slot = sent % kRing, bar = smem_u32(&full[warp][slot]);
+        const uint32_t dst = smem_u32(ring + slot * SM::kTile);
+        // a page that does not exist: any page of the pool stands in, its keys are hidden
+        const int p0 = max(o < 32 ? c0 : n0, 0), p1 = max(o < 32 ? c1 : n1, 0);
+        const int row = key_of(i) & ((1 << a.page_shift) - 1);
+        (void)QATTN_IN_BOUNDS(p0 < a.n_pages && p1 < a.n_pages && row >= 0 &&
+                              row + min(kStep, 1 << a.page_shift) <= (1 << a.page_shift));  // TMA coordinates
+        const CUtensorMap* map = n & 1 ? &tmV : &tmK;
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(SM::kTile));
+        tma_load_3d(dst, map, bar, 0, row, p0 * a.Hkv + sg.hkv);
+        if (a.page_shift == 5) tma_load_3d(dst + SM::kTile / 2, map, bar, 0, 0, p1 * a.Hkv + sg.hkv);
+      }
+      ++sent;
+    };
+    for (int n = 0; n < min(kRing, 2 * nstep); ++n) issue(n);
+    if (nstep > 16) nxt = look_up(16);
+    uint32_t qa[KS][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
-        x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && QATTN_IN_BOUNDS(sg.b < a.B && hq < a.Hq && tok < a.T))
-          x[k] = *reinterpret_cast<const uint4*>(src + 8 * k);
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const uint32_t w[4] = {xq[h][k].x, xq[h][k].y, xq[h][k].z, xq[h][k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
       }
@@ -210,10 +220,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       float up, down;
       pg_row_shift(top, up, down);
       rf[h] = __fmul_rn(__fmul_rn(a.sm_scale, kPgLog2e), down);
-      lim[h] = in ? min(pg_limit(a, sg.seq, tok), len) : 0;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        const uint32_t w[4] = {xq[h][k].x, xq[h][k].y, xq[h][k].z, xq[h][k].w};
         uint32_t f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -227,73 +236,111 @@ __global__ void __launch_bounds__(kThreads, 2)
         qa[2 * k + 1][2 + h] = f[3];
       }
     }
+    // the current window: what its scales mean, and its halves out of the ordinary
+    float wk, we, winv;
+    uint32_t hidden, zero_v, bad;
+    auto settle = [&](const Window& w) {
+      const PageScale ps = pg_scale(w.ks, w.vs);
+      pages = w.page;
+      wk = ps.k;
+      we = ps.e;
+      winv = ps.inv;
+      hidden = __ballot_sync(0xffffffffu, w.page < 0);
+      zero_v = __ballot_sync(0xffffffffu, ps.keep == 0u);
+      bad = __ballot_sync(0xffffffffu, ps.nan);
+    };
+    settle(raw);
     float o[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m[2] = {-kPgInf, -kPgInf}, l[2] = {0.f, 0.f};
 
-    for (int i = 0; i < ntile; ++i) {
-      if (i - base == 32) {
+    for (int i = 0; i < nstep; ++i) {
+      if (i - base == 16) {
         base = i;
-        cur = nxt;
-        if (i + 32 < ntile) nxt = look_up(i + 32);
+        settle(nxt);
+        nxt = Window{-1, 0.f, 0.f};
+        if (i + 16 < nstep) nxt = look_up(i + 16);
       }
-      if (i + kRing - 1 < ntile) issue(i + kRing - 1);
-      const int page = __shfl_sync(0xffffffffu, cur.page, i - base);
-      const PageScale ps = pg_scale(__shfl_sync(0xffffffffu, cur.ks, i - base),
-                                    __shfl_sync(0xffffffffu, cur.vs, i - base));
-      const uint32_t q = used + i, slot = q % kRing;
-      const bool ok = mbar_wait(smem_u32(&full[warp][slot]), (q / kRing) & 1, &abort_flag, a.err, kErrTimeout);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint8_t* st = ring + slot * SM::kStage;
+      const int q0 = 2 * (i - base);
+      float c[2][2], e[2], inv[2];  // [row][half], [half]
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float k = __shfl_sync(0xffffffffu, wk, q0 + x);
+        e[x] = __shfl_sync(0xffffffffu, we, q0 + x);
+        inv[x] = __shfl_sync(0xffffffffu, winv, q0 + x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) c[h][x] = fmaxf(rf[h] * k, 1e-30f);
+      }
+      const uint32_t rare = ((hidden | zero_v | bad) >> q0) & 3u;
       const int key = key_of(i);
-      int room[2];  // visible keys of the step
-      float cf[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        room[h] = page < 0 ? 0 : lim[h] - key;
-        bool f;
-        cf[h] = pg_factor(rf[h], ps.k, f);
-        if (room[h] > 0 && (ps.nan || !f)) fin[h] = false;
-      }
-      const bool masked = __any_sync(0xffffffffu, room[0] < kStep || room[1] < kStep);
+      const int room[2] = {lim[0] - key, lim[1] - key};  // visible keys of the step
+      const bool masked = __any_sync(0xffffffffu, room[0] < kStep || room[1] < kStep || rare != 0u);
+      auto tile = [&](const uint8_t*& at) {  // the next tile, once it is there
+        const uint32_t slot = used % kRing;
+        at = ring + slot * SM::kTile;
+        const bool ok = mbar_wait(smem_u32(&full[warp][slot]), (used / kRing) & 1, &abort_flag, a.err, kErrTimeout);
+        return __all_sync(0xffffffffu, ok);
+      };
+      const uint8_t* st;
+      if (!tile(st)) break;
       // ---- scores
-      float s[4][4];
+      float s[8][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
         for (int w4 = 0; w4 < KS / 4; ++w4) {
           const uint4 kw = *reinterpret_cast<const uint4*>(st + swz<D>(8 * j + g, (KS / 4) * t4 + w4));
           const uint32_t kx[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int q = 0; q < 4; ++q) {
             uint32_t b0, b1;
-            widen4<E4M3>(kx[e], b0, b1);
-            const uint32_t(&qv)[4] = qa[4 * w4 + e];
+            widen4<E4M3>(kx[q], b0, b1);
+            const uint32_t(&qv)[4] = qa[4 * w4 + q];
             mma16816(s[j], qv[0], qv[1], qv[2], qv[3], b0, b1);
           }
         }
       }
+      __syncwarp();  // the tile is read
+      ++used;
+      if (2 * i + kRing < 2 * nstep) issue(2 * i + kRing);
+      float top[2] = {-kPgInf, -kPgInf};
       if (masked) {
-        const uint32_t vis[2] = {pg_first_bits(room[0]), pg_first_bits(room[1])};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int x = 0; x < 2; ++x) {
+          uint32_t vis[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!((vis[e >> 1] >> (8 * j + 2 * t4 + (e & 1))) & 1u)) s[j][e] = -kPgInf;
+          for (int h = 0; h < 2; ++h) {
+            vis[h] = pg_first_bits(((hidden >> (q0 + x)) & 1u) ? 0 : room[h] - 32 * x);
+            if (vis[h] != 0u && ((bad >> (q0 + x)) & 1u)) fin[h] = false;
+          }
+#pragma unroll
+          for (int j = 4 * x; j < 4 * x + 4; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (!((vis[q >> 1] >> (8 * (j - 4 * x) + 2 * t4 + (q & 1))) & 1u)) s[j][q] = -kPgInf;
+        }
       }
       // ---- running maxima less kHead: max t = c max S + e (c > 0); -inf stays -inf
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float ex = ((zero_v >> (q0 + x)) & 1u) ? kPgZeroE : e[x];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y = fmax3(s[4 * x][2 * h], s[4 * x][2 * h + 1], s[4 * x + 1][2 * h]);
+          y = fmax3(y, s[4 * x + 1][2 * h + 1], s[4 * x + 2][2 * h]);
+          y = fmax3(y, s[4 * x + 2][2 * h + 1], s[4 * x + 3][2 * h]);
+          y = fmaxf(y, s[4 * x + 3][2 * h + 1]);
+          top[h] = fmaxf(top[h], fmaf(y, c[h][x], ex));
+        }
+      }
       float al[2], ref[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float x = -kPgInf;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x = fmax3(x, s[j][2 * h], s[j][2 * h + 1]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float top = fmaf(x, cf[h], ps.e_max);
-        const float mn = fmaxf(m[h], top - pg_head(top, kHead));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        const float mn = fmaxf(m[h], top[h] - pg_head(top[h], kHead));
         ref[h] = (mn == -kPgInf) ? 0.f : mn;
         al[h] = (m[h] == -kPgInf) ? 0.f : ex2_approx(m[h] - ref[h]);
         m[h] = mn;
@@ -309,27 +356,36 @@ __global__ void __launch_bounds__(kThreads, 2)
           o[n][3] *= al[1];
         }
       }
-      uint32_t pa[4][2];
-      float sum[2] = {0.f, 0.f};
-      const float off[2] = {ps.e - ref[0], ps.e - ref[1]};
+      uint32_t pa[8][2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float pr[4];
+      for (int x = 0; x < 2; ++x) {
+        float2 sum = make_float2(0.f, 0.f);
+        const float off[2] = {e[x] - ref[0], e[x] - ref[1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(fmaf(s[j][e], cf[e >> 1], off[e >> 1]));
-        sum[0] += pr[0] + pr[1];
-        sum[1] += pr[2] + pr[3];
-        pa[j][0] = pack_half2(pr[0], pr[1]) & ps.keep;
-        pa[j][1] = pack_half2(pr[2], pr[3]) & ps.keep;
+        for (int j = 4 * x; j < 4 * x + 4; ++j) {
+          float pr[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) pr[q] = ex2_approx(fmaf(s[j][q], c[q >> 1][x], off[q >> 1]));
+          sum.x += pr[0] + pr[1];
+          sum.y += pr[2] + pr[3];
+          pa[j][0] = pack_half2(pr[0], pr[1]);
+          pa[j][1] = pack_half2(pr[2], pr[3]);
+        }
+        l[0] = fmaf(sum.x, inv[x], l[0]);
+        l[1] = fmaf(sum.y, inv[x], l[1]);
+        if ((zero_v >> (q0 + x)) & 1u) {
+#pragma unroll
+          for (int j = 4 * x; j < 4 * x + 4; ++j) pa[j][0] = pa[j][1] = 0u;
+        }
       }
-      l[0] = fmaf(sum[0], ps.inv, l[0]);
-      l[1] = fmaf(sum[1], ps.inv, l[1]);
       // ---- O += P V
-      const uint8_t* sv = st + SM::kTile;
-      // rows behind the sequence may hold any byte: an e4m3 NaN there must not meet P = 0
-      const int rows = E4M3 && masked ? (page < 0 ? 0 : len - key) : kStep;
+      const uint8_t* sv;
+      if (!tile(sv)) break;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < 4; ++kk) {
+        // rows behind the sequence (or in no page) may hold any byte: an e4m3 NaN there must not
+        // meet P = 0
+        const int rows = E4M3 && masked ? (((hidden >> (q0 + (kk >> 1))) & 1u) ? 0 : len - key) : kStep;
         uint32_t vw[4][VW];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -357,14 +413,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           widen_pair<E4M3>(vw[0][w], vw[1][w], b0);
           widen_pair<E4M3>(vw[2][w], vw[3][w], b1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma16816(o[4 * w + e], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1],
-                     b0[e], b1[e]);
+          for (int q = 0; q < 4; ++q)
+            mma16816(o[4 * w + q], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1], b0[q], b1[q]);
         }
       }
-      __syncwarp();  // the stage is read
+      __syncwarp();  // the tile is read
+      ++used;
+      if (2 * i + 1 + kRing < 2 * nstep) issue(2 * i + 1 + kRing);
     }
-    used += ntile;
 
     // ---- join the four warps (their rings are free)
 #pragma unroll

@@ -357,7 +357,7 @@ PagedSplit paged_split(const qattn_shape* s) {
   t.blocks = static_cast<int>(blocks);
   t.lead = t.tc ? qattn::kPagedTcLead : qattn::kPagedWarpLead;
   t.steps = heads * (t.lead + head_steps);
-  t.cluster = t.tc ? 0 : qattn::tree_cluster(heads, head_steps);
+  t.cluster = t.tc ? 0 : qattn::tree_cluster(heads, 2 * head_steps);  // (its steps are half as long)
   const int64_t most = t.tc ? qattn::kPagedTcCtas : qattn::kPagedWarpCtas;
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
   if (t.cluster > 0) {
@@ -1452,10 +1452,11 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   if (sp.tc) return from_cuda(qattn::launch_paged_tc(a, cs));
   CUtensorMap tk, tv;
   const int64_t planes = paging->n_pages * shape->Hkv;
+  const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(sp.step, paging->page_size));
   if (!encode_cache(&tk, k_pages, planes, paging->page_size, paging->page_size, shape->d,
-                    static_cast<uint32_t>(sp.step)) ||
+                    box) ||
       !encode_cache(&tv, v_pages, planes, paging->page_size, paging->page_size, shape->d,
-                    static_cast<uint32_t>(sp.step)))
+                    box))
     return QATTN_ERR_CUDA;
   return from_cuda(qattn::launch_paged_warp(tk, tv, a, cs));
 }

@@ -438,8 +438,8 @@ constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
 // ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
 constexpr int kPagedRows = 16;                // query rows of the warp-level kernel's block
 constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
-constexpr int kPagedWarpStep = 32;            // keys of a step
-constexpr int kPagedWarpLead = 10;            // steps that a block's start counts for in equal shares
+constexpr int kPagedWarpStep = 64;            // keys of a step
+constexpr int kPagedWarpLead = 5;             // steps that a block's start counts for in equal shares
 constexpr int kPagedCluster = 8;              // most CTAs of a block's own cluster
 // More than kPagedRows query rows of a KV head (query heads of the group x tokens): the
 // tensor-core kernel.
@@ -470,7 +470,7 @@ struct PagedArgs {
   float *part_o, *part_m, *part_l;
   PagedPlan* plan;         // [ctas]
 };
-// tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x (keys of a step) x 1
+// tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x min(step, page) x 1
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
 cudaError_t launch_paged_warp(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                               cudaStream_t s);
