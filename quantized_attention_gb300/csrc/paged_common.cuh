@@ -64,22 +64,13 @@ __device__ __forceinline__ int pg_limit(const PagedArgs& a, const PagedSeq& s, i
   return a.causal ? s.len - s.n + i + 1 : s.len;
 }
 
-// Places of one KV head of a sequence, and of its blocks before rb (a whole warp).
+// Places of one KV head of a sequence (a whole warp).
 template <int ROWS, int STEP>
-__device__ __forceinline__ int pg_head_places(const PagedArgs& a, const PagedSeq& s, int rb, int& before) {
+__device__ __forceinline__ int pg_head_places(const PagedArgs& a, const PagedSeq& s) {
   const int nb = pg_blocks<ROWS>(a, s), lane = threadIdx.x & 31;
-  int total = 0, pre = 0;
-  if (!a.causal || nb <= 1) {
-    const int one = nb > 0 ? a.lead + pg_steps<ROWS, STEP>(a, s, nb - 1) : 0;
-    before = rb * one;
-    return nb * one;
-  }
-  for (int k = lane; k < nb; k += 32) {
-    const int c = a.lead + pg_steps<ROWS, STEP>(a, s, k);
-    total += c;
-    if (k < rb) pre += c;
-  }
-  before = __reduce_add_sync(0xffffffffu, pre);
+  if (!a.causal || nb <= 1) return nb > 0 ? nb * (a.lead + pg_steps<ROWS, STEP>(a, s, nb - 1)) : 0;
+  int total = 0;
+  for (int k = lane; k < nb; k += 32) total += a.lead + pg_steps<ROWS, STEP>(a, s, k);
   return __reduce_add_sync(0xffffffffu, total);
 }
 
@@ -100,29 +91,34 @@ struct PagedSeg {
   PagedSeq seq;
 };
 
-// Places of all sequences, those before sequence b0 (a whole warp).
+// Sequence b's places, where one number gives them (a lane for a sequence; 0 past the last).
+struct PagedPlaces {
+  PagedSeq seq;
+  int nb, one, n;  // blocks of a KV head, steps of each, places in all
+};
 template <int ROWS, int STEP>
-__device__ __forceinline__ void pg_totals(const PagedArgs& a, int b0, int& total, int& before) {
-  total = before = 0;
+__device__ __forceinline__ PagedPlaces pg_places(const PagedArgs& a, int b) {
+  PagedPlaces p{{0, 0}, 0, 0, 0};
+  if (b < a.B) {
+    p.seq = pg_seq(a, b);
+    p.nb = pg_blocks<ROWS>(a, p.seq);
+    if (p.nb > 0) p.one = pg_steps<ROWS, STEP>(a, p.seq, p.nb - 1);
+    p.n = p.nb > 0 ? a.Hkv * p.nb * (a.lead + p.one) : 0;
+  }
+  return p;
+}
+// Places of all sequences (a whole warp; `first`: the first 32's, a lane each).
+template <int ROWS, int STEP>
+__device__ __forceinline__ int pg_totals(const PagedArgs& a, const PagedPlaces& first) {
+  int total = first.n;
   const int lane = threadIdx.x & 31;
-  if (a.blocks == 1 || !a.causal) {  // a lane for a sequence
-    for (int b = lane; b < a.B; b += 32) {
-      const PagedSeq s = pg_seq(a, b);
-      const int nb = pg_blocks<ROWS>(a, s);
-      const int w = nb > 0 ? a.Hkv * nb * (a.lead + pg_steps<ROWS, STEP>(a, s, nb - 1)) : 0;
-      total += w;
-      if (b < b0) before += w;
-    }
-    total = __reduce_add_sync(0xffffffffu, total);
-    before = __reduce_add_sync(0xffffffffu, before);
-    return;
+  if (a.blocks == 1 || !a.causal) {
+    for (int b = 32 + lane; b < a.B; b += 32) total += pg_places<ROWS, STEP>(a, b).n;
+    return __reduce_add_sync(0xffffffffu, total);
   }
-  for (int b = 0; b < a.B; ++b) {
-    int pre;
-    const int w = a.Hkv * pg_head_places<ROWS, STEP>(a, pg_seq(a, b), 0, pre);
-    total += w;
-    if (b < b0) before += w;
-  }
+  total = 0;
+  for (int b = 0; b < a.B; ++b) total += a.Hkv * pg_head_places<ROWS, STEP>(a, pg_seq(a, b));
+  return total;
 }
 
 // Where the share of CTA c of G begins.  Called by whole warps, each for itself.
@@ -130,8 +126,9 @@ template <int ROWS, int STEP>
 __device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a, int c, int G) {
   const int lane = threadIdx.x & 31;
   PagedWalk w{};
-  int total, none;
-  pg_totals<ROWS, STEP>(a, 0, total, none);
+  PagedPlaces one{{0, 0}, 0, 0, 0};
+  if (a.blocks == 1 || !a.causal) one = pg_places<ROWS, STEP>(a, lane);
+  const int total = pg_totals<ROWS, STEP>(a, one);
   const int q = total / G, r = total - q * G;
   w.total = total;
   w.p = c * q + min(c, r);
@@ -140,15 +137,8 @@ __device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a, int c, int G) {
   int before = 0;
   if (a.blocks == 1 || !a.causal) {
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      PagedSeq s{0, 0};
-      int nb = 0, one = 0;
-      if (b0 + lane < a.B) {
-        s = pg_seq(a, b0 + lane);
-        nb = pg_blocks<ROWS>(a, s);
-        if (nb > 0) one = pg_steps<ROWS, STEP>(a, s, nb - 1);
-      }
-      const int n = nb > 0 ? a.Hkv * nb * (a.lead + one) : 0;
-      int inc = n;
+      if (b0 > 0) one = pg_places<ROWS, STEP>(a, b0 + lane);
+      int inc = one.n;
 #pragma unroll
       for (int sh = 1; sh < 32; sh <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, inc, sh);
@@ -157,12 +147,12 @@ __device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a, int c, int G) {
       const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w.p);
       if (past) {
         const int l = __ffs(past) - 1;
-        int off = w.p - before - __shfl_sync(0xffffffffu, inc - n, l);
+        int off = w.p - before - __shfl_sync(0xffffffffu, inc - one.n, l);
         w.b = b0 + l;
-        w.seq.len = __shfl_sync(0xffffffffu, s.len, l);
-        w.seq.n = __shfl_sync(0xffffffffu, s.n, l);
-        w.steps = __shfl_sync(0xffffffffu, one, l);
-        nb = __shfl_sync(0xffffffffu, nb, l);
+        w.seq.len = __shfl_sync(0xffffffffu, one.seq.len, l);
+        w.seq.n = __shfl_sync(0xffffffffu, one.seq.n, l);
+        w.steps = __shfl_sync(0xffffffffu, one.one, l);
+        const int nb = __shfl_sync(0xffffffffu, one.nb, l);
         const int per = a.lead + w.steps, blk = off / per;
         w.hkv = blk / nb;
         w.rb = blk - w.hkv * nb;
@@ -176,8 +166,7 @@ __device__ __forceinline__ PagedWalk pg_walk(const PagedArgs& a, int c, int G) {
   }
   for (int b = 0; b < a.B; ++b) {
     const PagedSeq s = pg_seq(a, b);
-    int none2;
-    const int per = pg_head_places<ROWS, STEP>(a, s, 0, none2), n = a.Hkv * per;
+    const int per = pg_head_places<ROWS, STEP>(a, s), n = a.Hkv * per;
     if (before + n <= w.p) {
       before += n;
       continue;

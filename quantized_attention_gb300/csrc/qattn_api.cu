@@ -351,7 +351,7 @@ PagedSplit paged_split(const qattn_shape* s) {
   const int64_t R = s->Hq / s->Hkv * s->Nq;
   t.tc = R > qattn::kPagedRows;
   t.step = t.tc ? qattn::kPagedTcStep : qattn::kPagedWarpStep;
-  t.rows = t.tc ? qattn::kPagedTcRows : qattn::kPagedRows;
+  t.rows = t.tc ? qattn::kPagedTcRows : R <= 8 ? 8 : qattn::kPagedRows;
   const int64_t blocks = (R + t.rows - 1) / t.rows, heads = s->B * s->Hkv * blocks;
   const int64_t head_steps = std::max<int64_t>(1, (s->Nk + t.step - 1) / t.step);
   t.blocks = static_cast<int>(blocks);
@@ -1417,6 +1417,7 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   a.max_pages = static_cast<int>(paging->max_pages);
   a.e4m3 = paging->code_dtype == QATTN_E4M3;
   a.blocks = sp.blocks;
+  a.rows = sp.rows;
   a.causal = params->causal;
   a.sm_scale = sm_scale_of(shape, params);
   a.q = Q;
@@ -1452,11 +1453,8 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   if (sp.tc) return from_cuda(qattn::launch_paged_tc(a, cs));
   CUtensorMap tk, tv;
   const int64_t planes = paging->n_pages * shape->Hkv;
-  const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(sp.step, paging->page_size));
-  if (!encode_cache(&tk, k_pages, planes, paging->page_size, paging->page_size, shape->d,
-                    box) ||
-      !encode_cache(&tv, v_pages, planes, paging->page_size, paging->page_size, shape->d,
-                    box))
+  if (!encode_cache(&tk, k_pages, planes, paging->page_size, paging->page_size, shape->d, 32) ||
+      !encode_cache(&tv, v_pages, planes, paging->page_size, paging->page_size, shape->d, 32))
     return QATTN_ERR_CUDA;
   return from_cuda(qattn::launch_paged_warp(tk, tv, a, cs));
 }

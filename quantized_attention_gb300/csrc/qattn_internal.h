@@ -436,10 +436,10 @@ constexpr int kAppendFew = 16;    // new tokens of a sequence up to which a warp
 constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
 
 // ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
-constexpr int kPagedRows = 16;                // query rows of the warp-level kernel's block
+constexpr int kPagedRows = 16;                // most query rows of a KV head in the warp-level kernel
 constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
 constexpr int kPagedWarpStep = 64;            // keys of a step
-constexpr int kPagedWarpLead = 5;             // steps that a block's start counts for in equal shares
+constexpr int kPagedWarpLead = 8;             // steps that a block's start counts for in equal shares
 constexpr int kPagedCluster = 8;              // most CTAs of a block's own cluster
 // More than kPagedRows query rows of a KV head (query heads of the group x tokens): the
 // tensor-core kernel.
@@ -451,7 +451,7 @@ struct PagedPlan;
 struct PagedArgs {
   int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
   int n_pages, page_shift, max_pages, e4m3;
-  int blocks;                     // row blocks of a KV head, at most
+  int blocks, rows;               // row blocks of a KV head, at most; rows of a block
   int causal;
   float sm_scale;
   const uint16_t* q;              // bf16, element strides
@@ -470,7 +470,7 @@ struct PagedArgs {
   float *part_o, *part_m, *part_l;
   PagedPlan* plan;         // [ctas]
 };
-// tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x min(step, page) x 1
+// tk, tv: maps over the codes [n_pages * Hkv][page][d], box d x 32 x 1
 // (128-byte swizzle for d = 128, 64-byte for d = 64).
 cudaError_t launch_paged_warp(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                               cudaStream_t s);
