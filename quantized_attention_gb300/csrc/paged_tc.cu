@@ -2,7 +2,7 @@
 // of a KV head: on the 5th-generation tensor cores.  Mathematics as in paged_warp.cu.
 //
 // A CTA works on a block of 256 query rows (two tiles of 128) in steps of 128 keys:
-//   warp 0       issues the MMAs
+//   warp 0       issues the MMAs (d = 64: warps 0 and 1, a tile each)
 //   warp 2       walks the share: its segments go to the others through shared memory
 //   warps 4-7    codes -> fp16 tiles K16, V16 [key][channel] in shared memory, straight
 //                from the pages: a warp takes 32 rows of every tile (they lie in one
@@ -59,17 +59,17 @@ struct Cfg {
 
 enum {
   kKFull = 0,   // [2] 128 converting threads
-  kKEmpty = 2,  // [2] the step's QK MMAs
+  kKEmpty = 2,  // [2] each issuer's: the step's QK MMAs
   kVFull = 4,   // [2] 128 converting threads
-  kVEmpty = 6,  // [2] the step's PV MMAs
+  kVEmpty = 6,  // [2] each issuer's: the step's PV MMAs
   kSFull = 8,   // [2 tiles] QK (and every MMA of the tile before it) is done
   kPFull = 10,  // [2 tiles][2 halves] 128 threads: P is there, O rescaled
   kQFull = 14,  // [2 tiles] 128 threads wrote Q
   kOFull = 16,  // [2 tiles] a segment's last PV is done
   kMerge = 18,  // [2] 256 threads: m and l are there; O has been read (dual)
-  kDrain = 20,
+  kDrain = 20,  // every issuer's MMAs
   kSegFull = 21,   // [2] the planning thread
-  kSegEmpty = 23,  // [2] every other thread that works: 1 + 128 + 256
+  kSegEmpty = 23,  // [2] every other thread that works: the issuers, 128 + 256
   kSFree = 25,     // [2 tiles] 128 threads have S in registers (kOwnP)
   kPvDone = 27,    // [2 tiles] a step's PV: P and O are free (kOwnP)
   kNumBars = 29
@@ -134,6 +134,7 @@ __device__ __forceinline__ void write_out32(const PagedArgs& a, size_t row, int 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a) {
   using C = Cfg<D>;
+  constexpr uint32_t kIssuers = C::kOwnP ? 2 : 1;  // threads that issue MMAs
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -152,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
           (i >= kQFull && i < kQFull + 2) || (i >= kSFree && i < kSFree + 2))
         n = 128;
       if (i >= kMerge && i < kMerge + 2) n = 256;
-      if (i >= kSegEmpty && i < kSegEmpty + 2) n = 1 + 128 + 256;
+      if (i >= kSegEmpty && i < kSegEmpty + 2) n = kIssuers + 128 + 256;
+      if ((i >= kKEmpty && i < kKEmpty + 2) || (i >= kVEmpty && i < kVEmpty + 2) || i == kDrain) n = kIssuers;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -194,11 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         if (!ok) *abort_flag = 1;
       }
       __syncwarp();
-    } else if (warp == 0 && elect_one()) {
+    } else if ((warp == 0 || (C::kOwnP && warp == 1)) && elect_one()) {
       // ------------------------------------------------------------ MMA
-      // One thread for both tiles.  With P in S's place its order keeps them half a step apart, so that one
-      // tile's MMAs run under the other's softmax.  (A thread for each lets both wait and
-      // then contend: 1021 us against 910 for 2048 tokens over 32K.)
       constexpr uint32_t idesc_qk = make_idesc(128, kStep, 0, 0);
       constexpr uint32_t idesc_pv = make_idesc(128, D, 0, 0) | kIdescBMnMajor;
       constexpr uint32_t high = desc_high(1024, kSwizzle128B);  // of Q, K16 and V16
@@ -207,9 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       const uint32_t v0 = static_cast<uint32_t>(smem_desc_mn(base + C::kOffV, kStep * 128, 1024));
       constexpr uint32_t tile = C::kTile >> 4;
       bool ok = true;
-      uint32_t it = 0;         // steps done
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // PVs and (kOwnP) QKs of each tile
-      auto ready = [&](int i, uint32_t k) { return mbar_test(bar(i), k & 1); };  // its k-th completion
+      uint32_t it = 0;  // steps done
       auto qk = [&](int t, uint32_t step) {
         const uint32_t qd = q0 + t * tile, kd = k0 + (step & 1) * tile, d = tmem + 128 * t;
         unroll<D / 16>([&](auto k) {
@@ -218,78 +215,77 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
         });
         mma_commit(bar(kSFull + t));
       };
-      for (uint32_t seg = 0;; ++seg) {
-        const PagedSeg* sg;
-        if (!(ok = fetch(seg, sg))) break;
-        const int n = sg->s1 - sg->s0;
-        const bool dual = is_dual(a, *sg);
-        mbar_arrive(bar(kSegEmpty + (seg & 1)));
-        if (n == 0) break;
-        if constexpr (C::kOwnP) {
-          // Whatever is ready first: a tile's QK once S has been read, its PV once P is there
-          ok = wait(kQFull, seg) && wait(kQFull + 1, seg);
-          const int ahead = dual ? 2 : 1;  // to a tile's next step
-          int q[2] = {0, dual ? 1 : 0}, p[2] = {0, dual ? 1 : 0};  // the tiles' next QK and PV
-          bool half[2] = {false, false};                           // PV's first half is issued
-          if (dual && n == 1) mbar_arrive(bar(kOFull + 1));         // no step for tile 1
-          uint32_t idle = 0;
-          unsigned long long since = 0;
-          while (ok && (p[0] < n || p[1] < n)) {
-            bool any = false;
-            unroll<2>([&](auto tile_no) {
-              constexpr int t = decltype(tile_no)::value;
-              const uint32_t qs = it + q[t], ps = it + p[t];
-              if (q[t] < n && q[t] - p[t] < 2 * ahead && ready(kKFull + (qs & 1), qs >> 1) &&
-                  (q[t] < ahead || ready(kSFree + t, nq[t] - 1))) {
-                tc_fence_after();
-                qk(t, qs);
-                if (dual || q[1 - t] > q[t]) mma_commit(bar(kKEmpty + (qs & 1)));
-                q[t] += ahead;
-                ++nq[t];
-                any = true;
-              }
-              if (p[t] < q[t] && p[t] < n) {
-                const uint32_t vd = v0 + (ps & 1) * tile, o = tmem + C::kTmO + D * t,
-                               pc = tmem + C::kTmP + C::kTmPStep * t;
-                if (!half[t] && ready(kVFull + (ps & 1), ps >> 1) && ready(kPFull + 2 * t, np[t])) {
-                  tc_fence_after();
-                  const uint32_t more = p[t] >= ahead ? 1u : 0u;
-                  unroll<4>([&](auto k) {
-                    constexpr int i = decltype(k)::value;
-                    mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, pc, vd, i > 0 ? 1u : more);
-                  });
-                  half[t] = any = true;
-                }
-                if (half[t] && ready(kPFull + 2 * t + 1, np[t])) {
-                  tc_fence_after();
-                  unroll<4>([&](auto k) {
-                    constexpr int i = 4 + decltype(k)::value;
-                    mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, pc, vd, 1u);
-                  });
-                  mma_commit(bar(kPvDone + t));
-                  if (dual || p[1 - t] > p[t]) mma_commit(bar(kVEmpty + (ps & 1)));
-                  p[t] += ahead;
-                  if (p[t] >= n) mma_commit(bar(kOFull + t));
-                  ++np[t];
-                  half[t] = false;
-                  any = true;
-                }
-              }
-            });
-            if (any) {
-              idle = 0;
-            } else if ((++idle & 255u) == 0) {
-              if (idle == 256u) since = cycles();
-              if (*abort_flag) ok = false;
-              if (cycles() - since > kWaitTimeoutCycles) {
-                atomicOr(a.err, kErrTimeout);
-                ok = false;
-              }
-            }
+      // half h (64 keys) of tile t's PV; more: O is added to
+      auto pv = [&](auto h, int t, uint32_t step, uint32_t more) {
+        const uint32_t vd = v0 + (step & 1) * tile;
+        const uint32_t o = tmem + C::kTmO + D * t, p = tmem + C::kTmP + C::kTmPStep * t;
+        unroll<4>([&](auto k) {
+          constexpr int i = 4 * decltype(h)::value + decltype(k)::value;
+          mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
+        });
+      };
+      if constexpr (C::kOwnP) {
+        // A thread for each tile: QK(j + 1) once S has been read, PV(j) once P is there.  (One
+        // thread that looks round for what is ready takes ~500 cycles to see it.)
+        const int t = warp;
+        uint32_t ns = 0, np = 0;  // the tile's QKs and PVs
+        for (uint32_t seg = 0;; ++seg) {
+          const PagedSeg* sg;
+          if (!(ok = fetch(seg, sg))) break;
+          const int n = sg->s1 - sg->s0;
+          const bool dual = is_dual(a, *sg);
+          mbar_arrive(bar(kSegEmpty + (seg & 1)));
+          if (n == 0) break;
+          const int ahead = dual ? 2 : 1;  // to the tile's next step
+          auto release = [&](int i) {      // (both tiles' MMAs, or the one tile's)
+            mma_commit(bar(i));
+            if (dual) mbar_arrive(bar(i));
+          };
+          if (!(ok = wait(kQFull + t, seg))) break;
+          const int first = dual ? t : 0;
+          auto next_qk = [&](int j) {
+            if (j >= n) return true;
+            const uint32_t step = it + j;
+            if (!wait(kKFull + (step & 1), step >> 1) || (j > first && !wait(kSFree + t, ns - 1))) return false;
+            tc_fence_after();
+            qk(t, step);
+            release(kKEmpty + (step & 1));
+            ++ns;
+            return true;
+          };
+          if (first >= n) mbar_arrive(bar(kOFull + t));  // no step for this tile
+          ok = next_qk(first);
+          for (int j = first; ok && j < n; j += ahead) {
+            const uint32_t step = it + j;
+            // (dual: two steps on, K comes after P)
+            if (!dual && !(ok = next_qk(j + ahead))) break;
+            if (!(ok = wait(kVFull + (step & 1), step >> 1) && wait(kPFull + 2 * t, np))) break;  // keys 0 - 63
+            tc_fence_after();
+            pv(Const<0>{}, t, step, j >= ahead ? 1u : 0u);
+            if (!(ok = wait(kPFull + 2 * t + 1, np))) break;  // keys 64 - 127
+            tc_fence_after();
+            pv(Const<1>{}, t, step, 1u);
+            mma_commit(bar(kPvDone + t));
+            release(kVEmpty + (step & 1));
+            if (j + ahead >= n) mma_commit(bar(kOFull + t));
+            ++np;
+            if (dual) ok = next_qk(j + ahead);
           }
+          if (!ok) break;
           it += n;
-        } else {
-          // In turn, which keeps the tiles half a step apart
+        }
+      } else {
+        // One thread for both tiles, in turn: that keeps them half a step apart, so that one
+        // tile's MMAs run under the other's softmax.  (A thread for each lets both wait and
+        // then contend: 1021 us against 910 for 2048 tokens over 32K.)
+        uint32_t np[2] = {0, 0};  // PVs of each tile
+        for (uint32_t seg = 0;; ++seg) {
+          const PagedSeg* sg;
+          if (!(ok = fetch(seg, sg))) break;
+          const int n = sg->s1 - sg->s0;
+          const bool dual = is_dual(a, *sg);
+          mbar_arrive(bar(kSegEmpty + (seg & 1)));
+          if (n == 0) break;
           // the first QK of each tile
           for (int t = 0; ok && t < 2; ++t) {
             if (!(ok = wait(kQFull + t, seg))) break;
@@ -319,20 +315,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
                 return true;
               };
               if (t == t0 && !(ok = wait(kVFull + st, it >> 1))) break;
-              const uint32_t vd = v0 + st * tile;
-              const uint32_t o = tmem + C::kTmO + D * t, p = tmem + C::kTmP + C::kTmPStep * t, more = j >= ahead ? 1u : 0u;
               if (!(ok = wait(kPFull + 2 * t, done))) break;  // keys 0 - 63
               tc_fence_after();
-              unroll<4>([&](auto k) {
-                constexpr int i = decltype(k)::value;
-                mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, i > 0 ? 1u : more);
-              });
+              pv(Const<0>{}, t, it, j >= ahead ? 1u : 0u);
               if (!(ok = wait(kPFull + 2 * t + 1, done))) break;  // keys 64 - 127
               tc_fence_after();
-              unroll<4>([&](auto k) {
-                constexpr int i = 4 + decltype(k)::value;
-                mma_f16_ts_at<8 * i, 128 * i, high, idesc_pv>(o, p, vd, 1u);
-              });
+              pv(Const<1>{}, t, it, 1u);
               if (t == 0) ++np[0];
               else ++np[1];
               if (t == t1 - 1) mma_commit(bar(kVEmpty + st));
@@ -340,13 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
               ok = next_qk();
             }
           }
+          if (!ok) break;
         }
-        if (!ok) break;
       }
+      if (!ok) *abort_flag = 1;
       mma_commit(bar(kDrain));
       volatile int never = 0;
       mbar_wait(bar(kDrain), 0, &never, a.err, kErrTimeout);
-      if (!ok) *abort_flag = 1;
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -355,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
     // Warp w takes rows 32 w .. 32 w + 31 of every tile, K and V of a step in turn, so that
     // each waits for every stage in order.  The eight lanes of a store take four chunks of
     // rows r and r ^ 5, which differ in the swizzle's low and high bit: eight bank groups.
-    constexpr int NB = D / 64, NL = 4 * NB;  // 64-channel blocks; 16-byte loads of a batch a lane
+    constexpr int NB = D / 64;  // 64-channel blocks
     const int w = warp - 4;
     const int cc = lane & 3, u = (lane >> 3) ^ (((lane >> 2) & 1) * 5);  // chunk of a block, row of eight
     const uint32_t dst = base + (32 * w + u) * 128;
@@ -393,12 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
                               (key & ((1 << a.page_shift) - 1)) + u;
         return row * D + 16 * cc;
       };
-      uint4 x[2][NL / 2];  // a tile's rows in two halves of 16
+      // x: d = 128: a tile's rows in two halves of 16; d = 64: K's and V's rows
+      uint4 x[2][4];
       auto load = [&](int h, const uint8_t* pages, long long at, int j) {
         const int left = len - (sg.s0 + j) * kStep - 32 * w - u;
 #pragma unroll
-        for (int k = 0; k < NL / 2; ++k) {
-          const int r = 16 * h + 8 * (k / NB);
+        for (int k = 0; k < 4; ++k) {
+          const int r = (D == 128 ? 16 * h : 0) + 8 * (k / NB);
           x[h][k] = make_uint4(0u, 0u, 0u, 0u);
           // rows behind the sequence may hold any byte: zeros stand in
           if (at >= 0 && r < left) x[h][k] = *reinterpret_cast<const uint4*>(pages + at + r * D + 64 * (k % NB));
@@ -406,36 +395,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
       };
       auto convert = [&](int h, uint32_t tile) {
 #pragma unroll
-        for (int k = 0; k < NL / 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
           uint32_t y[8];
           widen16<E4M3>(x[h][k], y);
-          const uint32_t d = dst + tile + (k % NB) * (128 * 128) + (16 * h + 8 * (k / NB)) * 128;
+          const uint32_t d = dst + tile + (k % NB) * (128 * 128) + ((D == 128 ? 16 * h : 0) + 8 * (k / NB)) * 128;
           sts128(d + c0, y[0], y[1], y[2], y[3]);
           sts128(d + c1, y[4], y[5], y[6], y[7]);
         }
       };
       long long at = place(0);
       load(0, a.k_pages, at, 0);
-      load(1, a.k_pages, at, 0);
+      load(1, D == 128 ? a.k_pages : a.v_pages, at, 0);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t st = it & 1;
         ok = it < 2 || wait(kKEmpty + st, (it >> 1) - 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const uint32_t tk = C::kOffK + st * C::kTile, tv = C::kOffV + st * C::kTile;
-        convert(0, tk);
-        load(0, a.v_pages, at, j);
-        convert(1, tk);
-        load(1, a.v_pages, at, j);
+        const bool more = j + 1 < n;
+        if constexpr (D == 128) {
+          convert(0, tk);
+          load(0, a.v_pages, at, j);
+          convert(1, tk);
+          load(1, a.v_pages, at, j);
+        } else {
+          if (more) at = place(j + 1);
+          convert(0, tk);
+          if (more) load(0, a.k_pages, at, j + 1);
+        }
         fence_proxy_async_smem();
         mbar_arrive(bar(kKFull + st));
-        const bool more = j + 1 < n;
-        if (more) at = place(j + 1);
+        if (D == 128 && more) at = place(j + 1);
         ok = it < 2 || wait(kVEmpty + st, (it >> 1) - 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        convert(0, tv);
-        if (more) load(0, a.k_pages, at, j + 1);
-        convert(1, tv);
-        if (more) load(1, a.k_pages, at, j + 1);
+        if constexpr (D == 128) {
+          convert(0, tv);
+          if (more) load(0, a.k_pages, at, j + 1);
+          convert(1, tv);
+          if (more) load(1, a.k_pages, at, j + 1);
+        } else {
+          convert(1, tv);
+          if (more) load(1, a.v_pages, at, j + 1);
+        }
         fence_proxy_async_smem();
         mbar_arrive(bar(kVFull + st));
       }

@@ -349,7 +349,7 @@ struct PagedSplit {
 PagedSplit paged_split(const qattn_shape* s) {
   PagedSplit t{};
   const int64_t R = s->Hq / s->Hkv * s->Nq;
-  t.tc = R > qattn::kPagedRows;
+  t.tc = R > qattn::kPagedFew;
   t.step = t.tc ? qattn::kPagedTcStep : qattn::kPagedWarpStep;
   t.rows = t.tc ? qattn::kPagedTcRows : R <= 8 ? 8 : qattn::kPagedRows;
   const int64_t blocks = (R + t.rows - 1) / t.rows, heads = s->B * s->Hkv * blocks;

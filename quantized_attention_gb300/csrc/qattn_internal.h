@@ -437,6 +437,7 @@ constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
 
 // ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
 constexpr int kPagedRows = 16;                // most query rows of a KV head in the warp-level kernel
+constexpr int kPagedFew = 16;
 constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
 constexpr int kPagedWarpStep = 64;            // keys of a step
 constexpr int kPagedWarpLead = 8;             // steps that a block's start counts for in equal shares
