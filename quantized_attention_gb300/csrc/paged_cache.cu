@@ -287,10 +287,6 @@ __device__ __forceinline__ void append_page(const PagedAppendArgs& a, const Team
     }
     ok |= 1u << k;
   }
-  if (page < 0 || page >= a.n_pages) {  // no such page: its rows are not written
-    if (team.rank() == 0) atomicOr(a.err, kErrDomain);
-    return;
-  }
   uint8_t* const pages = is_v ? a.v_pages : a.k_pages;
   float* const scales = is_v ? a.v_scales : a.k_scales;
   Raw<8> x[NP];
@@ -301,14 +297,18 @@ __device__ __forceinline__ void append_page(const PagedAppendArgs& a, const Team
   };
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
-    const size_t sc = static_cast<size_t>(page) * a.Hkv + h;
-    const float was = held ? scales[sc] : 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       x[k] = Raw<8>{};
       if (((ok >> k) & 1u) && QATTN_IN_BOUNDS(t0 + rw + per * k < a.T && h < a.Hkv))
         x[k] = load_raw<8>(X + h * sH + (t0 + rw + per * k) * sN, pl);
     }
+    if (page < 0 || page >= a.n_pages) {  // no such page: its rows are not written
+      if (team.rank() == 0) atomicOr(a.err, kErrDomain);
+      return;
+    }
+    const size_t sc = static_cast<size_t>(page) * a.Hkv + h;
+    const float was = held ? scales[sc] : 0.f;
     // the largest magnitude, as bits: NaN lies above infinity, infinity above every number
     uint32_t top = 0;
 #pragma unroll
@@ -412,12 +412,14 @@ __global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendA
     append_page<E4M3, kPageItems, true>(a, Team<true>{red}, b, s, j, is_v, g * a.heads, min(a.Hkv, (g + 1) * a.heads));
     return;
   }
+  // Q: a part of a page's tokens (as many as the CTA has rows of items) and a head group
   g -= 2 * a.kv_groups;
+  constexpr int kParts = 8 * kPageItems / WQ;
   const int items = a.d / WQ, per = blockDim.x / items;
-  // a page's tokens in as many rounds as it takes
-  const int t0 = blockIdx.y << a.page_shift, t1 = min(s.n, t0 + (1 << a.page_shift));
-  for (int t = t0 + threadIdx.x / items; t < t1; t += per)
-    append_q<WQ>(a, b, s, t, threadIdx.x % items, g * a.q_heads, min(a.Hq, (g + 1) * a.q_heads));
+  const int part = g % kParts;
+  g /= kParts;
+  const int t = (blockIdx.y << a.page_shift) + part * per + threadIdx.x / items;
+  append_q<WQ>(a, b, s, t, threadIdx.x % items, g * a.q_heads, min(a.Hq, (g + 1) * a.q_heads));
 }
 
 // A few tokens: a warp a page and head of K or V; then warps that rotate Q, a token and a
@@ -481,9 +483,11 @@ cudaError_t launch_append(PagedAppendArgs a, cudaStream_t s) {
   a.heads = kAppendHeads;
   a.q_heads = kAppendQHeads;
   a.kv_groups = (a.Hkv + a.heads - 1) / a.heads;
-  const dim3 grid(2 * a.kv_groups + (a.q ? (a.Hq + a.q_heads - 1) / a.q_heads : 0), a.touched, a.B);
+  const bool wide = a.rope.rot % 16 == 0;
+  const int parts = 8 * kPageItems / (wide ? 16 : 8);
+  const dim3 grid(2 * a.kv_groups + (a.q ? parts * ((a.Hq + a.q_heads - 1) / a.q_heads) : 0), a.touched, a.B);
   const dim3 block(page * (a.d / 8) / kPageItems);
-  return a.rope.rot % 16 == 0 ? launch_pdl(paged_append_kernel<E4M3, 16>, grid, block, 0, s, a)
+  return wide ? launch_pdl(paged_append_kernel<E4M3, 16>, grid, block, 0, s, a)
                               : launch_pdl(paged_append_kernel<E4M3, 8>, grid, block, 0, s, a);
 }
 }  // namespace

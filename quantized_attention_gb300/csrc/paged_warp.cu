@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tma_prefetch_desc(&tmV);
     }
   }
+  __syncthreads();  // the abort flag is set
   pdl_wait();
   pdl_trigger();
   PagedWalk walk;
@@ -142,8 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool some = true;  // CL: the block has rows
   if constexpr (CL) some = pg_cluster_seg<kRows, kStep>(a, sg);
   else walk = pg_walk<kRows, kStep>(a, blockIdx.x, gridDim.x);
-  if (!CL && threadIdx.x == 0) pg_put_plan(a, walk);
-  __syncthreads();  // the abort flag is set
+  if (!CL && threadIdx.x == kThreads - 32) pg_put_plan(a, walk);  // (the warp with the fewest steps)
   uint32_t used = 0;  // tiles this warp has taken through its ring
   uint32_t sent = 0;  // and issued
 
