@@ -349,7 +349,9 @@ struct PagedSplit {
 PagedSplit paged_split(const qattn_shape* s) {
   PagedSplit t{};
   const int64_t R = s->Hq / s->Hkv * s->Nq;
-  t.tc = R > qattn::kPagedFew;
+  const int64_t few = s->B * s->Hkv * ((R + qattn::kPagedRows - 1) / qattn::kPagedRows);
+  t.tc = R > qattn::kPagedRows &&
+         (R > qattn::kPagedFewRows || few > qattn::kPagedFewWork / std::max<int64_t>(1, s->Nk));
   t.step = t.tc ? qattn::kPagedTcStep : qattn::kPagedWarpStep;
   t.rows = t.tc ? qattn::kPagedTcRows : R <= 8 ? 8 : qattn::kPagedRows;
   const int64_t blocks = (R + t.rows - 1) / t.rows, heads = s->B * s->Hkv * blocks;

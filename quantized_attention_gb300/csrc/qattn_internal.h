@@ -435,19 +435,27 @@ constexpr int kRotateHeads = 4;   // heads a thread turns by the same angles
 constexpr int kAppendFew = 16;    // new tokens of a sequence up to which a warp takes a page
 constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
 
-// ---- paged_warp.cu (paged_common.cuh): qattn_paged_fwd
-constexpr int kPagedRows = 16;                // most query rows of a KV head in the warp-level kernel
-constexpr int kPagedFew = 16;
-constexpr int kPagedWarpCtas = 304;           // its CTAs, at most (two an SM)
-constexpr int kPagedWarpStep = 64;            // keys of a step
-constexpr int kPagedWarpLead = 8;             // steps that a block's start counts for in equal shares
-constexpr int kPagedCluster = 8;              // most CTAs of a block's own cluster
-// More than kPagedRows query rows of a KV head (query heads of the group x tokens): the
-// tensor-core kernel.
-constexpr int kPagedTcRows = 256;             // query rows of its block
-constexpr int kPagedTcStep = 128;
-constexpr int kPagedTcCtas = 152;             // one an SM
-constexpr int kPagedTcLead = 4;
+// ---- paged_warp.cu, paged_tc.cu (paged_common.cuh): qattn_paged_fwd
+// Query rows of a KV head (query heads of the group x tokens) of a block of the warp-level
+// kernel, at most; keys of its step; its CTAs, at most (two an SM: a third, at 168
+// registers a thread, 32 sequences 68 us against 53).
+constexpr int kPagedRows = 16, kPagedWarpStep = 64, kPagedWarpCtas = 304;
+// Steps that a block's start counts for in equal shares (5, 8, 10, 14: 32 sequences of 211
+// to 8191 rows 53.5, 53.2, 53.0, 56.3 us).
+constexpr int kPagedWarpLead = 8;
+constexpr int kPagedCluster = 8;  // most CTAs of a block's own cluster
+// More rows go to the tensor-core kernel, which widens a code once for 256 rows, but takes
+// some 10 us longer to start and to join: up to kPagedFewRows, while the warp-level kernel's
+// blocks have no more than kPagedFewWork keys to pass over in all, that one is the faster.
+// Measured, warp-level against tensor cores, us, with a cold L2, B sequences of L rows, 8 KV
+// heads: d = 128, 64 rows: B = 1, L = 1K (32K keys) 15 / 23, 4K (131K) 19 / 29; B = 16 of 1K
+// (524K) 46 / 42, 1 of 32K (1M) 64 / 52, 16 of 4K (2M) 119 / 83; 32 rows: 4 of 4K (262K) 25 /
+// 39, 64 of 1K (1M) 114 / 101, 16 of 4K (1M) 72 / 84.  d = 64, 64 rows: 1 of 4K 15 / 21, 4 of
+// 4K (524K) 27 / 27, 16 of 1K 35 / 29; 32 rows: 16 of 1K (262K) 21 / 30, 16 of 4K (1M) 57 / 53.
+constexpr int kPagedFewRows = 64;
+constexpr long long kPagedFewWork = 3LL << 17;
+// The tensor-core kernel: rows of a block, keys of a step, CTAs at most, a start's steps.
+constexpr int kPagedTcRows = 256, kPagedTcStep = 128, kPagedTcCtas = 152, kPagedTcLead = 4;
 struct PagedPlan;
 struct PagedArgs {
   int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
