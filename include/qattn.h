@@ -636,8 +636,9 @@ typedef struct {
  *   a page without rows of the sequence before these:  s = fp32(a * fp32(1 / top)),
  *          0 if a < 2^-64
  *   else:  s = its scale, doubled as often as a > fp32(top s) asks (a scale of 0 or
- *          below 2^-100 starts anew, its rows' codes 0); the codes of the rows that were there are divided
- *          along and rounded (half to even; e4m3 as the type rounds)
+ *          below 2^-100 starts anew, its rows' codes 0); the codes of the rows that
+ *          were there are divided along and rounded (half to even; e4m3 as the type
+ *          rounds)
  *   code = clamp(rint(x inv), -127, 127), or e4m3(x inv) saturated;  inv = fp32(1 / s)
  * Doublings keep what an old row loses to rounding below one step in all, however
  * often its page's scale grows.  A page that meets a value that is not finite gets
@@ -671,8 +672,9 @@ qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, con
  * use, or (params->causal) the rows up to p:
  *   t = sm_scale * s_k * (q . kc);  O = sum e^t s_v vc / sum e^t;  lse = log sum e^t
  * q is taken as it is, the codes as they are, sums and statistics are fp32; e^t s_v
- * is rounded once, to fp16, relative to the row's largest (11 bits down to 2^-29 of
- * it, absolute beyond).  V scales lie within 2^-48 and 2^48: a smaller one counts as 0.
+ * is rounded once, to fp16: 11 bits where it is down to 2^-21 of the row's largest,
+ * off by at most 2^-32 of that below.  V scales lie within 2^-48 and 2^48: a smaller
+ * one counts as 0.
  * A row that sees nothing gives O = 0 and lse = -inf; one that sees a key through a
  * scale that is negative or not finite or a V scale above 2^48, or whose q is not
  * finite, gives NaN for both.
@@ -691,7 +693,8 @@ qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, con
  * in 0 .. n_pages - 1 hidden; both are reported: qattn_get_error() returns
  * QATTN_ERR_INVALID_ARG.  Codes of rows in use are numbers (e4m3: no NaN).  Limits: d
  * in {64, 128}, n_pages * Hkv <= 2^31 - 1, T * Hq / Hkv < 2^31 - 256, fewer than 2^31
- * steps of work (of 32 keys x 16 rows or 128 x 128; a block of rows starts as up to 18). */
+ * steps of work (64 keys for 8 or 16 rows of a KV head, or 128 keys for 256; a block of
+ * rows counts for up to 8 more). */
 qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const qattn_shape* shape,
                              const qattn_params* params, const int32_t* lengths,
                              const int32_t* n_new, const qattn_paging* paging,

@@ -353,27 +353,26 @@ __device__ __forceinline__ PagedPlan pg_get_plan(const PagedArgs& a, int c) {
 }
 
 // The join for few rows a block (blockIdx.x: a boundary between shares, as PagedPlan has
-// it): NW warps for a row (blockIdx.y: 4 / NW rows), which
-// take every NW-th share: the weights 2^(m_c - m) of 32 shares come first, one a
-// lane, then the shares' rows in independent loads.
-template <int D, int HEAD, int ROWS, int NW>
+// it; blockIdx.y: a row): four warps for a row, which take every fourth share: the weights
+// 2^(m_c - m) of 32 shares come first, one a lane, then the shares' rows in independent
+// loads.  (A warp for a row: 8 sequences of 16K to 32K rows 72.8 us against 71.4.)
+template <int D, int HEAD, int ROWS>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedArgs a) {
-  constexpr int CPL = D / 32;                    // channels per lane
-  constexpr int RPC = kPgJoinThreads / 32 / NW;  // rows of a CTA
-  __shared__ float sm[RPC][NW], sl[RPC][NW];
-  __shared__ __align__(16) float so[RPC][NW][D];
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW, rw = (threadIdx.x >> 5) / NW;
-  const int r = blockIdx.y * RPC + rw;
+  constexpr int CPL = D / 32;  // channels per lane
+  constexpr int NW = kPgJoinThreads / 32;
+  __shared__ float sm[NW], sl[NW];
+  __shared__ __align__(16) float so[NW][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   const PagedPlan own = pg_get_plan(a, blockIdx.x + 1);
   const int c0 = own.c0, c1 = own.c1;
-  const bool in = own.rb * ROWS + r < own.n * a.G;
-  if (c1 < 0) return;
+  if (c1 < 0 || own.rb * ROWS + r >= own.n * a.G) return;  // (the whole CTA)
   float m = -kPgInf, l = 0.f, o[CPL];
 #pragma unroll
   for (int k = 0; k < CPL; ++k) o[k] = 0.f;
-  for (int cb = c0 + warp; in && cb <= c1; cb += 32 * NW) {
+  for (int cb = c0 + warp; cb <= c1; cb += 32 * NW) {
     const int c = cb + lane * NW;
     const size_t slot = 2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0);
     const bool mine = c <= c1 && QATTN_IN_BOUNDS(slot < a.slots);
@@ -414,24 +413,23 @@ __global__ void __launch_bounds__(kPgJoinThreads) paged_join_kernel(const PagedA
     }
   }
   if (lane == 0) {
-    sm[rw][warp] = m;
-    sl[rw][warp] = l;
+    sm[warp] = m;
+    sl[warp] = l;
   }
 #pragma unroll
-  for (int k = 0; k < CPL; ++k) so[rw][warp][CPL * lane + k] = o[k];
-  if constexpr (NW > 1) __syncthreads();
-  else __syncwarp();
-  const int c = 4 * (NW > 1 ? static_cast<int>(threadIdx.x) : lane);
-  if (in && c < D) {
+  for (int k = 0; k < CPL; ++k) so[warp][CPL * lane + k] = o[k];
+  __syncthreads();
+  const int c = 4 * static_cast<int>(threadIdx.x);
+  if (c < D) {
     float mx = -kPgInf, lt = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[rw][w]);
+    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w]);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float f = sm[rw][w] == -kPgInf ? 0.f : ex2_approx(sm[rw][w] - mx);
-      lt = fmaf(f, sl[rw][w], lt);
-      const float4 y = *reinterpret_cast<const float4*>(&so[rw][w][c]);
+      const float f = sm[w] == -kPgInf ? 0.f : ex2_approx(sm[w] - mx);
+      lt = fmaf(f, sl[w], lt);
+      const float4 y = *reinterpret_cast<const float4*>(&so[w][c]);
       x.x = fmaf(f, y.x, x.x);
       x.y = fmaf(f, y.y, x.y);
       x.z = fmaf(f, y.z, x.z);

@@ -15,7 +15,11 @@
 // the unrounded P in fp32.  Parts of a row (steps of 64 keys dealt to warps, shares of
 // steps dealt to CTAs) are joined by 2^(m_part - m).
 //
-// What it cannot do without: the cache's bytes, 2 D per key and KV head.  The keys are the
+// What it cannot do without: the cache's bytes, 2 D per key and KV head.  32 sequences of
+// 211 to 8191 rows, 8 KV heads of 128 channels (276 MB): 52 us, 5.3 TB/s, 78% of a copy; 8 of
+// 16K to 32K in e4m3 (403 MB): 71 us, 83%.  Between these and the copy lie ~5 us of start
+// (lengths, page numbers, the first tiles: each waits for the one before) and join, and a
+// block's start in the middle of a share.  The keys are the
 // products' M: S^T = K Q^T and O^T = V^T P^T by mma.m16n8k16, so that a decode step's few
 // rows (N, eight at a time) leave no product half empty, and a lane holds 2 rows' worth of
 // everything; P^T turns from result to operand by movmatrix.  The codes are widened in
@@ -34,9 +38,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kPagedWarpStep;
 constexpr int kHead = 15;   // of the exponentials' reference (pg_head)
 constexpr int kTileKeys = 32;
-constexpr int kRing = 4;    // tiles of a warp's ring (K or V of half a step)
-// Shares a block, on average, from which four warps join a row.
-constexpr int kJoinShares = 4;
+// Tiles of a warp's ring (K or V of half a step).  3, 4, 5, 6: 32 sequences 53.3, 53.2, 54.9,
+// 56.5 us; 8 of 16K to 32K rows 71.9, 71.5, 73.3, 74.2.
+constexpr int kRing = 4;
 static_assert(kStep == 2 * kTileKeys, "a step is two tiles of K and two of V");
 
 template <int D, int NB>
@@ -585,10 +589,7 @@ cudaError_t launch_nb(const CUtensorMap& tk, const CUtensorMap& tv, const PagedA
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_warp_kernel<D, E4M3, NB, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
-  const int blocks = a.B * a.Hkv * a.blocks;
-  if (a.ctas < kJoinShares * blocks)  // a block in few shares: a warp for a row
-    return launch_pdl(paged_join_kernel<D, kHead, kRows, 1>, dim3(a.ctas - 1, kRows / 4), dim3(kPgJoinThreads), 0, s, a);
-  return launch_pdl(paged_join_kernel<D, kHead, kRows, 4>, dim3(a.ctas - 1, kRows), dim3(kPgJoinThreads), 0, s, a);
+  return launch_pdl(paged_join_kernel<D, kHead, kRows>, dim3(a.ctas - 1, kRows), dim3(kPgJoinThreads), 0, s, a);
 }
 template <int D, bool E4M3>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {

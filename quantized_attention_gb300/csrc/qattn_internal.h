@@ -431,9 +431,17 @@ struct PagedAppendArgs {
   int heads, kv_groups, q_heads, touched;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
-constexpr int kRotateHeads = 4;   // heads a thread turns by the same angles
-constexpr int kAppendFew = 16;    // new tokens of a sequence up to which a warp takes a page
-constexpr int kFewQHeads = 8, kAppendHeads = 1, kAppendQHeads = 8;
+// Heads a thread turns by the same angles: more save angles, fewer make more CTAs (4 against
+// 8, 32 heads, cold L2: 512 / 2K / 4K / 8K / 16K tokens 10.9 / 12.9 / 21.1 / 33.4 / 55.9 us
+// against 12.9 / 15.0 / 19.1 / 31.4 / 55.9).
+constexpr int kRotateHeads = 4;
+// New tokens of a sequence up to which a warp takes a page of a head, not a CTA.  Measured, 1,
+// 16 and 64 sequences of 8 KV heads, us: 4 tokens 8.9 / 10.9 / 10.9 against 13.0 / 13.0 / 19.1, 16
+// tokens 13.0 / 15.0 / 21.2 against 12.9 / 15.0 / 21.2.
+constexpr int kAppendFew = 16;
+// Q heads of a warp or CTA, KV heads of a CTA (uneven prompts: 8 and 1, 61 us; 4 and 1, 66;
+// 8 and 2, 62).
+constexpr int kFewQHeads = 8, kAppendQHeads = 8, kAppendHeads = 1;
 
 // ---- paged_warp.cu, paged_tc.cu (paged_common.cuh): qattn_paged_fwd
 // Query rows of a KV head (query heads of the group x tokens) of a block of the warp-level
@@ -454,7 +462,9 @@ constexpr int kPagedCluster = 8;  // most CTAs of a block's own cluster
 // 4K (524K) 27 / 27, 16 of 1K 35 / 29; 32 rows: 16 of 1K (262K) 21 / 30, 16 of 4K (1M) 57 / 53.
 constexpr int kPagedFewRows = 64;
 constexpr long long kPagedFewWork = 3LL << 17;
-// The tensor-core kernel: rows of a block, keys of a step, CTAs at most, a start's steps.
+// The tensor-core kernel: rows of a block, keys of a step, CTAs at most (one an SM), steps
+// that a block's start counts for (2, 4, 8: a few tokens of 8 sequences 50.4, 45.9, 46.6 us,
+// uneven prompts 148.5, 145.3, 150.8).
 constexpr int kPagedTcRows = 256, kPagedTcStep = 128, kPagedTcCtas = 152, kPagedTcLead = 4;
 struct PagedPlan;
 struct PagedArgs {
