@@ -784,15 +784,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
 }
 
 // The join: CTAs (c, y) work for the boundary between the shares of CTAs c and c + 1, if
-// it is the first one inside a block (PagedPlan).  A lane for a row, a warp for four channels of it
-// (blockIdx.y: 32 rows, then 16 channels), so that every load of a share takes 512
+// it is the first one inside a block (PagedPlan).  A lane for a row, a warp for four channels
+// of it (blockIdx.y: 16 channels, then 32 rows), so that every load of a share takes 512
 // consecutive bytes; eight shares' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_rows_kernel(const PagedArgs a) {
   constexpr int U = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = 32 * (blockIdx.y % (kRows / 32)) + lane;
-  const int c = 4 * (4 * (blockIdx.y / (kRows / 32)) + warp);
+  const int r = 32 * (blockIdx.y / (D / 16)) + lane;
+  const int c = 4 * (4 * (blockIdx.y % (D / 16)) + warp);
   pdl_wait();
   pdl_trigger();
   const PagedPlan w = pg_get_plan(a, blockIdx.x + 1);
@@ -842,7 +842,8 @@ cudaError_t launch_d(const PagedArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_tc_kernel<D, E4M3>, dim3(a.ctas), dim3(kThreads), smem, s, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
-  return launch_pdl(paged_join_rows_kernel<D>, dim3(a.ctas - 1, (kRows / 32) * (D / 16)), dim3(kPgJoinThreads), 0, s, a);
+  const int groups = (min(kRows, a.G * a.T) + 31) / 32;  // of 32 rows, in the longest block
+  return launch_pdl(paged_join_rows_kernel<D>, dim3(a.ctas - 1, groups * (D / 16)), dim3(kPgJoinThreads), 0, s, a);
 }
 
 }  // namespace

@@ -589,7 +589,8 @@ cudaError_t launch_nb(const CUtensorMap& tk, const CUtensorMap& tv, const PagedA
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_warp_kernel<D, E4M3, NB, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
-  return launch_pdl(paged_join_kernel<D, kHead, kRows>, dim3(a.ctas - 1, kRows), dim3(kPgJoinThreads), 0, s, a);
+  return launch_pdl(paged_join_kernel<D, kHead, kRows>, dim3(a.ctas - 1, min(kRows, a.G * a.T)),
+                    dim3(kPgJoinThreads), 0, s, a);
 }
 template <int D, bool E4M3>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {
