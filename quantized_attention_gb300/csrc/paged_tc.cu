@@ -1,23 +1,34 @@
-// Attention over a paged 8-bit KV cache (qattn_paged_fwd), for more than 16 query rows
-// of a KV head: on the 5th-generation tensor cores.  Mathematics as in paged_warp.cu.
+// Attention over a paged 8-bit KV cache (qattn_paged_fwd), for many query rows of a KV head
+// (kPagedFewRows): on the 5th-generation tensor cores.  Mathematics as in paged_warp.cu.
 //
 // A CTA works on a block of 256 query rows (two tiles of 128) in steps of 128 keys:
 //   warp 0       issues the MMAs (d = 64: warps 0 and 1, a tile each)
 //   warp 2       walks the share: its segments go to the others through shared memory
 //   warps 4-7    codes -> fp16 tiles K16, V16 [key][channel] in shared memory, straight
 //                from the pages: a warp takes 32 rows of every tile (they lie in one
-//                page), the next step's loads in flight
+//                page), the next half tile's (d = 64: the next step's) loads in flight
 //   warps 8-11   softmax of tile 0, warps 12-15 of tile 1: a thread a row
 // Per tile and step: S = Q K16^T (both in shared memory), P = 2^(t - m) rounded to fp16
 // in place of S, O += P V16 (P in TMEM, V16 as it lies: the B operand with its N index
 // fastest).  TMEM: S0, S1 and O0, O1, 512 columns at d = 128, so P lies in S's columns
 // and a tile's QK follows its PV; the other tile's MMAs run under a tile's softmax.  The
 // issuing order PV(0, j), QK(0, j + 1), PV(1, j), QK(1, j + 1) makes one barrier do for
-// "S is there", "O is done" and "P has been read".
+// "S is there", "O is done" and "P has been read".  d = 64 leaves room for a P beside S: a
+// tile's next QK follows the moment S has been read.
 // A block of at most 128 rows gives both tiles the same rows and every other step each
 // (dual); their parts are joined from TMEM at the end.
 // Codes widened once serve 256 rows: 64 KB written and 192 KB read by the MMAs a step,
-// ~2050 cycles of shared memory against as many of tensor work.
+// ~2050 cycles of shared memory against as many of tensor work (d = 128).
+//
+// What bounds it.  d = 128, 2048 tokens of 32 heads on 8 at the end of 32K rows: 758 us,
+// 1.41 PFLOP/s, 73% of a bf16 matrix product's rate; ~3450 cycles a step, of which the tensor
+// pipe works 62%: shared memory, which conversion and MMAs share, and a tile's softmax
+// between its QK and its PV.  d = 64, four whole prompts of 1.4K to 4.1K tokens, 12 heads:
+// 146 us, 455 TFLOP/s: the two softmax warps of a scheduler take ~3850 cycles a step for what
+// is 1020 of exponentials, with 192 registers each too few instructions in flight (46% of the
+// issue slots used); per block ~9K cycles to bring Q and to write O.  Dual: the converting
+// warps, ~2000 cycles a step at d = 64 and ~3300 at d = 128; a few tokens of 8 sequences of 1K
+// to 16K rows, d = 64: 44 us, 1.6 TB/s.
 // The reference m is set 7 below a row's maximum and moves only when that has grown by
 // another 8 (P stays at or below 2^15), so O is rarely rescaled: P keeps its eleven bits
 // where P s_v is down to 2^-21 of the row's largest, and is off by at most 2^-32 of it.
