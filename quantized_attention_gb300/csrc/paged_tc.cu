@@ -24,7 +24,7 @@
 // 1.41 PFLOP/s, 73% of a bf16 matrix product's rate; ~3450 cycles a step, of which the tensor
 // pipe works 62%: shared memory, which conversion and MMAs share, and a tile's softmax
 // between its QK and its PV.  d = 64, four whole prompts of 1.4K to 4.1K tokens, 12 heads:
-// 146 us, 455 TFLOP/s: the two softmax warps of a scheduler take ~3850 cycles a step for what
+// 144 us, 460 TFLOP/s: the two softmax warps of a scheduler take ~3850 cycles a step for what
 // is 1020 of exponentials, with 192 registers each too few instructions in flight (46% of the
 // issue slots used); per block ~9K cycles to bring Q and to write O.  Dual: the converting
 // warps, ~2000 cycles a step at d = 64 and ~3300 at d = 128; a few tokens of 8 sequences of 1K
@@ -797,10 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
 // The join: CTAs (c, y) work for the boundary between the shares of CTAs c and c + 1, if
 // it is the first one inside a block (PagedPlan).  A lane for a row, a warp for four channels
 // of it (blockIdx.y: 16 channels, then 32 rows), so that every load of a share takes 512
-// consecutive bytes; eight shares' loads in flight.
+// consecutive bytes; four shares' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(kPgJoinThreads) paged_join_rows_kernel(const PagedArgs a) {
-  constexpr int U = 8;
+  constexpr int U = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = 32 * (blockIdx.y / (D / 16)) + lane;
   const int c = 4 * (4 * (blockIdx.y % (D / 16)) + warp);
