@@ -685,7 +685,7 @@ qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, con
  *   lengths        int32 [B], device, 0 .. Nk
  *   n_new          NULL (T everywhere), or int32 [B], device, 0 .. T
  *   O, lse (out)   [B][Hq][T][d] and (nullable) fp32 [B][Hq][T]; rows t >= n_new[b]
- *                  are left as they were
+ *                  are left as they were.  They overlap no input
  *   workspace      at least qattn_paged_workspace_size() bytes; calls that may
  *                  overlap need one each
  * The order of the additions depends on the shape and the lengths alone: equal calls

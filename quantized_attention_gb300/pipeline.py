@@ -505,6 +505,18 @@ class PagedCache:
         self._new.copy_(torch.tensor(n, dtype=torch.int32))
         self._upload(stream)
 
+    def _shrink(self, n, stream):
+        """Take the last grow back, its pages in the order in which they lay in the pool."""
+        page = self.paging.page_size
+        for b, x in reversed(list(enumerate(n))):
+            have = int(self._len[b])
+            s, e = -(-(have - x) // page), -(-have // page)
+            self._free.extend(reversed(self._pt[b, s:e].tolist()))
+            self._pt[b, s:e] = -1
+            self._len[b] = have - x
+            self._new[b] = 0
+        self._upload(stream)
+
     def release(self, b, stream=None):
         """Sequence b is done: its pages go back to the pool."""
         used = -(-int(self._len[b]) // self.paging.page_size)
@@ -552,9 +564,17 @@ class PagedCache:
     def step(self, Q, K, V, n_new=None, stream=None):
         """grow, append and attend: Q bf16 [B, Hq, T, d], K, V bf16 [B, Hkv, T, d] (any
         strides), n_new: tokens of each sequence (host numbers; None: T each).  Rows
-        behind a sequence's tokens in the returned O are left as they were."""
-        self.grow([Q.shape[2]] * self._dims[0] if n_new is None else n_new, stream)
-        return self.attend(self.append(Q, K, V, stream), stream)
+        behind a sequence's tokens in the returned O are left as they were.  Arguments
+        that are refused leave the sequences as they were."""
+        n = [Q.shape[2]] * self._dims[0] if n_new is None else [int(x) for x in n_new]
+        if max(n, default=0) > Q.shape[2]:
+            raise ValueError(f"n_new: more tokens than the {Q.shape[2]} of Q")
+        self.grow(n, stream)
+        try:
+            return self.attend(self.append(Q, K, V, stream), stream)
+        except Exception:
+            self._shrink(n, stream)
+            raise
 
 
 def problem_for(wl, **kw) -> Problem:

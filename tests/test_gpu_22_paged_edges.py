@@ -226,3 +226,60 @@ def test_a_step_on_another_stream_than_the_inputs():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got, want)
     assert qb.get_error() == 0
+
+
+def test_a_refused_step_leaves_the_sequences():
+    B, Hq, Hkv, d = 2, 4, 2, 64
+    C, E = (PagedCache(12, 32, Hq, Hkv, d, B, 128, rope=qb.make_rope(rope_table(128, d)), out_dtype=qb.DT_F32)
+            for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def new(T):
+        return [torch.randn(B, h, T, d, generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv)]
+
+    x = new(40)
+    for c in (C, E):
+        c.step(*x, n_new=[40, 3])
+    Q, K, V = new(30)
+    for bad, error in (((Q, K.float(), V), TypeError), ((Q, K, V[:, :1]), ValueError), ((Q, K[:, :, :29], V), ValueError)):
+        with pytest.raises(error):
+            C.step(*bad)
+        assert C.free_pages() == E.free_pages() and C.rows(0) == 40 and C.rows(1) == 3
+        assert torch.equal(C.page_table, E.page_table) and torch.equal(C.lengths, E.lengths)
+    with pytest.raises(ValueError, match="n_new"):
+        C.step(Q, K, V, n_new=[31, 1])
+    assert C.rows(0) == 40
+    assert torch.equal(C.step(Q, K, V), E.step(Q, K, V)) and torch.equal(C.k_pages, E.k_pages)
+    assert qb.get_error() == 0
+
+
+def test_a_cache_without_rows():
+    """Nk = 0: nothing is seen, whatever the pool holds."""
+    P = Pool(43, 2, 2, 64, 32, "e4m3", 32)
+    for T in (1, 30):
+        shape, params = qb.make_shape(2, 8, 2, T, 0, 64), qb.make_params(causal=True, out_dtype=qb.DT_F32)
+        paging = qb.make_paging(P.n, 32, 1)
+        paging.code_dtype = qb.DT_E4M3
+        O, lse = torch.full((2, 8, T, 64), 7.0, device="cuda"), torch.full((2, 8, T), 7.0, device="cuda")
+        ws = torch.full((max(qb.paged_workspace_size(shape, params, paging), 256),), 0xFF, dtype=torch.uint8, device="cuda")
+        q = torch.randn(2, 8, T, 64, device="cuda").to(torch.bfloat16)
+        pt = torch.full((2, 1), -1, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+        qb.paged_fwd(q, shape, params, paging, pt, lens, *P.arrays(), O, lse, ws)
+        assert qb.get_error() == 0 and (O == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("T", [3, 50], ids=str)
+def test_append_rotates_q_in_place(T):
+    P = Pool(44, 2, 2, 128, 64, "int8", 64)
+    tab = R.table(64, 128)
+    K, V, Q = (tokens(P.rng, 2 * h, T, 128).reshape(2, h, T, 128) for h in (2, 2, 6))
+    q, lens = dev(Q, torch.bfloat16), np.full(2, T, np.int32)
+    got = P.arrays()
+    qb.paged_append(dev(K, torch.bfloat16), dev(V, torch.bfloat16), qb.make_shape(2, 6, 2, T, 64, 128), P.paging,
+                    P.table(lens), dev(lens), *got, rope=qb.make_rope(dev(tab), interleaved=True), Q=q, Q_out=q)
+    pos = np.arange(T)
+    for b in range(2):
+        P.put(b, 0, R.rotate(K[b], pos, tab, True), V[b])
+    assert qb.get_error() == 0 and same_bits(got, P.arrays())
+    assert torch.equal(q, dev(np.stack([R.rotate(Q[b], pos, tab, True) for b in range(2)]), torch.bfloat16))
