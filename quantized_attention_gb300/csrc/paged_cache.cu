@@ -401,9 +401,9 @@ __device__ __forceinline__ void append_q(const PagedAppendArgs& a, int b, const 
   }
 }
 
-// Many tokens: a CTA a page and KV head (x: kind and head group, y: page, z: sequence);
-// then, behind a.kv_groups, CTAs that rotate Q, a part of a page's tokens and a head group
-// each.  Four prompts of 1.4K to 4.1K tokens, 32 + 2 x 8 heads of 128 channels, 252 MB: 59 us,
+// Many tokens (y: page, z: sequence): x begins with CTAs that rotate Q, a part of a page's
+// tokens and a head group each, the larger pieces (last: 1 to 2% slower); then a CTA a kind and
+// KV head.  Four prompts of 1.4K to 4.1K tokens, 32 + 2 x 8 heads of 128 channels, 252 MB: 59 us,
 // 4.3 TB/s (63%).  Q alone would take 34 us at the rate of the rotation; K and V, 67 MB, are
 // bound by latency: a CTA's way from the lengths to the rows, the maximum over the page, the
 // codes, with two CTAs an SM at 64 registers (three, which spill: 74 us).
@@ -416,8 +416,9 @@ __global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendA
   const int b = blockIdx.z;
   const NewRows s = new_rows(a, b, threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0);
   if (s.n == 0) return;
-  int g = blockIdx.x;
-  if (g < 2 * a.kv_groups) {
+  const int q_ctas = gridDim.x - 2 * a.kv_groups;
+  int g = static_cast<int>(blockIdx.x) - q_ctas;
+  if (g >= 0) {
     const bool is_v = g >= a.kv_groups;
     if (is_v) g -= a.kv_groups;
     const int j = (s.first >> a.page_shift) + blockIdx.y;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendA
     return;
   }
   // Q: a part of a page's tokens (as many as the CTA has rows of items) and a head group
-  g -= 2 * a.kv_groups;
+  g = blockIdx.x;
   constexpr int kParts = 8 * kPageItems / WQ;
   const int items = a.d / WQ, per = blockDim.x / items;
   const int part = g % kParts;
