@@ -33,8 +33,6 @@
 namespace qattn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = kPagedWarpStep;
 constexpr int kHead = 15;   // of the exponentials' reference (pg_head)
 constexpr int kTileKeys = 32;
@@ -43,11 +41,11 @@ constexpr int kTileKeys = 32;
 constexpr int kRing = 4;
 static_assert(kStep == 2 * kTileKeys, "a step is two tiles of K and two of V");
 
-template <int D, int NB>
+template <int D, int NB, int W>
 struct WarpSmem {
   static constexpr int kTile = kTileKeys * D;
   static constexpr int kWarp = kRing * kTile;    // one warp's ring
-  static constexpr int kShare = kWarps * kWarp;  // a CTA's O
+  static constexpr int kShare = W * kWarp;       // a CTA's O
   static constexpr int kBytes = kShare + 8 * NB * D * 4 + 1024;
   static_assert(8 * NB * D * 4 <= kWarp, "a warp's O does not fit its ring");
 };
@@ -108,23 +106,24 @@ struct Window {
 // ------------------------------------------------------------------ attention
 // Each CTA takes an equal share of the flattened list of steps (sequence, KV head,
 // row block, step), or (CL) its part of its cluster's block.  Each run of steps
-// inside one block is a segment; its steps go round the four warps, each with its own
+// inside one block is a segment; its steps go round the W warps, each with its own
 // ring of TMA tiles and its own (m, l, O), so the main loop has no CTA barrier.
 // NB: eights of rows of a block.  A lane (g, t4) holds rows 2 t4 and 2 t4 + 1 of each eight
 // in its results, row g of it in the products' N operands.
-template <int D, bool E4M3, int NB, bool CL>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, bool E4M3, int NB, bool CL, int W>
+__global__ void __launch_bounds__(32 * W, W == 4 ? 2 : 1)
     paged_warp_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedArgs a) {
-  using SM = WarpSmem<D, NB>;
+  using SM = WarpSmem<D, NB, W>;
+  constexpr int kThreads = 32 * W;
   constexpr int kRows = 8 * NB;
   constexpr int KS = D / 16;   // k-steps of K Q^T = words of K a lane holds per key
   constexpr int MT = D / 16;   // m-tiles of V^T P^T
   constexpr int VW = D / 32;   // V words a lane reads per key: channels 4 VW g ..
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t full[kWarps][kRing];
-  __shared__ float red_m[kWarps][kRows], red_l[kWarps][kRows];
+  __shared__ __align__(8) uint64_t full[W][kRing];
+  __shared__ float red_m[W][kRows], red_l[W][kRows];
   __shared__ float cl_m[kRows], cl_l[kRows];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,10 +152,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   while (CL ? some : pg_next<kRows, kStep>(a, walk, sg)) {
     const int len = sg.seq.len;
-    // this warp's steps: sg.s0 + warp, + kWarps, ...
+    // this warp's steps: sg.s0 + warp, + W, ...
     const int first = sg.s0 + warp;
-    const int nstep = first < sg.s1 ? (sg.s1 - first + kWarps - 1) / kWarps : 0;
-    auto key_of = [&](int i) { return (first + i * kWarps) * kStep; };
+    const int nstep = first < sg.s1 ? (sg.s1 - first + W - 1) / W : 0;
+    auto key_of = [&](int i) { return (first + i * W) * kStep; };
     auto look_up = [&](int i0) {  // the window of steps i0 .. i0 + 15
       Window w{-1, 0.f, 0.f};
       const int i = i0 + (lane >> 1);
@@ -455,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) break;
     }
 
-    // ---- join the four warps (their rings are free)
+    // ---- join the warps (their rings are free)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = 8 * nb + 2 * t4 + r;
         float mx = -kPgInf;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w][row]);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, red_m[w][row]);
         const float f = (m[nb][r] == -kPgInf) ? 0.f : ex2_approx(m[nb][r] - mx);
         // channels 4 VW g + 2 p, + 1 are the slots g and g + 8 of m-tile p
 #pragma unroll
@@ -505,10 +504,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int r = idx / (D / 4), c = 4 * (idx % (D / 4));
       float mx = -kPgInf, lt = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w][r]);
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, red_m[w][r]);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float mw = red_m[w][r];
         lt += (mw == -kPgInf) ? 0.f : red_l[w][r] * ex2_approx(mw - mx);
         const float4 y =
@@ -575,19 +574,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+template <int D, bool E4M3, int NB, int W>
+cudaError_t launch_clusters(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {
+  constexpr int smem = WarpSmem<D, NB, W>::kBytes;
+  const auto kernel = paged_warp_kernel<D, E4M3, NB, true, W>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e != cudaSuccess ? e : launch_pdl_cluster(kernel, dim3(a.ctas), dim3(32 * W), a.cluster, smem, s, tk, tv, a);
+}
 template <int D, bool E4M3, int NB>
 cudaError_t launch_nb(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a, cudaStream_t s) {
-  constexpr int smem = WarpSmem<D, NB>::kBytes, kRows = 8 * NB;
-  cudaError_t e;
-  if (a.cluster > 0) {
-    e = cudaFuncSetAttribute(paged_warp_kernel<D, E4M3, NB, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(paged_warp_kernel<D, E4M3, NB, true>, dim3(a.ctas), dim3(kThreads), a.cluster, smem, s,
-                              tk, tv, a);
-  }
-  e = cudaFuncSetAttribute(paged_warp_kernel<D, E4M3, NB, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (a.cluster > 0)
+    return a.wide ? launch_clusters<D, E4M3, NB, 8>(tk, tv, a, s) : launch_clusters<D, E4M3, NB, 4>(tk, tv, a, s);
+  constexpr int W = 4, smem = WarpSmem<D, NB, W>::kBytes, kRows = 8 * NB;
+  const auto kernel = paged_warp_kernel<D, E4M3, NB, false, W>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(paged_warp_kernel<D, E4M3, NB, false>, dim3(a.ctas), dim3(kThreads), smem, s, tk, tv, a);
+  e = launch_pdl(kernel, dim3(a.ctas), dim3(32 * W), smem, s, tk, tv, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
   return launch_pdl(paged_join_kernel<D, kHead, kRows>, dim3(a.ctas - 1, min(kRows, a.G * a.T)),
                     dim3(kPgJoinThreads), 0, s, a);

@@ -341,7 +341,7 @@ qattn_status tree_shape_ok(const qattn_shape* shape) {
 
 // qattn_paged_fwd's split, as TreeSplit.
 struct PagedSplit {
-  bool tc;
+  bool tc, wide;
   int cluster, step, rows, blocks, ctas, lead;
   int64_t steps;
   size_t slots, off_m, off_l, off_plan, bytes;
@@ -359,11 +359,14 @@ PagedSplit paged_split(const qattn_shape* s) {
   t.blocks = static_cast<int>(blocks);
   t.lead = t.tc ? qattn::kPagedTcLead : qattn::kPagedWarpLead;
   t.steps = heads * (t.lead + head_steps);
-  t.cluster = t.tc ? 0 : qattn::tree_cluster(heads, 2 * head_steps);  // (its steps are half as long)
+  const bool wide = heads * qattn::kPagedCluster <= qattn::kPagedWideCtas && head_steps <= qattn::kPagedWideSteps;
+  // (tree_cluster's steps are half as long)
+  t.cluster = t.tc ? 0 : wide ? qattn::kPagedCluster : qattn::tree_cluster(heads, 2 * head_steps);
   const int64_t most = t.tc ? qattn::kPagedTcCtas : qattn::kPagedWarpCtas;
   t.ctas = static_cast<int>(std::max<int64_t>(1, std::min(most, t.tc ? t.steps : (t.steps + 3) / 4)));
   if (t.cluster > 0) {
     t.ctas = static_cast<int>(heads * t.cluster);
+    t.wide = wide && head_steps > 4 * t.cluster;  // (else four warps have a step each at most)
     t.lead = 0;
   }
   t.slots = t.cluster > 0 ? 0 : 2 * static_cast<size_t>(t.ctas);
@@ -1420,6 +1423,7 @@ qattn_status qattn_paged_fwd(const uint16_t* Q, const int64_t* q_strides, const 
   a.e4m3 = paging->code_dtype == QATTN_E4M3;
   a.blocks = sp.blocks;
   a.rows = sp.rows;
+  a.wide = sp.wide;
   a.causal = params->causal;
   a.sm_scale = sm_scale_of(shape, params);
   a.q = Q;

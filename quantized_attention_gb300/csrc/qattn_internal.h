@@ -452,6 +452,14 @@ constexpr int kPagedRows = 16, kPagedWarpStep = 64, kPagedWarpCtas = 304;
 // to 8191 rows 53.5, 53.2, 53.0, 56.3 us).
 constexpr int kPagedWarpLead = 8;
 constexpr int kPagedCluster = 8;  // most CTAs of a block's own cluster
+// As many blocks as the chip places clusters of 8 for with one CTA an SM take those, eight
+// warps a CTA, up to as many steps; else tree_cluster (which see) decides between clusters and
+// shares, four warps a CTA.  Measured, one token, 8 KV heads of 2K / 4K / 8K / 12K / 16K rows, us in a
+// replayed graph: d = 128: eight warps 7.4 / 9.3 / 10.9 / 13.4 / 15.9, four 7.5 / 10.3 / 13.0 / 16.5 /
+// 20.0, shares 9.8 / 11.0 / 11.8 / 15.5 / 15.9; d = 64: 6.1 / 7.6 / 8.4 / 10.2 / 12.5, 6.1 / 8.7 /
+// 10.2 / 13.1 / 16.3, 8.6 / 9.7 / 10.9 / 12.3 / 13.5.  (Of two sequences of uneven length shares
+// would be faster from 8K on: the bound lies between.)
+constexpr int kPagedWideCtas = 64, kPagedWideSteps = 192;
 // More rows go to the tensor-core kernel, which widens a code once for 256 rows, but takes
 // some 10 us longer to start and to join: up to kPagedFewRows, while the warp-level kernel's
 // blocks have no more than kPagedFewWork keys to pass over in all, that one is the faster.
@@ -471,6 +479,7 @@ struct PagedArgs {
   int B, Hq, Hkv, G, T, Nk, d;    // G = Hq / Hkv; Nk: most rows in use
   int n_pages, page_shift, max_pages, e4m3;
   int blocks, rows;               // row blocks of a KV head, at most; rows of a block
+  int wide;                       // clusters of CTAs of eight warps, not four
   int causal;
   float sm_scale;
   const uint16_t* q;              // bf16, element strides

@@ -26,7 +26,7 @@ class Call:
         B, Hq, T, d = P.q.shape
         width = -(-Nk // P.page)
         self.pt = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
-        t = P.table(P.lens)
+        t = P.table(P.lens)[:, :width]
         self.pt[:, :t.shape[1]] = t
         self.shape = qb.make_shape(B, Hq, P.Hkv, T, Nk, d)
         self.params = qb.make_params(causal=causal, out_dtype=qb.DT_F32)
@@ -62,7 +62,7 @@ FEW = [
 
 
 @pytest.mark.parametrize("shape", FEW, ids=[f"{s[5]}-{s[1] // s[2] * s[6]}rows-d{s[3]}" for s in FEW])
-@pytest.mark.parametrize("bound", [2048, 1 << 19], ids=["short", "long"])
+@pytest.mark.parametrize("bound", [2048, 8192, 1 << 19], ids=["short", "middling", "long"])
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "all"])
 def test_few_rows_of_a_short_and_of_a_long_cache(shape, bound, causal):
     P = make(31, *shape)
@@ -124,6 +124,17 @@ def test_a_prefix_in_two_sequences():
     O, lse = run(P)
     assert qb.get_error() == 0 and torch.equal(O[0], O[1]) and torch.equal(lse[0], lse[1])
     check(P, O, lse)
+
+
+@pytest.mark.parametrize("Nk", [4160, 12288, 12352])
+@pytest.mark.parametrize("Hkv,d,code", [(8, 128, "int8"), (3, 64, "e4m3")])
+def test_one_long_sequence(Nk, Hkv, d, code):
+    """Up to eight KV heads of one sequence around the bound to which they take wide clusters."""
+    for L in (Nk, Nk - 63, 33):
+        P = make(37, 1, 2 * Hkv, Hkv, d, 64, code, 2, [L])
+        O, lse = run_bound(P, Nk)
+        assert qb.get_error() == 0
+        check(P, O, lse)
 
 
 @pytest.mark.parametrize("T", [1, 6, 90], ids=str)
