@@ -458,7 +458,10 @@ constexpr int kPagedCluster = 8;  // most CTAs of a block's own cluster
 // replayed graph: d = 128: eight warps 7.4 / 9.3 / 10.9 / 13.4 / 15.9, four 7.5 / 10.3 / 13.0 / 16.5 /
 // 20.0, shares 9.8 / 11.0 / 11.8 / 15.5 / 15.9; d = 64: 6.1 / 7.6 / 8.4 / 10.2 / 12.5, 6.1 / 8.7 /
 // 10.2 / 13.1 / 16.3, 8.6 / 9.7 / 10.9 / 12.3 / 13.5.  (Of two sequences of uneven length shares
-// would be faster from 8K on: the bound lies between.)
+// would be faster from 8K on: the bound lies between.)  tree_cluster's choice here, clusters against
+// shares, us with a cold L2, d = 128: 16 heads of 2K / 4K / 8K 13 / 17 / 21 against 17 / 19 / 23; 64 of
+// 500 / 4K / 16K 13 / 25 / 62 against 17 / 30 / 66, of 0.2 to 16K 48 / 43; 128 of 4K / 8K 40 / 62 against
+// 44 / 68, of 0.2 to 16K 85 / 69; 256 of 500 / 2K 17 / 38 against 24 / 42.
 constexpr int kPagedWideCtas = 64, kPagedWideSteps = 192;
 // More rows go to the tensor-core kernel, which widens a code once for 256 rows, but takes
 // some 10 us longer to start and to join: up to kPagedFewRows, while the warp-level kernel's
