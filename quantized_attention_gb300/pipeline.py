@@ -444,7 +444,8 @@ class PagedCache:
     the device in step by one copy (which waits until the host's numbers are read);
     ``append`` and ``attend`` wait for nothing and can be captured in a graph, replayed
     after each ``grow`` (grow is not captured).  All calls go to the current stream
-    (or ``stream``)."""
+    (or ``stream``); calls on several streams are ordered by the caller, the
+    constructor's among them, and the cache is kept until those streams are done with it."""
 
     def __init__(self, n_pages, page_size, Hq, Hkv, d, B, max_rows, *, code_dtype=qb.DT_I8, rope=None,
                  out_dtype=qb.DT_BF16, sm_scale=0.0, device="cuda"):
@@ -526,24 +527,25 @@ class PagedCache:
         self._new[b] = 0
         self._upload(stream)
 
-    def _buffers(self, T):
-        """Shape, output buffers and workspace of steps of up to T tokens."""
+    def _buffers(self, T, stream=None):
+        """Shape, output buffers and workspace of steps of T tokens."""
         if T not in self._steps:
             B, Hq, Hkv, d = self._dims
             dev = self._meta.device
             shape = qb.make_shape(B, Hq, Hkv, T, self.max_rows, d)
             ws = max(qb.paged_workspace_size(shape, self.params, self.paging), 256)
             dt = torch.bfloat16 if self._out_dtype == qb.DT_BF16 else torch.float32
-            self._steps[T] = (shape, torch.zeros((B, Hq, T, d), dtype=torch.bfloat16, device=dev),
-                              torch.zeros((B, Hq, T, d), dtype=dt, device=dev),
-                              torch.zeros((B, Hq, T), dtype=torch.float32, device=dev),
-                              torch.empty(ws, dtype=torch.uint8, device=dev))
+            with torch.cuda.stream(stream):  # what is allocated and filled here belongs to the call's stream
+                self._steps[T] = (shape, torch.zeros((B, Hq, T, d), dtype=torch.bfloat16, device=dev),
+                                  torch.zeros((B, Hq, T, d), dtype=dt, device=dev),
+                                  torch.zeros((B, Hq, T), dtype=torch.float32, device=dev),
+                                  torch.empty(ws, dtype=torch.uint8, device=dev))
         return self._steps[T]
 
     def append(self, Q, K, V, stream=None):
         """Enter the tokens that the last ``grow`` made room for; returns Q rotated
         (Q itself without a rope)."""
-        shape, q_out = self._buffers(Q.shape[2])[:2]
+        shape, q_out = self._buffers(Q.shape[2], stream)[:2]
         turn = self.rope is not None
         qb.paged_append(K, V, shape, self.paging, self.page_table, self.lengths, self.k_pages, self.v_pages,
                         self.k_scales, self.v_scales, n_new=self.n_new, rope=self.rope, Q=Q if turn else None,
@@ -553,13 +555,14 @@ class PagedCache:
     def attend(self, Q, stream=None):
         """Attention of the last n_new[b] rows of each sequence; Q as ``append`` gave it.
         Returns O; ``lse(T)`` has the rows' lse."""
-        shape, _, O, lse, ws = self._buffers(Q.shape[2])
+        shape, _, O, lse, ws = self._buffers(Q.shape[2], stream)
         qb.paged_fwd(Q, shape, self.params, self.paging, self.page_table, self.lengths, self.k_pages,
                      self.v_pages, self.k_scales, self.v_scales, O, lse, ws, n_new=self.n_new, stream=stream)
         return O
 
-    def lse(self, T):
-        return self._buffers(T)[3]
+    def lse(self, T, stream=None):
+        """lse of the rows of the last step of T tokens (before the first: zeros)."""
+        return self._buffers(T, stream)[3]
 
     def step(self, Q, K, V, n_new=None, stream=None):
         """grow, append and attend: Q bf16 [B, Hq, T, d], K, V bf16 [B, Hkv, T, d] (any
