@@ -445,7 +445,12 @@ class PagedCache:
     ``append`` and ``attend`` wait for nothing and can be captured in a graph, replayed
     after each ``grow`` (grow is not captured).  All calls go to the current stream
     (or ``stream``); calls on several streams are ordered by the caller, the
-    constructor's among them, and the cache is kept until those streams are done with it."""
+    constructor's among them, and the cache is kept until those streams are done with it.
+
+    The rotated Q, O and lse that a call returns are the cache's own: one set, made of
+    zeros at the first step of its size, for all T up to the same power of two, written
+    over by the next step of that size.  A step is captured after an eager one of its
+    size: what a capture allocates belongs to the graph's memory."""
 
     def __init__(self, n_pages, page_size, Hq, Hkv, d, B, max_rows, *, code_dtype=qb.DT_I8, rope=None,
                  out_dtype=qb.DT_BF16, sm_scale=0.0, device="cuda"):
@@ -469,7 +474,7 @@ class PagedCache:
         self._pt.fill_(-1)
         self._meta.copy_(self._host)
         self._free = list(range(n_pages - 1, -1, -1))
-        self._steps = {}
+        self._sizes, self._steps = {}, {}
 
     def _views(self, t):
         B, width = self._dims[0], self.paging.max_pages
@@ -528,18 +533,29 @@ class PagedCache:
         self._upload(stream)
 
     def _buffers(self, T, stream=None):
-        """Shape, output buffers and workspace of steps of T tokens."""
+        """Shape, rotated Q (None without a rope), O, lse and workspace of steps of T tokens:
+        dense views of what is kept for T's size, the next power of two."""
         if T not in self._steps:
             B, Hq, Hkv, d = self._dims
-            dev = self._meta.device
-            shape = qb.make_shape(B, Hq, Hkv, T, self.max_rows, d)
-            ws = max(qb.paged_workspace_size(shape, self.params, self.paging), 256)
-            dt = torch.bfloat16 if self._out_dtype == qb.DT_BF16 else torch.float32
+            dev, size = self._meta.device, 1 << max(T - 1, 0).bit_length()
+            shape, largest = (qb.make_shape(B, Hq, Hkv, n, self.max_rows, d) for n in (T, size))
+            ws = max(256, *(qb.paged_workspace_size(s, self.params, self.paging) for s in (shape, largest)))
             with torch.cuda.stream(stream):  # what is allocated and filled here belongs to the call's stream
-                self._steps[T] = (shape, torch.zeros((B, Hq, T, d), dtype=torch.bfloat16, device=dev),
-                                  torch.zeros((B, Hq, T, d), dtype=dt, device=dev),
-                                  torch.zeros((B, Hq, T), dtype=torch.float32, device=dev),
-                                  torch.empty(ws, dtype=torch.uint8, device=dev))
+                if size not in self._sizes:
+                    dt, rows = torch.bfloat16 if self._out_dtype == qb.DT_BF16 else torch.float32, B * Hq * size
+                    q_out = None if self.rope is None else torch.zeros(rows * d, dtype=torch.bfloat16, device=dev)
+                    self._sizes[size] = (q_out, torch.zeros(rows * d, dtype=dt, device=dev),
+                                         torch.zeros(rows, dtype=torch.float32, device=dev), [])
+                q_out, O, lse, spaces = self._sizes[size]
+                # (one that turns out too small is kept all the same: a captured step may use it)
+                if not spaces or spaces[-1].numel() < ws:
+                    spaces.append(torch.empty(ws, dtype=torch.uint8, device=dev))
+            if len(self._steps) >= 64:  # views alone: they are made again
+                self._steps.clear()
+            dims = (B, Hq, T, d)
+            n = B * Hq * T
+            self._steps[T] = (shape, None if q_out is None else q_out[:n * d].view(dims), O[:n * d].view(dims),
+                              lse[:n].view(dims[:3]), spaces[-1])
         return self._steps[T]
 
     def append(self, Q, K, V, stream=None):
@@ -561,7 +577,7 @@ class PagedCache:
         return O
 
     def lse(self, T, stream=None):
-        """lse of the rows of the last step of T tokens (before the first: zeros)."""
+        """lse of the rows of the last step, if that was one of T tokens."""
         return self._buffers(T, stream)[3]
 
     def step(self, Q, K, V, n_new=None, stream=None):

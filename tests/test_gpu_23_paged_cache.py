@@ -45,3 +45,66 @@ def test_steps_on_a_given_stream(rope):
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(E.lse(T), lse)
     assert qb.get_error() == 0
+
+
+@pytest.mark.parametrize("rope", [True, False], ids=["rope", "plain"])
+def test_token_counts_share_their_buffers(rope):
+    """Steps of many token counts keep what the largest of a power of two needs, and no
+    more; each gives what the calls give in buffers of their own."""
+    B, Hq, Hkv, d = 2, 8, 2, 64
+    C, = caches(1, B, Hq, Hkv, d, 4096, rope=rope, out_dtype=qb.DT_F32)
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def step(T):
+        q, k, v = tokens(C, g, T)
+        O, lse = C.step(q, k, v), C.lse(T)
+        assert O.shape == (B, Hq, T, d) and O.is_contiguous() and lse.shape == (B, Hq, T) and lse.is_contiguous()
+        turned = q
+        if rope:
+            turned = torch.empty_like(q)
+            row = torch.arange(C.rows(0) - T, C.rows(0), dtype=torch.int32, device="cuda")
+            qb.rotate(q, turned, C.rope, positions=row.repeat(B, 1))
+        shape = qb.make_shape(B, Hq, Hkv, T, C.max_rows, d)
+        own, own_lse = torch.empty_like(O), torch.empty_like(lse)
+        ws = torch.empty(max(qb.paged_workspace_size(shape, C.params, C.paging), 256), dtype=torch.uint8, device="cuda")
+        qb.paged_fwd(turned, shape, C.params, C.paging, C.page_table, C.lengths, C.k_pages, C.v_pages, C.k_scales,
+                     C.v_scales, own, own_lse, ws, n_new=C.n_new)
+        assert torch.equal(O, own) and torch.equal(lse, own_lse)
+
+    step(33)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for T in (64, 34, 47, 63, 50, 33, 48, 64):
+        step(T)
+    assert torch.cuda.memory_allocated() == before
+    for T in (1, 2, 3, 5, 8, 13, 17, 32, 100):  # seven more sizes: 1, 2, 4, 8, 16, 32, 128
+        step(T)
+    row = B * Hq * (4 * d + 4 + (2 * d if rope else 0))  # O and lse, and Q if it is rotated
+    spaces = sum(max(qb.paged_workspace_size(qb.make_shape(B, Hq, Hkv, T, C.max_rows, d), C.params, C.paging), 256)
+                 for T in (1, 2, 4, 8, 16, 32, 128))
+    assert torch.cuda.memory_allocated() - before <= row * (1 + 2 + 4 + 8 + 16 + 32 + 128) + 2 * spaces + 28 * 512
+    assert qb.get_error() == 0
+
+
+def test_a_captured_step_keeps_its_buffers():
+    """A graph of steps of five tokens, replayed between eager steps of other counts."""
+    C, E = caches(2, 2, 4, 2, 64, 2048, out_dtype=qb.DT_F32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = tokens(C, g, 5)
+    for c in (C, E):
+        c.step(*x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O = C.attend(C.append(*x))
+    for T in (5, 8, 200, 5, 7, 6, 300, 1, 5):
+        if T == 5:
+            for t, y in zip(x, tokens(C, g, 5)):
+                t.copy_(y)
+            C.grow([5, 5])
+            graph.replay()
+            assert torch.equal(O, E.step(*x))
+        else:
+            y = tokens(C, g, T)
+            assert torch.equal(C.step(*y), E.step(*y))
+    assert torch.equal(C.k_pages, E.k_pages) and torch.equal(C.v_scales, E.v_scales)
+    assert qb.get_error() == 0
