@@ -570,6 +570,21 @@ def _strided_ptr(dev: int, name: str, t, dtype, shape):
     return t.data_ptr(), None if t.is_contiguous() else (ctypes.c_int64 * 4)(*t.stride())
 
 
+def paged_input(name, t, shape):
+    """Raises what paged_append and paged_fwd raise of a bf16 input of this shape that
+    they do not take; nothing is launched."""
+    ptr, strides = _strided_ptr(torch.cuda.current_device(), name, t, torch.bfloat16, shape)
+    if t.numel() and (ptr % 16 or strides and (strides[3] != 1 or any(s % 8 for s in strides[:3]))):
+        raise QattnError(ERR_INVALID_ARG, f"{name}, whose rows are not dense or not on 16-byte boundaries")
+
+
+def paged_params(shape, params, paging):
+    """Raises what paged_fwd raises of parameters that it does not take; nothing is
+    launched (the problem has no queries)."""
+    none = Shape(shape.B, shape.Hq, shape.Hkv, 0, shape.Nk, shape.d)
+    _check(lib().qattn_paged_fwd(None, None, none, params, None, None, paging, *[None] * 8, 0, None), "qattn_paged_fwd")
+
+
 def rotate(X, Y, rope, *, positions=None, stream=None):
     """Rotary positions: X [B, H, T, d] (bf16 or fp32, any strides) rotated into the
     dense Y (see qattn_rotate in include/qattn.h).  positions: int32 [B, T] (None:

@@ -492,8 +492,8 @@ class PagedCache:
         return int(self._len[b])
 
     def grow(self, n_new, stream=None):
-        """Pages for n_new[b] (host numbers) more rows of each sequence; ValueError, and
-        nothing changed, where a sequence would pass max_rows or the pool runs out."""
+        """Pages for n_new[b] (host numbers) more rows of each sequence; ValueError where a
+        sequence would pass max_rows or the pool runs out.  A call that fails changes nothing."""
         B, page = self._dims[0], self.paging.page_size
         n = [int(x) for x in n_new]
         if len(n) != B or min(n, default=0) < 0:
@@ -504,15 +504,21 @@ class PagedCache:
         want = [(-(-h // page), -(-(h + x) // page)) for h, x in zip(have, n)]
         if sum(e - s for s, e in want) > len(self._free):
             raise ValueError("the pool has too few free pages")
+        last = self._new.clone()
         for b, (s, e) in enumerate(want):
             for j in range(s, e):
                 self._pt[b, j] = self._free.pop()
         self._len += torch.tensor(n, dtype=torch.int32)
         self._new.copy_(torch.tensor(n, dtype=torch.int32))
-        self._upload(stream)
+        try:
+            self._upload(stream)
+        except Exception:
+            self._shrink(n, last)
+            raise
 
-    def _shrink(self, n, stream):
-        """Take the last grow back, its pages in the order in which they lay in the pool."""
+    def _shrink(self, n, last):
+        """Take the last grow back on the host, its pages in the order in which they lay in
+        the pool; last: n_new before it."""
         page = self.paging.page_size
         for b, x in reversed(list(enumerate(n))):
             have = int(self._len[b])
@@ -520,8 +526,7 @@ class PagedCache:
             self._free.extend(reversed(self._pt[b, s:e].tolist()))
             self._pt[b, s:e] = -1
             self._len[b] = have - x
-            self._new[b] = 0
-        self._upload(stream)
+        self._new.copy_(last)
 
     def release(self, b, stream=None):
         """Sequence b is done: its pages go back to the pool."""
@@ -539,6 +544,7 @@ class PagedCache:
             B, Hq, Hkv, d = self._dims
             dev, size = self._meta.device, 1 << max(T - 1, 0).bit_length()
             shape, largest = (qb.make_shape(B, Hq, Hkv, n, self.max_rows, d) for n in (T, size))
+            qb.paged_params(shape, self.params, self.paging)  # (append does not look at all of them)
             ws = max(256, *(qb.paged_workspace_size(s, self.params, self.paging) for s in (shape, largest)))
             with torch.cuda.stream(stream):  # what is allocated and filled here belongs to the call's stream
                 if size not in self._sizes:
@@ -563,6 +569,8 @@ class PagedCache:
         (Q itself without a rope)."""
         shape, q_out = self._buffers(Q.shape[2], stream)[:2]
         turn = self.rope is not None
+        if not turn:  # (attend's to refuse, but K and V would be in the pages by then)
+            qb.paged_input("Q", Q, (shape.B, shape.Hq, shape.Nq, shape.d))
         qb.paged_append(K, V, shape, self.paging, self.page_table, self.lengths, self.k_pages, self.v_pages,
                         self.k_scales, self.v_scales, n_new=self.n_new, rope=self.rope, Q=Q if turn else None,
                         Q_out=q_out if turn else None, stream=stream)
@@ -584,15 +592,17 @@ class PagedCache:
         """grow, append and attend: Q bf16 [B, Hq, T, d], K, V bf16 [B, Hkv, T, d] (any
         strides), n_new: tokens of each sequence (host numbers; None: T each).  Rows
         behind a sequence's tokens in the returned O are left as they were.  Arguments
-        that are refused leave the sequences as they were."""
+        that are refused leave the sequences and their pages as they were."""
         n = [Q.shape[2]] * self._dims[0] if n_new is None else [int(x) for x in n_new]
         if max(n, default=0) > Q.shape[2]:
             raise ValueError(f"n_new: more tokens than the {Q.shape[2]} of Q")
+        last = self._new.clone()
         self.grow(n, stream)
         try:
             return self.attend(self.append(Q, K, V, stream), stream)
         except Exception:
-            self._shrink(n, stream)
+            self._shrink(n, last)
+            self._upload(stream)
             raise
 
 

@@ -108,3 +108,46 @@ def test_a_captured_step_keeps_its_buffers():
             assert torch.equal(C.step(*y), E.step(*y))
     assert torch.equal(C.k_pages, E.k_pages) and torch.equal(C.v_scales, E.v_scales)
     assert qb.get_error() == 0
+
+
+@pytest.mark.parametrize("rope", [True, False], ids=["rope", "plain"])
+def test_a_refused_step_leaves_the_pages(rope):
+    """A Q that attention refuses, beside K and V that would make the held pages' scales
+    grow or end them: nothing of the step has reached the cache."""
+    B, Hq, Hkv, d = 2, 4, 2, 64
+    C, E = caches(2, B, Hq, Hkv, d, 128, rope=rope, out_dtype=qb.DT_F32)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = tokens(C, g, 40)
+    for c in (C, E):
+        c.step(*x, n_new=[40, 3])
+    Q, K, V = tokens(C, g, 9, 50.0)
+    V[1, 0, 2, 5] = float("inf")
+    shifted = torch.empty(Q.numel() + 1, dtype=Q.dtype, device="cuda")[1:].view(Q.shape)  # two bytes off
+    odd = torch.empty(B, Hq, 9, d + 1, dtype=Q.dtype, device="cuda")[..., :d]             # rows 130 bytes apart
+    split = torch.empty(B, Hq, 9, 2 * d, dtype=Q.dtype, device="cuda")[..., ::2]          # channels apart
+    for bad, error in ((Q.float(), TypeError), (Q[:, :3], ValueError), (Q[:1], ValueError), (Q[..., :32], ValueError),
+                       (Q.cpu(), ValueError), (shifted, qb.QattnError), (odd, qb.QattnError), (split, qb.QattnError)):
+        with pytest.raises(error):
+            C.step(bad, K, V)
+        for a, b in ((C.k_pages, E.k_pages), (C.v_pages, E.v_pages), (C.k_scales, E.k_scales), (C.v_scales, E.v_scales),
+                     (C.page_table, E.page_table), (C.lengths, E.lengths), (C.n_new, E.n_new)):
+            assert torch.equal(a, b)
+        assert C.free_pages() == E.free_pages() and C.rows(0) == 40 and C.rows(1) == 3
+    for side in (5, "side"):  # no stream
+        with pytest.raises(AttributeError):
+            C.step(Q, K, V, stream=side)
+        assert C.free_pages() == E.free_pages() and C.rows(0) == 40 and torch.equal(C.n_new, E.n_new)
+    V[1, 0, 2, 5] = 1.0
+    assert torch.equal(C.step(Q, K, V), E.step(Q, K, V)) and torch.equal(C.k_pages, E.k_pages)
+    assert qb.get_error() == 0
+
+
+@pytest.mark.parametrize("rope", [True, False], ids=["rope", "plain"])
+def test_parameters_that_attention_refuses(rope):
+    """They are found before the tokens are entered."""
+    for kw in (dict(sm_scale=-1.0), dict(sm_scale=float("nan")), dict(out_dtype=qb.DT_I8)):
+        C, = caches(1, 1, 4, 2, 64, 64, rope=rope, **kw)
+        x = tokens(C, torch.Generator(device="cuda").manual_seed(5), 3)
+        with pytest.raises(qb.QattnError):
+            C.step(*x)
+        assert not C.k_pages.any() and not C.v_scales.any() and C.rows(0) == 0 and C.free_pages() == 3
