@@ -653,10 +653,12 @@ typedef struct {
  *   Q_out (out)    bf16 [B][Hq][T][d]; rows t >= n_new[b] are left as they were
  * The pages that a call writes belong to one sequence each (a page shared with
  * another is copied first).  A sequence whose length or n_new is out of range is left
- * as it is; so are the rows of a page that is not in 0 .. n_pages - 1 and tokens
- * whose position is outside the table.  Each is reported: qattn_get_error() returns
- * QATTN_ERR_INVALID_ARG.  Limits: d in {64, 128}, n_pages * Hkv <= 2^31 - 1, T <=
- * 65534 * page_size.  No workspace. */
+ * as it is; so are the rows of a page that is not in 0 .. n_pages - 1.  A token whose
+ * position is outside the table has no rotation: its row of K and of Q_out is not
+ * written and does not count for K's scale; its V, which does not turn, is entered as
+ * any other.  Each is reported: qattn_get_error() returns QATTN_ERR_INVALID_ARG.
+ * Limits: d in {64, 128}, n_pages * Hkv <= 2^31 - 1, T <= 65534 * page_size.  No
+ * workspace. */
 qattn_status qattn_paged_append(const uint16_t* Q, const int64_t* q_strides, const uint16_t* K,
                                 const int64_t* k_strides, const uint16_t* V,
                                 const int64_t* v_strides, const qattn_shape* shape,
