@@ -245,10 +245,14 @@ struct Team {
   uint32_t (*red)[32];  // [2][warps] (CTA)
   __device__ __forceinline__ int size() const { return CTA ? blockDim.x : 32; }
   __device__ __forceinline__ int rank() const { return CTA ? threadIdx.x : threadIdx.x & 31; }
-  // The largest x of the team; between what its threads did before and do after it.
+  // The largest x of the team.  What its threads read and wrote before lies before what they
+  // do after it (the page's scale: all read it, one then writes it; a warp's reduction alone
+  // does not order memory).
   __device__ __forceinline__ uint32_t largest(uint32_t x, int turn) const {
     x = __reduce_max_sync(0xffffffffu, x);
-    if constexpr (CTA) {
+    if constexpr (!CTA) {
+      __syncwarp();
+    } else {
       if ((threadIdx.x & 31) == 0) red[turn & 1][threadIdx.x >> 5] = x;
       __syncthreads();
       x = 0;
