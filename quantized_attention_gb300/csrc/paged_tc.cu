@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const PagedArgs a
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  pdl_trigger();  // after the wait: the join reads the lengths before its own
+  pdl_trigger();
   // Segment `seg` (from 0) of this CTA's share; n() == 0: there is none.
   PagedSeg* const slots = reinterpret_cast<PagedSeg*>(smem + C::kOffSeg);
   auto fetch = [&](uint32_t seg, const PagedSeg*& sg) {
