@@ -650,7 +650,8 @@ typedef struct {
  *   n_new          NULL (T everywhere), or int32 [B], device, 0 .. T
  *   positions      NULL (token's row), or int32 [B][T], device
  *   rope           NULL (K and Q as they are), or the rotation
- *   Q_out (out)    bf16 [B][Hq][T][d]; rows t >= n_new[b] are left as they were
+ *   Q_out (out)    bf16 [B][Hq][T][d], Q itself if Q is dense; rows t >= n_new[b] are
+ *                  left as they were
  * The pages that a call writes belong to one sequence each (a page shared with
  * another is copied first).  A sequence whose length or n_new is out of range is left
  * as it is; so are the rows of a page that is not in 0 .. n_pages - 1.  A token whose

@@ -410,7 +410,8 @@ __device__ __forceinline__ void append_q(const PagedAppendArgs& a, int b, const 
 // KV head.  Four prompts of 1.4K to 4.1K tokens, 32 + 2 x 8 heads of 128 channels, 252 MB: 59 us,
 // 4.3 TB/s (63%).  Q alone would take 34 us at the rate of the rotation; K and V, 67 MB, are
 // bound by latency: a CTA's way from the lengths to the rows, the maximum over the page, the
-// codes, with two CTAs an SM at 64 registers (three, which spill: 74 us).
+// codes, with two CTAs an SM at 64 registers, 28 bytes of them spilled (three, at 40
+// registers: 74 us).
 constexpr int kPageItems = 4;  // items of a page that a thread holds
 template <bool E4M3, int WQ>
 __global__ void __launch_bounds__(512, 2) paged_append_kernel(const PagedAppendArgs a) {

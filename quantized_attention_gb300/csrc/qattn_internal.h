@@ -431,13 +431,16 @@ struct PagedAppendArgs {
   int heads, kv_groups, q_heads, touched;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
-// Heads a thread turns by the same angles: more save angles, fewer make more CTAs (4 against
-// 8, 32 heads, cold L2: 512 / 2K / 4K / 8K / 16K tokens 10.9 / 12.9 / 21.1 / 33.4 / 55.9 us
-// against 12.9 / 15.0 / 19.1 / 31.4 / 55.9).
+// (Figures of these rules, here and below: us of one call behind a flush of L2 in a replayed
+// graph, the flush's own time taken off; they repeat to 0.3 us.)
+// Heads a thread turns by the same angles: more save angles, fewer make more CTAs.  4 against
+// 8: 32 heads of 512 / 1K / 2K / 4K / 8K / 16K tokens 6.0 / 7.0 / 9.2 / 15.8 / 28.3 / 51.2 against
+// 8.8 / 9.6 / 11.0 / 15.2 / 27.7 / 51.4; half of 12 heads turned back, 8 x 512 / 1K / 2K 7.0 / 8.8 /
+// 14.9 against 10.0 / 11.3 / 14.1.
 constexpr int kRotateHeads = 4;
 // New tokens of a sequence up to which a warp takes a page of a head, not a CTA.  Measured, 1,
-// 16 and 64 sequences of 8 KV heads, us: 4 tokens 8.9 / 10.9 / 10.9 against 13.0 / 13.0 / 19.1, 16
-// tokens 13.0 / 15.0 / 21.2 against 12.9 / 15.0 / 21.2.
+// 16 and 64 sequences of 8 KV heads: 1 token 5.5 / 5.6 / 6.1 against 7.8 / 8.5 / 13.4, 4 tokens 5.4 /
+// 5.9 / 7.0 against 7.9 / 9.2 / 15.4, 16 tokens 8.5 / 9.4 / 17.6 against 8.3 / 9.8 / 17.6.
 constexpr int kAppendFew = 16;
 // Q heads of a warp or CTA, KV heads of a CTA (uneven prompts: 8 and 1, 61 us; 4 and 1, 66;
 // 8 and 2, 62).
@@ -459,18 +462,22 @@ constexpr int kPagedCluster = 8;  // most CTAs of a block's own cluster
 // 20.0, shares 9.8 / 11.0 / 11.8 / 15.5 / 15.9; d = 64: 6.1 / 7.6 / 8.4 / 10.2 / 12.5, 6.1 / 8.7 /
 // 10.2 / 13.1 / 16.3, 8.6 / 9.7 / 10.9 / 12.3 / 13.5.  (Of two sequences of uneven length shares
 // would be faster from 8K on: the bound lies between.)  tree_cluster's choice here, clusters against
-// shares, us with a cold L2, d = 128: 16 heads of 2K / 4K / 8K 13 / 17 / 21 against 17 / 19 / 23; 64 of
-// 500 / 4K / 16K 13 / 25 / 62 against 17 / 30 / 66, of 0.2 to 16K 48 / 43; 128 of 4K / 8K 40 / 62 against
-// 44 / 68, of 0.2 to 16K 85 / 69; 256 of 500 / 2K 17 / 38 against 24 / 42.
+// shares, d = 128: 16 heads of 2K / 4K / 8K 8.6 / 11.0 / 16.1 against 10.9 / 13.4 / 17.0; 64 of 500 /
+// 4K / 16K 8.9 / 19.9 / 57.9 against 11.5 / 23.5 / 62.0, of 0.2 to 16K 43.4 / 37.4; 128 of 4K / 8K 33.2 /
+// 58.0 against 36.9 / 62.3, of 0.2 to 16K 80.2 / 63.2; 256 of 500 / 2K 13.3 / 33.1 against 18.5 / 37.2.
+// It takes shares for 16 of 8K, 64 of 16K and 128 of 8K: heads of equal length lose 1 to 4 us by
+// that, and uneven ones, which it cannot tell from them, gain more.
 constexpr int kPagedWideCtas = 64, kPagedWideSteps = 192;
 // More rows go to the tensor-core kernel, which widens a code once for 256 rows, but takes
-// some 10 us longer to start and to join: up to kPagedFewRows, while the warp-level kernel's
+// some 4 us longer to start and to join: up to kPagedFewRows, while the warp-level kernel's
 // blocks have no more than kPagedFewWork keys to pass over in all, that one is the faster.
-// Measured, warp-level against tensor cores, us, with a cold L2, B sequences of L rows, 8 KV
-// heads: d = 128, 64 rows: B = 1, L = 1K (32K keys) 15 / 23, 4K (131K) 19 / 29; B = 16 of 1K
-// (524K) 46 / 42, 1 of 32K (1M) 64 / 52, 16 of 4K (2M) 119 / 83; 32 rows: 4 of 4K (262K) 25 /
-// 39, 64 of 1K (1M) 114 / 101, 16 of 4K (1M) 72 / 84.  d = 64, 64 rows: 1 of 4K 15 / 21, 4 of
-// 4K (524K) 27 / 27, 16 of 1K 35 / 29; 32 rows: 16 of 1K (262K) 21 / 30, 16 of 4K (1M) 57 / 53.
+// Measured, warp-level against tensor cores, B sequences of L rows, 8 KV heads (in brackets the
+// keys).  d = 128, 64 rows: B = 1 of 1K (32K) 10.6 / 14.8, 4K (131K) 14.0 / 18.6, 32K (1M) 59.9 /
+// 41.9; 4 of 4K (524K) 32.3 / 27.4, 16 of 1K 40.6 / 29.8, of 4K (2M) 117 / 73; 32 rows: 4 of 4K
+// (262K) 20.2 / 26.4, 16 of 1K 21.7 / 28.0, 1 of 32K (524K) 39.9 / 41.0, 16 of 4K (1M) 69.8 / 71.8,
+// 64 of 1K 112 / 87.  d = 64, 64 rows: 1 of 4K 11.2 / 15.1, 4 of 4K 23.5 / 20.2, 16 of 1K 30.0 / 22.8,
+// of 4K 85.7 / 46.6; 32 rows: 4 of 4K 15.5 / 19.5, 16 of 1K 16.0 / 22.2, 1 of 32K 28.9 / 27.8, 16 of 4K
+// 53.3 / 46.0, 64 of 1K 90.2 / 64.3.
 constexpr int kPagedFewRows = 64;
 constexpr long long kPagedFewWork = 3LL << 17;
 // The tensor-core kernel: rows of a block, keys of a step, CTAs at most (one an SM), steps

@@ -441,7 +441,8 @@ class PagedCache:
     n_pages pages of page_size rows; max_rows: most rows of a sequence; rope: the
     rotation (None: none), its table for max_rows positions.  Pages are dealt on the
     host: ``grow`` and ``release`` keep ``page_table``, ``lengths`` and ``n_new`` on
-    the device in step by one copy (which waits until the host's numbers are read);
+    the device in step by one copy from pageable memory, for which the host waits, and so
+    for what the stream holds, the step before included;
     ``append`` and ``attend`` wait for nothing and can be captured in a graph, replayed
     after each ``grow`` (grow is not captured).  All calls go to the current stream
     (or ``stream``); calls on several streams are ordered by the caller, the
