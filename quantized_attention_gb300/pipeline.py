@@ -505,21 +505,21 @@ class PagedCache:
         want = [(-(-h // page), -(-(h + x) // page)) for h, x in zip(have, n)]
         if sum(e - s for s, e in want) > len(self._free):
             raise ValueError("the pool has too few free pages")
-        last = self._new.clone()
         for b, (s, e) in enumerate(want):
             for j in range(s, e):
                 self._pt[b, j] = self._free.pop()
-        self._len += torch.tensor(n, dtype=torch.int32)
-        self._new.copy_(torch.tensor(n, dtype=torch.int32))
+        self._last, counts = self._new.clone(), torch.tensor(n, dtype=torch.int32)  # (_last: for _shrink)
+        self._len += counts
+        self._new.copy_(counts)
         try:
             self._upload(stream)
         except Exception:
-            self._shrink(n, last)
+            self._shrink(n)
             raise
 
-    def _shrink(self, n, last):
+    def _shrink(self, n):
         """Take the last grow back on the host, its pages in the order in which they lay in
-        the pool; last: n_new before it."""
+        the pool."""
         page = self.paging.page_size
         for b, x in reversed(list(enumerate(n))):
             have = int(self._len[b])
@@ -527,7 +527,7 @@ class PagedCache:
             self._free.extend(reversed(self._pt[b, s:e].tolist()))
             self._pt[b, s:e] = -1
             self._len[b] = have - x
-        self._new.copy_(last)
+        self._new.copy_(self._last)
 
     def release(self, b, stream=None):
         """Sequence b is done: its pages go back to the pool."""
@@ -597,12 +597,11 @@ class PagedCache:
         n = [Q.shape[2]] * self._dims[0] if n_new is None else [int(x) for x in n_new]
         if max(n, default=0) > Q.shape[2]:
             raise ValueError(f"n_new: more tokens than the {Q.shape[2]} of Q")
-        last = self._new.clone()
         self.grow(n, stream)
         try:
             return self.attend(self.append(Q, K, V, stream), stream)
         except Exception:
-            self._shrink(n, last)
+            self._shrink(n)
             self._upload(stream)
             raise
 
